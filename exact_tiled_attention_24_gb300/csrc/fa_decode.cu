@@ -636,6 +636,22 @@ __global__ void __launch_bounds__(THREADS, Cfg<GM>::CTAS) decode_mma_kernel(
           }
         }
       }
+      // A box brings whole cache blocks: slots past the context hold whatever
+      // the cache holds there, and a NaN of theirs would outlive its zero
+      // probability. The last tile's dead value rows are zeroed (gathered
+      // tiles arrive zero-filled). The scores run a tile ahead, so V_{j-1} may
+      // not have landed yet: O_{j-1} first (exact, as above), after which
+      // v_full is at phase j or past it and its parity wait is exact too.
+      if (LOAD == BOXES && (tile0 + j + 1) * TK > t_end) {
+        const int vs = j % VST;
+        if (ok && j > 0) ok = mbar_wait(o_done, (j - 1) & 1, err);
+        if (ok) ok = mbar_wait(&v_full[vs], (j / VST) & 1, err);
+        if (ok && !live)
+          for (int i = 0; i < L::KPANELS * 8; ++i)
+            *reinterpret_cast<uint4*>(sV + vs * L::V_TILE + (i >> 3) * L::PANEL + r * 128 + (i & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
       // P_j (bf16) into Pᵀ buffer j % PB once O_{j-PB} has read it.
       if (ok) ok = mbar_wait(&p_empty[pb], ((j / PB) & 1) ^ 1, err);
       uint8_t* pbuf = sP + pb * 2 * L::QPANEL + (r / 64) * L::QPANEL;

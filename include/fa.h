@@ -332,7 +332,8 @@ int fa_attn_merge(const float* o_parts, const float* lse_parts, int n_parts, voi
  *   block_table  [B][max_blocks_per_seq] int32 device array.
  *   seq_lens     [B] int32 device array: cached tokens per request (clamped
  *                to [0, max_blocks_per_seq·block_size]; 0 gives o = 0,
- *                lse = -inf).
+ *                lse = -inf). Slots past a request's length may hold
+ *                anything.
  *   o, lse       [B][H][d] bf16 and [B][H] fp32 outputs: attention of each
  *                query row over its request's tokens (no mask beyond the
  *                context length); query head h reads K/V head h / (H/Hkv).
