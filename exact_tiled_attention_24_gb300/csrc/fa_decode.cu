@@ -40,9 +40,16 @@ namespace dec {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
+// Larger of two, NaN if either is: a part whose lse is NaN makes its row NaN
+// and is not taken for one without keys.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -66,7 +73,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ o_
   const long long prt = static_cast<long long>(S) * rows;  // rows of the partial results
   float m = -INFINITY;
   for (int s = lane; s < S; s += 32)
-    if (in_range(s * rows + row, 1, prt, err)) m = fmaxf(m, lse_parts[s * rows + row]);
+    if (in_range(s * rows + row, 1, prt, err)) m = max_nan(m, lse_parts[s * rows + row]);
   m = warp_max(m);
   float l = 0.f;
   float acc[CPL];
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ o_
     if (in_range(row * D + lane * CPL + j, 2, rows * D, err))
       *reinterpret_cast<__nv_bfloat162*>(o + row * D + lane * CPL + j) =
           __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
-  if (lane == 0 && in_range(row, 1, rows, err)) lse[row] = l > 0.f ? m + __logf(l) : -INFINITY;
+  if (lane == 0 && in_range(row, 1, rows, err)) lse[row] = l == 0.f ? -INFINITY : m + __logf(l);
 }
 
 }  // namespace dec

@@ -24,3 +24,18 @@ def test_slots_past_the_length_may_hold_anything(fa, d, bs, lens, S):  # noqa: F
         o, lse = run_case(fa, q, kc, vc, table, L, S, d ** -0.5)
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_merge_keeps_nan_rows_nan(fa, d):  # noqa: F811
+    g = torch.Generator().manual_seed(d)
+    o_parts, lse_parts = torch.randn((3, 8, d), generator=g), torch.randn((3, 8), generator=g)
+    clean = fa.attn_merge(o_parts.cuda(), lse_parts.cuda())
+    nan, inf = float("nan"), float("inf")
+    lse_parts[0, 0] = nan                                          # one part of a row
+    lse_parts[:, 1] = torch.tensor([-inf, nan, -inf])              # the only part with keys
+    lse_parts[:, 2] = nan
+    lse_parts[:, 3] = -inf
+    o, lse = fa.attn_merge(o_parts.cuda(), lse_parts.cuda())
+    assert bool(o[:3].isnan().all()) and bool(lse[:3].isnan().all())
+    assert bool((o[3] == 0).all()) and bool(torch.isneginf(lse[3]))
+    assert torch.equal(o[4:], clean[0][4:]) and torch.equal(lse[4:], clean[1][4:])
