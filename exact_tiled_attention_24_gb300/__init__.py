@@ -35,6 +35,14 @@ __all__ = [
     "fwd_host",
     "fwd_bwd_host",
     "softmax_host",
+    "rope_tables",
+    "qk_norm_rope",
+    "qk_norm_rope_bwd",
+    "qk_norm_rope_bwd_workspace_bytes",
+    "append_paged",
+    "append_paged_q4",
+    "decode_paged_q4",
+    "decode_q4_splits",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -82,12 +90,29 @@ EXPORTED_SYMBOLS = (
     "fa_fwd_bwd_host",
     "fa_softmax_host",
     "fa_debug_checks",
+    "fa_qk_norm_rope",
+    "fa_qk_norm_rope_bwd_workspace_bytes",
+    "fa_qk_norm_rope_bwd",
+    "fa_append_paged",
+    "fa_append_paged_q4",
+    "fa_decode_q4_splits",
+    "fa_decode_paged_q4",
 )
 
 
 class Tensors(ctypes.Structure):
     """fa_tensors: addresses of one problem's q, k, v, dO, o, lse, dq, dk, dv."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "dO", "o", "lse", "dq", "dk", "dv")]
+
+
+class Heads(ctypes.Structure):
+    """fa_heads: address and strides (elements) of a [B][heads][N][d] tensor."""
+    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in ("stride_b", "stride_h", "stride_n")]
+
+
+class Tokens(ctypes.Structure):
+    """fa_tokens: address and strides (elements) of a [T][heads][d] tensor."""
+    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in ("stride_t", "stride_h")]
 
 
 class FAError(RuntimeError):
@@ -147,6 +172,21 @@ def lib() -> ctypes.CDLL:
         L.fa_fwd_bwd_host.restype = i
         L.fa_softmax_host.argtypes = [vp, vp, vp, vp, ctypes.c_longlong, i, i, i, vp]
         L.fa_softmax_host.restype = i
+        hp, kp = ctypes.POINTER(Heads), ctypes.POINTER(Tokens)
+        L.fa_qk_norm_rope.argtypes = [hp] * 4 + [vp, vp, vp, i, vp, vp] + [i] * 8 + [f, i, vp]
+        L.fa_qk_norm_rope.restype = i
+        L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i]
+        L.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        L.fa_qk_norm_rope_bwd.argtypes = [hp] * 6 + [vp] * 5 + [i, vp, vp, i, vp, sz] + [i] * 7 + [f, i, vp]
+        L.fa_qk_norm_rope_bwd.restype = i
+        L.fa_append_paged.argtypes = [kp] * 4 + [vp] * 9 + [i] * 11 + [f, i, vp]
+        L.fa_append_paged.restype = i
+        L.fa_append_paged_q4.argtypes = [kp] * 4 + [vp] * 13 + [i] * 11 + [f, i, vp]
+        L.fa_append_paged_q4.restype = i
+        L.fa_decode_q4_splits.argtypes = [i] * 5
+        L.fa_decode_q4_splits.restype = i
+        L.fa_decode_paged_q4.argtypes = [vp] * 10 + [sz] + [i] * 7 + [f, i, vp]
+        L.fa_decode_paged_q4.restype = i
         L.fa_last_device_error.argtypes = [vp]
         L.fa_last_device_error.restype = i
         L.fa_selftest_wait_limit.argtypes = [vp]
@@ -511,3 +551,314 @@ def softmax_host(x_host, y_host, x_dev, y_dev, online=True, n_chunks=0):
     rows = x_host.numel() // n if n else 0
     _check(lib().fa_softmax_host(_ptr(x_host), _ptr(y_host), _ptr(x_dev), _ptr(y_dev), rows, n,
                                  int(bool(online)), int(n_chunks), _stream(x_dev.device)), "fa_softmax_host")
+
+
+# ---------------------------------- norms, rotation, paged appends, 4-bit cache
+
+def rope_tables(n_pos, rot, base=10000.0, device=None):
+    """cos, sin [n_pos, rot/2] fp32 of the usual rotary angles, position ·
+    base^(-2i/rot), formed in 64 bits (a far position's angle has no correct
+    digits left in 32) and rounded once. Make them once and keep them."""
+    if n_pos < 1 or rot < 2 or rot % 2:
+        raise ValueError("n_pos must be at least 1 and rot even")
+    device = torch.device(_DEVICE_TYPE) if device is None else device
+    freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def _strided_rows(t, name, shape, device, out=False):
+    """Raise unless t is a bf16 tensor of `shape` on `device` whose last
+    dimension is contiguous and whose rows sit on 16-byte boundaries (for an
+    output: with no two rows overlapping)."""
+    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != torch.bfloat16
+            or t.device != device):
+        raise ValueError(f"{name}: expected a {torch.bfloat16} tensor of shape {tuple(shape)} on {device}")
+    st = t.stride()
+    if st[-1] != 1 or any(s % 8 for s, n in zip(st[:-1], shape) if n > 1):
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8")
+    if out:
+        need = shape[-1]
+        for s, n in sorted((s, n) for s, n in zip(st[:-1], shape) if n > 1):
+            if s < need:
+                raise ValueError(f"{name}: an output's rows must not overlap")
+            need = s * n
+    return t
+
+
+def _strides(t):
+    """Strides but the last; a dimension of one element has no stride to speak of."""
+    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+def _heads(t):
+    return Heads(t.data_ptr(), *_strides(t))
+
+
+def _tokens_of(t):
+    return Tokens(t.data_ptr(), *_strides(t))
+
+
+def _rope_args(cos, sin, q_weight, k_weight, d, device):
+    """Check tables and weights; returns (rot, n_pos, weight_fp32)."""
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot = n_pos = 0
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos and sin must be [n_pos, rot/2]")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if n_pos < 1 or rot < 1:
+            raise ValueError("cos and sin must not be empty")
+        _expect(cos, "cos", cos.shape, torch.float32, device)
+        _expect(sin, "sin", cos.shape, torch.float32, device)
+    w32 = False
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        w32 = isinstance(w, torch.Tensor) and w.dtype == torch.float32
+        _expect(w, name, (d,), torch.float32 if w32 else torch.bfloat16, device)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    return rot, n_pos, int(w32)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, H, N, d = q.shape
+    _on_device(q, "q")
+    _strided_rows(q, "q", (B, H, N, d), q.device)
+    _strided_rows(k, "k", (B, k.shape[1], N, d), q.device)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if cos is None and q_weight is None:
+        raise ValueError("neither weights (norm) nor cos and sin (rotation) given")
+    rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, q.device)
+    per_batch = 0
+    if positions is not None:
+        per_batch = int(isinstance(positions, torch.Tensor) and positions.dim() == 2)
+        _expect(positions, "positions", (B, N) if per_batch else (N,), torch.int32, q.device)
+    elif rot and n_pos < N:
+        raise ValueError("cos and sin must have a row for every token")
+    return B, H, k.shape[1], N, d, rot, n_pos, w32, per_batch
+
+
+def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None):
+    """Per-head norm (with q_weight, k_weight [d], bf16 or fp32) and position
+    rotation (with cos, sin [n_pos, rot/2] fp32) of q [B, H, N, d] and k
+    [B, Hkv, N, d], in one pass. Returns (q_out, k_out), contiguous unless
+    given: what fwd takes.
+
+    q, k and given outputs may be strided views whose last dimension is
+    contiguous, such as those of a packed projection; an output may be its
+    input. positions: int32 [N] or [B, N], the token's row of the tables
+    (default: token n is at position n). interleaved pairs dimensions
+    (2i, 2i + 1), else (i, i + rot/2)."""
+    B, H, Hkv, N, d, rot, n_pos, w32, per_batch = _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _strided_rows(q_out, "q_out", (B, H, N, d), dev, out=True)
+    if k_out is None:
+        k_out = torch.empty((B, Hkv, N, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _strided_rows(k_out, "k_out", (B, Hkv, N, d), dev, out=True)
+    _check(lib().fa_qk_norm_rope(_heads(q), _heads(k), _heads(q_out), _heads(k_out), _addr(cos), _addr(sin),
+                                 _addr(positions), per_batch, _addr(q_weight), _addr(k_weight), w32, B, H, Hkv, N, d,
+                                 rot, n_pos, float(eps), int(bool(interleaved)), _stream(dev)), "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(B, N, d) -> int:
+    return int(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, N, d))
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None,
+                     eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None):
+    """Gradient of qk_norm_rope for the output gradients dq_out, dk_out (bwd's
+    dq and dk). Returns (dq, dk, dq_weight, dk_weight): dq and dk contiguous
+    bf16 unless given (strided views are allowed, as in qk_norm_rope), the
+    weight gradients fp32 [d] whatever the weights' type (None without
+    weights; q and k are then not read and may be None)."""
+    if q_weight is None and k_weight is None:
+        q, k = dq_out, dk_out
+    B, H, Hkv, N, d, rot, n_pos, w32, per_batch = _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    dev = q.device
+    _strided_rows(dq_out, "dq_out", (B, H, N, d), dev)
+    _strided_rows(dk_out, "dk_out", (B, Hkv, N, d), dev)
+    if dq is None:
+        dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _strided_rows(dq, "dq", (B, H, N, d), dev, out=True)
+    if dk is None:
+        dk = torch.empty((B, Hkv, N, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _strided_rows(dk, "dk", (B, Hkv, N, d), dev, out=True)
+    dqw = dkw = None
+    ws_bytes = 0
+    if q_weight is not None:
+        dqw = torch.empty((d,), dtype=torch.float32, device=dev)
+        dkw = torch.empty((d,), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
+        _expect_workspace(workspace, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().fa_qk_norm_rope_bwd(_heads(dq_out), _heads(dk_out), _heads(q), _heads(k), _heads(dq), _heads(dk),
+                                     _addr(dqw), _addr(dkw), _addr(cos), _addr(sin), _addr(positions), per_batch,
+                                     _addr(q_weight), _addr(k_weight), w32, _addr(workspace), ws_bytes, B, H, Hkv, N,
+                                     d, rot, n_pos, float(eps), int(bool(interleaved)), _stream(dev)),
+           "fa_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
+def _append_args(k, v, block_table, positions, requests, cos, sin, q, q_weight, k_weight, q_out):
+    """Check an append's arguments but the caches; returns (q_out, arguments
+    before and after the caches in the C call's order)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected k and v [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    dev = k.device
+    _on_device(k, "k")
+    _strided_rows(k, "k", (T, Hkv, d), dev)
+    _strided_rows(v, "v", (T, Hkv, d), dev)
+    H = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("expected q [T, H, d]")
+        H = q.shape[1]
+        _strided_rows(q, "q", (T, H, d), dev)
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight go together")
+        if q_out is None:
+            q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _strided_rows(q_out, "q_out", (T, H, d), dev, out=True)
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks] int32")
+    B, max_blocks = block_table.shape
+    _expect(block_table, "block_table", (B, max_blocks), torch.int32, dev)
+    _expect(positions, "positions", (T,), torch.int32, dev)
+    if requests is not None:
+        _expect(requests, "requests", (T,), torch.int32, dev)
+    elif T > B:
+        raise ValueError("more tokens than requests: say which request each token belongs to")
+    rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
+    rows = [_tokens_of(q) if q is not None else None, _tokens_of(k), _tokens_of(v),
+            _tokens_of(q_out) if q is not None else None]
+    rest = (_addr(block_table), _addr(positions), _addr(requests), _addr(cos), _addr(sin), _addr(q_weight),
+            _addr(k_weight), w32, T, B, H, Hkv, d)
+    return q_out, rows, rest, max_blocks, rot, n_pos
+
+
+def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, cos=None, sin=None, q=None,
+                 q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None):
+    """Write new tokens' keys (after norm and rotation, as in qk_norm_rope)
+    and values k, v [T, Hkv, d] into the paged cache k_cache, v_cache
+    [num_blocks, Hkv, block_size, d] bf16, in place. Token t goes to position
+    positions[t] of request requests[t] (int32 [T] both; requests=None: token
+    t is request t's), through block_table [B, max_blocks] int32; a negative
+    request or position marks padding, which is skipped.
+
+    With q [T, H, d] the tokens' queries get the same norm and rotation;
+    returns them ([T, H, d]: decode_paged's q), else None. k, v, q and q_out
+    may be strided views, such as those of a packed projection."""
+    q_out, rows, rest, max_blocks, rot, n_pos = _append_args(k, v, block_table, positions, requests, cos, sin, q,
+                                                             q_weight, k_weight, q_out)
+    T, Hkv, d = k.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
+    num_blocks, bs = k_cache.shape[0], k_cache.shape[2]
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(c, name, (num_blocks, Hkv, bs, d), torch.bfloat16, k.device)
+    _check(lib().fa_append_paged(*rows, _addr(k_cache), _addr(v_cache), *rest, num_blocks, bs, max_blocks, rot, n_pos,
+                                 float(eps), int(bool(interleaved)), _stream(k.device)), "fa_append_paged")
+    return q_out
+
+
+def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
+    """Check a 4-bit cache's codes and (step, centre) pairs; returns (num_blocks, block_size)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d/2] uint8")
+    num_blocks, bs = k_cache.shape[0], k_cache.shape[2]
+    for name, c, s in (("k", k_cache, k_scale), ("v", v_cache, v_scale)):
+        _expect(c, name + "_cache", (num_blocks, Hkv, bs, d // 2), torch.uint8, device)
+        _expect(s, name + "_scale", (num_blocks, Hkv, bs, d // 64, 2), torch.bfloat16, device)
+    return num_blocks, bs
+
+
+def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, positions, requests=None, cos=None,
+                    sin=None, q=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                    k_values=None, v_values=None):
+    """append_paged into a cache held in 4 bits: k_cache, v_cache
+    [num_blocks, Hkv, block_size, d/2] uint8 codes and k_scale, v_scale
+    [num_blocks, Hkv, block_size, d/64, 2] bf16 (step, centre) of each group
+    of 64 dimensions (see fa_append_paged_q4). k_values, v_values [T, Hkv, d]
+    bf16, if given, receive the values that the cache now holds."""
+    q_out, rows, rest, max_blocks, rot, n_pos = _append_args(k, v, block_table, positions, requests, cos, sin, q,
+                                                             q_weight, k_weight, q_out)
+    T, Hkv, d = k.shape
+    num_blocks, bs = _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, k.device)
+    if (k_values is None) != (v_values is None):
+        raise ValueError("k_values and v_values go together")
+    if k_values is not None:
+        _expect(k_values, "k_values", (T, Hkv, d), torch.bfloat16, k.device)
+        _expect(v_values, "v_values", (T, Hkv, d), torch.bfloat16, k.device)
+    _check(lib().fa_append_paged_q4(*rows, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale),
+                                    _addr(k_values), _addr(v_values), *rest, num_blocks, bs, max_blocks, rot, n_pos,
+                                    float(eps), int(bool(interleaved)), _stream(k.device)), "fa_append_paged_q4")
+    return q_out
+
+
+def decode_q4_splits(B, H, Hkv, block_size, max_blocks) -> int:
+    """The n_splits that decode_paged_q4 takes for n_splits=0."""
+    return int(lib().fa_decode_q4_splits(B, H, Hkv, block_size, max_blocks))
+
+
+def decode_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, n_splits=0, scale=None,
+                    workspace=None, out=None, lse=None):
+    """decode_paged over a cache held in 4 bits (append_paged_q4's): q
+    [B, H, d] bf16, block_table [B, max_blocks] and seq_lens [B] int32.
+    n_splits=0 takes decode_q4_splits(...); the workspace is
+    decode_workspace_bytes(B, H, d, n_splits) bytes. Returns (o [B, H, d]
+    bf16, lse [B, H] fp32)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("expected q [B, H, d]")
+    B, H, d = q.shape
+    dev = q.device
+    _on_device(q, "q")
+    _expect(q, "q", (B, H, d), torch.bfloat16, dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d/2] uint8")
+    Hkv = k_cache.shape[1]
+    num_blocks, bs = _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks] int32")
+    max_blocks = block_table.shape[1]
+    _expect(block_table, "block_table", (B, max_blocks), torch.int32, dev)
+    _expect(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if n_splits == 0:
+        n_splits = decode_q4_splits(B, H, Hkv, bs, max_blocks)
+    ws_bytes = decode_workspace_bytes(B, H, d, n_splits)
+    if workspace is None:
+        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    _expect_workspace(workspace, dev)
+    if out is not None:
+        _expect(out, "out", q.shape, torch.bfloat16, dev)
+    if lse is not None:
+        _expect(lse, "lse", (B, H), torch.float32, dev)
+    o = torch.empty_like(q) if out is None else out
+    lse_t = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
+    _check(lib().fa_decode_paged_q4(_addr(q), _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale),
+                                    _addr(block_table), _addr(seq_lens), _addr(o), _addr(lse_t), _addr(workspace),
+                                    workspace.numel() * workspace.element_size(), B, H, Hkv, d, num_blocks, bs,
+                                    max_blocks, _scale(d, scale), n_splits, _stream(dev)), "fa_decode_paged_q4")
+    return o, lse_t

@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libfa.so")
 DEBUG_LIB_PATH = os.path.join(OUT_DIR, "libfa_debug.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_softmax.cu", "fa_decode.cu",
-           "fa_host.cu", "fa_selftest.cu"]
+           "fa_host.cu", "fa_selftest.cu", "fa_rope.cu", "fa_append.cu", "fa_decode_q4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "-I", os.path.join(ROOT, "include")]

@@ -68,6 +68,83 @@ cudaError_t launch_decode_paged(const void* q, const void* k_cache, const void* 
 cudaError_t launch_attn_merge(const float* o_parts, const float* lse_parts, int S, void* o, float* lse,
                               long long rows, int d, cudaStream_t stream);
 
+// ---- between the projections and the attention kernels (fa_rope.cu)
+// A [B][heads][N][d] bf16 tensor with unit stride in d: strides of the other
+// dimensions in elements, and the elements from p to the last one's end.
+struct HeadRows {
+  __nv_bfloat16* p;
+  long long sb, sh, sn;
+  long long extent;
+};
+// Arguments of the norm and rotation kernels. No norm: the weights are null.
+// No rotation: rot = 0. The backward takes dy in q_out and k_out.
+struct NormRope {
+  HeadRows q, k, q_out, k_out, dq, dk;
+  const float* cos;      // [n_pos][rot / 2]
+  const float* sin;
+  const int* positions;  // [N], or [B][N] with pos_sb = N; null: token n is at position n
+  long long pos_sb;
+  const void* q_weight;  // [d], bf16, or fp32 with w32
+  const void* k_weight;
+  bool w32, interleaved;
+  int B, H, Hkv, N, rot, n_pos;
+  float eps;
+  int q_groups;  // set by the launcher
+};
+cudaError_t launch_norm_rope(const NormRope& p, int d, cudaStream_t stream);
+// Partial rows of the weight gradients: [2][parts][d] fp32 of workspace.
+int norm_rope_bwd_parts(int B, int N, int d);
+cudaError_t launch_norm_rope_bwd(const NormRope& p, int d, float* partial, float* dqw, float* dkw,
+                                 cudaStream_t stream);
+
+// ---- appending to a paged cache (fa_append.cu)
+// A [T][heads][d] bf16 tensor with unit stride in d.
+struct TokenRows {
+  __nv_bfloat16* p;
+  long long st, sh;
+  long long extent;
+};
+struct Append {
+  TokenRows q, k, v, q_out;  // q.p null: no queries (H = 0)
+  void* k_cache;             // bf16 [num_blocks][Hkv][bs][d], or codes [...][d / 2]
+  void* v_cache;
+  __nv_bfloat16* k_scale;    // [num_blocks][Hkv][bs][d / 64][2], 4-bit caches only
+  __nv_bfloat16* v_scale;
+  __nv_bfloat16* k_values;   // [T][Hkv][d] values held, or null
+  __nv_bfloat16* v_values;
+  const int* block_table;    // [B][max_blocks]
+  const int* positions;      // [T]
+  const int* requests;       // [T], or null: token t is request t's
+  const float* cos;
+  const float* sin;
+  const void* q_weight;
+  const void* k_weight;
+  bool w32, interleaved;
+  int T, B, H, Hkv, num_blocks, bs, max_blocks, rot, n_pos;
+  float eps;
+  int q_groups, kv_groups;  // set by the launcher
+};
+cudaError_t launch_append(const Append& p, int d, bool q4, cudaStream_t stream);
+
+// ---- decode over a cache in 4-bit codes (fa_decode_q4.cu)
+struct DecodeQ4 {
+  const __nv_bfloat16* q;    // [B][H][d]
+  const uint8_t* k_cache;    // [num_blocks][Hkv][bs][d / 2]
+  const uint8_t* v_cache;
+  const uint32_t* k_scale;   // (s, z) pairs, [num_blocks][Hkv][bs][d / 64]
+  const uint32_t* v_scale;
+  const int* block_table;
+  const int* seq_lens;
+  __nv_bfloat16* o;
+  float* lse;
+  float* o_part;             // [S][B·H][d], [S][B·H]: partial results, S > 1
+  float* lse_part;
+  int B, H, Hkv, num_blocks, bs, max_blocks;
+  float scale_log2;
+};
+int decode_q4_splits(int B, int H, int Hkv, long long max_ctx);
+cudaError_t launch_decode_q4(const DecodeQ4& p, int d, int S, cudaStream_t stream);
+
 // The calling host thread's side stream on the current device (a
 // non-blocking stream the library creates on first use and keeps).
 cudaError_t side_stream(cudaStream_t* out);
@@ -79,5 +156,8 @@ cudaError_t read_and_clear_fwd_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_bwd_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_decode_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_softmax_error(uint32_t* out, cudaStream_t stream);
+cudaError_t read_and_clear_rope_error(uint32_t* out, cudaStream_t stream);
+cudaError_t read_and_clear_append_error(uint32_t* out, cudaStream_t stream);
+cudaError_t read_and_clear_decode_q4_error(uint32_t* out, cudaStream_t stream);
 
 }  // namespace fa

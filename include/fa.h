@@ -62,7 +62,7 @@ typedef enum {
   FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (launch error) */
   FA_ERR_TIMEOUT = 5,     /* device pipeline wait exceeded its limit */
   FA_ERR_WORKSPACE = 6,   /* workspace pointer null or smaller than required */
-  FA_ERR_BAD_INDEX = 7,   /* (device) a block-table entry outside [0, num_blocks) */
+  FA_ERR_BAD_INDEX = 7,   /* (device) a block-table entry, request or position out of range */
   FA_ERR_BOUNDS = 8       /* (device, FA_DEBUG build) a computed address left its buffer */
 } fa_status;
 
@@ -363,13 +363,166 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, con
                     float scale, int n_splits, void* stream);
 
 /*
+ * ---- Between a layer's projections and attention ----
+ *
+ * The calls above take queries and keys as they enter the products, and a
+ * cache that already holds the new tokens. The calls below bring them there:
+ * per-head norms and the position rotation of q and k (with their gradient),
+ * and the writes into a paged cache, in bf16 or in 4-bit codes. The pages
+ * this library follows stop at the attention formula; the layouts and
+ * conventions here are this library's own.
+ *
+ *   norm      r = 1 / sqrt(mean_c x_c^2 + eps), y_c = x_c · r · w_c over the
+ *             d values of one head of one token. Weights are bf16, or fp32
+ *             with weight_fp32 = 1, [d], one for queries and one for keys;
+ *             NULL weights: no norm.
+ *   rotation  pair (a, b) of y becomes (a cos − b sin, b cos + a sin), with
+ *             the cosine and sine of the token's position and of the pair:
+ *             cos, sin [n_pos][rot/2] fp32 tables, which the caller makes
+ *             (any base, scaling or position mapping). Pair i is dimensions
+ *             (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0;
+ *             dimensions rot .. d-1 are left as they are. rot is a multiple
+ *             of 16, at most d; rot = 0: no rotation (cos, sin unused).
+ *   Values are fp32 from the loads to one rounding of the result.
+ *
+ * A bf16 tensor [B][heads][N][d] whose last dimension is contiguous; the
+ * other strides in elements, not negative, multiples of 8 (16 bytes), e.g. a
+ * view of a packed projection [B][N][heads][d]. An output's rows must not
+ * overlap; an output may be its input itself (same strides).
+ */
+typedef struct {
+  void* ptr;
+  long long stride_b, stride_h, stride_n;
+} fa_heads;
+
+/* The same for [T][heads][d]: T tokens of any requests. */
+typedef struct {
+  void* ptr;
+  long long stride_t, stride_h;
+} fa_tokens;
+
+/*
+ * Norm and rotation of q [B][H][N][d] and k [B][Hkv][N][d] into q_out and
+ * k_out (any Hkv >= 1), as fa_fwd_gqa takes them when those are contiguous.
+ *   positions  device int32, [N] (positions_per_batch = 0) or [B][N]
+ *              (positions_per_batch = 1): the token's row of the tables;
+ *              NULL: token n is at position n (then n_pos >= N). A position
+ *              outside [0, n_pos) is never used as an index: the token's
+ *              rows are written as zeros and fa_last_device_error reports
+ *              FA_ERR_BAD_INDEX.
+ * Errors: a NULL struct or pointer it must hold, sizes < 1, one weight
+ * without the other, neither weights nor rotation, negative strides, eps
+ * negative or not finite (with weights) -> FA_ERR_INVALID_ARG; d, rot, H or
+ * Hkv > 65536, or B·H·N past 2^31 -> FA_ERR_UNSUPPORTED; pointers or strides
+ * not 16-byte aligned (positions: 4) -> FA_ERR_MISALIGNED.
+ */
+int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out, const fa_heads* k_out,
+                    const float* cos, const float* sin, const int* positions, int positions_per_batch,
+                    const void* q_weight, const void* k_weight, int weight_fp32, int B, int H, int Hkv, int N, int d,
+                    int rot, int n_pos, float eps, int interleaved, void* stream);
+
+/*
+ * Its gradient: dq, dk for the output gradients dq_out, dk_out (for instance
+ * fa_bwd's dq and dk), and dq_weight, dk_weight [d] fp32, summed over every
+ * head of every token in a fixed order (the same inputs give the same bits).
+ * q and k are the forward's inputs; without weights they and the weight
+ * gradients are not touched and may be NULL, and no workspace is needed.
+ *   workspace  fa_qk_norm_rope_bwd_workspace_bytes(B, N, d) bytes, 16-byte
+ *              aligned; contents on entry are ignored.
+ * Errors as the forward's, and FA_ERR_WORKSPACE.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d);
+int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q, const fa_heads* k,
+                        const fa_heads* dq, const fa_heads* dk, float* dq_weight, float* dk_weight, const float* cos,
+                        const float* sin, const int* positions, int positions_per_batch, const void* q_weight,
+                        const void* k_weight, int weight_fp32, void* workspace, size_t ws_bytes, int B, int H, int Hkv,
+                        int N, int d, int rot, int n_pos, float eps, int interleaved, void* stream);
+
+/*
+ * Append tokens to a paged cache (the cache and table of fa_decode_paged):
+ * token t of request r at position p is written to block
+ * block_table[r][p / block_size], slot p % block_size, its key after norm
+ * and rotation, its value as it is. One call takes the prompts and the
+ * single new tokens of any requests, in any order; other cache rows are left
+ * as they were.
+ *   k, v       [T][Hkv][d] new keys and values.
+ *   q, q_out   [T][H][d] the same tokens' queries, in, and after norm and
+ *              rotation, out (for fa_decode_paged); both NULL: none.
+ *   positions  [T] device int32: each token's position in its request, which
+ *              is both its cache slot and its row of the tables.
+ *   requests   [T] device int32: each token's request (row of block_table);
+ *              NULL: token t is request t's (a decode step; T <= B).
+ * A token with a negative request or position is padding: nothing is read
+ * or written for it, and its q_out row stays as it was. A request >= B, a
+ * position past the table's blocks or (with rotation) past n_pos, and a
+ * block outside [0, num_blocks) are never used as an index: the token is
+ * skipped the same way and fa_last_device_error reports FA_ERR_BAD_INDEX.
+ * Two tokens with one slot in one call: which of them it holds then is not
+ * defined. A token's slot is what fa_decode_paged reads for seq_lens >
+ * position, in order on the stream.
+ * Errors: as fa_qk_norm_rope's (a norm of keys alone when q is NULL) and
+ * fa_decode_paged's for the cache; neither weights nor rotation is allowed
+ * here (a plain copy); H or Hkv > 16384 -> FA_ERR_UNSUPPORTED.
+ */
+int fa_append_paged(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out, void* k_cache,
+                    void* v_cache, const int* block_table, const int* positions, const int* requests, const float* cos,
+                    const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B, int H,
+                    int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot, int n_pos,
+                    float eps, int interleaved, void* stream);
+
+/*
+ * A paged cache held in 4 bits. Per token and K/V head: d codes n in 0..15,
+ * two a byte (the even dimension in the low half), and for each group of 64
+ * dimensions a bf16 pair (s, z); the value held is z + s (n − 8).
+ *   k_cache, v_cache  [num_blocks][Hkv][block_size][d/2] bytes,
+ *   k_scale, v_scale  [num_blocks][Hkv][block_size][d/64][2] bf16,
+ * 16-byte aligned each: d/2 + d/16 bytes a key or value where bf16 has 2 d.
+ * For a group with smallest value a and largest b:
+ *   s = bf16((b − a)/2 · fl32(1/7.5)), z = bf16((a + b)/2 + s/2),
+ *   n = clamp(rint((x − z)/s) + 8, 0, 15), and 8 where s = 0,
+ * in fp32, each operation rounded by itself. Each value held is off by at
+ * most max(s/2, 2^-9 (|z| + 8 s)) beside fp32 rounding. A group with a value
+ * that is not finite is held as NaN.
+ *
+ * fa_append_paged_q4: fa_append_paged into such a cache.
+ *   k_values, v_values  [T][Hkv][d] bf16 outputs, both or neither (NULL):
+ *                       the values held for the new tokens, rounded to bf16,
+ *                       e.g. for a prompt's own attention over what later
+ *                       steps will read. Rows of skipped tokens stay as they
+ *                       were.
+ */
+int fa_append_paged_q4(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out,
+                       void* k_cache, void* k_scale, void* v_cache, void* v_scale, void* k_values, void* v_values,
+                       const int* block_table, const int* positions, const int* requests, const float* cos,
+                       const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B,
+                       int H, int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot,
+                       int n_pos, float eps, int interleaved, void* stream);
+
+/*
+ * Decode step over a 4-bit cache: fa_decode_paged's arguments, conventions
+ * and errors with the caches' codes and scales; any block_size >= 1, any
+ * number of query heads per K/V head. Values are never written out in full:
+ * both products run on the codes. Workspace as for fa_decode_paged
+ * (fa_decode_workspace_bytes). Slots past a request's length may hold
+ * anything.
+ * fa_decode_q4_splits gives an n_splits that fills the GPU for these sizes
+ * (a host function; 0 for invalid sizes).
+ */
+int fa_decode_q4_splits(int B, int H, int Hkv, int block_size, int max_blocks_per_seq);
+int fa_decode_paged_q4(const void* q, const void* k_cache, const void* k_scale, const void* v_cache,
+                       const void* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse,
+                       void* workspace, size_t ws_bytes, int B, int H, int Hkv, int d, int num_blocks, int block_size,
+                       int max_blocks_per_seq, float scale, int n_splits, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word set by
  * any kernel of this library on the current device. Returns FA_OK,
  * FA_ERR_TIMEOUT (a pipeline wait gave up; outputs of the calls since the
  * last check are undefined), FA_ERR_BOUNDS (FA_DEBUG build only: an address
  * a kernel computed fell outside its buffer; that access was skipped and the
- * outputs are undefined), FA_ERR_BAD_INDEX (a decode block table pointed
- * outside the cache) or FA_ERR_CUDA.
+ * outputs are undefined), FA_ERR_BAD_INDEX (a block table pointed outside
+ * the cache, or a request or position lay outside what it indexes) or
+ * FA_ERR_CUDA.
  */
 int fa_last_device_error(void* stream);
 

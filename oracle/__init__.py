@@ -22,3 +22,12 @@ from .attention import (  # noqa: F401
     softmax_online_blocks,
     softmax_safe,
 )
+from .cached import (  # noqa: F401
+    append_slots,
+    norm_rope,
+    norm_rope_bwd,
+    q4_encode,
+    q4_pack,
+    q4_unpack,
+    q4_values,
+)
