@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -105,14 +106,12 @@ class Tensors(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "dO", "o", "lse", "dq", "dk", "dv")]
 
 
-class Heads(ctypes.Structure):
-    """fa_heads: address and strides (elements) of a [B][heads][N][d] tensor."""
-    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in ("stride_b", "stride_h", "stride_n")]
-
-
-class Tokens(ctypes.Structure):
-    """fa_tokens: address and strides (elements) of a [T][heads][d] tensor."""
-    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in ("stride_t", "stride_h")]
+# Layouts of the argument structs (native alignment), packed for the call:
+# building a ctypes structure field by field costs several times as much.
+_HEADS, _TOKENS = "Pqqq", "Pqq"  # fa_heads, fa_tokens: address, strides
+_NORM_ROPE_ARGS = struct.Struct("@" + 4 * _HEADS + "5P10if")
+_NORM_ROPE_GRADS = struct.Struct("@" + 2 * _HEADS + "3PN")
+_APPEND_ARGS = struct.Struct("@" + 4 * _TOKENS + "13P12if")
 
 
 class FAError(RuntimeError):
@@ -172,16 +171,15 @@ def lib() -> ctypes.CDLL:
         L.fa_fwd_bwd_host.restype = i
         L.fa_softmax_host.argtypes = [vp, vp, vp, vp, ctypes.c_longlong, i, i, i, vp]
         L.fa_softmax_host.restype = i
-        hp, kp = ctypes.POINTER(Heads), ctypes.POINTER(Tokens)
-        L.fa_qk_norm_rope.argtypes = [hp] * 4 + [vp, vp, vp, i, vp, vp] + [i] * 8 + [f, i, vp]
+        L.fa_qk_norm_rope.argtypes = [vp, vp]
         L.fa_qk_norm_rope.restype = i
         L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i]
         L.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
-        L.fa_qk_norm_rope_bwd.argtypes = [hp] * 6 + [vp] * 5 + [i, vp, vp, i, vp, sz] + [i] * 7 + [f, i, vp]
+        L.fa_qk_norm_rope_bwd.argtypes = [vp, vp, vp]
         L.fa_qk_norm_rope_bwd.restype = i
-        L.fa_append_paged.argtypes = [kp] * 4 + [vp] * 9 + [i] * 11 + [f, i, vp]
+        L.fa_append_paged.argtypes = [vp, vp]
         L.fa_append_paged.restype = i
-        L.fa_append_paged_q4.argtypes = [kp] * 4 + [vp] * 13 + [i] * 11 + [f, i, vp]
+        L.fa_append_paged_q4.argtypes = [vp, vp]
         L.fa_append_paged_q4.restype = i
         L.fa_decode_q4_splits.argtypes = [i] * 5
         L.fa_decode_q4_splits.restype = i
@@ -206,7 +204,10 @@ def _ptr(t):
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the address behind torch.cuda.current_stream(device).cuda_stream,
+    # without the stream object around it (2 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if device.index is None else device.index))
 
 
 # Device type of every tensor the kernels touch. The library launches on the
@@ -227,7 +228,7 @@ def _expect(t, name, shape, dtype, device):
     """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on
     `device`: a buffer the kernels read or write in full, so a smaller one
     would be overrun."""
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype
+    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype
             or not t.is_contiguous() or t.device != device):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
@@ -567,85 +568,86 @@ def rope_tables(n_pos, rot, base=10000.0, device=None):
     return angle.cos().float(), angle.sin().float()
 
 
-def _strided_rows(t, name, shape, device, out=False):
-    """Raise unless t is a bf16 tensor of `shape` on `device` whose last
-    dimension is contiguous and whose rows sit on 16-byte boundaries (for an
-    output: with no two rows overlapping)."""
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != torch.bfloat16
-            or t.device != device):
-        raise ValueError(f"{name}: expected a {torch.bfloat16} tensor of shape {tuple(shape)} on {device}")
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _rows(t, name, shape, device, out=False):
+    """(address, strides but the last) of t, a bf16 tensor of `shape` on
+    `device` whose last dimension is contiguous and whose rows sit on 16-byte
+    boundaries (for an output: no two rows overlapping); raises otherwise."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not _BF16 or t.device != device:
+        raise ValueError(f"{name}: expected a {_BF16} tensor of shape {tuple(shape)} on {device}")
     st = t.stride()
-    if st[-1] != 1 or any(s % 8 for s, n in zip(st[:-1], shape) if n > 1):
+    lead = st[:-1]
+    for s in lead:
+        if s & 7:  # a dimension of one element has no stride to speak of
+            lead = tuple(s if n > 1 else 0 for s, n in zip(lead, shape))
+            break
+    if st[-1] != 1 or any([s & 7 for s in lead]):
         raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8")
-    if out:
+    if out and not t.is_contiguous():
         need = shape[-1]
-        for s, n in sorted((s, n) for s, n in zip(st[:-1], shape) if n > 1):
+        for s, n in sorted((s, n) for s, n in zip(lead, shape) if n > 1):
             if s < need:
                 raise ValueError(f"{name}: an output's rows must not overlap")
             need = s * n
-    return t
-
-
-def _strides(t):
-    """Strides but the last; a dimension of one element has no stride to speak of."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
-
-
-def _heads(t):
-    return Heads(t.data_ptr(), *_strides(t))
-
-
-def _tokens_of(t):
-    return Tokens(t.data_ptr(), *_strides(t))
+    return (t.data_ptr(), *lead)
 
 
 def _rope_args(cos, sin, q_weight, k_weight, d, device):
-    """Check tables and weights; returns (rot, n_pos, weight_fp32)."""
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    rot = n_pos = 0
-    if cos is not None:
-        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-            raise ValueError("cos and sin must be [n_pos, rot/2]")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    """Check tables and weights; returns their addresses, and rot, n_pos, weight_fp32."""
+    rot = n_pos = w32 = cp = sp = qp = kp = 0
+    if cos is not None or sin is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2 or sin is None:
+            raise ValueError("cos and sin go together, [n_pos, rot/2] both")
+        n_pos, rot = cos.shape
+        rot *= 2
         if n_pos < 1 or rot < 1:
             raise ValueError("cos and sin must not be empty")
-        _expect(cos, "cos", cos.shape, torch.float32, device)
-        _expect(sin, "sin", cos.shape, torch.float32, device)
-    w32 = False
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        w32 = isinstance(w, torch.Tensor) and w.dtype == torch.float32
-        _expect(w, name, (d,), torch.float32 if w32 else torch.bfloat16, device)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one dtype")
-    return rot, n_pos, int(w32)
+        _expect(cos, "cos", cos.shape, _F32, device)
+        _expect(sin, "sin", cos.shape, _F32, device)
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    if k_weight is not None:
+        w32 = int(isinstance(k_weight, torch.Tensor) and k_weight.dtype is _F32)
+        _expect(k_weight, "k_weight", (d,), _F32 if w32 else _BF16, device)
+        kp = k_weight.data_ptr()
+        if q_weight is not None:  # both of one dtype
+            _expect(q_weight, "q_weight", (d,), k_weight.dtype, device)
+            qp = q_weight.data_ptr()
+    return (cp, sp), (qp, kp), rot, n_pos, w32
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight):
+def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, interleaved, names, out):
+    """Check qk_norm_rope's arguments; a and b are the tensors beside q and k
+    (the outputs, made here if None, or their gradients). Returns a, b and the
+    packed fa_norm_rope_args."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise ValueError("expected [B, H, N, d] tensors")
-    B, H, N, d = q.shape
+    B, H, N, d = qs = q.shape
+    Hkv = k.shape[1]
+    ks = (B, Hkv, N, d)
+    dev = q.device
     _on_device(q, "q")
-    _strided_rows(q, "q", (B, H, N, d), q.device)
-    _strided_rows(k, "k", (B, k.shape[1], N, d), q.device)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     if cos is None and q_weight is None:
         raise ValueError("neither weights (norm) nor cos and sin (rotation) given")
-    rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, q.device)
-    per_batch = 0
+    tables, weights, rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
+    per_batch = pp = 0
     if positions is not None:
         per_batch = int(isinstance(positions, torch.Tensor) and positions.dim() == 2)
-        _expect(positions, "positions", (B, N) if per_batch else (N,), torch.int32, q.device)
+        _expect(positions, "positions", (B, N) if per_batch else (N,), _I32, dev)
+        pp = positions.data_ptr()
     elif rot and n_pos < N:
         raise ValueError("cos and sin must have a row for every token")
-    return B, H, k.shape[1], N, d, rot, n_pos, w32, per_batch
+    qr, kr = _rows(q, "q", qs, dev), _rows(k, "k", ks, dev)
+    if a is None:
+        a = torch.empty(qs, dtype=_BF16, device=dev)
+    if b is None:
+        b = torch.empty(ks, dtype=_BF16, device=dev)
+    return a, b, _NORM_ROPE_ARGS.pack(
+        *qr, *kr, *_rows(a, names[0], qs, dev, out), *_rows(b, names[1], ks, dev, out), *tables, pp, *weights, B, H,
+        Hkv, N, d, rot, n_pos, per_batch, w32, 1 if interleaved else 0, eps)
 
 
 def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -660,19 +662,9 @@ def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weig
     input. positions: int32 [N] or [B, N], the token's row of the tables
     (default: token n is at position n). interleaved pairs dimensions
     (2i, 2i + 1), else (i, i + rot/2)."""
-    B, H, Hkv, N, d, rot, n_pos, w32, per_batch = _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight)
-    dev = q.device
-    if q_out is None:
-        q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _strided_rows(q_out, "q_out", (B, H, N, d), dev, out=True)
-    if k_out is None:
-        k_out = torch.empty((B, Hkv, N, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _strided_rows(k_out, "k_out", (B, Hkv, N, d), dev, out=True)
-    _check(lib().fa_qk_norm_rope(_heads(q), _heads(k), _heads(q_out), _heads(k_out), _addr(cos), _addr(sin),
-                                 _addr(positions), per_batch, _addr(q_weight), _addr(k_weight), w32, B, H, Hkv, N, d,
-                                 rot, n_pos, float(eps), int(bool(interleaved)), _stream(dev)), "fa_qk_norm_rope")
+    q_out, k_out, args = _norm_rope_args(q, k, q_out, k_out, cos, sin, positions, q_weight, k_weight, eps,
+                                         interleaved, ("q_out", "k_out"), True)
+    _check(lib().fa_qk_norm_rope(args, _stream(q.device)), "fa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -689,74 +681,81 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos=None, sin=None, positions=None, q
     weights; q and k are then not read and may be None)."""
     if q_weight is None and k_weight is None:
         q, k = dq_out, dk_out
-    B, H, Hkv, N, d, rot, n_pos, w32, per_batch = _norm_rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    if dq_out is None or dk_out is None:
+        raise ValueError("expected output gradients of both q and k")
+    _, _, args = _norm_rope_args(q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, eps, interleaved,
+                                 ("dq_out", "dk_out"), False)
     dev = q.device
-    _strided_rows(dq_out, "dq_out", (B, H, N, d), dev)
-    _strided_rows(dk_out, "dk_out", (B, Hkv, N, d), dev)
     if dq is None:
-        dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _strided_rows(dq, "dq", (B, H, N, d), dev, out=True)
+        dq = torch.empty(q.shape, dtype=_BF16, device=dev)
     if dk is None:
-        dk = torch.empty((B, Hkv, N, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _strided_rows(dk, "dk", (B, Hkv, N, d), dev, out=True)
+        dk = torch.empty(k.shape, dtype=_BF16, device=dev)
     dqw = dkw = None
-    ws_bytes = 0
+    wp = qp = kp = ws_bytes = 0
     if q_weight is not None:
-        dqw = torch.empty((d,), dtype=torch.float32, device=dev)
-        dkw = torch.empty((d,), dtype=torch.float32, device=dev)
+        B, _, N, d = q.shape
+        dqw, dkw = torch.empty((d,), dtype=_F32, device=dev), torch.empty((d,), dtype=_F32, device=dev)
         if workspace is None:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
-        _expect_workspace(workspace, dev)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().fa_qk_norm_rope_bwd(_heads(dq_out), _heads(dk_out), _heads(q), _heads(k), _heads(dq), _heads(dk),
-                                     _addr(dqw), _addr(dkw), _addr(cos), _addr(sin), _addr(positions), per_batch,
-                                     _addr(q_weight), _addr(k_weight), w32, _addr(workspace), ws_bytes, B, H, Hkv, N,
-                                     d, rot, n_pos, float(eps), int(bool(interleaved)), _stream(dev)),
-           "fa_qk_norm_rope_bwd")
+            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(B, N, d), dtype=_U8, device=dev)
+        else:
+            _expect_workspace(workspace, dev)
+        wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        qp, kp = dqw.data_ptr(), dkw.data_ptr()
+    grads = _NORM_ROPE_GRADS.pack(*_rows(dq, "dq", q.shape, dev, True), *_rows(dk, "dk", k.shape, dev, True), qp, kp,
+                                  wp, ws_bytes)
+    _check(lib().fa_qk_norm_rope_bwd(args, grads, _stream(dev)), "fa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
-def _append_args(k, v, block_table, positions, requests, cos, sin, q, q_weight, k_weight, q_out):
-    """Check an append's arguments but the caches; returns (q_out, arguments
-    before and after the caches in the C call's order)."""
+def _append(entry, k, v, caches, values, block_table, positions, requests, cos, sin, q, q_weight, k_weight, eps,
+            interleaved, q_out):
+    """Check an append's arguments (the caches' own by the caller) and call it."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
-    T, Hkv, d = k.shape
+    T, Hkv, d = shape = k.shape
     dev = k.device
     _on_device(k, "k")
-    _strided_rows(k, "k", (T, Hkv, d), dev)
-    _strided_rows(v, "v", (T, Hkv, d), dev)
-    H = 0
+    kr, vr = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+    H, qr, qor = 0, (0, 0, 0), (0, 0, 0)
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("expected q [T, H, d]")
         H = q.shape[1]
-        _strided_rows(q, "q", (T, H, d), dev)
+        qr = _rows(q, "q", (T, H, d), dev)
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
         if q_out is None:
-            q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _strided_rows(q_out, "q_out", (T, H, d), dev, out=True)
+            q_out = torch.empty((T, H, d), dtype=_BF16, device=dev)
+        qor = _rows(q_out, "q_out", (T, H, d), dev, True)
     elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out need q")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks] int32")
     B, max_blocks = block_table.shape
-    _expect(block_table, "block_table", (B, max_blocks), torch.int32, dev)
-    _expect(positions, "positions", (T,), torch.int32, dev)
+    _expect(block_table, "block_table", (B, max_blocks), _I32, dev)
+    _expect(positions, "positions", (T,), _I32, dev)
+    rp = 0
     if requests is not None:
-        _expect(requests, "requests", (T,), torch.int32, dev)
+        _expect(requests, "requests", (T,), _I32, dev)
+        rp = requests.data_ptr()
     elif T > B:
         raise ValueError("more tokens than requests: say which request each token belongs to")
-    rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
-    rows = [_tokens_of(q) if q is not None else None, _tokens_of(k), _tokens_of(v),
-            _tokens_of(q_out) if q is not None else None]
-    rest = (_addr(block_table), _addr(positions), _addr(requests), _addr(cos), _addr(sin), _addr(q_weight),
-            _addr(k_weight), w32, T, B, H, Hkv, d)
-    return q_out, rows, rest, max_blocks, rot, n_pos
+    tables, weights, rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
+    k_cache = caches[0]
+    ks, vs, kv, vv = (caches[1].data_ptr(), caches[3].data_ptr(), *values) if len(caches) == 4 else (0, 0, 0, 0)
+    args = _APPEND_ARGS.pack(
+        *qr, *kr, *vr, *qor, k_cache.data_ptr(), caches[-1 if len(caches) == 2 else 2].data_ptr(), ks, vs, kv, vv,
+        block_table.data_ptr(), positions.data_ptr(), rp, *tables, *weights, T, B, H, Hkv, d, k_cache.shape[0],
+        k_cache.shape[2], max_blocks, rot, n_pos, w32, 1 if interleaved else 0, eps)
+    _check(getattr(lib(), entry)(args, _stream(dev)), entry)
+    return q_out
+
+
+def _expect_cache(t, name, Hkv, last, dtype, device):
+    """Check one tensor [num_blocks, Hkv, block_size, *last] of a cache."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 + len(last):
+        raise ValueError(f"{name}: expected a tensor of {3 + len(last)} dimensions")
+    _expect(t, name, (t.shape[0], Hkv, t.shape[2], *last), dtype, device)
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, cos=None, sin=None, q=None,
@@ -771,28 +770,21 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
     With q [T, H, d] the tokens' queries get the same norm and rotation;
     returns them ([T, H, d]: decode_paged's q), else None. k, v, q and q_out
     may be strided views, such as those of a packed projection."""
-    q_out, rows, rest, max_blocks, rot, n_pos = _append_args(k, v, block_table, positions, requests, cos, sin, q,
-                                                             q_weight, k_weight, q_out)
-    T, Hkv, d = k.shape
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
-    num_blocks, bs = k_cache.shape[0], k_cache.shape[2]
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _expect(c, name, (num_blocks, Hkv, bs, d), torch.bfloat16, k.device)
-    _check(lib().fa_append_paged(*rows, _addr(k_cache), _addr(v_cache), *rest, num_blocks, bs, max_blocks, rot, n_pos,
-                                 float(eps), int(bool(interleaved)), _stream(k.device)), "fa_append_paged")
-    return q_out
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected k and v [T, Hkv, d]")
+    _expect_cache(k_cache, "k_cache", k.shape[1], (k.shape[2],), _BF16, k.device)
+    _expect(v_cache, "v_cache", k_cache.shape, _BF16, k.device)
+    return _append("fa_append_paged", k, v, (k_cache, v_cache), None, block_table, positions, requests, cos, sin, q,
+                   q_weight, k_weight, eps, interleaved, q_out)
 
 
 def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
-    """Check a 4-bit cache's codes and (step, centre) pairs; returns (num_blocks, block_size)."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d/2] uint8")
-    num_blocks, bs = k_cache.shape[0], k_cache.shape[2]
-    for name, c, s in (("k", k_cache, k_scale), ("v", v_cache, v_scale)):
-        _expect(c, name + "_cache", (num_blocks, Hkv, bs, d // 2), torch.uint8, device)
-        _expect(s, name + "_scale", (num_blocks, Hkv, bs, d // 64, 2), torch.bfloat16, device)
-    return num_blocks, bs
+    """Check a 4-bit cache's codes and (step, centre) pairs."""
+    _expect_cache(k_cache, "k_cache", Hkv, (d // 2,), _U8, device)
+    _expect(v_cache, "v_cache", k_cache.shape, _U8, device)
+    pairs = (*k_cache.shape[:3], d // 64, 2)
+    _expect(k_scale, "k_scale", pairs, _BF16, device)
+    _expect(v_scale, "v_scale", pairs, _BF16, device)
 
 
 def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, positions, requests=None, cos=None,
@@ -803,19 +795,16 @@ def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, posit
     [num_blocks, Hkv, block_size, d/64, 2] bf16 (step, centre) of each group
     of 64 dimensions (see fa_append_paged_q4). k_values, v_values [T, Hkv, d]
     bf16, if given, receive the values that the cache now holds."""
-    q_out, rows, rest, max_blocks, rot, n_pos = _append_args(k, v, block_table, positions, requests, cos, sin, q,
-                                                             q_weight, k_weight, q_out)
-    T, Hkv, d = k.shape
-    num_blocks, bs = _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, k.device)
-    if (k_values is None) != (v_values is None):
-        raise ValueError("k_values and v_values go together")
-    if k_values is not None:
-        _expect(k_values, "k_values", (T, Hkv, d), torch.bfloat16, k.device)
-        _expect(v_values, "v_values", (T, Hkv, d), torch.bfloat16, k.device)
-    _check(lib().fa_append_paged_q4(*rows, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale),
-                                    _addr(k_values), _addr(v_values), *rest, num_blocks, bs, max_blocks, rot, n_pos,
-                                    float(eps), int(bool(interleaved)), _stream(k.device)), "fa_append_paged_q4")
-    return q_out
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected k and v [T, Hkv, d]")
+    _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, k.shape[1], k.shape[2], k.device)
+    values = (0, 0)
+    if k_values is not None or v_values is not None:
+        _expect(k_values, "k_values", k.shape, _BF16, k.device)
+        _expect(v_values, "v_values", k.shape, _BF16, k.device)
+        values = (k_values.data_ptr(), v_values.data_ptr())
+    return _append("fa_append_paged_q4", k, v, (k_cache, k_scale, v_cache, v_scale), values, block_table, positions,
+                   requests, cos, sin, q, q_weight, k_weight, eps, interleaved, q_out)
 
 
 def decode_q4_splits(B, H, Hkv, block_size, max_blocks) -> int:
@@ -828,37 +817,42 @@ def decode_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens
     """decode_paged over a cache held in 4 bits (append_paged_q4's): q
     [B, H, d] bf16, block_table [B, max_blocks] and seq_lens [B] int32.
     n_splits=0 takes decode_q4_splits(...); the workspace is
-    decode_workspace_bytes(B, H, d, n_splits) bytes. Returns (o [B, H, d]
-    bf16, lse [B, H] fp32)."""
+    decode_workspace_bytes(B, H, d, n_splits) bytes (none for one split).
+    Returns (o [B, H, d] bf16, lse [B, H] fp32)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("expected q [B, H, d]")
-    B, H, d = q.shape
+    B, H, d = shape = q.shape
     dev = q.device
     _on_device(q, "q")
-    _expect(q, "q", (B, H, d), torch.bfloat16, dev)
+    _expect(q, "q", shape, _BF16, dev)
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d/2] uint8")
-    Hkv = k_cache.shape[1]
-    num_blocks, bs = _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, dev)
+    num_blocks, Hkv, bs, _ = k_cache.shape
+    _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks] int32")
     max_blocks = block_table.shape[1]
-    _expect(block_table, "block_table", (B, max_blocks), torch.int32, dev)
-    _expect(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    _expect(block_table, "block_table", (B, max_blocks), _I32, dev)
+    _expect(seq_lens, "seq_lens", (B,), _I32, dev)
     if n_splits == 0:
         n_splits = decode_q4_splits(B, H, Hkv, bs, max_blocks)
-    ws_bytes = decode_workspace_bytes(B, H, d, n_splits)
-    if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
-    _expect_workspace(workspace, dev)
-    if out is not None:
-        _expect(out, "out", q.shape, torch.bfloat16, dev)
-    if lse is not None:
-        _expect(lse, "lse", (B, H), torch.float32, dev)
-    o = torch.empty_like(q) if out is None else out
-    lse_t = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
-    _check(lib().fa_decode_paged_q4(_addr(q), _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale),
-                                    _addr(block_table), _addr(seq_lens), _addr(o), _addr(lse_t), _addr(workspace),
-                                    workspace.numel() * workspace.element_size(), B, H, Hkv, d, num_blocks, bs,
-                                    max_blocks, _scale(d, scale), n_splits, _stream(dev)), "fa_decode_paged_q4")
-    return o, lse_t
+    wp = ws_bytes = 0
+    if workspace is not None:
+        _expect_workspace(workspace, dev)
+    elif n_splits > 1:
+        workspace = torch.empty(max(decode_workspace_bytes(B, H, d, n_splits), 16), dtype=_U8, device=dev)
+    if workspace is not None:
+        wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        _expect(out, "out", shape, _BF16, dev)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=_F32, device=dev)
+    else:
+        _expect(lse, "lse", (B, H), _F32, dev)
+    _check(lib().fa_decode_paged_q4(q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                                    v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                                    lse.data_ptr(), wp, ws_bytes, B, H, Hkv, d, num_blocks, bs, max_blocks,
+                                    _scale(d, scale), n_splits, _stream(dev)), "fa_decode_paged_q4")
+    return out, lse

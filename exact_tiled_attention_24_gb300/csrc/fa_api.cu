@@ -302,50 +302,47 @@ static fa::HeadRows head_rows(const fa_heads* t, int B, int H, int N, int d) {
           t->stride_b * (B - 1) + t->stride_h * (H - 1) + t->stride_n * (N - 1) + d};
 }
 
-// Checks of the training form; on FA_OK fills p (tensors in q, k and their
-// counterparts a, b: the outputs, or the output gradients).
-static int norm_rope_args(fa::NormRope* p, const fa_heads* q, const fa_heads* k, const fa_heads* a, const fa_heads* b,
-                          const float* cos, const float* sin, const int* positions, int positions_per_batch,
-                          const void* q_weight, const void* k_weight, int weight_fp32, int B, int H, int Hkv, int N,
-                          int d, int rot, int n_pos, float eps, int interleaved) {
-  const fa_heads* ts[] = {q, k, a, b};
+// Checks of the training form; on FA_OK fills p.
+static int norm_rope_args(fa::NormRope* p, const fa_norm_rope_args* a, const fa_heads* q, const fa_heads* k) {
+  const fa_heads* ts[] = {q, k, &a->q_out, &a->k_out};
   for (const fa_heads* t : ts)
-    if (!t || !t->ptr || !heads_strides_ok(t)) return FA_ERR_INVALID_ARG;
-  if (Hkv < 1 || (!q_weight) != (!k_weight)) return FA_ERR_INVALID_ARG;
-  int st = check_sizes(B, H, N, d);
+    if (!t->ptr || !heads_strides_ok(t)) return FA_ERR_INVALID_ARG;
+  if (a->Hkv < 1 || (!a->q_weight) != (!a->k_weight)) return FA_ERR_INVALID_ARG;
+  int st = check_sizes(a->B, a->H, a->N, a->d);
+  if (st == FA_OK) st = check_sizes(a->B, a->Hkv, a->N, a->d);
   if (st != FA_OK) return st;
-  if ((st = check_rope(cos, sin, d, rot, n_pos, q_weight, k_weight, weight_fp32, eps)) != FA_OK) return st;
-  if (rot == 0 && !q_weight) return FA_ERR_INVALID_ARG;               // nothing to do
-  if (rot > 0 && !positions && n_pos < N) return FA_ERR_INVALID_ARG;  // token n is at position n
-  if (H > 65536 || Hkv > 65536) return FA_ERR_UNSUPPORTED;
+  if ((st = check_rope(a->cos, a->sin, a->d, a->rot, a->n_pos, a->q_weight, a->k_weight, a->weight_fp32, a->eps)) !=
+      FA_OK)
+    return st;
+  if (a->rot == 0 && !a->q_weight) return FA_ERR_INVALID_ARG;                     // nothing to do
+  if (a->rot > 0 && !a->positions && a->n_pos < a->N) return FA_ERR_INVALID_ARG;  // token n is at position n
+  if (a->H > 65536 || a->Hkv > 65536) return FA_ERR_UNSUPPORTED;
   for (const fa_heads* t : ts)
     if (!heads_aligned(t)) return FA_ERR_MISALIGNED;
-  if (!rope_aligned(cos, sin, rot, q_weight, k_weight) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+  if (!rope_aligned(a->cos, a->sin, a->rot, a->q_weight, a->k_weight) ||
+      (reinterpret_cast<uintptr_t>(a->positions) & 3u))
     return FA_ERR_MISALIGNED;
   *p = fa::NormRope{};
-  p->q = head_rows(q, B, H, N, d);
-  p->k = head_rows(k, B, Hkv, N, d);
-  p->q_out = head_rows(a, B, H, N, d);
-  p->k_out = head_rows(b, B, Hkv, N, d);
-  p->cos = cos, p->sin = sin;
-  p->positions = rot > 0 ? positions : nullptr;
-  p->pos_sb = positions_per_batch ? N : 0;
-  p->q_weight = q_weight, p->k_weight = k_weight;
-  p->w32 = weight_fp32 != 0, p->interleaved = interleaved != 0;
-  p->B = B, p->H = H, p->Hkv = Hkv, p->N = N, p->rot = rot, p->n_pos = n_pos;
-  p->eps = eps;
+  p->q = head_rows(q, a->B, a->H, a->N, a->d);
+  p->k = head_rows(k, a->B, a->Hkv, a->N, a->d);
+  p->q_out = head_rows(&a->q_out, a->B, a->H, a->N, a->d);
+  p->k_out = head_rows(&a->k_out, a->B, a->Hkv, a->N, a->d);
+  p->cos = a->cos, p->sin = a->sin;
+  p->positions = a->rot > 0 ? a->positions : nullptr;
+  p->pos_sb = a->positions_per_batch ? a->N : 0;
+  p->q_weight = a->q_weight, p->k_weight = a->k_weight;
+  p->w32 = a->weight_fp32 != 0, p->interleaved = a->interleaved != 0;
+  p->B = a->B, p->H = a->H, p->Hkv = a->Hkv, p->N = a->N, p->rot = a->rot, p->n_pos = a->n_pos;
+  p->eps = a->eps;
   return FA_OK;
 }
 
-int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out, const fa_heads* k_out,
-                    const float* cos, const float* sin, const int* positions, int positions_per_batch,
-                    const void* q_weight, const void* k_weight, int weight_fp32, int B, int H, int Hkv, int N, int d,
-                    int rot, int n_pos, float eps, int interleaved, void* stream) {
+int fa_qk_norm_rope(const fa_norm_rope_args* a, void* stream) {
+  if (!a) return FA_ERR_INVALID_ARG;
   fa::NormRope p;
-  const int st = norm_rope_args(&p, q, k, q_out, k_out, cos, sin, positions, positions_per_batch, q_weight, k_weight,
-                                weight_fp32, B, H, Hkv, N, d, rot, n_pos, eps, interleaved);
+  const int st = norm_rope_args(&p, a, &a->q, &a->k);
   if (st != FA_OK) return st;
-  return map_cuda(fa::launch_norm_rope(p, d, static_cast<cudaStream_t>(stream)));
+  return map_cuda(fa::launch_norm_rope(p, a->d, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d) {
@@ -353,25 +350,23 @@ size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d) {
   return static_cast<size_t>(2) * fa::norm_rope_bwd_parts(B, N, d) * d * sizeof(float);
 }
 
-int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q, const fa_heads* k,
-                        const fa_heads* dq, const fa_heads* dk, float* dq_weight, float* dk_weight, const float* cos,
-                        const float* sin, const int* positions, int positions_per_batch, const void* q_weight,
-                        const void* k_weight, int weight_fp32, void* workspace, size_t ws_bytes, int B, int H, int Hkv,
-                        int N, int d, int rot, int n_pos, float eps, int interleaved, void* stream) {
-  if (!q_weight && !k_weight) q = dq_out, k = dk_out;  // no norm: q and k are not read
+int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream) {
+  if (!a || !g) return FA_ERR_INVALID_ARG;
+  const bool norm = a->q_weight || a->k_weight;
   fa::NormRope p;
-  const int st = norm_rope_args(&p, q, k, dq_out, dk_out, cos, sin, positions, positions_per_batch, q_weight, k_weight,
-                                weight_fp32, B, H, Hkv, N, d, rot, n_pos, eps, interleaved);
+  // no norm: q and k are not read
+  const int st = norm_rope_args(&p, a, norm ? &a->q : &a->q_out, norm ? &a->k : &a->k_out);
   if (st != FA_OK) return st;
-  if (!dq || !dk || !dq->ptr || !dk->ptr || !heads_strides_ok(dq) || !heads_strides_ok(dk)) return FA_ERR_INVALID_ARG;
-  if (q_weight && (!dq_weight || !dk_weight)) return FA_ERR_INVALID_ARG;
-  if (q_weight && (!workspace || ws_bytes < fa_qk_norm_rope_bwd_workspace_bytes(B, N, d))) return FA_ERR_WORKSPACE;
-  if (!heads_aligned(dq) || !heads_aligned(dk) || !aligned16(workspace) || !aligned16(dq_weight) ||
-      !aligned16(dk_weight))
+  if (!g->dq.ptr || !g->dk.ptr || !heads_strides_ok(&g->dq) || !heads_strides_ok(&g->dk)) return FA_ERR_INVALID_ARG;
+  if (norm && (!g->dq_weight || !g->dk_weight)) return FA_ERR_INVALID_ARG;
+  if (norm && (!g->workspace || g->ws_bytes < fa_qk_norm_rope_bwd_workspace_bytes(a->B, a->N, a->d)))
+    return FA_ERR_WORKSPACE;
+  if (!heads_aligned(&g->dq) || !heads_aligned(&g->dk) || !aligned16(g->workspace) || !aligned16(g->dq_weight) ||
+      !aligned16(g->dk_weight))
     return FA_ERR_MISALIGNED;
-  p.dq = head_rows(dq, B, H, N, d);
-  p.dk = head_rows(dk, B, Hkv, N, d);
-  return map_cuda(fa::launch_norm_rope_bwd(p, d, static_cast<float*>(workspace), dq_weight, dk_weight,
+  p.dq = head_rows(&g->dq, a->B, a->H, a->N, a->d);
+  p.dk = head_rows(&g->dk, a->B, a->Hkv, a->N, a->d);
+  return map_cuda(fa::launch_norm_rope_bwd(p, a->d, static_cast<float*>(g->workspace), g->dq_weight, g->dk_weight,
                                            static_cast<cudaStream_t>(stream)));
 }
 
@@ -393,80 +388,57 @@ static fa::TokenRows token_rows(const fa_tokens* t, int T, int H, int d) {
           t->stride_t * (T - 1) + t->stride_h * (H - 1) + d};
 }
 
-static int append_args(fa::Append* p, const fa_tokens* q, const fa_tokens* k, const fa_tokens* v,
-                       const fa_tokens* q_out, void* k_cache, void* v_cache, const int* block_table,
-                       const int* positions, const int* requests, const float* cos, const float* sin,
-                       const void* q_weight, const void* k_weight, int weight_fp32, int T, int B, int H, int Hkv, int d,
-                       int num_blocks, int block_size, int max_blocks, int rot, int n_pos, float eps,
-                       int interleaved) {
-  if (!k || !v || !k->ptr || !v->ptr || !k_cache || !v_cache || !block_table || !positions) return FA_ERR_INVALID_ARG;
-  if (!tokens_strides_ok(k) || !tokens_strides_ok(v)) return FA_ERR_INVALID_ARG;
-  const bool queries = q != nullptr;
-  if (queries != (q_out != nullptr)) return FA_ERR_INVALID_ARG;
-  if (queries && (!q->ptr || !q_out->ptr || H < 1 || !tokens_strides_ok(q) || !tokens_strides_ok(q_out)))
+static int append(const fa_append_args* a, bool q4, void* stream) {
+  if (!a || !a->k.ptr || !a->v.ptr || !a->k_cache || !a->v_cache || !a->block_table || !a->positions)
     return FA_ERR_INVALID_ARG;
-  if (!queries && q_weight) return FA_ERR_INVALID_ARG;
-  if (queries && (!q_weight) != (!k_weight)) return FA_ERR_INVALID_ARG;
-  if (T < 1 || B < 1 || (!requests && T > B)) return FA_ERR_INVALID_ARG;
-  int st = check_cache(Hkv, num_blocks, block_size, max_blocks);
+  if (!tokens_strides_ok(&a->k) || !tokens_strides_ok(&a->v)) return FA_ERR_INVALID_ARG;
+  if (q4 && (!a->k_scale || !a->v_scale || (!a->k_values) != (!a->v_values))) return FA_ERR_INVALID_ARG;
+  const bool queries = a->q.ptr != nullptr;
+  if (queries != (a->q_out.ptr != nullptr)) return FA_ERR_INVALID_ARG;
+  if (queries && (a->H < 1 || !tokens_strides_ok(&a->q) || !tokens_strides_ok(&a->q_out))) return FA_ERR_INVALID_ARG;
+  if (!queries && a->q_weight) return FA_ERR_INVALID_ARG;
+  if (queries && (!a->q_weight) != (!a->k_weight)) return FA_ERR_INVALID_ARG;
+  if (a->T < 1 || a->B < 1 || (!a->requests && a->T > a->B)) return FA_ERR_INVALID_ARG;
+  int st = check_cache(a->Hkv, a->num_blocks, a->block_size, a->max_blocks_per_seq);
   if (st != FA_OK) return st;
-  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if ((st = check_rope(cos, sin, d, rot, n_pos, q_weight, k_weight, weight_fp32, eps)) != FA_OK) return st;
-  if (H > 16384 || Hkv > 16384) return FA_ERR_UNSUPPORTED;
-  if (!tokens_aligned(k) || !tokens_aligned(v) || (queries && (!tokens_aligned(q) || !tokens_aligned(q_out))) ||
-      !aligned16(k_cache) || !aligned16(v_cache) || !rope_aligned(cos, sin, rot, q_weight, k_weight) ||
-      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(positions) |
-        reinterpret_cast<uintptr_t>(requests)) & 3u))
+  if (a->d != 64 && a->d != 128) return FA_ERR_UNSUPPORTED;
+  if ((st = check_rope(a->cos, a->sin, a->d, a->rot, a->n_pos, a->q_weight, a->k_weight, a->weight_fp32, a->eps)) !=
+      FA_OK)
+    return st;
+  if (a->H > 16384 || a->Hkv > 16384) return FA_ERR_UNSUPPORTED;
+  if (!tokens_aligned(&a->k) || !tokens_aligned(&a->v) ||
+      (queries && (!tokens_aligned(&a->q) || !tokens_aligned(&a->q_out))) || !aligned16(a->k_cache) ||
+      !aligned16(a->v_cache) || !rope_aligned(a->cos, a->sin, a->rot, a->q_weight, a->k_weight) ||
+      ((reinterpret_cast<uintptr_t>(a->block_table) | reinterpret_cast<uintptr_t>(a->positions) |
+        reinterpret_cast<uintptr_t>(a->requests)) & 3u))
     return FA_ERR_MISALIGNED;
-  *p = fa::Append{};
+  if (q4 && (!aligned16(a->k_scale) || !aligned16(a->v_scale) || !aligned16(a->k_values) || !aligned16(a->v_values)))
+    return FA_ERR_MISALIGNED;
+  fa::Append p{};
   if (queries) {
-    p->q = token_rows(q, T, H, d);
-    p->q_out = token_rows(q_out, T, H, d);
+    p.q = token_rows(&a->q, a->T, a->H, a->d);
+    p.q_out = token_rows(&a->q_out, a->T, a->H, a->d);
   }
-  p->k = token_rows(k, T, Hkv, d);
-  p->v = token_rows(v, T, Hkv, d);
-  p->k_cache = k_cache, p->v_cache = v_cache;
-  p->block_table = block_table, p->positions = positions, p->requests = requests;
-  p->cos = cos, p->sin = sin;
-  p->q_weight = q_weight, p->k_weight = k_weight;
-  p->w32 = weight_fp32 != 0, p->interleaved = interleaved != 0;
-  p->T = T, p->B = B, p->H = queries ? H : 0, p->Hkv = Hkv;
-  p->num_blocks = num_blocks, p->bs = block_size, p->max_blocks = max_blocks, p->rot = rot, p->n_pos = n_pos;
-  p->eps = eps;
-  return FA_OK;
+  p.k = token_rows(&a->k, a->T, a->Hkv, a->d);
+  p.v = token_rows(&a->v, a->T, a->Hkv, a->d);
+  p.k_cache = a->k_cache, p.v_cache = a->v_cache;
+  if (q4) {
+    p.k_scale = static_cast<__nv_bfloat16*>(a->k_scale), p.v_scale = static_cast<__nv_bfloat16*>(a->v_scale);
+    p.k_values = static_cast<__nv_bfloat16*>(a->k_values), p.v_values = static_cast<__nv_bfloat16*>(a->v_values);
+  }
+  p.block_table = a->block_table, p.positions = a->positions, p.requests = a->requests;
+  p.cos = a->cos, p.sin = a->sin;
+  p.q_weight = a->q_weight, p.k_weight = a->k_weight;
+  p.w32 = a->weight_fp32 != 0, p.interleaved = a->interleaved != 0;
+  p.T = a->T, p.B = a->B, p.H = queries ? a->H : 0, p.Hkv = a->Hkv;
+  p.num_blocks = a->num_blocks, p.bs = a->block_size, p.max_blocks = a->max_blocks_per_seq;
+  p.rot = a->rot, p.n_pos = a->n_pos;
+  p.eps = a->eps;
+  return map_cuda(fa::launch_append(p, a->d, q4, static_cast<cudaStream_t>(stream)));
 }
 
-int fa_append_paged(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out, void* k_cache,
-                    void* v_cache, const int* block_table, const int* positions, const int* requests, const float* cos,
-                    const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B, int H,
-                    int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot, int n_pos,
-                    float eps, int interleaved, void* stream) {
-  fa::Append p;
-  const int st = append_args(&p, q, k, v, q_out, k_cache, v_cache, block_table, positions, requests, cos, sin,
-                             q_weight, k_weight, weight_fp32, T, B, H, Hkv, d, num_blocks, block_size,
-                             max_blocks_per_seq, rot, n_pos, eps, interleaved);
-  if (st != FA_OK) return st;
-  return map_cuda(fa::launch_append(p, d, false, static_cast<cudaStream_t>(stream)));
-}
-
-int fa_append_paged_q4(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out,
-                       void* k_cache, void* k_scale, void* v_cache, void* v_scale, void* k_values, void* v_values,
-                       const int* block_table, const int* positions, const int* requests, const float* cos,
-                       const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B,
-                       int H, int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot,
-                       int n_pos, float eps, int interleaved, void* stream) {
-  if (!k_scale || !v_scale || (!k_values) != (!v_values)) return FA_ERR_INVALID_ARG;
-  fa::Append p;
-  const int st = append_args(&p, q, k, v, q_out, k_cache, v_cache, block_table, positions, requests, cos, sin,
-                             q_weight, k_weight, weight_fp32, T, B, H, Hkv, d, num_blocks, block_size,
-                             max_blocks_per_seq, rot, n_pos, eps, interleaved);
-  if (st != FA_OK) return st;
-  if (!aligned16(k_scale) || !aligned16(v_scale) || !aligned16(k_values) || !aligned16(v_values))
-    return FA_ERR_MISALIGNED;
-  p.k_scale = static_cast<__nv_bfloat16*>(k_scale), p.v_scale = static_cast<__nv_bfloat16*>(v_scale);
-  p.k_values = static_cast<__nv_bfloat16*>(k_values), p.v_values = static_cast<__nv_bfloat16*>(v_values);
-  return map_cuda(fa::launch_append(p, d, true, static_cast<cudaStream_t>(stream)));
-}
+int fa_append_paged(const fa_append_args* a, void* stream) { return append(a, false, stream); }
+int fa_append_paged_q4(const fa_append_args* a, void* stream) { return append(a, true, stream); }
 
 int fa_decode_q4_splits(int B, int H, int Hkv, int block_size, int max_blocks_per_seq) {
   if (B < 1 || H < 1 || check_heads(H, Hkv) != FA_OK || check_cache(Hkv, 1, block_size, max_blocks_per_seq) != FA_OK)
@@ -488,7 +460,8 @@ int fa_decode_paged_q4(const void* q, const void* k_cache, const void* k_scale, 
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B > 65535 || static_cast<long long>(Hkv) * ((H / Hkv + 7) / 8) > 65535 || n_splits > 4096)
     return FA_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < fa_decode_workspace_bytes(B, H, d, n_splits)) return FA_ERR_WORKSPACE;
+  if (n_splits > 1 && (!workspace || ws_bytes < fa_decode_workspace_bytes(B, H, d, n_splits)))
+    return FA_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(k_scale) || !aligned16(v_cache) || !aligned16(v_scale) ||
       !aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
@@ -500,9 +473,11 @@ int fa_decode_paged_q4(const void* q, const void* k_cache, const void* k_scale, 
   p.k_scale = static_cast<const uint32_t*>(k_scale), p.v_scale = static_cast<const uint32_t*>(v_scale);
   p.block_table = block_table, p.seq_lens = seq_lens;
   p.o = static_cast<__nv_bfloat16*>(o), p.lse = lse;
-  p.o_part = static_cast<float*>(workspace);
-  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        ((rows * d * sizeof(float) + 255) & ~static_cast<size_t>(255)));
+  if (n_splits > 1) {
+    p.o_part = static_cast<float*>(workspace);
+    p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          ((rows * d * sizeof(float) + 255) & ~static_cast<size_t>(255)));
+  }
   p.B = B, p.H = H, p.Hkv = Hkv, p.num_blocks = num_blocks, p.bs = block_size, p.max_blocks = max_blocks_per_seq;
   p.scale_log2 = scale * 1.4426950408889634f;
   return map_cuda(fa::launch_decode_q4(p, d, n_splits, static_cast<cudaStream_t>(stream)));

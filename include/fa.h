@@ -401,42 +401,82 @@ typedef struct {
   long long stride_t, stride_h;
 } fa_tokens;
 
+/* Arguments of the norm and rotation of q and k. Unused ones are 0. */
+typedef struct {
+  fa_heads q, k;         /* [B][H][N][d], [B][Hkv][N][d] */
+  fa_heads q_out, k_out; /* the outputs (their gradients in the backward) */
+  const float* cos;      /* [n_pos][rot/2]; NULL with rot = 0 */
+  const float* sin;
+  const int* positions;  /* device, [N] or [B][N], or NULL */
+  const void* q_weight;  /* [d]; NULL: no norm */
+  const void* k_weight;
+  int B, H, Hkv, N, d;
+  int rot, n_pos;
+  int positions_per_batch; /* 1: positions are [B][N] */
+  int weight_fp32;         /* 1: the weights are fp32 */
+  int interleaved;
+  float eps;
+} fa_norm_rope_args;
+
 /*
  * Norm and rotation of q [B][H][N][d] and k [B][Hkv][N][d] into q_out and
  * k_out (any Hkv >= 1), as fa_fwd_gqa takes them when those are contiguous.
- *   positions  device int32, [N] (positions_per_batch = 0) or [B][N]
- *              (positions_per_batch = 1): the token's row of the tables;
- *              NULL: token n is at position n (then n_pos >= N). A position
- *              outside [0, n_pos) is never used as an index: the token's
- *              rows are written as zeros and fa_last_device_error reports
- *              FA_ERR_BAD_INDEX.
+ *   positions  the token's row of the tables; NULL: token n is at position n
+ *              (then n_pos >= N). A position outside [0, n_pos) is never
+ *              used as an index: the token's rows are written as zeros and
+ *              fa_last_device_error reports FA_ERR_BAD_INDEX.
  * Errors: a NULL struct or pointer it must hold, sizes < 1, one weight
  * without the other, neither weights nor rotation, negative strides, eps
  * negative or not finite (with weights) -> FA_ERR_INVALID_ARG; d, rot, H or
- * Hkv > 65536, or B·H·N past 2^31 -> FA_ERR_UNSUPPORTED; pointers or strides
- * not 16-byte aligned (positions: 4) -> FA_ERR_MISALIGNED.
+ * Hkv > 65536, or B·H·N or B·Hkv·N past 2^31 -> FA_ERR_UNSUPPORTED; pointers
+ * or strides not 16-byte aligned (positions: 4) -> FA_ERR_MISALIGNED.
  */
-int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out, const fa_heads* k_out,
-                    const float* cos, const float* sin, const int* positions, int positions_per_batch,
-                    const void* q_weight, const void* k_weight, int weight_fp32, int B, int H, int Hkv, int N, int d,
-                    int rot, int n_pos, float eps, int interleaved, void* stream);
+int fa_qk_norm_rope(const fa_norm_rope_args* a, void* stream);
 
 /*
- * Its gradient: dq, dk for the output gradients dq_out, dk_out (for instance
- * fa_bwd's dq and dk), and dq_weight, dk_weight [d] fp32, summed over every
- * head of every token in a fixed order (the same inputs give the same bits).
- * q and k are the forward's inputs; without weights they and the weight
- * gradients are not touched and may be NULL, and no workspace is needed.
+ * Its gradient: dq, dk for the output gradients in a->q_out, a->k_out (for
+ * instance fa_bwd's dq and dk), and dq_weight, dk_weight [d] fp32, summed
+ * over every head of every token in a fixed order (the same inputs give the
+ * same bits). a->q and a->k are the forward's inputs; without weights they
+ * and the weight gradients are not touched and may be NULL, and no workspace
+ * is needed.
  *   workspace  fa_qk_norm_rope_bwd_workspace_bytes(B, N, d) bytes, 16-byte
  *              aligned; contents on entry are ignored.
  * Errors as the forward's, and FA_ERR_WORKSPACE.
  */
+typedef struct {
+  fa_heads dq, dk;
+  float* dq_weight;
+  float* dk_weight;
+  void* workspace;
+  size_t ws_bytes;
+} fa_norm_rope_grads;
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d);
-int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q, const fa_heads* k,
-                        const fa_heads* dq, const fa_heads* dk, float* dq_weight, float* dk_weight, const float* cos,
-                        const float* sin, const int* positions, int positions_per_batch, const void* q_weight,
-                        const void* k_weight, int weight_fp32, void* workspace, size_t ws_bytes, int B, int H, int Hkv,
-                        int N, int d, int rot, int n_pos, float eps, int interleaved, void* stream);
+int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream);
+
+/* Arguments of an append to a paged cache. Unused ones are 0. */
+typedef struct {
+  fa_tokens q, k, v, q_out; /* [T][H][d], [T][Hkv][d]; q.ptr NULL: no queries */
+  void* k_cache;
+  void* v_cache;
+  void* k_scale;  /* the last four for a 4-bit cache only */
+  void* v_scale;
+  void* k_values;
+  void* v_values;
+  const int* block_table; /* device, [B][max_blocks_per_seq] */
+  const int* positions;   /* device, [T] */
+  const int* requests;    /* device, [T], or NULL */
+  const float* cos;       /* [n_pos][rot/2]; NULL with rot = 0 */
+  const float* sin;
+  const void* q_weight;   /* [d]; NULL: no norm */
+  const void* k_weight;
+  int T, B, H, Hkv, d;
+  int num_blocks, block_size, max_blocks_per_seq;
+  int rot, n_pos;
+  int weight_fp32; /* 1: the weights are fp32 */
+  int interleaved;
+  float eps;
+} fa_append_args;
 
 /*
  * Append tokens to a paged cache (the cache and table of fa_decode_paged):
@@ -447,7 +487,7 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
  * as they were.
  *   k, v       [T][Hkv][d] new keys and values.
  *   q, q_out   [T][H][d] the same tokens' queries, in, and after norm and
- *              rotation, out (for fa_decode_paged); both NULL: none.
+ *              rotation, out (for fa_decode_paged); NULL pointers: none.
  *   positions  [T] device int32: each token's position in its request, which
  *              is both its cache slot and its row of the tables.
  *   requests   [T] device int32: each token's request (row of block_table);
@@ -464,11 +504,7 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
  * fa_decode_paged's for the cache; neither weights nor rotation is allowed
  * here (a plain copy); H or Hkv > 16384 -> FA_ERR_UNSUPPORTED.
  */
-int fa_append_paged(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out, void* k_cache,
-                    void* v_cache, const int* block_table, const int* positions, const int* requests, const float* cos,
-                    const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B, int H,
-                    int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot, int n_pos,
-                    float eps, int interleaved, void* stream);
+int fa_append_paged(const fa_append_args* a, void* stream);
 
 /*
  * A paged cache held in 4 bits. Per token and K/V head: d codes n in 0..15,
@@ -491,19 +527,15 @@ int fa_append_paged(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, 
  *                       steps will read. Rows of skipped tokens stay as they
  *                       were.
  */
-int fa_append_paged_q4(const fa_tokens* q, const fa_tokens* k, const fa_tokens* v, const fa_tokens* q_out,
-                       void* k_cache, void* k_scale, void* v_cache, void* v_scale, void* k_values, void* v_values,
-                       const int* block_table, const int* positions, const int* requests, const float* cos,
-                       const float* sin, const void* q_weight, const void* k_weight, int weight_fp32, int T, int B,
-                       int H, int Hkv, int d, int num_blocks, int block_size, int max_blocks_per_seq, int rot,
-                       int n_pos, float eps, int interleaved, void* stream);
+int fa_append_paged_q4(const fa_append_args* a, void* stream);
 
 /*
  * Decode step over a 4-bit cache: fa_decode_paged's arguments, conventions
  * and errors with the caches' codes and scales; any block_size >= 1, any
  * number of query heads per K/V head. Values are never written out in full:
  * both products run on the codes. Workspace as for fa_decode_paged
- * (fa_decode_workspace_bytes). Slots past a request's length may hold
+ * (fa_decode_workspace_bytes), but NULL and 0 will do for n_splits = 1.
+ * Slots past a request's length may hold
  * anything.
  * fa_decode_q4_splits gives an n_splits that fills the GPU for these sizes
  * (a host function; 0 for invalid sizes).

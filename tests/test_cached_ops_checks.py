@@ -1,7 +1,7 @@
 """Argument checks, on CPU, of the norm and rotation calls, the paged appends
 and the 4-bit decode: by the library (bad arguments are refused before any
 CUDA call) and by the binding (a fake library, tensors without storage)."""
-import ctypes
+import struct
 
 import pytest
 import torch
@@ -10,7 +10,7 @@ import exact_tiled_attention_24_gb300 as fa
 from exact_tiled_attention_24_gb300 import build as fabuild
 from test_binding_checks import F32, I32, fake, m, rejects  # noqa: F401
 
-FAKE, MIS, NUL = 0x10000, 0x10008, None
+FAKE, MIS, NUL = 0x10000, 0x10008, 0
 INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 1, 2, 3, 6
 
 
@@ -21,21 +21,25 @@ def L():
 
 
 def heads(ptr=FAKE, sb=4096, sh=128, sn=1024):
-    return fa.Heads(ptr, sb, sh, sn)
+    return ptr, sb, sh, sn
 
 
 def tokens(ptr=FAKE, st=1024, sh=128):
-    return fa.Tokens(ptr, st, sh)
+    return ptr, st, sh
+
+
+NO_HEADS, NO_TOKENS = (0, 0, 0, 0), (0, 0, 0)
 
 
 def test_norm_rope_refusals(L):
     def call(q=heads(), k=heads(), qo=heads(), ko=heads(), cos=FAKE, sin=FAKE, pos=FAKE, per=0, qw=FAKE, kw=FAKE,
              w32=0, B=1, H=4, Hkv=2, N=16, d=128, rot=128, n_pos=64, eps=1e-6):
-        return L.fa_qk_norm_rope(q, k, qo, ko, cos, sin, pos, per, qw, kw, w32, B, H, Hkv, N, d, rot, n_pos, eps, 0,
-                                 NUL)
+        return L.fa_qk_norm_rope(fa._NORM_ROPE_ARGS.pack(*q, *k, *qo, *ko, cos, sin, pos, qw, kw, B, H, Hkv, N, d, rot,
+                                                         n_pos, per, w32, 0, eps), None)
 
-    assert call(q=None) == INVALID and call(ko=None) == INVALID
-    assert call(q=heads(ptr=None)) == INVALID and call(qo=heads(ptr=None)) == INVALID
+    assert L.fa_qk_norm_rope(None, None) == INVALID
+    for name in ("q", "k", "qo", "ko"):
+        assert call(**{name: heads(ptr=0)}) == INVALID
     assert call(q=heads(sn=-128)) == INVALID
     assert call(cos=NUL) == INVALID and call(sin=NUL) == INVALID and call(n_pos=0) == INVALID
     assert call(qw=NUL) == INVALID and call(kw=NUL) == INVALID       # one weight without the other
@@ -62,18 +66,19 @@ def test_norm_rope_bwd_refusals(L):
 
     def call(dqo=heads(), dko=heads(), q=heads(), k=heads(), dq=heads(), dk=heads(), dqw=FAKE, dkw=FAKE, qw=FAKE,
              kw=FAKE, work=FAKE, ws_bytes=ws, d=128, rot=128):
-        return L.fa_qk_norm_rope_bwd(dqo, dko, q, k, dq, dk, dqw, dkw, FAKE, FAKE, NUL, 0, qw, kw, 0, work, ws_bytes,
-                                     1, 4, 2, 16, d, rot, 16, 1e-6, 0, NUL)
+        a = fa._NORM_ROPE_ARGS.pack(*q, *k, *dqo, *dko, FAKE, FAKE, NUL, qw, kw, 1, 4, 2, 16, d, rot, 16, 0, 0, 0, 1e-6)
+        return L.fa_qk_norm_rope_bwd(a, fa._NORM_ROPE_GRADS.pack(*dq, *dk, dqw, dkw, work, ws_bytes), None)
 
-    assert call(dqo=None) == INVALID and call(q=None) == INVALID and call(dk=None) == INVALID
-    assert call(dq=heads(ptr=None)) == INVALID and call(dq=heads(sb=-8)) == INVALID
+    assert L.fa_qk_norm_rope_bwd(None, None, None) == INVALID
+    assert call(dqo=NO_HEADS) == INVALID and call(q=NO_HEADS) == INVALID and call(dk=NO_HEADS) == INVALID
+    assert call(dq=heads(ptr=0)) == INVALID and call(dq=heads(sb=-8)) == INVALID
     assert call(dqw=NUL) == INVALID and call(dkw=NUL) == INVALID and call(kw=NUL) == INVALID
     assert call(work=NUL) == WORKSPACE and call(ws_bytes=ws - 1) == WORKSPACE
     assert call(d=80) == UNSUPPORTED and call(rot=8) == UNSUPPORTED
     assert call(work=MIS) == MISALIGNED and call(dqw=MIS) == MISALIGNED and call(dk=heads(sh=4)) == MISALIGNED
     # without weights neither q, k, the weight gradients nor a workspace are asked for
-    assert call(q=None, k=None, qw=NUL, kw=NUL, dqw=NUL, dkw=NUL, work=NUL, dq=heads(ptr=MIS)) == MISALIGNED
-    assert call(q=None, k=None, qw=NUL, kw=NUL, rot=0) == INVALID
+    assert call(q=NO_HEADS, k=NO_HEADS, qw=NUL, kw=NUL, dqw=NUL, dkw=NUL, work=NUL, dq=heads(ptr=MIS)) == MISALIGNED
+    assert call(q=NO_HEADS, k=NO_HEADS, qw=NUL, kw=NUL, rot=0) == INVALID
 
 
 @pytest.mark.parametrize("q4", [False, True])
@@ -81,15 +86,14 @@ def test_append_refusals(L, q4):
     def call(q=tokens(), k=tokens(), v=tokens(), qo=tokens(), kc=FAKE, ks=FAKE, vc=FAKE, vs=FAKE, kv=FAKE, vv=FAKE,
              table=FAKE, pos=FAKE, req=FAKE, cos=FAKE, sin=FAKE, qw=FAKE, kw=FAKE, w32=0, T=5, B=3, H=4, Hkv=2, d=128,
              num_blocks=10, bs=16, max_blocks=8, rot=128, n_pos=64, eps=1e-6):
-        rest = (table, pos, req, cos, sin, qw, kw, w32, T, B, H, Hkv, d, num_blocks, bs, max_blocks, rot, n_pos, eps,
-                0, NUL)
-        if q4:
-            return L.fa_append_paged_q4(q, k, v, qo, kc, ks, vc, vs, kv, vv, *rest)
-        return L.fa_append_paged(q, k, v, qo, kc, vc, *rest)
+        args = fa._APPEND_ARGS.pack(*q, *k, *v, *qo, kc, vc, ks, vs, kv, vv, table, pos, req, cos, sin, qw, kw, T, B,
+                                    H, Hkv, d, num_blocks, bs, max_blocks, rot, n_pos, w32, 0, eps)
+        return (L.fa_append_paged_q4 if q4 else L.fa_append_paged)(args, None)
 
-    for bad in (dict(k=None), dict(v=None), dict(k=tokens(ptr=None)), dict(kc=NUL), dict(vc=NUL), dict(table=NUL),
-                dict(pos=NUL), dict(q=None), dict(qo=None), dict(q=tokens(ptr=None)), dict(v=tokens(st=-8)),
-                dict(q=None, qo=None), dict(qw=NUL), dict(kw=NUL), dict(T=0), dict(B=0), dict(H=0), dict(Hkv=0),
+    assert L.fa_append_paged(None, None) == INVALID and L.fa_append_paged_q4(None, None) == INVALID
+    for bad in (dict(k=NO_TOKENS), dict(v=NO_TOKENS), dict(k=tokens(ptr=0)), dict(kc=NUL), dict(vc=NUL), dict(table=NUL),
+                dict(pos=NUL), dict(q=NO_TOKENS), dict(qo=NO_TOKENS), dict(v=tokens(st=-8)),
+                dict(q=NO_TOKENS, qo=NO_TOKENS), dict(qw=NUL), dict(kw=NUL), dict(T=0), dict(B=0), dict(H=0), dict(Hkv=0),
                 dict(num_blocks=0), dict(bs=0), dict(max_blocks=0), dict(req=NUL), dict(cos=NUL), dict(rot=-16),
                 dict(n_pos=0), dict(eps=float("inf"))):
         assert call(**bad) == INVALID, bad
@@ -113,7 +117,7 @@ def test_decode_q4_refusals(L):
     def call(q=FAKE, kc=FAKE, ks=FAKE, vc=FAKE, vs=FAKE, table=FAKE, lens=FAKE, o=FAKE, lse=FAKE, work=FAKE,
              ws_bytes=ws, B=2, H=8, Hkv=2, d=128, num_blocks=10, bs=16, max_blocks=8, scale=0.1, S=4):
         return L.fa_decode_paged_q4(q, kc, ks, vc, vs, table, lens, o, lse, work, ws_bytes, B, H, Hkv, d, num_blocks,
-                                    bs, max_blocks, scale, S, NUL)
+                                    bs, max_blocks, scale, S, None)
 
     for name in ("q", "kc", "ks", "vc", "vs", "table", "lens", "o", "lse"):
         assert call(**{name: NUL}) == INVALID, name
@@ -123,6 +127,7 @@ def test_decode_q4_refusals(L):
     for bad in (dict(d=96), dict(B=70000), dict(S=5000), dict(max_blocks=1 << 27), dict(num_blocks=1 << 28, bs=8)):
         assert call(**bad) == UNSUPPORTED, bad
     assert call(work=NUL) == WORKSPACE and call(ws_bytes=ws - 1) == WORKSPACE
+    assert call(work=NUL, ws_bytes=0, S=1, q=MIS) == MISALIGNED   # one split asks for no workspace
     for name in ("q", "kc", "ks", "vc", "vs", "o", "work"):
         assert call(**{name: MIS}) == MISALIGNED, name
     for name in ("table", "lens", "lse"):
@@ -253,5 +258,36 @@ def test_rope_tables_far_positions():
             fa.rope_tables(*bad, device="cpu")
 
 
-def test_structs_match_the_header():
-    assert ctypes.sizeof(fa.Heads) == 32 and ctypes.sizeof(fa.Tokens) == 24
+def test_structs_match_the_header(tmp_path):
+    """The packed argument structs have the C structs' layout."""
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "layout.c"
+    src.write_text('''
+#include <stdio.h>
+#include "fa.h"
+#define AT(s, f) printf("%zu ", offsetof(s, f));
+int main(void) {
+  AT(fa_norm_rope_args, q_out) AT(fa_norm_rope_args, cos) AT(fa_norm_rope_args, k_weight)
+  AT(fa_norm_rope_args, B) AT(fa_norm_rope_args, interleaved) AT(fa_norm_rope_args, eps)
+  AT(fa_norm_rope_grads, dq_weight) AT(fa_norm_rope_grads, ws_bytes)
+  AT(fa_append_args, q_out) AT(fa_append_args, k_cache) AT(fa_append_args, block_table) AT(fa_append_args, k_weight)
+  AT(fa_append_args, T) AT(fa_append_args, n_pos) AT(fa_append_args, eps)
+  return 0;
+}
+''')
+    exe = tmp_path / "layout"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
+    at = lambda fmt: struct.calcsize("@" + fmt)  # noqa: E731
+    h, t = "Pqqq", "Pqq"
+    a, b = 4 * h, 4 * t
+    assert got == [at(2 * h), at(a), at(a + "4P"), at(a + "5P"), at(a + "5P9i"), at(a + "5P10i"), at(2 * h), at(2 * h + "3P"),
+                   at(3 * t), at(b), at(b + "6P"), at(b + "12P"), at(b + "13P"), at(b + "13P9i"), at(b + "13P12i")]
