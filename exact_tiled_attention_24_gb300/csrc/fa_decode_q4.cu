@@ -29,6 +29,7 @@
 // the values subtract it first, since their sums run over the whole context.
 // Each warp walks its own 16-key tiles; the CTA's warps are merged at its end.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -43,13 +44,47 @@ static __device__ uint32_t g_decq4_err;
 namespace decq4 {
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int TK = 16;  // keys per warp tile
+constexpr int TK = 32;  // keys a warp takes at a time: one stage of its ring
 constexpr float LN2 = 0.69314718055994531f;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t NO_ROW = 0xffffffffu;
 
-// d (+)= A (16x16 bf16) B (16x8 bf16), fp32.
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// Each warp has a ring of its own in shared memory, so no two warps wait on
+// one another before the end. A stage holds 32 keys: K codes, V codes, K
+// pairs, V pairs. With up to 8 query heads a warp's state fits 128 registers
+// and 16 warps share an SM.
+template <int D, int NT>
+struct Ring {
+  static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM
+  static constexpr int CODES = TK * D / 2, PAIRS = TK * D / 16;
+  static constexpr int KC = 0, VC = CODES, KS = 2 * CODES, VS = KS + PAIRS;
+  static constexpr int STAGE = 2 * CODES + 2 * PAIRS;
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int BAR_OFF = WARPS * WARP;                 // [WARPS][STAGES] barriers
+  static constexpr int MASK_OFF = BAR_OFF + WARPS * STAGES * 8;  // [WARPS][STAGES] live keys
+  static constexpr int BYTES = MASK_OFF + WARPS * STAGES * 4;
+  static_assert(CTAS * (BYTES + 1024) <= 233472, "the CTAs must fit an SM");
+  // at the end each warp's ring takes its result: [8 NT heads][D + 1] fp32
+  static_assert(WARP >= 8 * NT * (D + 1 + 2 + WARPS) * 4, "a ring holds the warp's result");
+};
+
+// d (+)= A (16x16) B (16x8), fp32; both operands fp16, or both bf16.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with d = c + A B for c = (c0, c1, c0, c1).
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                             float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -61,30 +96,89 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return d;
 }
 
-// 16 + n for nibble I of each 16-bit half, as two bf16.
-template <int I>
-__device__ __forceinline__ uint32_t nibbles16(uint32_t w) {
-  const uint32_t v = I == 0 ? w << 3 : w >> (4 * I - 3);
-  return (v & 0x00780078u) | 0x41804180u;
-}
-// n − 8 (exact: both are bf16 integers).
-template <int I>
-__device__ __forceinline__ uint32_t nibbles_centred(uint32_t w) {
-  uint32_t v = nibbles16<I>(w), d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x41c041c0u));  // 24
+// (v & mask) | base in one instruction. The bases come in as kernel
+// arguments: as constants beside a constant mask they would take a second
+// instruction each.
+struct Bases {
+  uint32_t key, value;  // two fp16 1024, two bf16 16
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "r"(mask), "r"(base));
   return d;
 }
+
+// Keys: the four nibbles of each 16-bit half as four pairs of fp16, 1024 + n
+// (nibbles 0 and 2, in the lowest mantissa bits of 1024) and 16 (64 + n)
+// (nibbles 1 and 3, four bits up): one shift and four and-ors for 8 values.
+__device__ __forceinline__ void key_pairs(uint32_t w, uint32_t base, uint32_t (&v)[4]) {
+  const uint32_t h = w >> 8;
+  v[0] = and_or(w, 0x000f000fu, base);
+  v[1] = and_or(w, 0x00f000f0u, base);
+  v[2] = and_or(h, 0x000f000fu, base);
+  v[3] = and_or(h, 0x00f000f0u, base);
+}
+// Values: 16 + n for nibble I of each half, as two bf16 (n in the top four
+// mantissa bits of 16).
+template <int I>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t base) {
+  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), 0x00780078u, base);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Contiguous copy global -> shared by the copy engine, completing bytes on
+// the mbarrier: addresses and size are multiples of 16.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// 4- or 8-byte asynchronous copy global -> shared.
+template <int N>
+__device__ __forceinline__ void cp_async_small(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(__cvta_generic_to_global(src)),
+               "n"(N)
+               : "memory");
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// x / n for x < 2^30 and a fixed n, by a product with ceil(2^(30 + k) / n),
+// 2^(k-1) < n <= 2^k: the multiplier is off by less than n 2^-k <= 1 in units
+// of 2^-30 / n, too little to carry any x < 2^30 past the next integer.
+struct Divide {
+  uint32_t mul, shift;
+  static Divide of(int n) {
+    int k = 0;
+    while ((1ll << k) < n) ++k;
+    return {static_cast<uint32_t>(((1ull << (30 + k)) + n - 1) / n), static_cast<uint32_t>(30 + k)};
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(x)) * mul) >> shift);
+  }
+};
+
+// How a stage is filled. BULK (a block size with a factor of 8): runs of
+// `run` = 8, 16 or 32 consecutive slots of one block are contiguous, and a
+// lane copies one run of codes or pairs in one piece. GATHER (any other): a
+// lane looks up one key's row and the rows go over in 16-byte pieces.
+enum Fill : int { BULK = 0, GATHER = 1 };
+
 // One CTA: split s of request b's context, K/V head hk, 8·NT query heads.
-template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
+template <int D, int NT, int FILL>
+__global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
+    decode_q4_kernel(const DecodeQ4 p, int run, Divide by_bs, Bases bases) {
+  using R = Ring<D, NT>;
   constexpr int NG = D / 64;    // groups of a row
   constexpr int NH = 8 * NT;    // query heads of the CTA
   constexpr int MT = D / 16;    // 16-dimension tiles of the output
-  __shared__ float sm_o[WARPS][NH][D + 1];
-  __shared__ float sm_m[WARPS][NH], sm_l[WARPS][NH];
+  constexpr int ST = R::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* err = &g_decq4_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -101,39 +195,157 @@ __global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
   const int n_tiles = (L + TK - 1) / TK;
   const int tps = (n_tiles + S - 1) / S;
   const int tile0 = s * tps, tile1 = min(n_tiles, tile0 + tps);
+  const int my0 = tile0 + warp;  // this warp's tiles: my0, my0 + WARPS, ...
+  const int n_my = my0 < tile1 ? (tile1 - my0 + WARPS - 1) / WARPS : 0;
+
+  uint8_t* ring = smem + warp * R::WARP;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::BAR_OFF) + warp * ST;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + R::MASK_OFF) + warp * ST;
+  if (lane == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&full[i], FILL == BULK ? 1 : 32);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  // The token a lane looks up for a tile, and its table entry: the first of
+  // its run (BULK; lane = 4 run + part), or its key (GATHER).
+  const long long rows = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
+  auto token_of = [&](int tile) { return tile * TK + (FILL == BULK ? (lane >> 2) * run : lane); };
+  auto entry_of = [&](int j) -> int {  // -1: no such token, or outside the table
+    const int tok = token_of(my0 + j * WARPS);
+    if (j >= n_my || tok >= L || (FILL == BULK && (lane >> 2) * run >= TK)) return -1;
+    const long long ti = static_cast<long long>(b) * p.max_blocks + by_bs(tok);
+    return in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
+  };
+  // Fill stage st with tile j of this warp, from the lanes' table entries.
+  auto fill = [&](int j, int st, int entry) {
+    const int tok = token_of(my0 + j * WARPS);
+    const bool there = tok < L && (FILL == GATHER || (lane >> 2) * run < TK);
+    const bool live = there && entry >= 0 && entry < p.num_blocks;
+    if (there && !live) atomicExch(err, DEV_BAD_INDEX);
+    const uint32_t row = live ? (static_cast<uint32_t>(entry) * p.Hkv + hk) * static_cast<uint32_t>(p.bs) +
+                                    static_cast<uint32_t>(tok - by_bs(tok) * p.bs)
+                              : NO_ROW;
+    uint8_t* stage = ring + st * R::STAGE;
+    if (FILL == BULK) {
+      // parts: 0 K codes, 1 V codes, 2 K pairs, 3 V pairs
+      const int part = lane & 3, r = lane >> 2;
+      const int per_key = part < 2 ? D / 2 : D / 16;
+      const uint8_t* base = part == 0 ? p.k_cache : part == 1 ? p.v_cache
+                            : reinterpret_cast<const uint8_t*>(part == 2 ? p.k_scale : p.v_scale);
+      const int off = part == 0 ? R::KC : part == 1 ? R::VC : part == 2 ? R::KS : R::VS;
+      const bool ok = live && in_range(static_cast<long long>(row) * per_key, run * per_key, rows * per_key, err);
+      const uint32_t bytes = ok ? run * per_key : 0;
+      const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+      // keys whose run is there and before the context's end
+      uint32_t mask = live && part == 0 ? (run == 32 ? 0xffffffffu : ((1u << run) - 1u) << (r * run)) : 0u;
+      mask = __reduce_or_sync(0xffffffffu, mask);
+      if (lane == 0) {
+        masks[st] = mask;
+        mbar_arrive_expect_tx(&full[st], total);
+      }
+      __syncwarp();
+      if (ok) bulk_load(stage + off + r * run * per_key, base + static_cast<long long>(row) * per_key, bytes, &full[st]);
+    } else {
+      constexpr int CH = D / 32;     // 16-byte chunks of a row of codes
+      constexpr int RPI = 32 / CH;   // rows per warp instruction
+      const uint32_t mask = __ballot_sync(0xffffffffu, live);
+      if (lane == 0) masks[st] = mask;
+      const int c = lane % CH;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int key = i * RPI + lane / CH;
+        const uint32_t rw = __shfl_sync(0xffffffffu, row, key);
+        const long long off = static_cast<long long>(rw) * (D / 2) + c * 16;
+        if (rw != NO_ROW && in_range(off, 16, rows * (D / 2), err)) {
+          cp_async_16(stage + R::KC + key * (D / 2) + c * 16, p.k_cache + off, 16);
+          cp_async_16(stage + R::VC + key * (D / 2) + c * 16, p.v_cache + off, 16);
+        }
+      }
+      const long long so = static_cast<long long>(row) * NG;
+      if (live && in_range(so, NG, rows * NG, err)) {
+        cp_async_small<NG * 4>(stage + R::KS + lane * (NG * 4), p.k_scale + so);
+        cp_async_small<NG * 4>(stage + R::VS + lane * (NG * 4), p.v_scale + so);
+      }
+      cp_async_arrive_noinc(&full[st]);
+    }
+  };
+  int first[ST];  // the first stages' entries, loaded together
+#pragma unroll
+  for (int i = 0; i < ST; ++i) first[i] = entry_of(i);
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < n_my) fill(i, i, first[i]);
+  int issued = min(ST, n_my);
+  int entry = entry_of(issued);  // of the next tile to fill: loaded a tile ahead
 
   // Query operand: for group gr and word w of a lane quarter's 16 dimensions
-  // 64 gr + 16 t + 8 w + 0..7, K step 2 h' (h' = 0, 1) multiplies elements
-  // (2h', 2h'+4) and (2h'+1, 2h'+5).
+  // 64 gr + 16 t + 8 w + 0..7, K step 2 w + h (h = 0, 1) multiplies elements
+  // (2h, 2h + 4), whose codes come as 1024 + n, and (2h + 1, 2h + 5), whose
+  // come as 16 (64 + n): the latter's q carry the 1/16. A head's q are scaled
+  // by a power of two to a largest magnitude in [1, 2): fp16 then holds all
+  // that counts of them exactly. The accumulators start at
+  // -Σ q (offset + 8), so that a group's product ends as Σ q (n − 8).
   uint32_t qf[NT][NG][4][2];
-  float qsum[NT][NG][2];  // Σ q over a group, of this lane's heads 2t, 2t + 1
+  float qsum[NT][NG][2], qoff[NT][NG][2];  // of this lane's heads 2t, 2t + 1
+  float sc[NT][2];                         // score units to log2 units
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    uint4 v[NG][2];
+    float top = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        v[gr][w] = make_uint4(0, 0, 0, 0);
+        const long long off = static_cast<long long>(head0 + nt * 8 + g) * D + gr * 64 + t * 16 + w * 8;
+        if (nt * 8 + g < G && in_range(off, 8, static_cast<long long>(p.B) * p.H * D, err))
+          v[gr][w] = *reinterpret_cast<const uint4*>(p.q + off);
+        const uint32_t u[4] = {v[gr][w].x, v[gr][w].y, v[gr][w].z, v[gr][w].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(u[i])), fabsf(bf_hi(u[i]))));
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^-e with 2^e <= top < 2^(e+1), kept within the normal range
+    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    e = e < -126 ? -126 : e > 126 ? 126 : e;
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // of head g; never 0, or a masked score's -inf would become NaN
+    const float up = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, 1.17549435e-38f);
+    sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t);      // lanes of head 2t
+    sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);  // and of head 2t + 1
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        const long long off = static_cast<long long>(head0 + nt * 8 + g) * D + gr * 64 + t * 16 + w * 8;
-        if (nt * 8 + g < G && in_range(off, 8, static_cast<long long>(p.B) * p.H * D, err))
-          v = *reinterpret_cast<const uint4*>(p.q + off);
-        // v.x = (e0, e1), v.y = (e2, e3), v.z = (e4, e5), v.w = (e6, e7)
-        qf[nt][gr][2 * w][0] = __byte_perm(v.x, v.z, 0x5410);
-        qf[nt][gr][2 * w][1] = __byte_perm(v.x, v.z, 0x7632);
-        qf[nt][gr][2 * w + 1][0] = __byte_perm(v.y, v.w, 0x5410);
-        qf[nt][gr][2 * w + 1][1] = __byte_perm(v.y, v.w, 0x7632);
+        const uint4 x = v[gr][w];  // elements (0, 1), (2, 3), (4, 5), (6, 7)
+        const float d16 = down * 0.0625f;
+        qf[nt][gr][2 * w][0] = pack_f16x2(bf_lo(x.x) * down, bf_lo(x.z) * down);
+        qf[nt][gr][2 * w][1] = pack_f16x2(bf_hi(x.x) * d16, bf_hi(x.z) * d16);
+        qf[nt][gr][2 * w + 1][0] = pack_f16x2(bf_lo(x.y) * down, bf_lo(x.w) * down);
+        qf[nt][gr][2 * w + 1][1] = pack_f16x2(bf_hi(x.y) * d16, bf_hi(x.w) * d16);
       }
-      const uint32_t one = 0x3f803f80u;
-      const uint32_t ones[4] = {one, one, one, one};
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      // Σ q and Σ q (offset + 8) of what fp16 holds: products with constants.
+      // Registers 2 and 3 of A meet the second half of a K step.
+      const uint32_t one = 0x3c003c00u, x16 = 0x4c004c00u;        // 1, 16
+      const uint32_t lo = 0x64086408u, hi = 0x64806480u;          // 1024 + 8, 16 (64 + 8)
+      const uint32_t ones[4] = {one, one, x16, x16}, offs[4] = {lo, lo, hi, hi};
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) mma(c, ones, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
-      qsum[nt][gr][0] = c[0];
-      qsum[nt][gr][1] = c[1];
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_f16(c, ones, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
+        mma_f16(o, offs, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
+      }
+      qsum[nt][gr][0] = c[0], qsum[nt][gr][1] = c[1];
+      qoff[nt][gr][0] = -o[0], qoff[nt][gr][1] = -o[1];
     }
+  }
 
   float acc[NT][MT][4];
-  float m[NT][2], l[NT][2], zc[NT][NG][2];
+  // Per head: the exponents' reference in log2 units (0 while no key has been
+  // seen), the score above which it is raised, and the running sums.
+  float m[NT][2], lim[NT][2], l[NT][2], zc[NT][NG][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -142,117 +354,109 @@ __global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
       for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[nt][e] = -INFINITY;
+      m[nt][e] = 0.f;
+      lim[nt][e] = -INFINITY;
       l[nt][e] = 0.f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) zc[nt][gr][e] = 0.f;
     }
   }
 
-  const long long rows = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
-  for (int tile = tile0 + warp; tile < tile1; tile += WARPS) {
-    // Lanes 0..15 look up the tile's rows of the cache.
-    uint32_t row = NO_ROW;
-    {
-      const int tok = tile * TK + (lane & 15);
-      if (tok < L) {
-        const int bi = tok / p.bs;
-        const long long ti = static_cast<long long>(b) * p.max_blocks + bi;
-        const int blk = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
-        if (blk >= 0 && blk < p.num_blocks)
-          row = (static_cast<uint32_t>(blk) * p.Hkv + hk) * static_cast<uint32_t>(p.bs) +
-                static_cast<uint32_t>(tok - bi * p.bs);
-        else
-          atomicExch(err, DEV_BAD_INDEX);
-      }
-    }
-    uint32_t krow[2], vrow[4];
-    krow[0] = __shfl_sync(0xffffffffu, row, g);
-    krow[1] = __shfl_sync(0xffffffffu, row, g + 8);
-    vrow[0] = __shfl_sync(0xffffffffu, row, 2 * t);
-    vrow[1] = __shfl_sync(0xffffffffu, row, 2 * t + 1);
-    vrow[2] = __shfl_sync(0xffffffffu, row, 2 * t + 8);
-    vrow[3] = __shfl_sync(0xffffffffu, row, 2 * t + 9);
+  bool ok = true;
+  int st = 0;
+  uint32_t phase = 0;
+  for (int j = 0; j < issued; ++j, phase ^= st + 1 == ST, st = st + 1 == ST ? 0 : st + 1) {
+    if (!mbar_wait_warp(&full[st], phase, err)) ok = false;
+    if (!ok) continue;  // wait for what is in flight, fill no more
+    __syncwarp();       // lane 0's mask
+    const uint8_t* stage = ring + st * R::STAGE;
+    uint32_t mask = masks[st];
+    const int left = L - (my0 + j * WARPS) * TK;
+    if (left < TK) mask &= (1u << left) - 1u;
 
-    uint2 kw[2][NG];
-    uint32_t ks_[2][NG], vs_[2][NG], vw[4][NG];
+    // Scores: x[nt][u][2 r + e] is key 16 u + g + 8 r, head 2 t + e.
+    float x[NT][2][4];
+    uint32_t vp[2][2][NG];  // the keys' value pairs
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int u = 0; u < 2; ++u) {
+      uint32_t kp[2][NG];
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        kw[r][gr] = make_uint2(0, 0);
-        ks_[r][gr] = vs_[r][gr] = 0;
-        if (krow[r] != NO_ROW) {
-          const long long c = static_cast<long long>(krow[r]) * (D / 2) + gr * 32 + t * 8;
-          const long long sc = static_cast<long long>(krow[r]) * NG + gr;
-          if (in_range(c, 8, rows * (D / 2), err)) kw[r][gr] = *reinterpret_cast<const uint2*>(p.k_cache + c);
-          if (in_range(sc, 1, rows * NG, err)) {
-            ks_[r][gr] = p.k_scale[sc];
-            vs_[r][gr] = p.v_scale[sc];
-          }
+      for (int r = 0; r < 2; ++r) {
+        const int key = 16 * u + g + 8 * r;
+        if (NG == 2) {
+          const uint2 a = *reinterpret_cast<const uint2*>(stage + R::KS + key * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(stage + R::VS + key * 8);
+          kp[r][0] = a.x, kp[r][NG - 1] = a.y, vp[u][r][0] = c.x, vp[u][r][NG - 1] = c.y;
+        } else {
+          kp[r][0] = *reinterpret_cast<const uint32_t*>(stage + R::KS + key * 4);
+          vp[u][r][0] = *reinterpret_cast<const uint32_t*>(stage + R::VS + key * 4);
         }
       }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        vw[r][gr] = 0;
-        const long long c = static_cast<long long>(vrow[r]) * (D / 2) + gr * 32 + g * 4;
-        if (vrow[r] != NO_ROW && in_range(c, 4, rows * (D / 2), err))
-          vw[r][gr] = *reinterpret_cast<const uint32_t*>(p.v_cache + c);
+        uint32_t a[4][4];  // per K step
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int key = 16 * u + g + 8 * r;
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + R::KC + key * (D / 2) + gr * 32 + t * 8);
+          uint32_t v[4];
+          key_pairs(w.x, bases.key, v);
+          a[0][r] = v[0], a[0][r + 2] = v[1], a[1][r] = v[2], a[1][r + 2] = v[3];
+          key_pairs(w.y, bases.key, v);
+          a[2][r] = v[0], a[2][r + 2] = v[1], a[3][r] = v[2], a[3][r + 2] = v[3];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[4];
+          mma_f16_from(c, a[0], qf[nt][gr][0][0], qf[nt][gr][0][1], qoff[nt][gr][0], qoff[nt][gr][1]);
+#pragma unroll
+          for (int ks = 1; ks < 4; ++ks) mma_f16(c, a[ks], qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float zq = bf_hi(kp[e >> 1][gr]) * qsum[nt][gr][e & 1];
+            x[nt][u][e] = fmaf(bf_lo(kp[e >> 1][gr]), c[e], gr == 0 ? zq : x[nt][u][e] + zq);
+          }
+        }
       }
-
-    // Scores, in log2 units: x[nt][2 r + e] is key g + 8 r, head 2 t + e.
-    float x[NT][4];
+    }
+    if (mask != 0xffffffffu) {
+      // Dead keys: their codes are finite whatever the slot holds, their
+      // pairs need not be.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+        for (int r = 0; r < 2; ++r) {
+          const bool dead = ((mask >> (16 * u + g + 8 * r)) & 1u) == 0;
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-      uint32_t a[4][4];  // per K step
+          for (int gr = 0; gr < NG; ++gr) vp[u][r][gr] = dead ? 0u : vp[u][r][gr];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        a[0][r] = nibbles16<0>(kw[r][gr].x), a[0][r + 2] = nibbles16<1>(kw[r][gr].x);
-        a[1][r] = nibbles16<2>(kw[r][gr].x), a[1][r + 2] = nibbles16<3>(kw[r][gr].x);
-        a[2][r] = nibbles16<0>(kw[r][gr].y), a[2][r + 2] = nibbles16<1>(kw[r][gr].y);
-        a[3][r] = nibbles16<2>(kw[r][gr].y), a[3][r + 2] = nibbles16<3>(kw[r][gr].y);
-      }
-      float st[2], zt[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        st[r] = bf_lo(ks_[r][gr]) * p.scale_log2;
-        zt[r] = fmaf(-24.f, st[r], bf_hi(ks_[r][gr]) * p.scale_log2);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma(c, a[ks], qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[nt][e] += fmaf(st[e >> 1], c[e], zt[e >> 1] * qsum[nt][gr][e & 1]);
-      }
+          for (int nt = 0; nt < NT; ++nt) {
+            x[nt][u][2 * r] = dead ? -INFINITY : x[nt][u][2 * r];
+            x[nt][u][2 * r + 1] = dead ? -INFINITY : x[nt][u][2 * r + 1];
+          }
+        }
     }
     bool need = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (krow[e >> 1] == NO_ROW) x[nt][e] = -INFINITY;
-        need |= x[nt][e] > m[nt][e & 1] + RESCALE_LOG2;
-      }
+      for (int e = 0; e < 2; ++e)
+        need |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2])) > lim[nt][e];
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(x[nt][e], x[nt][e + 2]);
+          float v = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          const float m_new = fmaxf(m[nt][e], v);
-          const float alpha = m_new == -INFINITY ? 1.f : ex2(m[nt][e] - m_new);
+          v *= sc[nt][e];
+          if (v == -INFINITY) continue;  // no key of this head yet, nothing to scale
+          const bool first = lim[nt][e] == -INFINITY;
+          const float m_new = first ? v : fmaxf(m[nt][e], v);
+          const float alpha = first ? 0.f : ex2(m[nt][e] - m_new);
           m[nt][e] = m_new;
+          lim[nt][e] = (m_new + RESCALE_LOG2) / sc[nt][e];
           l[nt][e] *= alpha;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) zc[nt][gr][e] *= alpha;
@@ -263,49 +467,82 @@ __global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
           }
         }
     }
-    // Probabilities, times the values' steps, as the output's B operand.
-    uint32_t pf[NT][NG][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float pr[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        pr[e] = krow[e >> 1] == NO_ROW ? 0.f : ex2(x[nt][e] - m[nt][e & 1]);
-        l[nt][e & 1] += pr[e];
-      }
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float sv = bf_lo(vs_[r][gr]), zv = bf_hi(vs_[r][gr]);
-          zc[nt][gr][0] = fmaf(pr[2 * r], zv, zc[nt][gr][0]);
-          zc[nt][gr][1] = fmaf(pr[2 * r + 1], zv, zc[nt][gr][1]);
-          // bf16: its range takes any step, and the products' errors
-          // (2^-9 each) average out over the keys.
-          pf[nt][gr][r] = transpose8x8(pack_bf16x2(pr[2 * r] * sv, pr[2 * r + 1] * sv));
-        }
-    }
-    // Output: tile 4 gr + i has dimension 64 gr + 8 g + i in row g, + 4 in row g + 8.
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-      const uint32_t lo0 = __byte_perm(vw[0][gr], vw[1][gr], 0x5410), hi0 = __byte_perm(vw[0][gr], vw[1][gr], 0x7632);
-      const uint32_t lo1 = __byte_perm(vw[2][gr], vw[3][gr], 0x5410), hi1 = __byte_perm(vw[2][gr], vw[3][gr], 0x7632);
-      const uint32_t a0[4] = {nibbles_centred<0>(lo0), nibbles_centred<0>(hi0), nibbles_centred<0>(lo1), nibbles_centred<0>(hi1)};
-      const uint32_t a1[4] = {nibbles_centred<1>(lo0), nibbles_centred<1>(hi0), nibbles_centred<1>(lo1), nibbles_centred<1>(hi1)};
-      const uint32_t a2[4] = {nibbles_centred<2>(lo0), nibbles_centred<2>(hi0), nibbles_centred<2>(lo1), nibbles_centred<2>(hi1)};
-      const uint32_t a3[4] = {nibbles_centred<3>(lo0), nibbles_centred<3>(hi0), nibbles_centred<3>(lo1), nibbles_centred<3>(hi1)};
+    for (int u = 0; u < 2; ++u) {
+      // Probabilities, times the values' steps, as the output's B operand.
+      uint32_t pf[NT][NG][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma(acc[nt][4 * gr], a0, pf[nt][gr][0], pf[nt][gr][1]);
-        mma(acc[nt][4 * gr + 1], a1, pf[nt][gr][0], pf[nt][gr][1]);
-        mma(acc[nt][4 * gr + 2], a2, pf[nt][gr][0], pf[nt][gr][1]);
-        mma(acc[nt][4 * gr + 3], a3, pf[nt][gr][0], pf[nt][gr][1]);
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pr[e] = ex2(fmaf(x[nt][u][e], sc[nt][e & 1], -m[nt][e & 1]));  // a dead key's -inf gives 0
+          l[nt][e & 1] += pr[e];
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float sv = bf_lo(vp[u][r][gr]), zv = bf_hi(vp[u][r][gr]);
+            zc[nt][gr][0] = fmaf(pr[2 * r], zv, zc[nt][gr][0]);
+            zc[nt][gr][1] = fmaf(pr[2 * r + 1], zv, zc[nt][gr][1]);
+            // bf16: its range takes any step, and the products' errors
+            // (2^-9 each) average out over the keys.
+            pf[nt][gr][r] = transpose8x8(pack_bf16x2(pr[2 * r] * sv, pr[2 * r + 1] * sv));
+          }
       }
+      // Output: tile 4 gr + i has dimension 64 gr + 8 g + i in row g, + 4 in row g + 8.
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        uint32_t w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          w[r] = *reinterpret_cast<const uint32_t*>(stage + R::VC + (16 * u + 2 * t + (r & 1) + 8 * (r >> 1)) * (D / 2) +
+                                                    gr * 32 + g * 4);
+        const uint32_t h[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                               __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
+        const uint32_t a0[4] = {value_pair<0>(h[0], bases.value), value_pair<0>(h[1], bases.value), value_pair<0>(h[2], bases.value), value_pair<0>(h[3], bases.value)};
+        const uint32_t a1[4] = {value_pair<1>(h[0], bases.value), value_pair<1>(h[1], bases.value), value_pair<1>(h[2], bases.value), value_pair<1>(h[3], bases.value)};
+        const uint32_t a2[4] = {value_pair<2>(h[0], bases.value), value_pair<2>(h[1], bases.value), value_pair<2>(h[2], bases.value), value_pair<2>(h[3], bases.value)};
+        const uint32_t a3[4] = {value_pair<3>(h[0], bases.value), value_pair<3>(h[1], bases.value), value_pair<3>(h[2], bases.value), value_pair<3>(h[3], bases.value)};
+        // Σ p s (16 + n), then Σ p s (−24) of the same 16 keys: a product more
+        // for each tile costs less than subtracting 24 from every operand
+        // register, and the running sums stay those of n − 8.
+        const uint32_t off[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = pf[nt][gr][0], b1 = pf[nt][gr][1];
+          mma_bf16(acc[nt][4 * gr], a0, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 1], a1, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 2], a2, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 3], a3, b0, b1);
+          mma_bf16(acc[nt][4 * gr], off, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 1], off, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 2], off, b0, b1);
+          mma_bf16(acc[nt][4 * gr + 3], off, b0, b1);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    if (issued < n_my) {
+      fill(issued, st, entry);
+      ++issued;
+      entry = entry_of(issued);
     }
   }
 
   // The warps' results: Σ over the lanes that hold other keys, then one
-  // (m, l, o) per head and warp in shared memory.
+  // (m, l, o) per head and warp, in the warp's own ring (all its copies have
+  // landed and been read).
+  constexpr int OROW = D + 1;
+  auto sm_o = [&](int w) { return reinterpret_cast<float*>(smem + w * R::WARP); };
+  auto sm_m = [&](int w) { return sm_o(w) + NH * OROW; };
+  auto sm_l = [&](int w) { return sm_m(w) + NH; };
+  if (FILL == GATHER) {  // nothing may land after this
+    cp_async_commit();
+    cp_async_wait<0>();
+  }
+  __syncwarp();
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -315,8 +552,8 @@ __global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, o);
       if (g == 0) {
-        sm_m[warp][h] = m[nt][e];
-        sm_l[warp][h] = lv;
+        sm_m(warp)[h] = m[nt][e];
+        sm_l(warp)[h] = lv;
       }
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
@@ -325,46 +562,68 @@ __global__ void __launch_bounds__(THREADS) decode_q4_kernel(const DecodeQ4 p) {
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sm_o[warp][h][64 * gr + 8 * g + i] = acc[nt][4 * gr + i][e] + z;
-          sm_o[warp][h][64 * gr + 8 * g + i + 4] = acc[nt][4 * gr + i][e + 2] + z;
+          sm_o(warp)[h * OROW + 64 * gr + 8 * g + i] = acc[nt][4 * gr + i][e] + z;
+          sm_o(warp)[h * OROW + 64 * gr + 8 * g + i + 4] = acc[nt][4 * gr + i][e + 2] + z;
         }
       }
     }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < G * D; idx += THREADS) {
-    const int h = idx / D, c = idx % D;
-    float mm = sm_m[0][h];
+  // One lane per head: the warps' weights e^(m_w − m) / Σ, in the first
+  // warp's place of m; then every thread sums a column of some heads.
+  float* weights = sm_m(0) + 2 * NH;  // [NH][WARPS]
+  if (threadIdx.x < G) {
+    const int h = threadIdx.x;
+    float mm = -INFINITY;
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) mm = fmaxf(mm, sm_m[w][h]);
-    float lt = 0.f, ot = 0.f;
+    for (int w = 0; w < WARPS; ++w)
+      if (sm_l(w)[h] != 0.f) mm = fmaxf(mm, sm_m(w)[h]);
+    float a[WARPS], lt = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       // l = 0: a warp that saw no key (and o = 0). A NaN score leaves l NaN,
-      // whatever m is, and the head's result with it.
-      const float a = sm_l[w][h] == 0.f ? 0.f : ex2(sm_m[w][h] - mm);
-      lt = fmaf(a, sm_l[w][h], lt);
-      ot = fmaf(a, sm_o[w][h][c], ot);
+      // and the head's result with it.
+      a[w] = sm_l(w)[h] == 0.f ? 0.f : ex2(sm_m(w)[h] - mm);
+      lt = fmaf(a[w], sm_l(w)[h], lt);
     }
-    const bool any = lt != 0.f;
-    const float ov = any ? ot / lt : 0.f;
-    const long long orow = prow + h;
-    if (in_range(orow * D + c, 1, part_rows * D, err)) {
-      if (S == 1) p.o[orow * D + c] = __float2bfloat16_rn(ov);
-      else p.o_part[orow * D + c] = ov;
-    }
-    if (c == 0 && in_range(orow, 1, part_rows, err))
-      (S == 1 ? p.lse : p.lse_part)[orow] = any ? (mm + __log2f(lt)) * LN2 : -INFINITY;
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) weights[h * WARPS + w] = a[w] * inv;
+    if (in_range(prow + h, 1, part_rows, err))
+      (S == 1 ? p.lse : p.lse_part)[prow + h] = lt == 0.f ? -INFINITY : (mm + __log2f(lt)) * LN2;
   }
+  __syncthreads();
+  const int c = threadIdx.x % D;
+  for (int h = threadIdx.x / D; h < G; h += THREADS / D) {
+    float ov = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) ov = fmaf(weights[h * WARPS + w], sm_o(w)[h * OROW + c], ov);
+    const long long at = (prow + h) * D + c;
+    if (in_range(at, 1, part_rows * D, err)) {
+      if (S == 1) p.o[at] = __float2bfloat16_rn(ov);
+      else p.o_part[at] = ov;
+    }
+  }
+}
+
+template <int D, int NT, int FILL>
+static cudaError_t launch_f(const DecodeQ4& p, int S, int run, cudaStream_t stream) {
+  auto kern = decode_q4_kernel<D, NT, FILL>;
+  const int smem = Ring<D, NT>::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int n_chunk = (p.H / p.Hkv + 8 * NT - 1) / (8 * NT);
+  const dim3 grid(static_cast<unsigned>(S), static_cast<unsigned>(p.Hkv * n_chunk), static_cast<unsigned>(p.B));
+  kern<<<grid, THREADS, smem, stream>>>(p, run, Divide::of(p.bs), Bases{0x64006400u, 0x41804180u});
+  return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
-  const int G = p.H / p.Hkv;
-  const int nt = G <= 8 ? 1 : 2, n_chunk = (G + 8 * nt - 1) / (8 * nt);
-  const dim3 grid(static_cast<unsigned>(S), static_cast<unsigned>(p.Hkv * n_chunk), static_cast<unsigned>(p.B));
-  if (nt == 1) decode_q4_kernel<D, 1><<<grid, THREADS, 0, stream>>>(p);
-  else decode_q4_kernel<D, 2><<<grid, THREADS, 0, stream>>>(p);
-  return cudaGetLastError();
+  int run = p.bs & -p.bs;  // slots of a block from a multiple of this on are contiguous for as many keys
+  if (run > TK) run = TK;
+  const bool bulk = run >= 8;
+  if (p.H / p.Hkv <= 8) return bulk ? launch_f<D, 1, BULK>(p, S, run, stream) : launch_f<D, 1, GATHER>(p, S, run, stream);
+  return bulk ? launch_f<D, 2, BULK>(p, S, run, stream) : launch_f<D, 2, GATHER>(p, S, run, stream);
 }
 
 }  // namespace decq4
