@@ -49,24 +49,26 @@ constexpr float LN2 = 0.69314718055994531f;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t NO_ROW = 0xffffffffu;
 
-// Each warp has a ring of its own in shared memory, so no two warps wait on
-// one another before the end. A stage holds 32 keys: K codes, V codes, K
-// pairs, V pairs. With up to 8 query heads a warp's state fits 128 registers
-// and 16 warps share an SM.
+constexpr int CK = WARPS * TK;  // keys of a CTA's tile: one stage of the ring
+
+// A stage of the ring holds a tile: K codes, V codes, K pairs, V pairs of its
+// 128 keys, 32 for each warp. With up to 8 query heads a warp's state fits
+// 128 registers and four CTAs share an SM.
 template <int D, int NT>
 struct Ring {
-  static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM
-  static constexpr int CODES = TK * D / 2, PAIRS = TK * D / 16;
+  static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : 2;  // per SM
+  static constexpr int CODES = CK * D / 2, PAIRS = CK * D / 16;
   static constexpr int KC = 0, VC = CODES, KS = 2 * CODES, VS = KS + PAIRS;
   static constexpr int STAGE = 2 * CODES + 2 * PAIRS;
-  static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int WARP = STAGES * STAGE;
-  static constexpr int BAR_OFF = WARPS * WARP;                 // [WARPS][STAGES] barriers
-  static constexpr int MASK_OFF = BAR_OFF + WARPS * STAGES * 8;  // [WARPS][STAGES] live keys
-  static constexpr int BYTES = MASK_OFF + WARPS * STAGES * 4;
+  static constexpr int STAGES = (D == 64 ? 6 : 3) + (CTAS == 3);
+  static constexpr int BAR_OFF = STAGES * STAGE;  // full [STAGES] (GATHER: [WARPS][STAGES]), empty [STAGES]
+  static constexpr int MASK_OFF = BAR_OFF + (WARPS + 1) * STAGES * 8;  // [STAGES][WARPS] keys that are there
+  static constexpr int BYTES = MASK_OFF + STAGES * WARPS * 4;
   static_assert(CTAS * (BYTES + 1024) <= 233472, "the CTAs must fit an SM");
-  // at the end each warp's ring takes its result: [8 NT heads][D + 1] fp32
-  static_assert(WARP >= 8 * NT * (D + 1 + 2 + WARPS) * 4, "a ring holds the warp's result");
+  // at the end the ring takes the warps' results: [8 NT heads][D + 1], m and
+  // l [8 NT], and the weights [8 NT][WARPS], fp32
+  static constexpr int RESULT = 8 * NT * (D + 1 + 2 + WARPS) * 4;
+  static_assert(WARPS * RESULT <= STAGES * STAGE, "the ring holds the warps' results");
 };
 
 // d (+)= A (16x16) B (16x8), fp32; both operands fp16, or both bf16.
@@ -164,9 +166,11 @@ struct Divide {
 };
 
 // How a stage is filled. BULK (a block size with a factor of 8): runs of
-// `run` = 8, 16 or 32 consecutive slots of one block are contiguous, and a
-// lane copies one run of codes or pairs in one piece. GATHER (any other): a
-// lane looks up one key's row and the rows go over in 16-byte pieces.
+// `run` = 8 .. 128 consecutive slots of one block are contiguous, and a lane
+// copies one run of codes or pairs in one piece; the warps take turns to fill
+// whole tiles, so the bookkeeping of a tile is done once for all four.
+// GATHER (any other): a lane looks up one key's row and the rows go over in
+// 16-byte pieces, each warp filling its own part of the tile.
 enum Fill : int { BULK = 0, GATHER = 1 };
 
 // One CTA: split s of request b's context, K/V head hk, 8·NT query heads.
@@ -192,92 +196,155 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
 
   int L = in_range(b, 1, p.B, err) ? p.seq_lens[b] : 0;
   L = L < 0 ? 0 : (L > p.max_blocks * p.bs ? p.max_blocks * p.bs : L);
-  const int n_tiles = (L + TK - 1) / TK;
+  const int n_tiles = (L + CK - 1) / CK;
   const int tps = (n_tiles + S - 1) / S;
-  const int tile0 = s * tps, tile1 = min(n_tiles, tile0 + tps);
-  const int my0 = tile0 + warp;  // this warp's tiles: my0, my0 + WARPS, ...
-  const int n_my = my0 < tile1 ? (tile1 - my0 + WARPS - 1) / WARPS : 0;
+  const int tile0 = s * tps;
+  const int n = max(0, min(n_tiles, tile0 + tps) - tile0);  // this CTA's tiles
 
-  uint8_t* ring = smem + warp * R::WARP;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::BAR_OFF) + warp * ST;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + R::MASK_OFF) + warp * ST;
-  if (lane == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(&full[i], FILL == BULK ? 1 : 32);
-    fence_mbar_init();
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::BAR_OFF) + (FILL == BULK ? 0 : warp * ST);
+  uint64_t* empty = reinterpret_cast<uint64_t*>(smem + R::BAR_OFF) + WARPS * ST;  // BULK
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + R::MASK_OFF);
+  if (FILL == BULK) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < ST; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], WARPS);
+      }
+      fence_mbar_init();
+    }
+    __syncthreads();
+  } else {
+    if (lane == 0) {
+      for (int i = 0; i < ST; ++i) mbar_init(&full[i], 32);
+      fence_mbar_init();
+    }
+    __syncwarp();
   }
-  __syncwarp();
 
-  // The token a lane looks up for a tile, and its table entry: the first of
-  // its run (BULK; lane = 4 run + part), or its key (GATHER).
+  // A lane's lookups for a tile. BULK: copy lane + 32 i of the tile's
+  // 4 · 128 / run, part (lane & 3) of a run; the run's first token. GATHER:
+  // the warp's key `lane`.
+  constexpr int LOOK = FILL == BULK ? 2 : 1;
   const long long rows = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
-  auto token_of = [&](int tile) { return tile * TK + (FILL == BULK ? (lane >> 2) * run : lane); };
-  auto entry_of = [&](int j) -> int {  // -1: no such token, or outside the table
-    const int tok = token_of(my0 + j * WARPS);
-    if (j >= n_my || tok >= L || (FILL == BULK && (lane >> 2) * run >= TK)) return -1;
-    const long long ti = static_cast<long long>(b) * p.max_blocks + by_bs(tok);
-    return in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
+  auto token_of = [&](int j, int i) {
+    return (tile0 + j) * CK + (FILL == BULK ? ((lane + 32 * i) >> 2) * run : warp * TK + lane);
   };
-  // Fill stage st with tile j of this warp, from the lanes' table entries.
-  auto fill = [&](int j, int st, int entry) {
-    const int tok = token_of(my0 + j * WARPS);
-    const bool there = tok < L && (FILL == GATHER || (lane >> 2) * run < TK);
-    const bool live = there && entry >= 0 && entry < p.num_blocks;
-    if (there && !live) atomicExch(err, DEV_BAD_INDEX);
-    const uint32_t row = live ? (static_cast<uint32_t>(entry) * p.Hkv + hk) * static_cast<uint32_t>(p.bs) +
-                                    static_cast<uint32_t>(tok - by_bs(tok) * p.bs)
-                              : NO_ROW;
-    uint8_t* stage = ring + st * R::STAGE;
-    if (FILL == BULK) {
+  auto there = [&](int j, int i) {
+    return j < n && token_of(j, i) < L && (FILL == GATHER || ((lane + 32 * i) >> 2) * run < CK);
+  };
+  struct Entries {
+    int e[LOOK];
+  };
+  auto look = [&](int j) {  // the table's entries
+    Entries x;
+#pragma unroll
+    for (int i = 0; i < LOOK; ++i) {
+      x.e[i] = -1;
+      if (there(j, i)) {
+        const long long ti = static_cast<long long>(b) * p.max_blocks + by_bs(token_of(j, i));
+        if (in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err)) x.e[i] = p.block_table[ti];
+      }
+    }
+    return x;
+  };
+  auto row_of = [&](int tok, int entry) {
+    return (static_cast<uint32_t>(entry) * p.Hkv + hk) * static_cast<uint32_t>(p.bs) +
+           static_cast<uint32_t>(tok - by_bs(tok) * p.bs);
+  };
+  // Fill stage st with tile j (the warp's part of it), run by a whole warp.
+  auto fill = [&](int j, int st, const Entries& x) {
+    uint8_t* stage = smem + st * R::STAGE;
+    if constexpr (FILL == BULK) {
       // parts: 0 K codes, 1 V codes, 2 K pairs, 3 V pairs
-      const int part = lane & 3, r = lane >> 2;
+      const int part = lane & 3;
       const int per_key = part < 2 ? D / 2 : D / 16;
       const uint8_t* base = part == 0 ? p.k_cache : part == 1 ? p.v_cache
                             : reinterpret_cast<const uint8_t*>(part == 2 ? p.k_scale : p.v_scale);
-      const int off = part == 0 ? R::KC : part == 1 ? R::VC : part == 2 ? R::KS : R::VS;
-      const bool ok = live && in_range(static_cast<long long>(row) * per_key, run * per_key, rows * per_key, err);
-      const uint32_t bytes = ok ? run * per_key : 0;
-      const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-      // keys whose run is there and before the context's end
-      uint32_t mask = live && part == 0 ? (run == 32 ? 0xffffffffu : ((1u << run) - 1u) << (r * run)) : 0u;
-      mask = __reduce_or_sync(0xffffffffu, mask);
-      if (lane == 0) {
-        masks[st] = mask;
-        mbar_arrive_expect_tx(&full[st], total);
+      uint8_t* dst = stage + (part == 0 ? R::KC : part == 1 ? R::VC : part == 2 ? R::KS : R::VS);
+      const uint32_t bytes = run * per_key;
+      uint32_t row[LOOK], mine = 0;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < LOOK; ++i) {
+        row[i] = NO_ROW;
+        if (!there(j, i)) continue;
+        if (x.e[i] >= 0 && x.e[i] < p.num_blocks) row[i] = row_of(token_of(j, i), x.e[i]);
+        else bad = true;
+        if (row[i] != NO_ROW &&
+            !in_range(static_cast<long long>(row[i]) * per_key, bytes, rows * per_key, err))
+          row[i] = NO_ROW;
+        if (row[i] != NO_ROW) mine += bytes;
+      }
+      const uint32_t total = __reduce_add_sync(0xffffffffu, mine);
+      if (lane < WARPS) masks[st * WARPS + lane] = 0xffffffffu;
+      if (__any_sync(0xffffffffu, bad)) {  // blocks outside the cache: their keys are skipped
+        if (bad) atomicExch(err, DEV_BAD_INDEX);
+        for (int w = 0; w < WARPS; ++w) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int i = 0; i < LOOK; ++i) {
+            const int k0 = ((lane + 32 * i) >> 2) * run - 32 * w;  // the run's first key in this word
+            if (part == 0 && row[i] != NO_ROW)
+              for (int k = max(k0, 0); k < min(k0 + run, 32); ++k) bits |= 1u << k;
+          }
+          bits = __reduce_or_sync(0xffffffffu, bits);
+          if (lane == 0) masks[st * WARPS + w] = bits;
+        }
       }
       __syncwarp();
-      if (ok) bulk_load(stage + off + r * run * per_key, base + static_cast<long long>(row) * per_key, bytes, &full[st]);
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < LOOK; ++i)
+        if (row[i] != NO_ROW)
+          bulk_load(dst + ((lane + 32 * i) >> 2) * bytes, base + static_cast<size_t>(row[i]) * per_key, bytes, &full[st]);
     } else {
       constexpr int CH = D / 32;     // 16-byte chunks of a row of codes
       constexpr int RPI = 32 / CH;   // rows per warp instruction
+      const bool in = there(j, 0), live = in && x.e[0] >= 0 && x.e[0] < p.num_blocks;
+      if (in && !live) atomicExch(err, DEV_BAD_INDEX);
+      const uint32_t row = live ? row_of(token_of(j, 0), x.e[0]) : NO_ROW;
       const uint32_t mask = __ballot_sync(0xffffffffu, live);
-      if (lane == 0) masks[st] = mask;
+      if (lane == 0) masks[st * WARPS + warp] = mask;
+      uint8_t* kc = stage + R::KC + warp * TK * (D / 2);
+      uint8_t* vc = stage + R::VC + warp * TK * (D / 2);
       const int c = lane % CH;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int key = i * RPI + lane / CH;
         const uint32_t rw = __shfl_sync(0xffffffffu, row, key);
-        const long long off = static_cast<long long>(rw) * (D / 2) + c * 16;
+        const size_t off = static_cast<size_t>(rw) * (D / 2) + c * 16;
         if (rw != NO_ROW && in_range(off, 16, rows * (D / 2), err)) {
-          cp_async_16(stage + R::KC + key * (D / 2) + c * 16, p.k_cache + off, 16);
-          cp_async_16(stage + R::VC + key * (D / 2) + c * 16, p.v_cache + off, 16);
+          cp_async_16(kc + key * (D / 2) + c * 16, p.k_cache + off, 16);
+          cp_async_16(vc + key * (D / 2) + c * 16, p.v_cache + off, 16);
         }
       }
-      const long long so = static_cast<long long>(row) * NG;
+      const size_t so = static_cast<size_t>(row) * NG;
       if (live && in_range(so, NG, rows * NG, err)) {
-        cp_async_small<NG * 4>(stage + R::KS + lane * (NG * 4), p.k_scale + so);
-        cp_async_small<NG * 4>(stage + R::VS + lane * (NG * 4), p.v_scale + so);
+        cp_async_small<NG * 4>(stage + R::KS + (warp * TK + lane) * (NG * 4), p.k_scale + so);
+        cp_async_small<NG * 4>(stage + R::VS + (warp * TK + lane) * (NG * 4), p.v_scale + so);
       }
       cp_async_arrive_noinc(&full[st]);
     }
   };
-  int first[ST];  // the first stages' entries, loaded together
+  // The first ST tiles: BULK, warp i mod 4 fills tile i; GATHER, all of them.
+  // `next` is the tile this warp fills next, with its entries in `ahead`.
+  int next;
+  Entries ahead;
+  if (FILL == BULK) {
+    for (int i = warp; i < min(ST, n); i += WARPS) fill(i, i, look(i));
+    next = ST + (warp + WARPS - 1) % WARPS;  // by turn: at the end of tile j warp j mod 4 fills j - 1 + ST
+    ahead = look(next);
+  } else {
+    Entries first[ST];
 #pragma unroll
-  for (int i = 0; i < ST; ++i) first[i] = entry_of(i);
+    for (int i = 0; i < ST; ++i) first[i] = look(i);
 #pragma unroll
-  for (int i = 0; i < ST; ++i)
-    if (i < n_my) fill(i, i, first[i]);
-  int issued = min(ST, n_my);
-  int entry = entry_of(issued);  // of the next tile to fill: loaded a tile ahead
+    for (int i = 0; i < ST; ++i)
+      if (i < n) fill(i, i, first[i]);
+    next = ST;
+    ahead = look(next);
+  }
 
   // Query operand: for group gr and word w of a lane quarter's 16 dimensions
   // 64 gr + 16 t + 8 w + 0..7, K step 2 w + h (h = 0, 1) multiplies elements
@@ -363,16 +430,23 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   }
 
   bool ok = true;
-  int st = 0;
+  int st = 0, stop = n;
   uint32_t phase = 0;
-  for (int j = 0; j < issued; ++j, phase ^= st + 1 == ST, st = st + 1 == ST ? 0 : st + 1) {
-    if (!mbar_wait_warp(&full[st], phase, err)) ok = false;
-    if (!ok) continue;  // wait for what is in flight, fill no more
-    __syncwarp();       // lane 0's mask
-    const uint8_t* stage = ring + st * R::STAGE;
-    uint32_t mask = masks[st];
-    const int left = L - (my0 + j * WARPS) * TK;
-    if (left < TK) mask &= (1u << left) - 1u;
+  for (int j = 0; j < stop; ++j, phase ^= st + 1 == ST, st = st + 1 == ST ? 0 : st + 1) {
+    if (!mbar_wait_warp(&full[st], phase, err) && ok) {
+      ok = false;
+      stop = min(n, j + ST);  // wait for what is in flight, fill no more
+    }
+    if (!ok) continue;
+    __syncwarp();  // the mask
+    const int left = L - (tile0 + j) * CK - warp * TK;
+    uint32_t mask = masks[st * WARPS + warp];
+    if (left < TK) mask &= left > 0 ? (1u << left) - 1u : 0u;
+    const uint8_t* stage = smem + st * R::STAGE;
+    const uint8_t* kc = stage + R::KC + warp * TK * (D / 2);
+    const uint8_t* vc = stage + R::VC + warp * TK * (D / 2);
+    const uint8_t* kps = stage + R::KS + warp * TK * (D / 16);
+    const uint8_t* vps = stage + R::VS + warp * TK * (D / 16);
 
     // Scores: x[nt][u][2 r + e] is key 16 u + g + 8 r, head 2 t + e.
     float x[NT][2][4];
@@ -384,12 +458,12 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
       for (int r = 0; r < 2; ++r) {
         const int key = 16 * u + g + 8 * r;
         if (NG == 2) {
-          const uint2 a = *reinterpret_cast<const uint2*>(stage + R::KS + key * 8);
-          const uint2 c = *reinterpret_cast<const uint2*>(stage + R::VS + key * 8);
+          const uint2 a = *reinterpret_cast<const uint2*>(kps + key * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(vps + key * 8);
           kp[r][0] = a.x, kp[r][NG - 1] = a.y, vp[u][r][0] = c.x, vp[u][r][NG - 1] = c.y;
         } else {
-          kp[r][0] = *reinterpret_cast<const uint32_t*>(stage + R::KS + key * 4);
-          vp[u][r][0] = *reinterpret_cast<const uint32_t*>(stage + R::VS + key * 4);
+          kp[r][0] = *reinterpret_cast<const uint32_t*>(kps + key * 4);
+          vp[u][r][0] = *reinterpret_cast<const uint32_t*>(vps + key * 4);
         }
       }
 #pragma unroll
@@ -398,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int key = 16 * u + g + 8 * r;
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + R::KC + key * (D / 2) + gr * 32 + t * 8);
+          const uint2 w = *reinterpret_cast<const uint2*>(kc + key * (D / 2) + gr * 32 + t * 8);
           uint32_t v[4];
           key_pairs(w.x, bases.key, v);
           a[0][r] = v[0], a[0][r + 2] = v[1], a[1][r] = v[2], a[1][r + 2] = v[3];
@@ -497,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         uint32_t w[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          w[r] = *reinterpret_cast<const uint32_t*>(stage + R::VC + (16 * u + 2 * t + (r & 1) + 8 * (r >> 1)) * (D / 2) +
+          w[r] = *reinterpret_cast<const uint32_t*>(vc + (16 * u + 2 * t + (r & 1) + 8 * (r >> 1)) * (D / 2) +
                                                     gr * 32 + g * 4);
         const uint32_t h[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
                                __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
@@ -524,25 +598,41 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
       }
     }
     __syncwarp();  // every lane has read the stage
-    if (issued < n_my) {
-      fill(issued, st, entry);
-      ++issued;
-      entry = entry_of(issued);
+    if (FILL == BULK) {
+      if (lane == 0) mbar_arrive(&empty[st]);
+      // The turn's warp fills the stage before this one, which every warp left
+      // a tile ago or is about to.
+      if (j % WARPS == warp && j > 0) {
+        const int before = st == 0 ? ST - 1 : st - 1;
+        if (next < n) {
+          if (mbar_wait_warp(&empty[before], st == 0 ? phase ^ 1 : phase, err)) {
+            fill(next, before, ahead);
+          } else {
+            ok = false;
+            stop = min(n, j + ST);
+          }
+        }
+        next += WARPS;
+        ahead = look(next);
+      }
+    } else if (next < n) {
+      fill(next, st, ahead);
+      ahead = look(++next);
     }
   }
 
   // The warps' results: Σ over the lanes that hold other keys, then one
-  // (m, l, o) per head and warp, in the warp's own ring (all its copies have
-  // landed and been read).
+  // (m, l, o) per head and warp, in the ring (every copy has landed and been
+  // read).
   constexpr int OROW = D + 1;
-  auto sm_o = [&](int w) { return reinterpret_cast<float*>(smem + w * R::WARP); };
+  auto sm_o = [&](int w) { return reinterpret_cast<float*>(smem + w * R::RESULT); };
   auto sm_m = [&](int w) { return sm_o(w) + NH * OROW; };
   auto sm_l = [&](int w) { return sm_m(w) + NH; };
   if (FILL == GATHER) {  // nothing may land after this
     cp_async_commit();
     cp_async_wait<0>();
   }
-  __syncwarp();
+  __syncthreads();
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -620,7 +710,7 @@ static cudaError_t launch_f(const DecodeQ4& p, int S, int run, cudaStream_t stre
 template <int D>
 static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
   int run = p.bs & -p.bs;  // slots of a block from a multiple of this on are contiguous for as many keys
-  if (run > TK) run = TK;
+  if (run > CK) run = CK;
   const bool bulk = run >= 8;
   if (p.H / p.Hkv <= 8) return bulk ? launch_f<D, 1, BULK>(p, S, run, stream) : launch_f<D, 1, GATHER>(p, S, run, stream);
   return bulk ? launch_f<D, 2, BULK>(p, S, run, stream) : launch_f<D, 2, GATHER>(p, S, run, stream);
@@ -628,11 +718,17 @@ static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
 
 }  // namespace decq4
 
+// Splits that fill the GPU: one wave of CTAs (three an SM) for one or two
+// requests, three waves for more, whose lengths differ (measured: two contexts
+// of 100k and 131k take 67.7 us at one wave, 76 at two; 32 of 2k to 8k 64.6 at
+// three, 91 at two). A split below 1024 keys costs more than it gives (16
+// requests of 1k to 8k tokens, 2 K/V heads: 21 us with 10 splits, 27 with 16).
 int decode_q4_splits(int B, int H, int Hkv, long long max_ctx) {
   const int G = H / Hkv, nh = G <= 8 ? 8 : 16;
-  const long long ctas = static_cast<long long>(B) * Hkv * ((G + nh - 1) / nh);
-  long long s = (152 * 8 + ctas - 1) / ctas;                       // about eight CTAs per SM
-  const long long most = (max_ctx + 255) / 256;                    // at least 256 keys a split
+  const long long pairs = static_cast<long long>(B) * Hkv * ((G + nh - 1) / nh);
+  const long long wave = 152 * (nh == 8 ? 3 : 2);
+  long long s = (B <= 2 ? 1 : 3) * wave / pairs;
+  const long long most = (max_ctx + 1023) / 1024;
   if (s > most) s = most;
   return s < 1 ? 1 : s > 4096 ? 4096 : static_cast<int>(s);
 }
