@@ -347,7 +347,7 @@ int fa_qk_norm_rope(const fa_norm_rope_args* a, void* stream) {
 
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d) {
   if (B < 1 || N < 1 || (d != 64 && d != 128) || static_cast<long long>(B) * N > INT_MAX) return 0;
-  return static_cast<size_t>(2) * fa::norm_rope_bwd_parts(B, N, d) * d * sizeof(float);
+  return fa::norm_rope_bwd_partial_bytes(d);
 }
 
 int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream) {

@@ -22,26 +22,27 @@ static __device__ uint32_t g_append_err;
 
 namespace append {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 using rope::Angles;
 using rope::Lane;
 using rope::Raw;
+using rope::Row;
 
 // Which rows a group of heads holds.
 enum Part : int { QUERIES = 0, KEYS = 1, VALUES = 2 };
 
 __device__ __forceinline__ Raw load_row(const TokenRows& t, long long off, const Lane& ln, uint32_t* err) {
   Raw r{};
-  if (in_range(off + ln.ca * 8, 8, t.extent, err)) r.a = *reinterpret_cast<const uint4*>(t.p + off + ln.ca * 8);
-  if (in_range(off + ln.cb * 8, 8, t.extent, err)) r.b = *reinterpret_cast<const uint4*>(t.p + off + ln.cb * 8);
+  if (in_range(off + ln.ca * 8, 8, t.extent, err)) r.a = rope::load16(t.p + off + ln.ca * 8);
+  if (in_range(off + ln.cb * 8, 8, t.extent, err)) r.b = rope::load16(t.p + off + ln.cb * 8);
   return r;
 }
 
 __device__ __forceinline__ void store_chunks(__nv_bfloat16* base, long long extent, long long off, const Lane& ln,
-                                             const float* a, const float* b, uint32_t* err) {
-  if (in_range(off + ln.ca * 8, 8, extent, err)) *reinterpret_cast<uint4*>(base + off + ln.ca * 8) = rope::pack8(a);
-  if (in_range(off + ln.cb * 8, 8, extent, err)) *reinterpret_cast<uint4*>(base + off + ln.cb * 8) = rope::pack8(b);
+                                             const Row& x, uint32_t* err) {
+  if (in_range(off + ln.ca * 8, 8, extent, err)) rope::store16(base + off + ln.ca * 8, rope::pack8(x.a));
+  if (in_range(off + ln.cb * 8, 8, extent, err)) rope::store16(base + off + ln.cb * 8, rope::pack8(x.b));
 }
 
 // Where token t goes: its position and cache block, or live = false for a
@@ -66,97 +67,104 @@ __device__ __forceinline__ Slot slot_of(const Append& p, long long t, uint32_t* 
   return s;
 }
 
-template <int D, int HPG, bool Q4>
-__global__ void __launch_bounds__(THREADS) append_kernel(const Append p) {
+// A row of lanes takes one token and a section of the heads of its queries,
+// keys or values (blockIdx.y says which), STEP heads at a time with the next
+// ones on their way.
+template <int D, int STEP, bool Q4, bool INTER>
+__global__ void __launch_bounds__(THREADS, 5) append_kernel(const Append p) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR, NG = D / 64;
   uint32_t* err = &g_append_err;
   const int i = threadIdx.x % LPR;
   const long long t = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / LPR;
-  int group = static_cast<int>(blockIdx.y);
-  const int part = group < p.q_groups ? QUERIES : group < p.q_groups + p.kv_groups ? KEYS : VALUES;
-  group -= part == QUERIES ? 0 : part == KEYS ? p.q_groups : p.q_groups + p.kv_groups;
-  const int h0 = group * HPG;
-  const int heads = min(HPG, (part == QUERIES ? p.H : p.Hkv) - h0);
+  int sec = static_cast<int>(blockIdx.y);
+  const int part = sec < p.q_sections ? QUERIES : sec < p.q_sections + p.kv_sections ? KEYS : VALUES;
+  sec -= part == QUERIES ? 0 : part == KEYS ? p.q_sections : p.q_sections + p.kv_sections;
+  const int n_sec = part == QUERIES ? p.q_sections : p.kv_sections, heads = part == QUERIES ? p.H : p.Hkv;
+  const int h0 = static_cast<int>(static_cast<long long>(sec) * heads / n_sec);  // sections as even as they go
+  const int h1 = static_cast<int>(static_cast<long long>(sec + 1) * heads / n_sec);
   const TokenRows& src = part == QUERIES ? p.q : part == KEYS ? p.k : p.v;
   const Lane ln(i, part == VALUES ? 0 : p.rot);
-
-  Raw raw[HPG];
+  auto load = [&](int h, Raw (&r)[STEP]) {
 #pragma unroll
-  for (int j = 0; j < HPG; ++j)
-    raw[j] = t < p.T && j < heads ? load_row(src, t * src.st + (h0 + j) * src.sh, ln, err) : Raw{};
+    for (int j = 0; j < STEP; ++j)
+      r[j] = t < p.T && h + j < h1 ? load_row(src, t * src.st + (h + j) * src.sh, ln, err) : Raw{};
+  };
+  Raw cur[STEP], next[STEP];
+  load(h0, cur);
   const Slot slot = slot_of(p, t, err);
   Angles ang;
   const bool turned = part != VALUES && ln.turned && slot.live;
-  if (turned) ang.load(p.cos, p.sin, slot.pos, p.rot, ln, p.interleaved);
+  if (turned) ang.load(p.cos, p.sin, slot.pos, p.rot, ln, INTER);
   const void* w = part == QUERIES ? p.q_weight : part == KEYS ? p.k_weight : nullptr;
-  float wa[8], wb[8];
+  Row wt;
   if (w) {
-    rope::load_weight8(w, p.w32, ln.ca, wa);
-    rope::load_weight8(w, p.w32, ln.cb, wb);
+    rope::load_weight8(w, p.w32, ln.ca, wt.a);
+    rope::load_weight8(w, p.w32, ln.cb, wt.b);
   }
-  const int in_block = slot.pos % p.bs;
+  // the cache's row of the token's slot in K/V head 0
+  const long long row0 = static_cast<long long>(slot.block) * p.Hkv * p.bs + slot.pos % p.bs;
+  const long long rows = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
+  for (int hh = h0; hh < h1; hh += STEP) {
+  load(hh + STEP, next);
 #pragma unroll
-  for (int j = 0; j < HPG; ++j) {
-    float a[8], c[8];
-    rope::unpack8(raw[j].a, a);
-    rope::unpack8(raw[j].b, c);
-    if (w) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(c[e], c[e], ss));
-      const float r = rsqrtf(rope::row_sum<LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = a[e] * r * wa[e];
-        c[e] = c[e] * r * wb[e];
-      }
-    }
-    if (turned) rope::turn(a, c, ang, p.interleaved, 1.f);
-    const bool mine = slot.live && j < heads;
-    const int h = h0 + j;
+  for (int j = 0; j < STEP; ++j) {
+    Row x = rope::unpack(cur[j]);
+    cur[j] = next[j];
+    const int h = hh + j;
+    if (w) x = rope::times(rope::times(x, rope::inv_rms<LPR>(x, p.eps)), wt);
+    if (turned) rope::turn<false>(x, ang, INTER);
+    const bool mine = slot.live && h < h1;
     if (part == QUERIES) {
-      if (mine) store_chunks(p.q_out.p, p.q_out.extent, t * p.q_out.st + h * p.q_out.sh, ln, a, c, err);
+      if (mine) store_chunks(p.q_out.p, p.q_out.extent, t * p.q_out.st + h * p.q_out.sh, ln, x, err);
       continue;
     }
-    // row of the cache: block, K/V head, slot
-    const long long row = (static_cast<long long>(slot.block) * p.Hkv + h) * p.bs + in_block;
-    const long long rows = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
+    const long long row = row0 + static_cast<long long>(h) * p.bs;
     if (!Q4) {
       if (mine)
-        store_chunks(static_cast<__nv_bfloat16*>(part == KEYS ? p.k_cache : p.v_cache), rows * D, row * D, ln, a, c,
+        store_chunks(static_cast<__nv_bfloat16*>(part == KEYS ? p.k_cache : p.v_cache), rows * D, row * D, ln, x,
                      err);
       continue;
     }
     q4::Grid grid[NG];
-    q4::grids<D>(a, c, ln, grid);
+    q4::grids<D>(x, ln, i, grid);
     if (mine) {
       uint8_t* codes = static_cast<uint8_t*>(part == KEYS ? p.k_cache : p.v_cache);
       __nv_bfloat16* pairs = part == KEYS ? p.k_scale : p.v_scale;
-      const q4::Grid ga = grid[NG == 1 ? 0 : ln.ca / 8], gb = grid[NG == 1 ? 0 : ln.cb / 8];
-      const uint32_t wa4 = q4::encode8(a, ga), wb4 = q4::encode8(c, gb);
+      const q4::Grid ga = NG == 1 || ln.ca / 8 == 0 ? grid[0] : grid[NG - 1];
+      const q4::Grid gb = NG == 1 || ln.cb / 8 == 0 ? grid[0] : grid[NG - 1];
+      Row n;
+      const uint32_t wa4 = q4::encode8(x.a, ga, n.a), wb4 = q4::encode8(x.b, gb, n.b);
       if (in_range(row * (D / 2) + ln.ca * 4, 4, rows * (D / 2), err))
         *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + ln.ca * 4) = wa4;
       if (in_range(row * (D / 2) + ln.cb * 4, 4, rows * (D / 2), err))
         *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + ln.cb * 4) = wb4;
-      if (i < NG && in_range((row * NG + i) * 2, 2, rows * NG * 2, err))
-        *reinterpret_cast<uint32_t*>(pairs + (row * NG + i) * 2) = q4::pair(grid[NG == 1 ? 0 : i]);
+      const int own = q4::own_group<D>(i);
+      if (i % (LPR / NG) == 0 && in_range((row * NG + own) * 2, 2, rows * NG * 2, err))
+        *reinterpret_cast<uint32_t*>(pairs + (row * NG + own) * 2) = q4::pair(grid[own]);
       __nv_bfloat16* held = part == KEYS ? p.k_values : p.v_values;
       if (held) {
-        q4::decode8(wa4, ga, a);
-        q4::decode8(wb4, gb, c);
-        store_chunks(held, static_cast<long long>(p.T) * p.Hkv * D, (t * p.Hkv + h) * D, ln, a, c, err);
+        q4::held8(n.a, ga, x.a);
+        q4::held8(n.b, gb, x.b);
+        store_chunks(held, static_cast<long long>(p.T) * p.Hkv * D, (t * p.Hkv + h) * D, ln, x, err);
       }
     }
+  }
   }
 }
 
 template <int D, bool Q4>
 static cudaError_t launch(Append p, cudaStream_t stream) {
-  constexpr int ROWS = THREADS / (D / 16), HPG = 4;
-  p.q_groups = (p.H + HPG - 1) / HPG;
-  p.kv_groups = (p.Hkv + HPG - 1) / HPG;
-  const dim3 grid(static_cast<unsigned>((p.T + ROWS - 1) / ROWS), static_cast<unsigned>(p.q_groups + 2 * p.kv_groups));
-  append_kernel<D, HPG, Q4><<<grid, THREADS, 0, stream>>>(p);
+  constexpr int ROWS = THREADS / (D / 16);
+  const long long tiles = (p.T + ROWS - 1) / ROWS;
+  // Sections of up to 16 heads, smaller ones until a wave of CTAs is there.
+  for (int hs = 16; hs > 1; hs /= 2) {
+    p.q_sections = (p.H + hs - 1) / hs;
+    p.kv_sections = (p.Hkv + hs - 1) / hs;
+    if (tiles * (p.q_sections + 2 * p.kv_sections) >= 152 * 5) break;
+  }
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.q_sections + 2 * p.kv_sections));
+  if (p.interleaved) append_kernel<D, 2, Q4, true><<<grid, THREADS, 0, stream>>>(p);
+  else append_kernel<D, 2, Q4, false><<<grid, THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -89,11 +89,11 @@ struct NormRope {
   bool w32, interleaved;
   int B, H, Hkv, N, rot, n_pos;
   float eps;
-  int q_groups;  // set by the launcher
+  int q_sections, k_sections;  // set by the launcher: parts that the heads are cut into
 };
 cudaError_t launch_norm_rope(const NormRope& p, int d, cudaStream_t stream);
-// Partial rows of the weight gradients: [2][parts][d] fp32 of workspace.
-int norm_rope_bwd_parts(int B, int N, int d);
+// Workspace of the weight gradients' partial rows.
+size_t norm_rope_bwd_partial_bytes(int d);
 cudaError_t launch_norm_rope_bwd(const NormRope& p, int d, float* partial, float* dqw, float* dkw,
                                  cudaStream_t stream);
 
@@ -122,7 +122,7 @@ struct Append {
   bool w32, interleaved;
   int T, B, H, Hkv, num_blocks, bs, max_blocks, rot, n_pos;
   float eps;
-  int q_groups, kv_groups;  // set by the launcher
+  int q_sections, kv_sections;  // set by the launcher: parts that the heads are cut into
 };
 cudaError_t launch_append(const Append& p, int d, bool q4, cudaStream_t stream);
 

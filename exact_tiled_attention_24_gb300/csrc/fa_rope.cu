@@ -21,19 +21,19 @@ static __device__ uint32_t g_rope_err;
 
 namespace rope {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 // Row of a strided [B][heads][N][D] tensor as two 16-byte chunks.
 __device__ __forceinline__ Raw load_row(const HeadRows& t, long long off, const Lane& ln, uint32_t* err) {
   Raw r{};
-  if (in_range(off + ln.ca * 8, 8, t.extent, err)) r.a = *reinterpret_cast<const uint4*>(t.p + off + ln.ca * 8);
-  if (in_range(off + ln.cb * 8, 8, t.extent, err)) r.b = *reinterpret_cast<const uint4*>(t.p + off + ln.cb * 8);
+  if (in_range(off + ln.ca * 8, 8, t.extent, err)) r.a = load16(t.p + off + ln.ca * 8);
+  if (in_range(off + ln.cb * 8, 8, t.extent, err)) r.b = load16(t.p + off + ln.cb * 8);
   return r;
 }
-__device__ __forceinline__ void store_row(const HeadRows& t, long long off, const Lane& ln, const float* a,
-                                          const float* b, uint32_t* err) {
-  if (in_range(off + ln.ca * 8, 8, t.extent, err)) *reinterpret_cast<uint4*>(t.p + off + ln.ca * 8) = pack8(a);
-  if (in_range(off + ln.cb * 8, 8, t.extent, err)) *reinterpret_cast<uint4*>(t.p + off + ln.cb * 8) = pack8(b);
+__device__ __forceinline__ void store_row(const HeadRows& t, long long off, const Lane& ln, const Row& x,
+                                          uint32_t* err) {
+  if (in_range(off + ln.ca * 8, 8, t.extent, err)) store16(t.p + off + ln.ca * 8, pack8(x.a));
+  if (in_range(off + ln.cb * 8, 8, t.extent, err)) store16(t.p + off + ln.cb * 8, pack8(x.b));
 }
 
 // The row of the tables for token (b, n), or -1 (reported) for a position
@@ -50,147 +50,173 @@ __device__ __forceinline__ int position_of(const NormRope& p, int b, int n, uint
   return -1;
 }
 
-// Forward. A row of lanes takes one token and HPG consecutive heads of q or
-// of k (blockIdx.y says which), so the token's angles are read once for
-// them; the rows of a warp are consecutive tokens, contiguous in the output.
-template <int D, int HPG>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRope p) {
+// Token `tok` of all B·N, split into batch and position in it.
+struct Token {
+  bool live;
+  int b, n;
+  __device__ __forceinline__ Token(const NormRope& p, long long tok) {
+    live = tok < static_cast<long long>(p.B) * p.N;
+    b = live ? static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.N)) : 0;
+    n = live ? static_cast<int>(tok - static_cast<long long>(b) * p.N) : 0;
+  }
+};
+
+// Heads of section i of n, as even as they go.
+__device__ __forceinline__ int section_start(int i, int n, int heads) {
+  return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(i)) * static_cast<uint32_t>(heads) /
+                          static_cast<uint32_t>(n));
+}
+
+// Forward. A row of lanes takes one token and a section of the heads of q or
+// of k (blockIdx.y says which), two heads at a time with the next two on
+// their way: the token's angles and the weights are read once for the
+// section. The rows of a warp are consecutive tokens, contiguous in the
+// output.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR;
   uint32_t* err = &g_rope_err;
-  const int i = threadIdx.x % LPR;
-  const long long tok = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / LPR;
-  const bool live = tok < static_cast<long long>(p.B) * p.N;
-  const int b = live ? static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.N)) : 0;
-  const int n = live ? static_cast<int>(tok - static_cast<long long>(b) * p.N) : 0;
-  const bool is_k = static_cast<int>(blockIdx.y) >= p.q_groups;
-  const int h0 = (static_cast<int>(blockIdx.y) - (is_k ? p.q_groups : 0)) * HPG;
-  const int heads = min(HPG, (is_k ? p.Hkv : p.H) - h0);
+  const Lane ln(threadIdx.x % LPR, p.rot);
+  const Token tk(p, static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / LPR);
+  const bool is_k = static_cast<int>(blockIdx.y) >= p.q_sections;
+  const int sec = static_cast<int>(blockIdx.y) - (is_k ? p.q_sections : 0);
+  const int n_sec = is_k ? p.k_sections : p.q_sections, heads = is_k ? p.Hkv : p.H;
+  const int h0 = section_start(sec, n_sec, heads), h1 = section_start(sec + 1, n_sec, heads);
   const HeadRows& src = is_k ? p.k : p.q;
   const HeadRows& dst = is_k ? p.k_out : p.q_out;
-  const Lane ln(i, p.rot);
-
-  Raw raw[HPG];
+  const long long in0 = tk.b * src.sb + tk.n * src.sn, out0 = tk.b * dst.sb + tk.n * dst.sn;
+  auto load2 = [&](int h, Raw (&r)[2]) {
 #pragma unroll
-  for (int j = 0; j < HPG; ++j)
-    raw[j] = live && j < heads ? load_row(src, b * src.sb + (h0 + j) * src.sh + n * src.sn, ln, err) : Raw{};
-  const int pos = live ? position_of(p, b, n, err) : 0;
+    for (int j = 0; j < 2; ++j) r[j] = tk.live && h + j < h1 ? load_row(src, in0 + (h + j) * src.sh, ln, err) : Raw{};
+  };
+  Raw cur[2], next[2];
+  load2(h0, cur);
+  const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : 0;
   Angles t;
-  if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, p.interleaved);
-  float wa[8], wb[8];
+  if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
+  Row wt;
   const void* w = is_k ? p.k_weight : p.q_weight;
   if (w) {
-    load_weight8(w, p.w32, ln.ca, wa);
-    load_weight8(w, p.w32, ln.cb, wb);
+    load_weight8(w, p.w32, ln.ca, wt.a);
+    load_weight8(w, p.w32, ln.cb, wt.b);
   }
+  for (int h = h0; h < h1; h += 2) {
+    load2(h + 2, next);
 #pragma unroll
-  for (int j = 0; j < HPG; ++j) {
-    float a[8], c[8];
-    unpack8(raw[j].a, a);
-    unpack8(raw[j].b, c);
-    if (w) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(c[e], c[e], ss));
-      const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = a[e] * r * wa[e];
-        c[e] = c[e] * r * wb[e];
-      }
+    for (int j = 0; j < 2; ++j) {
+      Row x = unpack(cur[j]);
+      if (w) x = times(times(x, inv_rms<LPR>(x, p.eps)), wt);
+      if (ln.turned && pos >= 0) turn<false>(x, t, INTER);
+      if (pos < 0) x = Row{};  // no angle to turn by: a zero row
+      if (tk.live && h + j < h1) store_row(dst, out0 + (h + j) * dst.sh, ln, x, err);
+      cur[j] = next[j];
     }
-    if (ln.turned && pos >= 0) turn(a, c, t, p.interleaved, 1.f);
-    if (pos < 0) {  // no angle to turn by: a zero row
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = c[e] = 0.f;
-    }
-    if (live && j < heads) store_row(dst, b * dst.sb + (h0 + j) * dst.sh + n * dst.sn, ln, a, c, err);
   }
 }
 
-// Backward. blockIdx.y: 0 for q, 1 for k. A CTA walks over (token, head)
-// rows of its tensor with its lanes' 16 dimensions of dw in registers, then
-// sums them over its rows in a fixed order into one partial row per CTA.
-template <int D, bool NORM>
-__global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const NormRope p, float* __restrict__ partial) {
+// Backward. The first parts_q CTAs take q, the others k. A CTA walks over
+// items (a row of lanes' token, a section of the heads) of its tensor with
+// its lanes' 16 dimensions of dw in registers and the next row on its way,
+// then sums them over its rows in a fixed order into one partial row.
+constexpr int MAX_PARTS = 760;  // five CTAs an SM
+template <int D, bool NORM, bool INTER>
+__global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRope p, int parts_q,
+                                                                   float* __restrict__ partial) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR, WARPS = THREADS / 32;
   uint32_t* err = &g_rope_err;
   __shared__ float red[WARPS][D];
-  const int i = threadIdx.x % LPR;
-  const bool is_k = blockIdx.y != 0;
+  __shared__ __align__(16) float weight[D];
+  const bool is_k = static_cast<int>(blockIdx.x) >= parts_q;
+  const int part = static_cast<int>(blockIdx.x) - (is_k ? parts_q : 0);
+  const int parts = is_k ? static_cast<int>(gridDim.x) - parts_q : parts_q;
   const HeadRows& x_t = is_k ? p.k : p.q;
   const HeadRows& dy_t = is_k ? p.k_out : p.q_out;
   const HeadRows& dx_t = is_k ? p.dk : p.dq;
   const int heads = is_k ? p.Hkv : p.H;
-  const Lane ln(i, p.rot);
-  float wa[8], wb[8], dwa[8], dwb[8];
-  if (NORM) {
-    load_weight8(is_k ? p.k_weight : p.q_weight, p.w32, ln.ca, wa);
-    load_weight8(is_k ? p.k_weight : p.q_weight, p.w32, ln.cb, wb);
+  const int sections = is_k ? p.k_sections : p.q_sections;
+  const Lane ln(threadIdx.x % LPR, p.rot);
+  Row dw{};
+  if constexpr (NORM) {  // the weights stay in shared memory: registers are what limits the CTAs an SM
+    const void* w = is_k ? p.k_weight : p.q_weight;
+    if (threadIdx.x < D)
+      weight[threadIdx.x] = p.w32 ? reinterpret_cast<const float*>(w)[threadIdx.x]
+                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[threadIdx.x]);
+    __syncthreads();
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) dwa[e] = dwb[e] = 0.f;
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  for (long long t0 = static_cast<long long>(blockIdx.x) * ROWS; t0 < tokens;
-       t0 += static_cast<long long>(gridDim.x) * ROWS) {
-    const long long tok = t0 + threadIdx.x / LPR;
-    const bool live = tok < tokens;
-    const int b = live ? static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.N)) : 0;
-    const int n = live ? static_cast<int>(tok - static_cast<long long>(b) * p.N) : 0;
-    const int pos = live ? position_of(p, b, n, err) : 0;
+  const float* wa = weight + ln.ca * 8;
+  const float* wb = weight + ln.cb * 8;
+  const long long tiles = (static_cast<long long>(p.B) * p.N + ROWS - 1) / ROWS;
+  for (long long item = part; item < tiles * sections; item += parts) {
+    const int sec = static_cast<int>(item / tiles);
+    const Token tk(p, (item - sec * tiles) * ROWS + threadIdx.x / LPR);
+    const int h0 = section_start(sec, sections, heads), h1 = section_start(sec + 1, sections, heads);
+    const long long dy0 = tk.b * dy_t.sb + tk.n * dy_t.sn, x0 = tk.b * x_t.sb + tk.n * x_t.sn,
+                    dx0 = tk.b * dx_t.sb + tk.n * dx_t.sn;
+    auto load = [&](int h, Raw& dy, Raw& x) {
+      dy = x = Raw{};
+      if (!tk.live || h >= h1) return;
+      dy = load_row(dy_t, dy0 + h * dy_t.sh, ln, err);
+      if (NORM) x = load_row(x_t, x0 + h * x_t.sh, ln, err);
+    };
+    Raw dy, x, dy_next, x_next;
+    load(h0, dy, x);
+    const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : 0;
     Angles t;
-    if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, p.interleaved);
-    for (int h = 0; h < heads; ++h) {
-      Raw dy{}, x{};
-      if (live) {
-        dy = load_row(dy_t, b * dy_t.sb + h * dy_t.sh + n * dy_t.sn, ln, err);
-        if (NORM) x = load_row(x_t, b * x_t.sb + h * x_t.sh + n * x_t.sn, ln, err);
-      }
-      float ga[8], gb[8];
-      unpack8(dy.a, ga);
-      unpack8(dy.b, gb);
-      if (ln.turned && pos >= 0) turn(ga, gb, t, p.interleaved, -1.f);
-      if (pos < 0) {  // the forward wrote a zero row: no gradient
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ga[e] = gb[e] = 0.f;
-      }
+    if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
+    for (int h = h0; h < h1; ++h) {
+      load(h + 1, dy_next, x_next);
+      Row g = unpack(dy);
+      if (ln.turned && pos >= 0) turn<true>(g, t, INTER);
+      if (pos < 0) g = Row{};  // the forward wrote a zero row: no gradient
       if (NORM) {
-        float xa[8], xb[8];
-        unpack8(x.a, xa);
-        unpack8(x.b, xb);
-        float ss = 0.f, hx = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
-          hx = fmaf(ga[e] * wa[e], xa[e], fmaf(gb[e] * wb[e], xb[e], hx));
+        // The sums first, then x unpacked and the weights read anew for the
+        // rest: at 128 registers a thread they cannot stay.
+        float r, m;
+        {
+          const Row xr = unpack(x), wt = shared_row(wa, wb);
+          r = inv_rms<LPR>(xr, p.eps);
+          m = row_sum<LPR>(dot(times(g, wt), xr)) * (1.f / D) * r;  // mean of h n
         }
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        const float m = row_sum<LPR>(hx) * (1.f / D) * r;  // mean of h n
+        forget(x);
+        const float2 r2 = make_float2(r, r), rm = make_float2(-r * m, -r * m);
+        auto rest = [&](float2& gv, float2& dwv, float2 xv, float2 wv) {
+          const float2 nv = fmul2(xv, r2);
+          dwv = ffma2(gv, nv, dwv);
+          gv = ffma2(fmul2(gv, wv), r2, fmul2(nv, rm));  // r (h − n m)
+        };
+        const Row wt = shared_row(wa, wb);
+        const uint32_t xa[4] = {x.a.x, x.a.y, x.a.z, x.a.w}, xb[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float na = xa[e] * r, nb = xb[e] * r;
-          dwa[e] = fmaf(ga[e], na, dwa[e]);
-          dwb[e] = fmaf(gb[e], nb, dwb[e]);
-          ga[e] = r * (ga[e] * wa[e] - na * m);
-          gb[e] = r * (gb[e] * wb[e] - nb * m);
+        for (int e = 0; e < 4; ++e) {
+          rest(g.a[e], dw.a[e], bf_pair(xa[e]), wt.a[e]);
+          rest(g.b[e], dw.b[e], bf_pair(xb[e]), wt.b[e]);
         }
       }
-      if (live) store_row(dx_t, b * dx_t.sb + h * dx_t.sh + n * dx_t.sn, ln, ga, gb, err);
+      if (tk.live) store_row(dx_t, dx0 + h * dx_t.sh, ln, g, err);
+      dy = dy_next;
+      x = x_next;
     }
   }
   if constexpr (NORM) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    launch_dependents();  // the sum over the CTAs may be set up; it waits for all of this grid's writes
+    auto over_rows = [](float2& v) {  // Σ over the warp's rows
 #pragma unroll
       for (int o = LPR; o < 32; o <<= 1) {
-        dwa[e] += __shfl_xor_sync(0xffffffffu, dwa[e], o);
-        dwb[e] += __shfl_xor_sync(0xffffffffu, dwb[e], o);
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
       }
+    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      over_rows(dw.a[e]);
+      over_rows(dw.b[e]);
     }
     if ((threadIdx.x & 31) < LPR) {
+      float* mine = red[threadIdx.x >> 5];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        red[threadIdx.x >> 5][ln.ca * 8 + e] = dwa[e];
-        red[threadIdx.x >> 5][ln.cb * 8 + e] = dwb[e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2*>(mine + ln.ca * 8 + 2 * e) = dw.a[e];
+        *reinterpret_cast<float2*>(mine + ln.cb * 8 + 2 * e) = dw.b[e];
       }
     }
     __syncthreads();
@@ -198,68 +224,108 @@ __global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const NormRope p
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) s += red[w][threadIdx.x];
-      const long long at = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + threadIdx.x;
-      if (in_range(at, 1, 2ll * gridDim.x * D, err)) partial[at] = s;
+      const long long at = static_cast<long long>(blockIdx.x) * D + threadIdx.x;
+      if (in_range(at, 1, static_cast<long long>(gridDim.x) * D, err)) partial[at] = s;
     }
   }
 }
 
 // dw = Σ of the CTAs' partial rows, in a fixed order and in 64 bits (a few
 // hundred values a dimension: the partial rows' own rounding is what stays).
+// A CTA takes 8 dimensions, a thread every 32nd partial row of one.
+constexpr int DW_COLS = 8, DW_SLICES = 32;
 template <int D>
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restrict__ partial, int n_parts,
-                                                           float* __restrict__ dqw, float* __restrict__ dkw) {
-  constexpr int SLICES = 1024 / D;
+__global__ void __launch_bounds__(DW_COLS * DW_SLICES) weight_grad_kernel(const float* __restrict__ partial,
+                                                                          int parts_q, int parts_k,
+                                                                          float* __restrict__ dqw,
+                                                                          float* __restrict__ dkw) {
   uint32_t* err = &g_rope_err;
-  __shared__ double red[SLICES][D];
-  const int c = threadIdx.x % D, slice = threadIdx.x / D;
+  __shared__ double red[DW_SLICES][DW_COLS];
+  const int c = threadIdx.x % DW_COLS, slice = threadIdx.x / DW_COLS;
+  const int col = blockIdx.x * DW_COLS + c;
+  const int n_parts = blockIdx.y ? parts_k : parts_q;
+  wait_for_primary();
+  const float* mine = partial + (blockIdx.y ? parts_q : 0) * D + col;
   double s = 0.0;
-  for (int i = slice; i < n_parts; i += SLICES) {
-    const long long at = (static_cast<long long>(blockIdx.x) * n_parts + i) * D + c;
-    if (in_range(at, 1, 2ll * n_parts * D, err)) s += partial[at];
-  }
+#pragma unroll 8
+  for (int i = slice; i < n_parts; i += DW_SLICES)
+    if (in_range(static_cast<long long>(i) * D + col, 1, static_cast<long long>(n_parts) * D, err))
+      s += mine[static_cast<long long>(i) * D];
   red[slice][c] = s;
   __syncthreads();
   if (slice == 0) {
     double v = 0.0;
 #pragma unroll
-    for (int i = 0; i < SLICES; ++i) v += red[i][c];
-    (blockIdx.x ? dkw : dqw)[c] = static_cast<float>(v);
+    for (int i = 0; i < DW_SLICES; ++i) v += red[i][c];
+    (blockIdx.y ? dkw : dqw)[col] = static_cast<float>(v);
   }
+}
+
+static void set_sections(NormRope* p, int hs) {
+  p->q_sections = (p->H + hs - 1) / hs;
+  p->k_sections = (p->Hkv + hs - 1) / hs;
 }
 
 template <int D>
 static cudaError_t fwd(NormRope p, cudaStream_t stream) {
-  constexpr int ROWS = THREADS / (D / 16), HPG = 4;
-  p.q_groups = (p.H + HPG - 1) / HPG;
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  const dim3 grid(static_cast<unsigned>((tokens + ROWS - 1) / ROWS),
-                  static_cast<unsigned>(p.q_groups + (p.Hkv + HPG - 1) / HPG));
-  norm_rope_kernel<D, HPG><<<grid, THREADS, 0, stream>>>(p);
+  constexpr int ROWS = THREADS / (D / 16);
+  const long long tiles = (static_cast<long long>(p.B) * p.N + ROWS - 1) / ROWS;
+  // Sections of up to 16 heads, smaller ones until a wave of CTAs is there.
+  set_sections(&p, 16);
+  for (int hs = 8; hs > 1 && tiles * (p.q_sections + p.k_sections) < 152 * 5; hs /= 2) set_sections(&p, hs);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.q_sections + p.k_sections));
+  if (p.interleaved) norm_rope_kernel<D, true><<<grid, THREADS, 0, stream>>>(p);
+  else norm_rope_kernel<D, false><<<grid, THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
-static cudaError_t bwd(const NormRope& p, float* partial, int parts, float* dqw, float* dkw, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(parts), 2);
+static cudaError_t bwd(NormRope p, float* partial, float* dqw, float* dkw, cudaStream_t stream) {
+  constexpr int ROWS = THREADS / (D / 16);
+  const long long tiles = (static_cast<long long>(p.B) * p.N + ROWS - 1) / ROWS;
+  // Sections of up to 8 heads; smaller ones while all items still fit one
+  // wave (a second, part-filled one costs more than longer items).
+  set_sections(&p, 8);
+  for (int hs = 4; hs > 0; hs /= 2) {
+    NormRope finer = p;
+    set_sections(&finer, hs);
+    if (tiles * (finer.q_sections + finer.k_sections) > MAX_PARTS) break;
+    p = finer;
+  }
+  const long long items_q = tiles * p.q_sections, items_k = tiles * p.k_sections;
+  // CTAs in proportion to the rows, at most as many as there are items
+  long long parts_k = static_cast<long long>(MAX_PARTS) * p.Hkv / (p.H + p.Hkv);
+  parts_k = parts_k < 1 ? 1 : parts_k > items_k ? items_k : parts_k;
+  long long parts_q = MAX_PARTS - parts_k;
+  parts_q = parts_q > items_q ? items_q : parts_q;
+  if (items_q + items_k <= MAX_PARTS) parts_q = items_q, parts_k = items_k;
+  const unsigned grid = static_cast<unsigned>(parts_q + parts_k);
   if (!p.q_weight) {
-    norm_rope_bwd_kernel<D, false><<<grid, THREADS, 0, stream>>>(p, nullptr);
+    if (p.interleaved) norm_rope_bwd_kernel<D, false, true><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), nullptr);
+    else norm_rope_bwd_kernel<D, false, false><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), nullptr);
     return cudaGetLastError();
   }
-  norm_rope_bwd_kernel<D, true><<<grid, THREADS, 0, stream>>>(p, partial);
+  if (p.interleaved) norm_rope_bwd_kernel<D, true, true><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), partial);
+  else norm_rope_bwd_kernel<D, true, false><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), partial);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  weight_grad_kernel<D><<<2, 1024, 0, stream>>>(partial, parts, dqw, dkw);
-  return cudaGetLastError();
+  // Launched while the rows' kernel drains (4 us of a small case's 17).
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(D / DW_COLS, 2);
+  cfg.blockDim = dim3(DW_COLS * DW_SLICES);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_grad_kernel<D>, static_cast<const float*>(partial), static_cast<int>(parts_q),
+                            static_cast<int>(parts_k), dqw, dkw);
 }
 
 }  // namespace rope
 
-int norm_rope_bwd_parts(int B, int N, int d) {
-  const long long rows = rope::THREADS / (d / 16);
-  const long long tiles = (static_cast<long long>(B) * N + rows - 1) / rows;
-  return static_cast<int>(tiles < 304 ? tiles : 304);
-}
+size_t norm_rope_bwd_partial_bytes(int d) { return static_cast<size_t>(rope::MAX_PARTS) * d * sizeof(float); }
 
 cudaError_t launch_norm_rope(const NormRope& p, int d, cudaStream_t stream) {
   return d == 64 ? rope::fwd<64>(p, stream) : rope::fwd<128>(p, stream);
@@ -267,9 +333,7 @@ cudaError_t launch_norm_rope(const NormRope& p, int d, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope_bwd(const NormRope& p, int d, float* partial, float* dqw, float* dkw,
                                  cudaStream_t stream) {
-  const int parts = norm_rope_bwd_parts(p.B, p.N, d);
-  return d == 64 ? rope::bwd<64>(p, partial, parts, dqw, dkw, stream)
-                 : rope::bwd<128>(p, partial, parts, dqw, dkw, stream);
+  return d == 64 ? rope::bwd<64>(p, partial, dqw, dkw, stream) : rope::bwd<128>(p, partial, dqw, dkw, stream);
 }
 
 cudaError_t read_and_clear_rope_error(uint32_t* out, cudaStream_t stream) {
