@@ -24,9 +24,9 @@
 //   output  Oᵀ[dim][head]: an operand register pairs two keys of one
 //           dimension, two words' halves merged by one byte permutation.
 // A nibble becomes a bf16 number by placing it in the top four mantissa bits
-// of 16.0 (16 + n: one shift, one and-or for two values). The scores keep
-// that offset and take it off with the centre (s Σ q (16 + n) + (z − 24 s) Σ q);
-// the values subtract it first, since their sums run over the whole context.
+// of 16.0 (16 + n: one shift, one and-or for two values), or an fp16 one in
+// the low bits of 1024; the scores start from minus the offsets' sum, and the
+// values' offsets cancel between the halves of a stage.
 // Each warp walks its own 16-key tiles; the CTA's warps are merged at its end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -110,6 +110,12 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
   return d;
 }
 
+__device__ __forceinline__ uint32_t andnot_or(uint32_t v, uint32_t mask, uint32_t base) {  // (~v & mask) | base
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xae;" : "=r"(d) : "r"(v), "r"(mask), "r"(base));
+  return d;
+}
+
 // Keys: the four nibbles of each 16-bit half as four pairs of fp16, 1024 + n
 // (nibbles 0 and 2, in the lowest mantissa bits of 1024) and 16 (64 + n)
 // (nibbles 1 and 3, four bits up): one shift and four and-ors for 8 values.
@@ -121,10 +127,11 @@ __device__ __forceinline__ void key_pairs(uint32_t w, uint32_t base, uint32_t (&
   v[3] = and_or(h, 0x00f000f0u, base);
 }
 // Values: 16 + n for nibble I of each half, as two bf16 (n in the top four
-// mantissa bits of 16).
-template <int I>
+// mantissa bits of 16), or 16 + 15 − n with FLIP (the complement's bits).
+template <int I, bool FLIP>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t base) {
-  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), 0x00780078u, base);
+  const uint32_t v = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return FLIP ? andnot_or(v, 0x00780078u, base) : and_or(v, 0x00780078u, base);
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -409,7 +416,12 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     }
   }
 
-  float acc[NT][MT][4];
+  // Output sums. The first 16 keys of a stage add p s (16 + n), the others
+  // −p s (31 − n): the offsets of the two nearly cancel, so the running sums
+  // stay as small as those of n − 8 and lose no more (the tensor core cuts
+  // sums off at 24 bits). `fix` takes Σ ∓24, 23 p s of the same rounded p s,
+  // what is left between the offsets and −8: one product for a group's four.
+  float acc[NT][MT][4], fix[NT][NG][4];
   // Per head: the exponents' reference in log2 units (0 while no key has been
   // seen), the score above which it is raised, and the running sums.
   float m[NT][2], lim[NT][2], l[NT][2], zc[NT][NG][2];
@@ -419,6 +431,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) fix[nt][gr][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       m[nt][e] = 0.f;
@@ -533,7 +549,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
           lim[nt][e] = (m_new + RESCALE_LOG2) / sc[nt][e];
           l[nt][e] *= alpha;
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) zc[nt][gr][e] *= alpha;
+          for (int gr = 0; gr < NG; ++gr) {
+            zc[nt][gr][e] *= alpha;
+            fix[nt][gr][e] *= alpha;  // (rows are alike: the first is read at the end)
+          }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             acc[nt][i][e] *= alpha;
@@ -557,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float sv = bf_lo(vp[u][r][gr]), zv = bf_hi(vp[u][r][gr]);
+            const float sv = u == 0 ? bf_lo(vp[u][r][gr]) : -bf_lo(vp[u][r][gr]), zv = bf_hi(vp[u][r][gr]);
             zc[nt][gr][0] = fmaf(pr[2 * r], zv, zc[nt][gr][0]);
             zc[nt][gr][1] = fmaf(pr[2 * r + 1], zv, zc[nt][gr][1]);
             // bf16: its range takes any step, and the products' errors
@@ -575,25 +594,26 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
                                                     gr * 32 + g * 4);
         const uint32_t h[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
                                __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
-        const uint32_t a0[4] = {value_pair<0>(h[0], bases.value), value_pair<0>(h[1], bases.value), value_pair<0>(h[2], bases.value), value_pair<0>(h[3], bases.value)};
-        const uint32_t a1[4] = {value_pair<1>(h[0], bases.value), value_pair<1>(h[1], bases.value), value_pair<1>(h[2], bases.value), value_pair<1>(h[3], bases.value)};
-        const uint32_t a2[4] = {value_pair<2>(h[0], bases.value), value_pair<2>(h[1], bases.value), value_pair<2>(h[2], bases.value), value_pair<2>(h[3], bases.value)};
-        const uint32_t a3[4] = {value_pair<3>(h[0], bases.value), value_pair<3>(h[1], bases.value), value_pair<3>(h[2], bases.value), value_pair<3>(h[3], bases.value)};
-        // Σ p s (16 + n), then Σ p s (−24) of the same 16 keys: a product more
-        // for each tile costs less than subtracting 24 from every operand
-        // register, and the running sums stay those of n − 8.
-        const uint32_t off[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+        uint32_t a[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (u == 0) {
+            a[0][r] = value_pair<0, false>(h[r], bases.value), a[1][r] = value_pair<1, false>(h[r], bases.value);
+            a[2][r] = value_pair<2, false>(h[r], bases.value), a[3][r] = value_pair<3, false>(h[r], bases.value);
+          } else {
+            a[0][r] = value_pair<0, true>(h[r], bases.value), a[1][r] = value_pair<1, true>(h[r], bases.value);
+            a[2][r] = value_pair<2, true>(h[r], bases.value), a[3][r] = value_pair<3, true>(h[r], bases.value);
+          }
+        }
+        // -24, and 23 of a negated probability
+        const uint32_t c = u == 0 ? 0xc1c0c1c0u : 0xc1b8c1b8u;
+        const uint32_t off[4] = {c, c, c, c};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint32_t b0 = pf[nt][gr][0], b1 = pf[nt][gr][1];
-          mma_bf16(acc[nt][4 * gr], a0, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 1], a1, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 2], a2, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 3], a3, b0, b1);
-          mma_bf16(acc[nt][4 * gr], off, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 1], off, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 2], off, b0, b1);
-          mma_bf16(acc[nt][4 * gr + 3], off, b0, b1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_bf16(acc[nt][4 * gr + i], a[i], b0, b1);
+          mma_bf16(fix[nt][gr], off, b0, b1);
         }
       }
     }
@@ -650,6 +670,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         float z = zc[nt][gr][e];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        z += fix[nt][gr][e];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           sm_o(warp)[h * OROW + 64 * gr + 8 * g + i] = acc[nt][4 * gr + i][e] + z;
