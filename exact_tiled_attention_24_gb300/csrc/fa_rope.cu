@@ -23,18 +23,30 @@ namespace rope {
 
 constexpr int THREADS = 128;
 
-// Row of a strided [B][heads][N][D] tensor as two 16-byte chunks.
-__device__ __forceinline__ Raw load_row(const HeadRows& t, long long off, const Lane& ln, uint32_t* err) {
-  Raw r{};
-  if (in_range(off + ln.ca * 8, 8, t.extent, err)) r.a = load16(t.p + off + ln.ca * 8);
-  if (in_range(off + ln.cb * 8, 8, t.extent, err)) r.b = load16(t.p + off + ln.cb * 8);
-  return r;
-}
-__device__ __forceinline__ void store_row(const HeadRows& t, long long off, const Lane& ln, const Row& x,
-                                          uint32_t* err) {
-  if (in_range(off + ln.ca * 8, 8, t.extent, err)) store16(t.p + off + ln.ca * 8, pack8(x.a));
-  if (in_range(off + ln.cb * 8, 8, t.extent, err)) store16(t.p + off + ln.cb * 8, pack8(x.b));
-}
+// A lane's place in the rows of one token, moved from head to head: the
+// address of its chunk a; chunk b is a fixed distance on.
+struct Cursor {
+  __nv_bfloat16* at;
+  long long step;  // one head
+  int to_b;        // chunk a to chunk b
+  const HeadRows* t;
+  __device__ __forceinline__ Cursor(const HeadRows& rows, int b, int n, int h, const Lane& ln)
+      : at(rows.p + (b * rows.sb + n * rows.sn + h * rows.sh + ln.ca * 8)),
+        step(rows.sh), to_b((ln.cb - ln.ca) * 8), t(&rows) {}
+  __device__ __forceinline__ bool fits(const __nv_bfloat16* p, uint32_t* err) const {
+    return in_range(p - t->p, 8, t->extent, err);
+  }
+  __device__ __forceinline__ Raw load(uint32_t* err) const {
+    Raw r{};
+    if (fits(at, err)) r.a = load16(at);
+    if (fits(at + to_b, err)) r.b = load16(at + to_b);
+    return r;
+  }
+  __device__ __forceinline__ void store(const Row& x, uint32_t* err) const {
+    if (fits(at, err)) store16(at, pack8(x.a));
+    if (fits(at + to_b, err)) store16(at + to_b, pack8(x.b));
+  }
+};
 
 // The row of the tables for token (b, n), or -1 (reported) for a position
 // outside them.
@@ -84,10 +96,13 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
   const int h0 = section_start(sec, n_sec, heads), h1 = section_start(sec + 1, n_sec, heads);
   const HeadRows& src = is_k ? p.k : p.q;
   const HeadRows& dst = is_k ? p.k_out : p.q_out;
-  const long long in0 = tk.b * src.sb + tk.n * src.sn, out0 = tk.b * dst.sb + tk.n * dst.sn;
+  Cursor in(src, tk.b, tk.n, h0, ln), out(dst, tk.b, tk.n, h0, ln);
   auto load2 = [&](int h, Raw (&r)[2]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) r[j] = tk.live && h + j < h1 ? load_row(src, in0 + (h + j) * src.sh, ln, err) : Raw{};
+    for (int j = 0; j < 2; ++j) {
+      r[j] = tk.live && h + j < h1 ? in.load(err) : Raw{};
+      in.at += in.step;
+    }
   };
   Raw cur[2], next[2];
   load2(h0, cur);
@@ -108,7 +123,8 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
       if (w) x = times(times(x, inv_rms<LPR>(x, p.eps)), wt);
       if (ln.turned && pos >= 0) turn<false>(x, t, INTER);
       if (pos < 0) x = Row{};  // no angle to turn by: a zero row
-      if (tk.live && h + j < h1) store_row(dst, out0 + (h + j) * dst.sh, ln, x, err);
+      if (tk.live && h + j < h1) out.store(x, err);
+      out.at += out.step;
       cur[j] = next[j];
     }
   }
@@ -150,19 +166,21 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
     const int sec = static_cast<int>(item / tiles);
     const Token tk(p, (item - sec * tiles) * ROWS + threadIdx.x / LPR);
     const int h0 = section_start(sec, sections, heads), h1 = section_start(sec + 1, sections, heads);
-    const long long dy0 = tk.b * dy_t.sb + tk.n * dy_t.sn, x0 = tk.b * x_t.sb + tk.n * x_t.sn,
-                    dx0 = tk.b * dx_t.sb + tk.n * dx_t.sn;
+    Cursor dy_at(dy_t, tk.b, tk.n, h0, ln), x_at(x_t, tk.b, tk.n, h0, ln), dx_at(dx_t, tk.b, tk.n, h0, ln);
     auto load = [&](int h, Raw& dy, Raw& x) {
       dy = x = Raw{};
       if (!tk.live || h >= h1) return;
-      dy = load_row(dy_t, dy0 + h * dy_t.sh, ln, err);
-      if (NORM) x = load_row(x_t, x0 + h * x_t.sh, ln, err);
+      dy = dy_at.load(err);
+      if (NORM) x = x_at.load(err);
+      dy_at.at += dy_at.step;
+      x_at.at += x_at.step;
     };
     Raw dy, x, dy_next, x_next;
     load(h0, dy, x);
     const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : 0;
     Angles t;
     if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
+#pragma unroll 1
     for (int h = h0; h < h1; ++h) {
       load(h + 1, dy_next, x_next);
       Row g = unpack(dy);
@@ -192,7 +210,8 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
           rest(g.b[e], dw.b[e], bf_pair(xb[e]), wt.b[e]);
         }
       }
-      if (tk.live) store_row(dx_t, dx0 + h * dx_t.sh, ln, g, err);
+      if (tk.live) dx_at.store(g, err);
+      dx_at.at += dx_at.step;
       dy = dy_next;
       x = x_next;
     }
