@@ -10,11 +10,11 @@
 // themselves, which bf16 holds exactly; steps and centres are applied to the
 // score accumulators and to the probabilities, in fp32.
 //
-// The step is bound by reading the codes: d/2 + d/16 bytes a key or value.
-// At 6.8 TB/s an SM takes in 23 bytes a clock, 47 values, and each has to be
-// turned into an operand. tcgen05 takes operands from shared memory or TMEM,
-// and writing 47 bf16 values a clock there and reading them back is more than
-// shared memory's 128 bytes a clock. So a warp keeps them in registers:
+// The step would be bound by reading the codes, d/2 + d/16 bytes a key or
+// value: at 6.8 TB/s an SM takes in 23 bytes a clock, 47 values, and each has
+// to be turned into an operand. tcgen05 takes operands from shared memory or
+// TMEM, and writing 47 bf16 values a clock to shared memory and reading them
+// back is more than its 128 bytes a clock. So a warp keeps them in registers:
 // mma.sync m16n8k16, whose A operand is 16 keys (scores) or 16 dimensions
 // (output) and whose 8 columns are query heads that share the K/V head.
 //   scores  Sᵀ[key][head]: rows g and g + 8 of a tile are keys; the words of
@@ -27,7 +27,15 @@
 // of 16.0 (16 + n: one shift, one and-or for two values), or an fp16 one in
 // the low bits of 1024; the scores start from minus the offsets' sum, and the
 // values' offsets cancel between the halves of a stage.
-// Each warp walks its own 16-key tiles; the CTA's warps are merged at its end.
+//
+// What bounds it, measured (32 requests of 2k to 8k tokens, 8 K/V heads, d =
+// 128, 189 MB): 63 us with the merge, 37 us with the copies alone, 53 us with
+// the products alone on whatever the ring holds. A stage of 32 keys costs a
+// warp about 550 instructions, half of them on the integer pipe at two clocks
+// each, and 36 mma.sync, which hold their scheduler for some 7 clocks each
+// (timed apart: integer and tensor instructions of different warps add up,
+// they do not overlap). 12, 16 or 20 warps an SM, other stage orders and
+// scores one tile ahead of the output all measured within 5%, or slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -44,16 +52,16 @@ static __device__ uint32_t g_decq4_err;
 namespace decq4 {
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int TK = 32;  // keys a warp takes at a time: one stage of its ring
+constexpr int TK = 32;          // keys a warp takes of a tile
+constexpr int CK = WARPS * TK;  // keys of a CTA's tile: one stage of the ring
 constexpr float LN2 = 0.69314718055994531f;
 constexpr float RESCALE_LOG2 = 8.f;
-constexpr uint32_t NO_ROW = 0xffffffffu;
-
-constexpr int CK = WARPS * TK;  // keys of a CTA's tile: one stage of the ring
+constexpr uint32_t NO_ROW = 0xffffffffu;  // the host keeps the cache below 2^32 - 1 rows
 
 // A stage of the ring holds a tile: K codes, V codes, K pairs, V pairs of its
-// 128 keys, 32 for each warp. With up to 8 query heads a warp's state fits
-// 128 registers and four CTAs share an SM.
+// 128 keys, 32 for each warp. Three CTAs an SM at d = 128 (160 registers a
+// thread; four at 128 registers measured the same, with more instructions),
+// four at d = 64, two with 16 query heads a CTA.
 template <int D, int NT>
 struct Ring {
   static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : 2;  // per SM
@@ -482,30 +490,38 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
           vp[u][r][0] = *reinterpret_cast<const uint32_t*>(vps + key * 4);
         }
       }
+      uint32_t a[NG][4][4];  // per K step
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        uint32_t a[4][4];  // per K step
+      for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int key = 16 * u + g + 8 * r;
           const uint2 w = *reinterpret_cast<const uint2*>(kc + key * (D / 2) + gr * 32 + t * 8);
           uint32_t v[4];
           key_pairs(w.x, bases.key, v);
-          a[0][r] = v[0], a[0][r + 2] = v[1], a[1][r] = v[2], a[1][r + 2] = v[3];
+          a[gr][0][r] = v[0], a[gr][0][r + 2] = v[1], a[gr][1][r] = v[2], a[gr][1][r + 2] = v[3];
           key_pairs(w.y, bases.key, v);
-          a[2][r] = v[0], a[2][r + 2] = v[1], a[3][r] = v[2], a[3][r + 2] = v[3];
+          a[gr][2][r] = v[0], a[gr][2][r + 2] = v[1], a[gr][3][r] = v[2], a[gr][3][r + 2] = v[3];
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[4];
-          mma_f16_from(c, a[0], qf[nt][gr][0][0], qf[nt][gr][0][1], qoff[nt][gr][0], qoff[nt][gr][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        float c[NG][4];
 #pragma unroll
-          for (int ks = 1; ks < 4; ++ks) mma_f16(c, a[ks], qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
+        for (int gr = 0; gr < NG; ++gr)
+          mma_f16_from(c[gr], a[gr][0], qf[nt][gr][0][0], qf[nt][gr][0][1], qoff[nt][gr][0], qoff[nt][gr][1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float zq = bf_hi(kp[e >> 1][gr]) * qsum[nt][gr][e & 1];
-            x[nt][u][e] = fmaf(bf_lo(kp[e >> 1][gr]), c[e], gr == 0 ? zq : x[nt][u][e] + zq);
+        for (int ks = 1; ks < 4; ++ks)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) mma_f16(c[gr], a[gr][ks], qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = bf_hi(kp[e >> 1][0]) * qsum[nt][0][e & 1];
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            if (gr > 0) v = fmaf(bf_hi(kp[e >> 1][gr]), qsum[nt][gr][e & 1], v);
+            v = fmaf(bf_lo(kp[e >> 1][gr]), c[gr][e], v);
           }
+          x[nt][u][e] = v;
         }
       }
     }
@@ -673,14 +689,16 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         z += fix[nt][gr][e];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sm_o(warp)[h * OROW + 64 * gr + 8 * g + i] = acc[nt][4 * gr + i][e] + z;
-          sm_o(warp)[h * OROW + 64 * gr + 8 * g + i + 4] = acc[nt][4 * gr + i][e + 2] + z;
+          const int at = h * OROW + 64 * gr + 8 * g + i;
+          if (!in_range(at, 5, NH * OROW, err)) continue;
+          sm_o(warp)[at] = acc[nt][4 * gr + i][e] + z;
+          sm_o(warp)[at + 4] = acc[nt][4 * gr + i][e + 2] + z;
         }
       }
     }
   __syncthreads();
-  // One lane per head: the warps' weights e^(m_w − m) / Σ, in the first
-  // warp's place of m; then every thread sums a column of some heads.
+  // One lane per head: the warps' weights e^(m_w − m) / Σ, behind the first
+  // warp's result; then every thread sums a column of some heads.
   float* weights = sm_m(0) + 2 * NH;  // [NH][WARPS]
   if (threadIdx.x < G) {
     const int h = threadIdx.x;

@@ -285,3 +285,42 @@ def test_training_step_through_attention(fa):
         assert np.abs(to_f64(dx) - rdx).max() <= gain * TOL_GRAD + 2.0 ** -8 * np.abs(rdx).max()
         n = np.abs(to_f64(x) * r)
         assert np.all(np.abs(f64(dw) - rdw) <= TOL_GRAD * n.sum(axis=(0, 1, 2)))
+
+
+def test_prefill_and_append_make_the_same_keys(fa):
+    # a prompt's rows from qk_norm_rope and from append_paged are the same bits
+    H, Hkv, N, d, bs = 6, 2, 75, 128, 16
+    for inter, rot in ((False, 128), (True, 64)):
+        q, k, cos, sin, pos, qw, kw = case(1, H, Hkv, N, d, rot, "packed", torch.bfloat16, "own", seed=14)
+        qo, ko = fa.qk_norm_rope(q, k, cos, sin, positions=pos, q_weight=qw, k_weight=kw, interleaved=inter)
+        mb = cos.shape[0] // bs + 1
+        table = torch.randperm(mb, device="cuda").to(torch.int32)[None].contiguous()
+        kc, vc = (torch.zeros((mb, Hkv, bs, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        uniq = torch.unique(pos[0], return_inverse=True)[1]
+        first = [int((uniq == i).nonzero()[0]) for i in range(int(uniq.max()) + 1)]   # one token a position
+        sel = torch.tensor(first, device="cuda")
+        kt, qt = k[0].transpose(0, 1)[sel], q[0].transpose(0, 1)[sel]
+        p = pos[0][sel].contiguous()
+        qa = fa.append_paged(kt, kt, kc, vc, table, p, torch.zeros_like(p), cos, sin, q=qt, q_weight=qw, k_weight=kw,
+                             interleaved=inter)
+        assert torch.equal(qa, qo[0].transpose(0, 1)[sel])
+        got = kc[table[0][(p // bs).long()].long(), :, (p % bs).long()]
+        assert torch.equal(got, ko[0].transpose(0, 1)[sel]) and fa.last_device_error() == 0
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,d", [(64, 3, 1, 1, 128), (1, 128, 128, 3, 64), (3, 33, 17, 5, 128), (1, 1, 1, 4096, 64)])
+def test_odd_shapes_against_small_calls(fa, B, H, Hkv, N, d):
+    # many heads, many batches, one token: the same bits as head by head
+    q, k, cos, sin, pos, qw, kw = case(B, H, Hkv, N, d, d, "packed", torch.float32, "own", seed=15)
+    qo, ko = fa.qk_norm_rope(q, k, cos, sin, positions=pos, q_weight=qw, k_weight=kw)
+    for h in sorted({0, H // 2, H - 1}):
+        one, _ = fa.qk_norm_rope(q[:, h:h + 1], k[:, :1], cos, sin, positions=pos, q_weight=qw, k_weight=kw)
+        assert torch.equal(one[:, 0], qo[:, h])
+    _, one = fa.qk_norm_rope(q[:, :1], k[:, Hkv - 1:], cos, sin, positions=pos, q_weight=qw, k_weight=kw)
+    assert torch.equal(one[:, 0], ko[:, Hkv - 1])
+    g = [torch.randn_like(x.float()).to(torch.bfloat16) for x in (qo, ko)]
+    dq, dk, dqw, dkw = fa.qk_norm_rope_bwd(*g, q, k, cos, sin, positions=pos, q_weight=qw, k_weight=kw)
+    one = fa.qk_norm_rope_bwd(g[0][:, H - 1:].contiguous(), g[1][:, :1].contiguous(), q[:, H - 1:], k[:, :1], cos, sin,
+                              positions=pos, q_weight=qw, k_weight=kw)
+    assert torch.equal(one[0][:, 0], dq[:, H - 1]) and torch.equal(one[1][:, 0], dk[:, 0])
+    assert bool(dqw.isfinite().all()) and bool(dkw.isfinite().all()) and fa.last_device_error() == 0
