@@ -25,8 +25,8 @@
 //           dimension, two words' halves merged by one byte permutation.
 // A nibble becomes a bf16 number by placing it in the top four mantissa bits
 // of 16.0 (16 + n: one shift, one and-or for two values), or an fp16 one in
-// the low bits of 1024; the scores start from minus the offsets' sum, and the
-// values' offsets cancel between the halves of a stage.
+// the low bits of 1024. Keys have the offset subtracted; the values' offsets
+// cancel between the halves of a stage.
 //
 // What bounds it, measured (32 requests of 2k to 8k tokens, 8 K/V heads, d =
 // 128, 189 MB): 63 us with the merge, 37 us with the copies alone, 53 us with
@@ -86,14 +86,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The same with d = c + A B for c = (c0, c1, c0, c1).
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
-                                             float c1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -124,15 +116,24 @@ __device__ __forceinline__ uint32_t andnot_or(uint32_t v, uint32_t mask, uint32_
   return d;
 }
 
-// Keys: the four nibbles of each 16-bit half as four pairs of fp16, 1024 + n
-// (nibbles 0 and 2, in the lowest mantissa bits of 1024) and 16 (64 + n)
-// (nibbles 1 and 3, four bits up): one shift and four and-ors for 8 values.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Keys: the four nibbles of each 16-bit half as four pairs of fp16: n − 8
+// (nibbles 0 and 2, in the lowest mantissa bits of 1024, less 1032) and
+// 16 (n − 8) (nibbles 1 and 3, four bits up, less 16 · 72), both exact: one
+// shift, four and-ors and four subtractions (on the other pipe) for 8 values.
+// Left in the operands, the offsets would be taken off a score at the end,
+// and what fp32 loses beside 1024 Σ q is 3e-5 of a score.
 __device__ __forceinline__ void key_pairs(uint32_t w, uint32_t base, uint32_t (&v)[4]) {
   const uint32_t h = w >> 8;
-  v[0] = and_or(w, 0x000f000fu, base);
-  v[1] = and_or(w, 0x00f000f0u, base);
-  v[2] = and_or(h, 0x000f000fu, base);
-  v[3] = and_or(h, 0x00f000f0u, base);
+  v[0] = sub_f16x2(and_or(w, 0x000f000fu, base), 0x64086408u);
+  v[1] = sub_f16x2(and_or(w, 0x00f000f0u, base), 0x64806480u);
+  v[2] = sub_f16x2(and_or(h, 0x000f000fu, base), 0x64086408u);
+  v[3] = sub_f16x2(and_or(h, 0x00f000f0u, base), 0x64806480u);
 }
 // Values: 16 + n for nibble I of each half, as two bf16 (n in the top four
 // mantissa bits of 16), or 16 + 15 − n with FLIP (the complement's bits).
@@ -363,14 +364,13 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
 
   // Query operand: for group gr and word w of a lane quarter's 16 dimensions
   // 64 gr + 16 t + 8 w + 0..7, K step 2 w + h (h = 0, 1) multiplies elements
-  // (2h, 2h + 4), whose codes come as 1024 + n, and (2h + 1, 2h + 5), whose
-  // come as 16 (64 + n): the latter's q carry the 1/16. A head's q are scaled
-  // by a power of two to a largest magnitude in [1, 2): fp16 then holds all
-  // that counts of them exactly. The accumulators start at
-  // -Σ q (offset + 8), so that a group's product ends as Σ q (n − 8).
+  // (2h, 2h + 4), whose codes come as n − 8, and (2h + 1, 2h + 5), whose come
+  // as 16 (n − 8): the latter's q carry the 1/16. A head's q are scaled by a
+  // power of two to a largest magnitude in [1, 2): fp16 then holds all that
+  // counts of them exactly.
   uint32_t qf[NT][NG][4][2];
-  float qsum[NT][NG][2], qoff[NT][NG][2];  // of this lane's heads 2t, 2t + 1
-  float sc[NT][2];                         // score units to log2 units
+  float qsum[NT][NG][2];  // Σ q of this lane's heads 2t, 2t + 1
+  float sc[NT][2];        // score units to log2 units
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint4 v[NG][2];
@@ -408,19 +408,14 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         qf[nt][gr][2 * w + 1][0] = pack_f16x2(bf_lo(x.y) * down, bf_lo(x.w) * down);
         qf[nt][gr][2 * w + 1][1] = pack_f16x2(bf_hi(x.y) * d16, bf_hi(x.w) * d16);
       }
-      // Σ q and Σ q (offset + 8) of what fp16 holds: products with constants.
-      // Registers 2 and 3 of A meet the second half of a K step.
-      const uint32_t one = 0x3c003c00u, x16 = 0x4c004c00u;        // 1, 16
-      const uint32_t lo = 0x64086408u, hi = 0x64806480u;          // 1024 + 8, 16 (64 + 8)
-      const uint32_t ones[4] = {one, one, x16, x16}, offs[4] = {lo, lo, hi, hi};
-      float c[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+      // Σ q of what fp16 holds: a product with constants. Registers 2 and 3
+      // of A meet the second half of a K step.
+      const uint32_t one = 0x3c003c00u, x16 = 0x4c004c00u;  // 1, 16
+      const uint32_t ones[4] = {one, one, x16, x16};
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        mma_f16(c, ones, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
-        mma_f16(o, offs, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
-      }
+      for (int ks = 0; ks < 4; ++ks) mma_f16(c, ones, qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
       qsum[nt][gr][0] = c[0], qsum[nt][gr][1] = c[1];
-      qoff[nt][gr][0] = -o[0], qoff[nt][gr][1] = -o[1];
     }
   }
 
@@ -505,12 +500,9 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float c[NG][4];
+        float c[NG][4] = {};
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
-          mma_f16_from(c[gr], a[gr][0], qf[nt][gr][0][0], qf[nt][gr][0][1], qoff[nt][gr][0], qoff[nt][gr][1]);
-#pragma unroll
-        for (int ks = 1; ks < 4; ++ks)
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) mma_f16(c[gr], a[gr][ks], qf[nt][gr][ks][0], qf[nt][gr][ks][1]);
 #pragma unroll

@@ -59,8 +59,7 @@ __device__ __forceinline__ void store16(void* p, const uint4& v) {
                : "memory");
 }
 
-// A lane's 16 values as fp32 pairs: one packed instruction works on two. The
-// packed products and sums round each value as the scalar ones do.
+// A lane's 16 values as fp32 pairs: one packed instruction works on two.
 struct Row {
   float2 a[4], b[4];
 };
@@ -174,6 +173,9 @@ struct Angles {
 // and sum of a rotation is rounded by itself, never contracted: a key's
 // values, and with them the codes of a 4-bit cache, then do not hang on how a
 // compiler fuses the expression, and every kernel here gives the same bits.
+// (Packed sums of packed products are contracted, whatever their rounding
+// says: one key group's step in 10^4 came out a bf16 step off. So products
+// are packed, sums are not.)
 __device__ __forceinline__ float2 turn1(float2 x, float c, float s) {
   return make_float2(__fsub_rn(__fmul_rn(x.x, c), __fmul_rn(x.y, s)), __fadd_rn(__fmul_rn(x.y, c), __fmul_rn(x.x, s)));
 }
@@ -189,9 +191,9 @@ __device__ __forceinline__ void turn(Row& x, const Angles& t, bool interleaved) 
       half[2 * (i & 1)] = turn1(half[2 * (i & 1)], t.c[i].x, s.x);
       half[2 * (i & 1) + 1] = turn1(half[2 * (i & 1) + 1], t.c[i].y, s.y);
     } else {
-      const float2 a = fsub2(fmul2(x.a[i], t.c[i]), fmul2(x.b[i], s));
-      x.b[i] = fadd2(fmul2(x.b[i], t.c[i]), fmul2(x.a[i], s));
-      x.a[i] = a;
+      const float2 ac = fmul2(x.a[i], t.c[i]), bs = fmul2(x.b[i], s), bc = fmul2(x.b[i], t.c[i]), as = fmul2(x.a[i], s);
+      x.a[i] = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+      x.b[i] = make_float2(__fadd_rn(bc.x, as.x), __fadd_rn(bc.y, as.y));
     }
   }
 }

@@ -170,19 +170,27 @@ def test_append_q4(fa, c):
             assert np.all(q[t] == 5.0) and all(bool((x[t] == 5).all()) for x in values)
 
 
-def test_q4_keys_without_norm_are_exact(fa):
-    # rotation alone is six fp32 operations rounded one by one: the codes are
-    # those of the same operations on the host
-    s = Case(fa, 60, 3, 4, 4, 128, 16, 128, False, seed=3, q4=True)
-    fa.append_paged_q4(s.k, s.v, *s.cache, s.table, s.pos, **s.kwargs())
+@pytest.mark.parametrize("rot,inter", [(128, False), (64, True)])
+def test_q4_keys_without_norm_are_exact(fa, rot, inter):
+    # rotation alone is products and sums in fp32, each rounded by itself: the
+    # codes are those of the same operations on the host. Enough keys that a
+    # contracted sum, which moves one group's step in 10^4, would show.
+    s = Case(fa, 6000, 3, 1, 8, 128, 16, rot, False, seed=3, q4=True)
+    fa.append_paged_q4(s.k, s.v, *s.cache, s.table, s.pos, s.req, s.cos, s.sin, interleaved=inter)
     x = s.k.float().cpu().numpy()
     cos, sin = (t.cpu().numpy()[s.pos_np][:, None] for t in (s.cos, s.sin))
-    a, b = x[..., :64], x[..., 64:]
-    y = np.concatenate([a * cos - b * sin, b * cos + a * sin], -1)
-    for t, blk, slot in s.slots():
-        codes, pairs = q4_encode(y[t])
-        assert np.array_equal(s.cache[0][blk, :, slot].cpu().numpy(), q4_pack(codes))
-        assert np.array_equal(to_f64(s.cache[1][blk, :, slot]), pairs)
+    i = np.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    y = x.copy()
+    y[..., a] = x[..., a] * cos - x[..., b] * sin
+    y[..., b] = x[..., b] * cos + x[..., a] * sin
+    slots = s.slots()
+    t, blk, slot = (np.array(c) for c in zip(*slots))
+    codes, pairs = q4_encode(y)
+    vcodes, vpairs = q4_encode(s.v.float().cpu().numpy())
+    for c, ref in zip(s.cache, (q4_pack(codes), pairs, q4_pack(vcodes), vpairs)):
+        got = c.float().cpu().numpy().transpose(0, 2, 1, *range(3, c.dim()))[blk, slot]
+        assert np.array_equal(got, ref[t].astype(np.float32))
 
 
 def test_q4_odd_groups(fa):
