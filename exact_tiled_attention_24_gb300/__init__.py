@@ -112,6 +112,7 @@ _HEADS, _TOKENS = "Pqqq", "Pqq"  # fa_heads, fa_tokens: address, strides
 _NORM_ROPE_ARGS = struct.Struct("@" + 4 * _HEADS + "5P10if")
 _NORM_ROPE_GRADS = struct.Struct("@" + 2 * _HEADS + "3PN")
 _APPEND_ARGS = struct.Struct("@" + 4 * _TOKENS + "13P12if")
+_DECODE_Q4_ARGS = struct.Struct("@10PN8if")
 
 
 class FAError(RuntimeError):
@@ -183,7 +184,7 @@ def lib() -> ctypes.CDLL:
         L.fa_append_paged_q4.restype = i
         L.fa_decode_q4_splits.argtypes = [i] * 5
         L.fa_decode_q4_splits.restype = i
-        L.fa_decode_paged_q4.argtypes = [vp] * 10 + [sz] + [i] * 7 + [f, i, vp]
+        L.fa_decode_paged_q4.argtypes = [vp, vp]
         L.fa_decode_paged_q4.restype = i
         L.fa_last_device_error.argtypes = [vp]
         L.fa_last_device_error.restype = i
@@ -206,8 +207,8 @@ def _ptr(t):
 def _stream(device):
     # the address behind torch.cuda.current_stream(device).cuda_stream,
     # without the stream object around it (2 us a call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
-        torch.cuda.current_device() if device.index is None else device.index))
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 # Device type of every tensor the kernels touch. The library launches on the
@@ -219,7 +220,7 @@ def _on_device(t, name):
     """Raise unless t is a tensor on a device the library can launch on."""
     if not isinstance(t, torch.Tensor) or t.device.type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a {_DEVICE_TYPE.upper()} tensor")
-    if _DEVICE_TYPE == "cuda" and t.device.index != torch.cuda.current_device():
+    if _DEVICE_TYPE == "cuda" and t.device.index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:"
                          f"{torch.cuda.current_device()}: call under torch.cuda.device({t.device})")
 
@@ -752,10 +753,11 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
 
 
 def _expect_cache(t, name, Hkv, last, dtype, device):
-    """Check one tensor [num_blocks, Hkv, block_size, *last] of a cache."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 + len(last):
-        raise ValueError(f"{name}: expected a tensor of {3 + len(last)} dimensions")
-    _expect(t, name, (t.shape[0], Hkv, t.shape[2], *last), dtype, device)
+    """Check one tensor [num_blocks, Hkv, block_size, last] of a cache."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name}: expected a tensor of four dimensions")
+    n, _, bs, _ = t.shape
+    _expect(t, name, (n, Hkv, bs, last), dtype, device)
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, cos=None, sin=None, q=None,
@@ -772,7 +774,7 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
     may be strided views, such as those of a packed projection."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
-    _expect_cache(k_cache, "k_cache", k.shape[1], (k.shape[2],), _BF16, k.device)
+    _expect_cache(k_cache, "k_cache", k.shape[1], k.shape[2], _BF16, k.device)
     _expect(v_cache, "v_cache", k_cache.shape, _BF16, k.device)
     return _append("fa_append_paged", k, v, (k_cache, v_cache), None, block_table, positions, requests, cos, sin, q,
                    q_weight, k_weight, eps, interleaved, q_out)
@@ -780,7 +782,7 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
 
 def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
     """Check a 4-bit cache's codes and (step, centre) pairs."""
-    _expect_cache(k_cache, "k_cache", Hkv, (d // 2,), _U8, device)
+    _expect_cache(k_cache, "k_cache", Hkv, d // 2, _U8, device)
     _expect(v_cache, "v_cache", k_cache.shape, _U8, device)
     pairs = (*k_cache.shape[:3], d // 64, 2)
     _expect(k_scale, "k_scale", pairs, _BF16, device)
@@ -834,25 +836,28 @@ def decode_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens
     max_blocks = block_table.shape[1]
     _expect(block_table, "block_table", (B, max_blocks), _I32, dev)
     _expect(seq_lens, "seq_lens", (B,), _I32, dev)
+    L = lib()
     if n_splits == 0:
-        n_splits = decode_q4_splits(B, H, Hkv, bs, max_blocks)
+        n_splits = L.fa_decode_q4_splits(B, H, Hkv, bs, max_blocks)
     wp = ws_bytes = 0
     if workspace is not None:
         _expect_workspace(workspace, dev)
-    elif n_splits > 1:
-        workspace = torch.empty(max(decode_workspace_bytes(B, H, d, n_splits), 16), dtype=_U8, device=dev)
-    if workspace is not None:
         wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif n_splits > 1:
+        ws_bytes = L.fa_decode_workspace_bytes(B, H, d, n_splits)
+        workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
+        wp = workspace.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
+        out = torch.empty_like(q)
     else:
         _expect(out, "out", shape, _BF16, dev)
     if lse is None:
         lse = torch.empty((B, H), dtype=_F32, device=dev)
     else:
         _expect(lse, "lse", (B, H), _F32, dev)
-    _check(lib().fa_decode_paged_q4(q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
-                                    v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                                    lse.data_ptr(), wp, ws_bytes, B, H, Hkv, d, num_blocks, bs, max_blocks,
-                                    _scale(d, scale), n_splits, _stream(dev)), "fa_decode_paged_q4")
+    args = _DECODE_Q4_ARGS.pack(
+        q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), wp, ws_bytes, B, H, Hkv, d,
+        num_blocks, bs, max_blocks, n_splits, _scale(d, scale))
+    _check(L.fa_decode_paged_q4(args, _stream(dev)), "fa_decode_paged_q4")
     return out, lse

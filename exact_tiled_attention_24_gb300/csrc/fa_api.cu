@@ -446,41 +446,40 @@ int fa_decode_q4_splits(int B, int H, int Hkv, int block_size, int max_blocks_pe
   return fa::decode_q4_splits(B, H, Hkv, static_cast<long long>(max_blocks_per_seq) * block_size);
 }
 
-int fa_decode_paged_q4(const void* q, const void* k_cache, const void* k_scale, const void* v_cache,
-                       const void* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse,
-                       void* workspace, size_t ws_bytes, int B, int H, int Hkv, int d, int num_blocks, int block_size,
-                       int max_blocks_per_seq, float scale, int n_splits, void* stream) {
-  if (!q || !k_cache || !k_scale || !v_cache || !v_scale || !block_table || !seq_lens || !o || !lse)
+int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream) {
+  if (!a || !a->q || !a->k_cache || !a->k_scale || !a->v_cache || !a->v_scale || !a->block_table || !a->seq_lens ||
+      !a->o || !a->lse)
     return FA_ERR_INVALID_ARG;
-  if (B < 1 || H < 1 || n_splits < 1) return FA_ERR_INVALID_ARG;
+  const int B = a->B, H = a->H, Hkv = a->Hkv, d = a->d, S = a->n_splits;
+  if (B < 1 || H < 1 || S < 1) return FA_ERR_INVALID_ARG;
   int st = check_heads(H, Hkv);
   if (st != FA_OK) return st;
-  if ((st = check_scale(scale)) != FA_OK) return st;
-  if ((st = check_cache(Hkv, num_blocks, block_size, max_blocks_per_seq)) != FA_OK) return st;
+  if ((st = check_scale(a->scale)) != FA_OK) return st;
+  if ((st = check_cache(Hkv, a->num_blocks, a->block_size, a->max_blocks_per_seq)) != FA_OK) return st;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if (B > 65535 || static_cast<long long>(Hkv) * ((H / Hkv + 7) / 8) > 65535 || n_splits > 4096)
-    return FA_ERR_UNSUPPORTED;
-  if (n_splits > 1 && (!workspace || ws_bytes < fa_decode_workspace_bytes(B, H, d, n_splits)))
-    return FA_ERR_WORKSPACE;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(k_scale) || !aligned16(v_cache) || !aligned16(v_scale) ||
-      !aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
-      (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
+  if (B > 65535 || static_cast<long long>(Hkv) * ((H / Hkv + 7) / 8) > 65535 || S > 4096) return FA_ERR_UNSUPPORTED;
+  if (S > 1 && (!a->workspace || a->ws_bytes < fa_decode_workspace_bytes(B, H, d, S))) return FA_ERR_WORKSPACE;
+  if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->k_scale) || !aligned16(a->v_cache) ||
+      !aligned16(a->v_scale) || !aligned16(a->o) || !aligned16(a->workspace) ||
+      ((reinterpret_cast<uintptr_t>(a->lse) | reinterpret_cast<uintptr_t>(a->block_table) |
+        reinterpret_cast<uintptr_t>(a->seq_lens)) & 3u))
     return FA_ERR_MISALIGNED;
-  const size_t rows = static_cast<size_t>(n_splits) * B * H;
   fa::DecodeQ4 p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = static_cast<const uint8_t*>(k_cache), p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.k_scale = static_cast<const uint32_t*>(k_scale), p.v_scale = static_cast<const uint32_t*>(v_scale);
-  p.block_table = block_table, p.seq_lens = seq_lens;
-  p.o = static_cast<__nv_bfloat16*>(o), p.lse = lse;
-  if (n_splits > 1) {
-    p.o_part = static_cast<float*>(workspace);
-    p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.k_cache = static_cast<const uint8_t*>(a->k_cache), p.v_cache = static_cast<const uint8_t*>(a->v_cache);
+  p.k_scale = static_cast<const uint32_t*>(a->k_scale), p.v_scale = static_cast<const uint32_t*>(a->v_scale);
+  p.block_table = a->block_table, p.seq_lens = a->seq_lens;
+  p.o = static_cast<__nv_bfloat16*>(a->o), p.lse = a->lse;
+  if (S > 1) {
+    const size_t rows = static_cast<size_t>(S) * B * H;
+    p.o_part = static_cast<float*>(a->workspace);
+    p.lse_part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) +
                                           ((rows * d * sizeof(float) + 255) & ~static_cast<size_t>(255)));
   }
-  p.B = B, p.H = H, p.Hkv = Hkv, p.num_blocks = num_blocks, p.bs = block_size, p.max_blocks = max_blocks_per_seq;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  return map_cuda(fa::launch_decode_q4(p, d, n_splits, static_cast<cudaStream_t>(stream)));
+  p.B = B, p.H = H, p.Hkv = Hkv;
+  p.num_blocks = a->num_blocks, p.bs = a->block_size, p.max_blocks = a->max_blocks_per_seq;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  return map_cuda(fa::launch_decode_q4(p, d, S, static_cast<cudaStream_t>(stream)));
 }
 
 int fa_selftest_wait_limit(void* stream) {

@@ -541,10 +541,24 @@ int fa_append_paged_q4(const fa_append_args* a, void* stream);
  * (a host function; 0 for invalid sizes).
  */
 int fa_decode_q4_splits(int B, int H, int Hkv, int block_size, int max_blocks_per_seq);
-int fa_decode_paged_q4(const void* q, const void* k_cache, const void* k_scale, const void* v_cache,
-                       const void* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse,
-                       void* workspace, size_t ws_bytes, int B, int H, int Hkv, int d, int num_blocks, int block_size,
-                       int max_blocks_per_seq, float scale, int n_splits, void* stream);
+typedef struct {
+  const void* q;       /* [B][H][d] bf16 */
+  const void* k_cache; /* the cache: codes and pairs */
+  const void* k_scale;
+  const void* v_cache;
+  const void* v_scale;
+  const int* block_table; /* [B][max_blocks_per_seq] */
+  const int* seq_lens;    /* [B] */
+  void* o;                /* [B][H][d] bf16, [B][H] fp32 */
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, d;
+  int num_blocks, block_size, max_blocks_per_seq;
+  int n_splits;
+  float scale;
+} fa_decode_q4_args;
+int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word set by

@@ -116,9 +116,11 @@ def test_decode_q4_refusals(L):
 
     def call(q=FAKE, kc=FAKE, ks=FAKE, vc=FAKE, vs=FAKE, table=FAKE, lens=FAKE, o=FAKE, lse=FAKE, work=FAKE,
              ws_bytes=ws, B=2, H=8, Hkv=2, d=128, num_blocks=10, bs=16, max_blocks=8, scale=0.1, S=4):
-        return L.fa_decode_paged_q4(q, kc, ks, vc, vs, table, lens, o, lse, work, ws_bytes, B, H, Hkv, d, num_blocks,
-                                    bs, max_blocks, scale, S, None)
+        args = fa._DECODE_Q4_ARGS.pack(q, kc, ks, vc, vs, table, lens, o, lse, work, ws_bytes, B, H, Hkv, d, num_blocks,
+                                       bs, max_blocks, S, scale)
+        return L.fa_decode_paged_q4(args, None)
 
+    assert L.fa_decode_paged_q4(None, None) == INVALID
     for name in ("q", "kc", "ks", "vc", "vs", "table", "lens", "o", "lse"):
         assert call(**{name: NUL}) == INVALID, name
     for bad in (dict(B=0), dict(H=0), dict(Hkv=0), dict(Hkv=3), dict(S=0), dict(bs=0), dict(num_blocks=0),
@@ -277,6 +279,7 @@ int main(void) {
   AT(fa_norm_rope_grads, dq_weight) AT(fa_norm_rope_grads, ws_bytes)
   AT(fa_append_args, q_out) AT(fa_append_args, k_cache) AT(fa_append_args, block_table) AT(fa_append_args, k_weight)
   AT(fa_append_args, T) AT(fa_append_args, n_pos) AT(fa_append_args, eps)
+  AT(fa_decode_q4_args, ws_bytes) AT(fa_decode_q4_args, B) AT(fa_decode_q4_args, n_splits) AT(fa_decode_q4_args, scale)
   return 0;
 }
 ''')
@@ -290,4 +293,5 @@ int main(void) {
     h, t = "Pqqq", "Pqq"
     a, b = 4 * h, 4 * t
     assert got == [at(2 * h), at(a), at(a + "4P"), at(a + "5P"), at(a + "5P9i"), at(a + "5P10i"), at(2 * h), at(2 * h + "3P"),
-                   at(3 * t), at(b), at(b + "6P"), at(b + "12P"), at(b + "13P"), at(b + "13P9i"), at(b + "13P12i")]
+                   at(3 * t), at(b), at(b + "6P"), at(b + "12P"), at(b + "13P"), at(b + "13P9i"), at(b + "13P12i"),
+                   at("10P"), at("10PN"), at("10PN7i"), at("10PN8i")]

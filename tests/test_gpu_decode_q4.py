@@ -4,11 +4,10 @@ that its codes stand for.
 Bounds. With p the softmax's weights (Σ p = 1) and v = z + s (n − 8), the
 kernel rounds each p s to bf16 (2^-8 relative) before the product with n − 8:
 at most 2^-8 Σ p |s (n − 8)|. The result is rounded to bf16 once: 2^-8 |o|.
-Scores are fp32 sums of at most 128 products |q| (16 + n) <= 31 |q| s and the
-same again taken off, under 2^9 roundings of 2^-24 (twice that where the
-tensor core truncates): a score is off by at most e = 2^-14 Σ|q| s · scale in
-natural units, so p by 2 e and o by 2 e max|v|; lse by e plus the logarithm's
-2^-20."""
+Scores are fp32 sums of at most 128 products |q (n − 8)| <= 8 |q|, scaled by
+s, under 2^7 roundings of 2^-24 (twice that where the tensor core truncates):
+a score is off by at most e = 2^-14 Σ|q| s · scale in natural units, so p by
+2 e and o by 2 e max|v|; lse by e plus the logarithm's 2^-20."""
 import numpy as np
 import pytest
 import torch
