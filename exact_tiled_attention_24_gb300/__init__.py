@@ -578,21 +578,31 @@ def _rows(t, name, shape, device, out=False):
     boundaries (for an output: no two rows overlapping); raises otherwise."""
     if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not _BF16 or t.device != device:
         raise ValueError(f"{name}: expected a {_BF16} tensor of shape {tuple(shape)} on {device}")
-    st = t.stride()
-    lead = st[:-1]
+    *lead, last = t.stride()
+    odd = 0
     for s in lead:
-        if s & 7:  # a dimension of one element has no stride to speak of
-            lead = tuple(s if n > 1 else 0 for s, n in zip(lead, shape))
-            break
-    if st[-1] != 1 or any([s & 7 for s in lead]):
-        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8")
+        odd |= s
+    if last != 1 or odd & 7:  # a dimension of one element has no stride to speak of
+        lead = [s if n > 1 else 0 for s, n in zip(lead, shape)]
+        if last != 1 or any([s & 7 for s in lead]):
+            raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8")
     if out and not t.is_contiguous():
         need = shape[-1]
         for s, n in sorted((s, n) for s, n in zip(lead, shape) if n > 1):
             if s < need:
                 raise ValueError(f"{name}: an output's rows must not overlap")
             need = s * n
-    return (t.data_ptr(), *lead)
+    return t.data_ptr(), *lead
+
+
+def _made(shape, device):
+    """A new contiguous bf16 tensor and its address and strides, as _rows gives them."""
+    t = torch.empty(shape, dtype=_BF16, device=device)
+    if len(shape) == 4:
+        _, H, N, d = shape
+        return t, (t.data_ptr(), H * N * d, N * d, d)
+    _, H, d = shape
+    return t, (t.data_ptr(), H * d, d)
 
 
 def _rope_args(cos, sin, q_weight, k_weight, d, device):
@@ -642,13 +652,10 @@ def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, in
     elif rot and n_pos < N:
         raise ValueError("cos and sin must have a row for every token")
     qr, kr = _rows(q, "q", qs, dev), _rows(k, "k", ks, dev)
-    if a is None:
-        a = torch.empty(qs, dtype=_BF16, device=dev)
-    if b is None:
-        b = torch.empty(ks, dtype=_BF16, device=dev)
-    return a, b, _NORM_ROPE_ARGS.pack(
-        *qr, *kr, *_rows(a, names[0], qs, dev, out), *_rows(b, names[1], ks, dev, out), *tables, pp, *weights, B, H,
-        Hkv, N, d, rot, n_pos, per_batch, w32, 1 if interleaved else 0, eps)
+    a, ar = _made(qs, dev) if a is None else (a, _rows(a, names[0], qs, dev, out))
+    b, br = _made(ks, dev) if b is None else (b, _rows(b, names[1], ks, dev, out))
+    return a, b, _NORM_ROPE_ARGS.pack(*qr, *kr, *ar, *br, *tables, pp, *weights, B, H, Hkv, N, d, rot, n_pos,
+                                      per_batch, w32, 1 if interleaved else 0, eps)
 
 
 def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -687,23 +694,22 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos=None, sin=None, positions=None, q
     _, _, args = _norm_rope_args(q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, eps, interleaved,
                                  ("dq_out", "dk_out"), False)
     dev = q.device
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=_BF16, device=dev)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=_BF16, device=dev)
+    dq, dqr = _made(q.shape, dev) if dq is None else (dq, _rows(dq, "dq", q.shape, dev, True))
+    dk, dkr = _made(k.shape, dev) if dk is None else (dk, _rows(dk, "dk", k.shape, dev, True))
     dqw = dkw = None
     wp = qp = kp = ws_bytes = 0
     if q_weight is not None:
         B, _, N, d = q.shape
         dqw, dkw = torch.empty((d,), dtype=_F32, device=dev), torch.empty((d,), dtype=_F32, device=dev)
         if workspace is None:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(B, N, d), dtype=_U8, device=dev)
+            ws_bytes = lib().fa_qk_norm_rope_bwd_workspace_bytes(B, N, d)
+            workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
         else:
             _expect_workspace(workspace, dev)
-        wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            ws_bytes = workspace.numel() * workspace.element_size()
+        wp = workspace.data_ptr()
         qp, kp = dqw.data_ptr(), dkw.data_ptr()
-    grads = _NORM_ROPE_GRADS.pack(*_rows(dq, "dq", q.shape, dev, True), *_rows(dk, "dk", k.shape, dev, True), qp, kp,
-                                  wp, ws_bytes)
+    grads = _NORM_ROPE_GRADS.pack(*dqr, *dkr, qp, kp, wp, ws_bytes)
     _check(lib().fa_qk_norm_rope_bwd(args, grads, _stream(dev)), "fa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
@@ -725,9 +731,7 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
         qr = _rows(q, "q", (T, H, d), dev)
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
-        if q_out is None:
-            q_out = torch.empty((T, H, d), dtype=_BF16, device=dev)
-        qor = _rows(q_out, "q_out", (T, H, d), dev, True)
+        q_out, qor = _made((T, H, d), dev) if q_out is None else (q_out, _rows(q_out, "q_out", (T, H, d), dev, True))
     elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out need q")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
