@@ -152,15 +152,21 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
   const int sections = is_k ? p.k_sections : p.q_sections;
   const Lane ln(threadIdx.x % LPR, p.rot);
   Row dw{};
-  if constexpr (NORM) {  // the weights stay in shared memory: registers are what limits the CTAs an SM
+  // The weights stay in shared memory (registers are what limits the CTAs an
+  // SM), quarter by quarter of a lane's 16, so that a row's lanes read
+  // consecutive 16 bytes.
+  if constexpr (NORM) {
     const void* w = is_k ? p.k_weight : p.q_weight;
-    if (threadIdx.x < D)
-      weight[threadIdx.x] = p.w32 ? reinterpret_cast<const float*>(w)[threadIdx.x]
-                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[threadIdx.x]);
+    for (int i = threadIdx.x; i < D; i += THREADS) {
+      const Lane of((i / 4) % LPR, p.rot);
+      const int quarter = i / (4 * LPR);
+      const int c = (quarter < 2 ? of.ca : of.cb) * 8 + (quarter & 1) * 4 + i % 4;
+      weight[i] = p.w32 ? reinterpret_cast<const float*>(w)[c]
+                        : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[c]);
+    }
     __syncthreads();
   }
-  const float* wa = weight + ln.ca * 8;
-  const float* wb = weight + ln.cb * 8;
+  const float* my_weight = weight + (threadIdx.x % LPR) * 4;
   const long long tiles = (static_cast<long long>(p.B) * p.N + ROWS - 1) / ROWS;
   for (long long item = part; item < tiles * sections; item += parts) {
     const int sec = static_cast<int>(item / tiles);
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
         // rest: at 128 registers a thread they cannot stay.
         float r, m;
         {
-          const Row xr = unpack(x), wt = shared_row(wa, wb);
+          const Row xr = unpack(x), wt = shared_row<4 * LPR>(my_weight);
           r = inv_rms<LPR>(xr, p.eps);
           m = row_sum<LPR>(dot(times(g, wt), xr)) * (1.f / D) * r;  // mean of h n
         }
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
           dwv = ffma2(gv, nv, dwv);
           gv = ffma2(fmul2(gv, wv), r2, fmul2(nv, rm));  // r (h − n m)
         };
-        const Row wt = shared_row(wa, wb);
+        const Row wt = shared_row<4 * LPR>(my_weight);
         const uint32_t xa[4] = {x.a.x, x.a.y, x.a.z, x.a.w}, xb[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

@@ -94,18 +94,19 @@ __device__ __forceinline__ void load_weight8(const void* w, bool w32, int chunk,
   }
 }
 
-// A lane's two chunks of a row of fp32 in shared memory, read each time.
-__device__ __forceinline__ void load_shared8(const float* p, float2* out) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(out[2 * i].x), "=f"(out[2 * i].y), "=f"(out[2 * i + 1].x), "=f"(out[2 * i + 1].y)
-                 : "r"(smem_u32(p + 4 * i)));
-}
-__device__ __forceinline__ Row shared_row(const float* a, const float* b) {
+// A lane's 16 fp32 values in shared memory, four by four STRIDE apart, read
+// each time.
+template <int STRIDE>
+__device__ __forceinline__ Row shared_row(const float* p) {
   Row x;
-  load_shared8(a, x.a);
-  load_shared8(b, x.b);
+  float2* out[2] = {x.a, x.b};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2* o = out[i >> 1] + 2 * (i & 1);
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(o[0].x), "=f"(o[0].y), "=f"(o[1].x), "=f"(o[1].y)
+                 : "r"(smem_u32(p + i * STRIDE)));
+  }
   return x;
 }
 
