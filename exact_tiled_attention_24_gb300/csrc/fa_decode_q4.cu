@@ -11,9 +11,9 @@
 // score accumulators and to the probabilities, in fp32.
 //
 // The step would be bound by reading the codes, d/2 + d/16 bytes a key or
-// value: at 6.8 TB/s an SM takes in 23 bytes a clock, 47 values, and each has
+// value: at 6.8 TB/s an SM takes in 21 bytes a clock, 38 values, and each has
 // to be turned into an operand. tcgen05 takes operands from shared memory or
-// TMEM, and writing 47 bf16 values a clock to shared memory and reading them
+// TMEM, and writing 38 bf16 values a clock to shared memory and reading them
 // back is more than its 128 bytes a clock. So a warp keeps them in registers:
 // mma.sync m16n8k16, whose A operand is 16 keys (scores) or 16 dimensions
 // (output) and whose 8 columns are query heads that share the K/V head.
@@ -29,13 +29,16 @@
 // cancel between the halves of a stage.
 //
 // What bounds it, measured (32 requests of 2k to 8k tokens, 8 K/V heads, d =
-// 128, 189 MB): 63 us with the merge, 37 us with the copies alone, 53 us with
-// the products alone on whatever the ring holds. A stage of 32 keys costs a
-// warp about 550 instructions, half of them on the integer pipe at two clocks
-// each, and 36 mma.sync, which hold their scheduler for some 7 clocks each
-// (timed apart: integer and tensor instructions of different warps add up,
-// they do not overlap). 12, 16 or 20 warps an SM, other stage orders and
-// scores one tile ahead of the output all measured within 5%, or slower.
+// 128, 189 MB): 69 us with the merge, where one cache is read again and again
+// 65; of those the copies alone take 37 and the products alone, on whatever
+// the ring holds, 53. A stage of 32 keys costs a warp about 640 instructions,
+// nearly half of them on the integer pipe at two clocks each, and 36 mma.sync
+// at 8 clocks of the tensor pipe each; fixed latencies between them keep the
+// schedulers to 54% of their issue slots. 12, 16 or 20 warps an SM, 16-key
+// steps and scores one tile ahead of the output all measured within 5%, or
+// slower; so did 8-bit products over the nibbles as they are (a byte n is
+// e4m3's n 2^-9), which the compiler expands into conversions and 16-bit
+// products: 77 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -750,10 +753,11 @@ static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
 }  // namespace decq4
 
 // Splits that fill the GPU: one wave of CTAs (three an SM) for one or two
-// requests, three waves for more, whose lengths differ (measured: two contexts
-// of 100k and 131k take 67.7 us at one wave, 76 at two; 32 of 2k to 8k 64.6 at
-// three, 91 at two). A split below 1024 keys costs more than it gives (16
-// requests of 1k to 8k tokens, 2 K/V heads: 21 us with 10 splits, 27 with 16).
+// requests, three waves for more, whose lengths differ (measured with the
+// cache read again and again: two contexts of 100k and 131k take 67.7 us at
+// one wave, 76 at two; 32 of 2k to 8k 64.6 at three, 91 at two). A split below
+// 1024 keys costs more than it gives (16 requests of 1k to 8k tokens, 2 K/V
+// heads: 21 us with 10 splits, 27 with 16).
 int decode_q4_splits(int B, int H, int Hkv, long long max_ctx) {
   const int G = H / Hkv, nh = G <= 8 ? 8 : 16;
   const long long pairs = static_cast<long long>(B) * Hkv * ((G + nh - 1) / nh);

@@ -129,7 +129,8 @@ __device__ __forceinline__ void grids(const rope::Row& x, const rope::Lane& ln, 
 // rounding. s has 8 significant bits, so d / s is never halfway between two
 // fp32 values and never nearer to it than 2^-9 of a last place: the rounded
 // sum is the rounded quotient. Far from the normal range's ends, that is:
-// below s = 2^-60 it is divided.
+// below s = 2^-60 it is divided. (16384 prompt tokens: 108 us with divisions,
+// 88 so.)
 __device__ __forceinline__ uint32_t encode8(const float2* x, const Grid& g, float2* n) {
   if (!(g.s > 0.f)) {
 #pragma unroll

@@ -45,7 +45,7 @@ __device__ __forceinline__ void forget(Raw& r) {
   asm volatile("" : "+r"(r.a.x), "+r"(r.a.y), "+r"(r.a.z), "+r"(r.a.w), "+r"(r.b.x), "+r"(r.b.y), "+r"(r.b.z), "+r"(r.b.w));
 }
 
-// Rows are read once and written once: past L1, and out of L2 first.
+// Rows are read once and written once: they are kept out of L1.
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

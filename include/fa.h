@@ -492,13 +492,14 @@ typedef struct {
  *              is both its cache slot and its row of the tables.
  *   requests   [T] device int32: each token's request (row of block_table);
  *              NULL: token t is request t's (a decode step; T <= B).
- * A token with a negative request or position is padding: nothing is read
- * or written for it, and its q_out row stays as it was. A request >= B, a
+ * A token with a negative request or position is padding: nothing is written
+ * for it (its input rows may hold anything), and its q_out row stays as it
+ * was. A request >= B, a
  * position past the table's blocks or (with rotation) past n_pos, and a
  * block outside [0, num_blocks) are never used as an index: the token is
  * skipped the same way and fa_last_device_error reports FA_ERR_BAD_INDEX.
- * Two tokens with one slot in one call: which of them it holds then is not
- * defined. A token's slot is what fa_decode_paged reads for seq_lens >
+ * Two tokens with one slot in one call: what it holds then is not defined
+ * (parts of either). A token's slot is what fa_decode_paged reads for seq_lens >
  * position, in order on the stream.
  * Errors: as fa_qk_norm_rope's (a norm of keys alone when q is NULL) and
  * fa_decode_paged's for the cache; neither weights nor rotation is allowed
@@ -535,8 +536,7 @@ int fa_append_paged_q4(const fa_append_args* a, void* stream);
  * number of query heads per K/V head. Values are never written out in full:
  * both products run on the codes. Workspace as for fa_decode_paged
  * (fa_decode_workspace_bytes), but NULL and 0 will do for n_splits = 1.
- * Slots past a request's length may hold
- * anything.
+ * Slots past a request's length may hold anything.
  * fa_decode_q4_splits gives an n_splits that fills the GPU for these sizes
  * (a host function; 0 for invalid sizes).
  */
