@@ -242,6 +242,30 @@ def test_other_stream_and_graph(fa):
         assert torch.equal(a, b)
 
 
+def test_gradients_that_share_a_workspace_or_run_at_once(fa):
+    """One workspace for call after call (the sum of one call's partial rows
+    against the next call's writes), then two streams at once with their own."""
+    def one(seed):
+        q, k, cos, sin, pos, qw, kw = case(2, 4, 2, 700, 128, 128, "packed", torch.bfloat16, "own", seed=seed)
+        g = [torch.randn((2, h, 700, 128), device="cuda").to(torch.bfloat16) for h in (4, 2)]
+        return lambda **ws: fa.qk_norm_rope_bwd(*g, q, k, cos, sin, positions=pos, q_weight=qw, k_weight=kw, **ws)
+    calls = [one(50 + i) for i in range(2)]
+    refs = [c() for c in calls]
+    torch.cuda.synchronize()
+    ws = torch.full((fa.qk_norm_rope_bwd_workspace_bytes(2, 700, 128),), 255, dtype=torch.uint8, device="cuda")
+    outs = [calls[i % 2](workspace=ws) for i in range(10)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(10):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(calls[i % 2]())
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        for x, y in zip(out, refs[i % 2]):
+            assert torch.equal(x, y)
+    assert fa.last_device_error() == 0
+
+
 def test_offsets_past_32_bits(fa):
     # a packed buffer of more than 2^31 elements: only its last rows are used
     H, d, N = 2, 64, 5
