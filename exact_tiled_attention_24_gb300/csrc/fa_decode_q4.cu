@@ -29,12 +29,13 @@
 // cancel between the halves of a stage.
 //
 // What bounds it, measured (32 requests of 2k to 8k tokens, 8 K/V heads, d =
-// 128, 189 MB): 69 us with the merge, where one cache is read again and again
-// 65; of those the copies alone take 37 and the products alone, on whatever
-// the ring holds, 53. A stage of 32 keys costs a warp about 640 instructions,
-// nearly half of them on the integer pipe at two clocks each, and 36 mma.sync
-// at 8 clocks of the tensor pipe each; fixed latencies between them keep the
-// schedulers to 54% of their issue slots. 12, 16 or 20 warps an SM, 16-key
+// 128, 189 MB): 70 us with the merge. Before probabilities went in as two
+// numbers (below) it was 69, where one cache is read again and again 65; of
+// those the copies alone took 37 and the products alone, on whatever the ring
+// holds, 53. A stage of 32 keys cost a warp about 640 instructions (with the
+// two numbers 40 more), nearly half of them on the integer pipe at two clocks
+// each, and 36 mma.sync at 8 clocks of the tensor pipe each; fixed latencies
+// between them kept the schedulers to 54% of their issue slots. 12, 16 or 20 warps an SM, 16-key
 // steps and scores one tile ahead of the output all measured within 5%, or
 // slower; so did 8-bit products over the nibbles as they are (a byte n is
 // e4m3's n 2^-9), which the compiler expands into conversions and 16-bit
@@ -192,13 +193,26 @@ struct Divide {
 // 16-byte pieces, each warp filling its own part of the tile.
 enum Fill : int { BULK = 0, GATHER = 1 };
 
-// One CTA: split s of request b's context, K/V head hk, 8·NT query heads.
-template <int D, int NT, int FILL>
+// One CTA: split s of request b's context, K/V head hk, NH query heads in
+// 8·NT columns of the products.
+//
+// A probability times a value's step, p s, goes into the output product as
+// two bf16 numbers, its rounding and what that leaves: 2^-16 of it is lost
+// (of one bf16 number 2^-8, by which the output was 1.35 times as far from 64
+// bits as its own rounding). With up to four query heads a K/V head (FOLD)
+// half of the columns would be empty: columns 4 .. 7 are the same heads again
+// and take the second part, so the products stay as many (the 32 requests of
+// the file's head: 69.4 us with one number, 70.2 so; two contexts of 100k and
+// 131k tokens 70.4 and 72.3). More heads take a second product for it (75 and
+// 80 us in those two cases; 16 requests of 1k to 8k tokens, one-token blocks,
+// 16 heads a K/V head: 24.8 us with one number, 28.6 so).
+template <int D, int NT, bool FOLD, int FILL>
 __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     decode_q4_kernel(const DecodeQ4 p, int run, Divide by_bs, Bases bases) {
   using R = Ring<D, NT>;
   constexpr int NG = D / 64;    // groups of a row
-  constexpr int NH = 8 * NT;    // query heads of the CTA
+  constexpr int NC = 8 * NT;    // columns
+  constexpr int NH = FOLD ? 4 : NC;  // query heads of the CTA
   constexpr int MT = D / 16;    // 16-dimension tiles of the output
   constexpr int ST = R::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -372,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   // power of two to a largest magnitude in [1, 2): fp16 then holds all that
   // counts of them exactly.
   uint32_t qf[NT][NG][4][2];
-  float qsum[NT][NG][2];  // Σ q of this lane's heads 2t, 2t + 1
+  float qsum[NT][NG][2];  // Σ q of this lane's columns 2t, 2t + 1
   float sc[NT][2];        // score units to log2 units
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -383,8 +397,9 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         v[gr][w] = make_uint4(0, 0, 0, 0);
-        const long long off = static_cast<long long>(head0 + nt * 8 + g) * D + gr * 64 + t * 16 + w * 8;
-        if (nt * 8 + g < G && in_range(off, 8, static_cast<long long>(p.B) * p.H * D, err))
+        const int h = FOLD ? g % NH : nt * 8 + g;
+        const long long off = static_cast<long long>(head0 + h) * D + gr * 64 + t * 16 + w * 8;
+        if (h < G && in_range(off, 8, static_cast<long long>(p.B) * p.H * D, err))
           v[gr][w] = *reinterpret_cast<const uint4*>(p.q + off);
         const uint32_t u[4] = {v[gr][w].x, v[gr][w].y, v[gr][w].z, v[gr][w].w};
 #pragma unroll
@@ -396,10 +411,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     e = e < -126 ? -126 : e > 126 ? 126 : e;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    // of head g; never 0, or a masked score's -inf would become NaN
+    // of column g; never 0, or a masked score's -inf would become NaN
     const float up = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, 1.17549435e-38f);
-    sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t);      // lanes of head 2t
-    sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);  // and of head 2t + 1
+    sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t);      // lanes of column 2t
+    sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);  // and of column 2t + 1
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
 #pragma unroll
@@ -428,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   // sums off at 24 bits). `fix` takes Σ ∓24, 23 p s of the same rounded p s,
   // what is left between the offsets and −8: one product for a group's four.
   float acc[NT][MT][4], fix[NT][NG][4];
-  // Per head: the exponents' reference in log2 units (0 while no key has been
+  // Per column: the exponents' reference in log2 units (0 while no key has been
   // seen), the score above which it is raised, and the running sums.
   float m[NT][2], lim[NT][2], l[NT][2], zc[NT][NG][2];
 #pragma unroll
@@ -451,6 +466,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     }
   }
 
+  // FOLD: the bytes of a pair's rounded numbers that are taken off its own
+  // (none in the columns of the first part), as fp32.
+  const uint32_t off_lo = FOLD && t < 2 ? 0x4444u : 0x1044u, off_hi = FOLD && t < 2 ? 0x4444u : 0x3244u;
+
   bool ok = true;
   int st = 0, stop = n;
   uint32_t phase = 0;
@@ -470,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     const uint8_t* kps = stage + R::KS + warp * TK * (D / 16);
     const uint8_t* vps = stage + R::VS + warp * TK * (D / 16);
 
-    // Scores: x[nt][u][2 r + e] is key 16 u + g + 8 r, head 2 t + e.
+    // Scores: x[nt][u][2 r + e] is key 16 u + g + 8 r, column 2 t + e.
     float x[NT][2][4];
     uint32_t vp[2][2][NG];  // the keys' value pairs
 #pragma unroll
@@ -574,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       // Probabilities, times the values' steps, as the output's B operand.
-      uint32_t pf[NT][NG][2];
+      uint32_t pf[NT][NG][2], pf2[NT][NG][2];  // pf2: the second parts of all heads, not FOLD
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
@@ -590,9 +609,14 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
             const float sv = u == 0 ? bf_lo(vp[u][r][gr]) : -bf_lo(vp[u][r][gr]), zv = bf_hi(vp[u][r][gr]);
             zc[nt][gr][0] = fmaf(pr[2 * r], zv, zc[nt][gr][0]);
             zc[nt][gr][1] = fmaf(pr[2 * r + 1], zv, zc[nt][gr][1]);
-            // bf16: its range takes any step, and the products' errors
-            // (2^-9 each) average out over the keys.
-            pf[nt][gr][r] = transpose8x8(pack_bf16x2(pr[2 * r] * sv, pr[2 * r + 1] * sv));
+            // (bf16 for its range: fp16 would need a reference of its own for
+            // the steps. A step times p <= 2^8 has to stay finite.)
+            const float p0 = pr[2 * r] * sv, p1 = pr[2 * r + 1] * sv;
+            const uint32_t rounded = pack_bf16x2(p0, p1);
+            const uint32_t left = pack_bf16x2(p0 - __uint_as_float(__byte_perm(rounded, 0u, off_lo)),
+                                              p1 - __uint_as_float(__byte_perm(rounded, 0u, off_hi)));
+            pf[nt][gr][r] = transpose8x8(FOLD ? left : rounded);
+            if (!FOLD) pf2[nt][gr][r] = transpose8x8(left);
           }
       }
       // Output: tile 4 gr + i has dimension 64 gr + 8 g + i in row g, + 4 in row g + 8.
@@ -621,10 +645,13 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         const uint32_t off[4] = {c, c, c, c};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t b0 = pf[nt][gr][0], b1 = pf[nt][gr][1];
+          auto products = [&](const uint32_t (&b)[2]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_bf16(acc[nt][4 * gr + i], a[i], b0, b1);
-          mma_bf16(fix[nt][gr], off, b0, b1);
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[nt][4 * gr + i], a[i], b[0], b[1]);
+            mma_bf16(fix[nt][gr], off, b[0], b[1]);
+          };
+          products(pf[nt][gr]);
+          if (!FOLD) products(pf2[nt][gr]);
         }
       }
     }
@@ -653,12 +680,12 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   }
 
   // The warps' results: Σ over the lanes that hold other keys, then one
-  // (m, l, o) per head and warp, in the ring (every copy has landed and been
+  // (m, l, o) per column and warp, in the ring (every copy has landed and been
   // read).
   constexpr int OROW = D + 1;
   auto sm_o = [&](int w) { return reinterpret_cast<float*>(smem + w * R::RESULT); };
-  auto sm_m = [&](int w) { return sm_o(w) + NH * OROW; };
-  auto sm_l = [&](int w) { return sm_m(w) + NH; };
+  auto sm_m = [&](int w) { return sm_o(w) + NC * OROW; };
+  auto sm_l = [&](int w) { return sm_m(w) + NC; };
   if (FILL == GATHER) {  // nothing may land after this
     cp_async_commit();
     cp_async_wait<0>();
@@ -668,24 +695,24 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int h = nt * 8 + 2 * t + e;
+      const int col = nt * 8 + 2 * t + e;
       float lv = l[nt][e];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, o);
       if (g == 0) {
-        sm_m(warp)[h] = m[nt][e];
-        sm_l(warp)[h] = lv;
+        sm_m(warp)[col] = m[nt][e];
+        sm_l(warp)[col] = lv;
       }
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float z = zc[nt][gr][e];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        z += fix[nt][gr][e];
+        z = (FOLD && t >= 2 ? 0.f : z) + fix[nt][gr][e];  // a head's centres count once
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = h * OROW + 64 * gr + 8 * g + i;
-          if (!in_range(at, 5, NH * OROW, err)) continue;
+          const int at = col * OROW + 64 * gr + 8 * g + i;
+          if (!in_range(at, 5, NC * OROW, err)) continue;
           sm_o(warp)[at] = acc[nt][4 * gr + i][e] + z;
           sm_o(warp)[at + 4] = acc[nt][4 * gr + i][e + 2] + z;
         }
@@ -694,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   __syncthreads();
   // One lane per head: the warps' weights e^(m_w − m) / Σ, behind the first
   // warp's result; then every thread sums a column of some heads.
-  float* weights = sm_m(0) + 2 * NH;  // [NH][WARPS]
+  float* weights = sm_m(0) + 2 * NC;  // [NH][WARPS]
   if (threadIdx.x < G) {
     const int h = threadIdx.x;
     float mm = -INFINITY;
@@ -720,7 +747,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   for (int h = threadIdx.x / D; h < G; h += THREADS / D) {
     float ov = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) ov = fmaf(weights[h * WARPS + w], sm_o(w)[h * OROW + c], ov);
+    for (int w = 0; w < WARPS; ++w) {
+      const float* o = sm_o(w) + h * OROW + c;
+      ov = fmaf(weights[h * WARPS + w], FOLD ? o[0] + o[NH * OROW] : o[0], ov);
+    }
     const long long at = (prow + h) * D + c;
     if (in_range(at, 1, part_rows * D, err)) {
       if (S == 1) p.o[at] = __float2bfloat16_rn(ov);
@@ -729,9 +759,9 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   }
 }
 
-template <int D, int NT, int FILL>
+template <int D, int NT, bool FOLD, int FILL>
 static cudaError_t launch_f(const DecodeQ4& p, int S, int run, cudaStream_t stream) {
-  auto kern = decode_q4_kernel<D, NT, FILL>;
+  auto kern = decode_q4_kernel<D, NT, FOLD, FILL>;
   const int smem = Ring<D, NT>::BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -746,8 +776,10 @@ static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
   int run = p.bs & -p.bs;  // slots of a block from a multiple of this on are contiguous for as many keys
   if (run > CK) run = CK;
   const bool bulk = run >= 8;
-  if (p.H / p.Hkv <= 8) return bulk ? launch_f<D, 1, BULK>(p, S, run, stream) : launch_f<D, 1, GATHER>(p, S, run, stream);
-  return bulk ? launch_f<D, 2, BULK>(p, S, run, stream) : launch_f<D, 2, GATHER>(p, S, run, stream);
+  const int G = p.H / p.Hkv;
+  if (G <= 4) return bulk ? launch_f<D, 1, true, BULK>(p, S, run, stream) : launch_f<D, 1, true, GATHER>(p, S, run, stream);
+  if (G <= 8) return bulk ? launch_f<D, 1, false, BULK>(p, S, run, stream) : launch_f<D, 1, false, GATHER>(p, S, run, stream);
+  return bulk ? launch_f<D, 2, false, BULK>(p, S, run, stream) : launch_f<D, 2, false, GATHER>(p, S, run, stream);
 }
 
 }  // namespace decq4
