@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
     };
     Raw dy, x, dy_next, x_next;
     load(h0, dy, x);
-    const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : 0;
+    const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : -1;
     Angles t;
     if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
 #pragma unroll 1
@@ -197,7 +197,14 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
       load(h + 1, dy_next, x_next);
       Row g = unpack(dy);
       if (ln.turned && pos >= 0) turn<true>(g, t, INTER);
-      if (pos < 0) g = Row{};  // the forward wrote a zero row: no gradient
+      // A row past the last token, or whose position the tables do not have
+      // (the forward wrote zeros), adds nothing to dw and has no gradient. Ones
+      // in place of x: a row of zeros has no finite r at eps = 0, and what the
+      // input holds there may be NaN.
+      if (pos < 0) {
+        g = Row{};
+        x.a = x.b = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+      }
       if (NORM) {
         // The sums first, then x unpacked and the weights read anew for the
         // rest: at 96 registers a thread they cannot stay.
