@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
         if (row[i] != NO_ROW) mine += bytes;
       }
       const uint32_t total = __reduce_add_sync(0xffffffffu, mine);
-      if (lane < WARPS) masks[st * WARPS + lane] = 0xffffffffu;
+      uint32_t present = 0xffffffffu;      // in lane w < WARPS: warp w's keys
       if (__any_sync(0xffffffffu, bad)) {  // blocks outside the cache: their keys are skipped
         if (bad) atomicExch(err, DEV_BAD_INDEX);
         for (int w = 0; w < WARPS; ++w) {
@@ -321,9 +321,10 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
               for (int k = max(k0, 0); k < min(k0 + run, 32); ++k) bits |= 1u << k;
           }
           bits = __reduce_or_sync(0xffffffffu, bits);
-          if (lane == 0) masks[st * WARPS + w] = bits;
+          if (lane == w) present = bits;
         }
       }
+      if (lane < WARPS) masks[st * WARPS + lane] = present;
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
       __syncwarp();
