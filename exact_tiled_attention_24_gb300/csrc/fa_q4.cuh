@@ -5,7 +5,7 @@
 //     s = bf16((b − a)/2 · (1/7.5)),  z = bf16((a + b)/2 + s/2),
 //     n = clamp(rint((x − z) / s) + 8, 0, 15)       (n = 8 where s = 0)
 // so the 16 levels span a .. b up to the rounding of s and z, and a value is
-// off by at most max(s/2, 2^-9 (|z| + 8 s)) (the second where the rounding
+// off by at most max(s/2, 2^-8 (|z| + 8 s)) (the second where the rounding
 // of z or s shifts the end levels by more than half a step). s and z are
 // bf16 because the values are: their range is bf16's (fp16 would overflow),
 // and the levels are then no coarser than bf16 values of that size. A group

@@ -518,7 +518,7 @@ int fa_append_paged(const fa_append_args* a, void* stream);
  *   s = bf16((b − a)/2 · fl32(1/7.5)), z = bf16((a + b)/2 + s/2),
  *   n = clamp(rint((x − z)/s) + 8, 0, 15), and 8 where s = 0,
  * in fp32, each operation rounded by itself. Each value held is off by at
- * most max(s/2, 2^-9 (|z| + 8 s)) beside fp32 rounding. A group with a value
+ * most max(s/2, 2^-8 (|z| + 8 s)) beside fp32 rounding. A group with a value
  * that is not finite is held as NaN.
  *
  * fa_append_paged_q4: fa_append_paged into such a cache.

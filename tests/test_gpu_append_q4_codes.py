@@ -47,3 +47,24 @@ def test_codes_of_normed_keys(fa, d, rot):  # noqa: F811
     codes, pairs = q4_encode(want)
     np.testing.assert_array_equal(cache[1][0, 0].float().cpu().numpy(), pairs)
     np.testing.assert_array_equal(cache[0][0, 0].cpu().numpy(), q4_pack(codes))
+
+
+def test_values_far_from_zero_are_within_the_bound(fa):  # noqa: F811
+    from oracle import q4_unpack, q4_values
+    from test_oracle_q4_bound import groups_far_from_zero
+    T = 400
+    x = groups_far_from_zero(np.random.default_rng(9), T)
+    v = torch.from_numpy(x).to(torch.bfloat16).cuda()[:, None]
+    cache = [t for _ in "kv" for t in (torch.zeros((1, 1, T, 64), dtype=torch.uint8, device="cuda"),
+                                       torch.zeros((1, 1, T, 2, 2), dtype=torch.bfloat16, device="cuda"))]
+    at = torch.arange(T, dtype=torch.int32, device="cuda")
+    fa.append_paged_q4(v, v, *cache, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), at, torch.zeros_like(at))
+    assert fa.last_device_error() == 0
+    codes, pairs = q4_encode(x)
+    for c, p in (cache[:2], cache[2:]):
+        np.testing.assert_array_equal(c[0, 0].cpu().numpy(), q4_pack(codes))
+        got = p[0, 0].double().cpu().numpy()
+        np.testing.assert_array_equal(got, pairs.astype(np.float64))
+        s, z = (got[..., i].repeat(64, -1) for i in (0, 1))
+        held = q4_values(q4_unpack(c[0, 0].cpu().numpy()), got)
+        assert np.all(np.abs(held - x) <= np.maximum(s / 2, 2.0 ** -8 * (np.abs(z) + 8 * s)) * (1 + 1e-5))
