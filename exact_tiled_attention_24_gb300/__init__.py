@@ -205,8 +205,9 @@ def _ptr(t):
 
 
 def _stream(device):
-    # the address behind torch.cuda.current_stream(device).cuda_stream,
-    # without the stream object around it (2 us a call)
+    # device: a torch.device. The address behind
+    # torch.cuda.current_stream(device).cuda_stream, without the stream object
+    # around it (2 us a call).
     index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
@@ -220,7 +221,7 @@ def _on_device(t, name):
     """Raise unless t is a tensor on a device the library can launch on."""
     if not isinstance(t, torch.Tensor) or t.device.type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a {_DEVICE_TYPE.upper()} tensor")
-    if _DEVICE_TYPE == "cuda" and t.device.index != torch._C._cuda_getDevice():
+    if _DEVICE_TYPE == "cuda" and t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:"
                          f"{torch.cuda.current_device()}: call under torch.cuda.device({t.device})")
 
@@ -371,7 +372,7 @@ def selftest_wait_limit(device=None) -> None:
     """Enqueue the error-path self-test on the current stream: a wait that
     nothing satisfies gives up after its limit, so the next
     last_device_error() returns 5 (FA_ERR_TIMEOUT)."""
-    dev = torch.device("cuda") if device is None else device
+    dev = torch.device("cuda" if device is None else device)
     _check(lib().fa_selftest_wait_limit(_stream(dev)), "fa_selftest_wait_limit")
 
 
@@ -382,7 +383,7 @@ def debug_checks() -> bool:
 
 def last_device_error(device=None) -> int:
     """Synchronise the current stream and return (and clear) the device error status."""
-    dev = torch.device("cuda") if device is None else device
+    dev = torch.device("cuda" if device is None else device)
     return int(lib().fa_last_device_error(_stream(dev)))
 
 
