@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
   // 64 gr + 16 t + 8 w + 0..7, K step 2 w + h (h = 0, 1) multiplies elements
   // (2h, 2h + 4), whose codes come as n − 8, and (2h + 1, 2h + 5), whose come
   // as 16 (n − 8): the latter's q carry the 1/16. A head's q are scaled by a
-  // power of two to a largest magnitude in [1, 2): fp16 then holds all that
-  // counts of them exactly.
+  // power of two to a largest magnitude in [1, 2): fp16 then holds elements
+  // down to 2^-13 of that (those without the 1/16: 2^-17) exactly, and smaller
+  // ones to within 2^-21 (2^-25) of it.
   uint32_t qf[NT][NG][4][2];
   float qsum[NT][NG][2];  // Σ q of this lane's columns 2t, 2t + 1
   float sc[NT][2];        // score units to log2 units
@@ -412,8 +413,9 @@ __global__ void __launch_bounds__(THREADS, (Ring<D, NT>::CTAS))
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     e = e < -126 ? -126 : e > 126 ? 126 : e;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    // of column g; never 0, or a masked score's -inf would become NaN
-    const float up = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, 1.17549435e-38f);
+    // of column g; never 0 (at least the smallest fp32 number), or a masked
+    // score's -inf would become NaN
+    const float up = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, __uint_as_float(1u));
     sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t);      // lanes of column 2t
     sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);  // and of column 2t + 1
 #pragma unroll

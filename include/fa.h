@@ -537,6 +537,9 @@ int fa_append_paged_q4(const fa_append_args* a, void* stream);
  * both products run on the codes. Workspace as for fa_decode_paged
  * (fa_decode_workspace_bytes), but NULL and 0 will do for n_splits = 1.
  * Slots past a request's length may hold anything.
+ * Scores, softmax and sums are fp32; a probability times a step is held to
+ * 2^-16 of it. Elements of q below 2^-13 of their head's largest are held to
+ * 2^-21 of that. Steps of values have to stay finite times 2^8 (up to 1e36).
  * fa_decode_q4_splits gives an n_splits that fills the GPU for these sizes
  * (a host function; 0 for invalid sizes).
  */
