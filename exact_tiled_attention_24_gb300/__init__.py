@@ -113,6 +113,7 @@ _NORM_ROPE_ARGS = struct.Struct("@" + 4 * _HEADS + "5P10if")
 _NORM_ROPE_GRADS = struct.Struct("@" + 2 * _HEADS + "3PN")
 _APPEND_ARGS = struct.Struct("@" + 4 * _TOKENS + "13P12if")
 _DECODE_Q4_ARGS = struct.Struct("@10PN8if")
+_ZERO_SKIPPED = 2  # FA_ZERO_SKIPPED
 
 
 class FAError(RuntimeError):
@@ -724,7 +725,7 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
     dev = k.device
     _on_device(k, "k")
     kr, vr = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
-    H, qr, qor = 0, (0, 0, 0), (0, 0, 0)
+    H, qr, qor, zero = 0, (0, 0, 0), (0, 0, 0), 0
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("expected q [T, H, d]")
@@ -732,7 +733,11 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
         qr = _rows(q, "q", (T, H, d), dev)
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
-        q_out, qor = _made((T, H, d), dev) if q_out is None else (q_out, _rows(q_out, "q_out", (T, H, d), dev, True))
+        if q_out is None:
+            q_out, qor = _made((T, H, d), dev)
+            zero = _ZERO_SKIPPED
+        else:
+            qor = _rows(q_out, "q_out", (T, H, d), dev, True)
     elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out need q")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -752,7 +757,7 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
     args = _APPEND_ARGS.pack(
         *qr, *kr, *vr, *qor, k_cache.data_ptr(), caches[-1 if len(caches) == 2 else 2].data_ptr(), ks, vs, kv, vv,
         block_table.data_ptr(), positions.data_ptr(), rp, *tables, *weights, T, B, H, Hkv, d, k_cache.shape[0],
-        k_cache.shape[2], max_blocks, rot, n_pos, w32, 1 if interleaved else 0, eps)
+        k_cache.shape[2], max_blocks, rot, n_pos, w32 | zero, 1 if interleaved else 0, eps)
     _check(getattr(lib(), entry)(args, _stream(dev)), entry)
     return q_out
 
@@ -775,8 +780,10 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
     request or position marks padding, which is skipped.
 
     With q [T, H, d] the tokens' queries get the same norm and rotation;
-    returns them ([T, H, d]: decode_paged's q), else None. k, v, q and q_out
-    may be strided views, such as those of a packed projection."""
+    returns them ([T, H, d]: decode_paged's q), else None. Rows of skipped
+    tokens are zeros in a q_out made here and stay as they were in a given one.
+    k, v, q and q_out may be strided views, such as those of a packed
+    projection."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
     _expect_cache(k_cache, "k_cache", k.shape[1], k.shape[2], _BF16, k.device)

@@ -402,8 +402,8 @@ static int append(const fa_append_args* a, bool q4, void* stream) {
   int st = check_cache(a->Hkv, a->num_blocks, a->block_size, a->max_blocks_per_seq);
   if (st != FA_OK) return st;
   if (a->d != 64 && a->d != 128) return FA_ERR_UNSUPPORTED;
-  if ((st = check_rope(a->cos, a->sin, a->d, a->rot, a->n_pos, a->q_weight, a->k_weight, a->weight_fp32, a->eps)) !=
-      FA_OK)
+  const int w32 = a->weight_fp32 & ~FA_ZERO_SKIPPED;
+  if ((st = check_rope(a->cos, a->sin, a->d, a->rot, a->n_pos, a->q_weight, a->k_weight, w32, a->eps)) != FA_OK)
     return st;
   if (a->H > 16384 || a->Hkv > 16384) return FA_ERR_UNSUPPORTED;
   if (!tokens_aligned(&a->k) || !tokens_aligned(&a->v) ||
@@ -429,7 +429,7 @@ static int append(const fa_append_args* a, bool q4, void* stream) {
   p.block_table = a->block_table, p.positions = a->positions, p.requests = a->requests;
   p.cos = a->cos, p.sin = a->sin;
   p.q_weight = a->q_weight, p.k_weight = a->k_weight;
-  p.w32 = a->weight_fp32 != 0, p.interleaved = a->interleaved != 0;
+  p.w32 = w32 != 0, p.interleaved = a->interleaved != 0, p.zero_skipped = (a->weight_fp32 & FA_ZERO_SKIPPED) != 0;
   p.T = a->T, p.B = a->B, p.H = queries ? a->H : 0, p.Hkv = a->Hkv;
   p.num_blocks = a->num_blocks, p.bs = a->block_size, p.max_blocks = a->max_blocks_per_seq;
   p.rot = a->rot, p.n_pos = a->n_pos;

@@ -122,7 +122,9 @@ __global__ void __launch_bounds__(THREADS, 5) append_kernel(const Append p) {
       if (turned) rope::turn<false>(x, ang, INTER);
       const bool mine = slot.live && h < h1;
       if (part == QUERIES) {
-        if (mine) store_chunks(p.q_out.p, p.q_out.extent, t * p.q_out.st + h * p.q_out.sh, ln, x, err);
+        const long long at = t * p.q_out.st + h * p.q_out.sh;
+        if (mine) store_chunks(p.q_out.p, p.q_out.extent, at, ln, x, err);
+        else if (p.zero_skipped && t < p.T && h < h1) store_chunks(p.q_out.p, p.q_out.extent, at, ln, Row{}, err);
         continue;
       }
       const long long row = row0 + static_cast<long long>(h) * p.bs;

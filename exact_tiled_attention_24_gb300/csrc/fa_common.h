@@ -119,7 +119,7 @@ struct Append {
   const float* sin;
   const void* q_weight;
   const void* k_weight;
-  bool w32, interleaved;
+  bool w32, interleaved, zero_skipped;
   int T, B, H, Hkv, num_blocks, bs, max_blocks, rot, n_pos;
   float eps;
   int q_sections, kv_sections;  // set by the launcher: parts that the heads are cut into

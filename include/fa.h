@@ -455,6 +455,7 @@ size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d);
 int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream);
 
 /* Arguments of an append to a paged cache. Unused ones are 0. */
+#define FA_ZERO_SKIPPED 2
 typedef struct {
   fa_tokens q, k, v, q_out; /* [T][H][d], [T][Hkv][d]; q.ptr NULL: no queries */
   void* k_cache;
@@ -473,7 +474,8 @@ typedef struct {
   int T, B, H, Hkv, d;
   int num_blocks, block_size, max_blocks_per_seq;
   int rot, n_pos;
-  int weight_fp32; /* 1: the weights are fp32 */
+  int weight_fp32; /* 1: the weights are fp32; plus FA_ZERO_SKIPPED: zeros go to
+                      the q_out rows of skipped tokens */
   int interleaved;
   float eps;
 } fa_append_args;
@@ -494,10 +496,10 @@ typedef struct {
  *              NULL: token t is request t's (a decode step; T <= B).
  * A token with a negative request or position is padding: nothing is written
  * for it (its input rows may hold anything), and its q_out row stays as it
- * was. A request >= B, a
- * position past the table's blocks or (with rotation) past n_pos, and a
- * block outside [0, num_blocks) are never used as an index: the token is
- * skipped the same way and fa_last_device_error reports FA_ERR_BAD_INDEX.
+ * was (with FA_ZERO_SKIPPED it gets zeros). A request >= B, a position past
+ * the table's blocks or (with rotation) past n_pos, and a block outside
+ * [0, num_blocks) are never used as an index: the token is skipped the same
+ * way and fa_last_device_error reports FA_ERR_BAD_INDEX.
  * Two tokens with one slot in one call: what it holds then is not defined
  * (parts of either). A token's slot is what fa_decode_paged reads for seq_lens >
  * position, in order on the stream.
