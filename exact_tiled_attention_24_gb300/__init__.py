@@ -808,7 +808,8 @@ def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, posit
     [num_blocks, Hkv, block_size, d/2] uint8 codes and k_scale, v_scale
     [num_blocks, Hkv, block_size, d/64, 2] bf16 (step, centre) of each group
     of 64 dimensions (see fa_append_paged_q4). k_values, v_values [T, Hkv, d]
-    bf16, if given, receive the values that the cache now holds."""
+    bf16, contiguous, if given, receive the values that the cache now holds
+    (fwd takes them as [B, Hkv, N, d]: transposed and copied)."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
     _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, k.shape[1], k.shape[2], k.device)

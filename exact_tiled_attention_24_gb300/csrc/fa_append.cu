@@ -10,7 +10,9 @@
 //
 // 16384 prompt tokens of 32 + 8 + 8 heads, d = 128: 70 us into a bf16 cache
 // (86% of the measured copy rate), 86 us into 4-bit codes with the values held
-// written beside them (73%: the integer pipe is at 46% then, DRAM at 59%). A
+// written beside them (73%: the integer pipe is at 46% then, DRAM at 59%, and
+// neither is full: one body for queries, keys and values keeps weights, angles
+// and four heads' loads, and spills 28 to 36 bytes a thread). A
 // decode step of 32 tokens takes 6 to 7 us, a chain of dependent loads
 // (position, block table, angles) and one launch.
 #include <cuda_bf16.h>

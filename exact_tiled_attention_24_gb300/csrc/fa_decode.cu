@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<GM>::CTAS) decode_mma_kernel(
       // tiles arrive zero-filled). The scores run a tile ahead, so V_{j-1} may
       // not have landed yet: O_{j-1} first (exact, as above), after which
       // v_full is at phase j or past it and its parity wait is exact too.
+      // (32 requests of 2k to 8k tokens: 114.8 us with this and without.)
       if (LOAD == BOXES && (tile0 + j + 1) * TK > t_end) {
         const int vs = j % VST;
         if (ok && j > 0) ok = mbar_wait(o_done, (j - 1) & 1, err);

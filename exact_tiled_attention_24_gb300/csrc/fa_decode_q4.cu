@@ -787,12 +787,23 @@ static cudaError_t launch(const DecodeQ4& p, int S, cudaStream_t stream) {
 
 }  // namespace decq4
 
-// Splits that fill the GPU: one wave of CTAs (three an SM) for one or two
-// requests, three waves for more, whose lengths differ (measured with the
-// cache read again and again: two contexts of 100k and 131k take 67.7 us at
-// one wave, 76 at two; 32 of 2k to 8k 64.6 at three, 91 at two). A split below
-// 1024 keys costs more than it gives (16 requests of 1k to 8k tokens, 2 K/V
-// heads: 21 us with 10 splits, 27 with 16).
+// Splits that fill the GPU. CTAs come three (with more than eight query heads a
+// K/V head two) to an SM; the rule takes one wave of them for one or two
+// requests and three waves for more, whose lengths the host does not know, and
+// no split below 1024 keys. GPU time in us by splits, the rule's in brackets:
+//     32 requests of 2k to 8k tokens, 8 K/V heads   2: 80   [5: 71]  10: 74  15: 79
+//     16 of 1k to 8k, 2 K/V heads of 16 heads       4: 38   [8: 29]  10: 27  16: 31
+//     1 of 131k, 8 K/V heads                        28: 68  [57: 55] 85: 74  114: 71
+//     2 of 100k and 131k                            14: 98  [28: 72] 42: 91  56: 82
+//     2 of 1k and 131k                              14: 97  [28: 72] 42: 68  56: 60
+//     3 of 87k                                      28: 106 [57: 99] 85: 112
+//     3 of 1k to 131k                               28: 80  [57: 80] 85: 90
+//     4 of 16k, 2 K/V heads                         8: 27   [16: 20] 32: 18  64: 25
+//     1 of 8k, 1 K/V head                           4: 27   [8: 19]  16: 14  32: 14
+//     3 of up to 700, 12 K/V heads, d = 64          [1: 12.3] 2: 11.7  3: 11.6  6: 10.3
+// So it misses where lengths are very uneven in two requests and where few CTAs
+// have short contexts: the limit of 1024 keys is for GPUs that are full already.
+// It does not look at d, though four CTAs an SM run at d = 64.
 int decode_q4_splits(int B, int H, int Hkv, long long max_ctx) {
   const int G = H / Hkv, nh = G <= 8 ? 8 : 16;
   const long long pairs = static_cast<long long>(B) * Hkv * ((G + nh - 1) / nh);

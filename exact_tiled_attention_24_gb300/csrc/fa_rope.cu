@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
 // items (a row of lanes' token, a section of the heads) of its tensor with
 // its lanes' 16 dimensions of dw in registers and the next row on its way,
 // then sums them over its rows in a fixed order into one partial row.
-constexpr int MAX_PARTS = 760;  // five CTAs an SM (95 us; four and 608 parts: 103)
+// Five CTAs an SM leave 96 registers a thread, and with a norm 72 to 104 bytes
+// a thread are spilled; still 95 us (four CTAs and 608 parts: 103).
+constexpr int MAX_PARTS = 760;
 template <int D, bool NORM, bool INTER>
 __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRope p, int parts_q,
                                                                    float* __restrict__ partial) {

@@ -383,7 +383,8 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, con
  *             (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0;
  *             dimensions rot .. d-1 are left as they are. rot is a multiple
  *             of 16, at most d; rot = 0: no rotation (cos, sin unused).
- *   Values are fp32 from the loads to one rounding of the result.
+ *   Values are fp32 from the loads to one rounding of the result (a row whose
+ *   sum of squares passes fp32's range, |x| past 2^60, has r = 0).
  *
  * A bf16 tensor [B][heads][N][d] whose last dimension is contiguous; the
  * other strides in elements, not negative, multiples of 8 (16 bytes), e.g. a
@@ -525,10 +526,11 @@ int fa_append_paged(const fa_append_args* a, void* stream);
  *
  * fa_append_paged_q4: fa_append_paged into such a cache.
  *   k_values, v_values  [T][Hkv][d] bf16 outputs, both or neither (NULL):
- *                       the values held for the new tokens, rounded to bf16,
- *                       e.g. for a prompt's own attention over what later
- *                       steps will read. Rows of skipped tokens stay as they
- *                       were.
+ *                       the values held for the new tokens, rounded to bf16:
+ *                       what later steps will read. Contiguous, token by
+ *                       token; fa_fwd takes [B][Hkv][N][d], so a prompt's
+ *                       attention over them needs a transposed copy first.
+ *                       Rows of skipped tokens stay as they were.
  */
 int fa_append_paged_q4(const fa_append_args* a, void* stream);
 
