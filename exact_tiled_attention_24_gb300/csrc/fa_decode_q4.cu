@@ -14,8 +14,9 @@
 // value: at 6.8 TB/s an SM takes in 21 bytes a clock, 38 values, and each has
 // to be turned into an operand. tcgen05 takes operands from shared memory or
 // TMEM, and writing 38 bf16 values a clock to shared memory and reading them
-// back is more than its 128 bytes a clock. So a warp keeps them in registers:
-// mma.sync m16n8k16, whose A operand is 16 keys (scores) or 16 dimensions
+// back, 153 bytes, is more than its 128 bytes a clock (one-byte operands, a
+// code as e4m3's n 2^-9, would be 77; not built). So a warp keeps them in
+// registers: mma.sync m16n8k16, whose A operand is 16 keys (scores) or 16 dimensions
 // (output) and whose 8 columns are query heads that share the K/V head.
 //   scores  Sᵀ[key][head]: rows g and g + 8 of a tile are keys; the words of
 //           a key's row go to the lane quarter t that needs them as they are
@@ -29,17 +30,18 @@
 // cancel between the halves of a stage.
 //
 // What bounds it, measured (32 requests of 2k to 8k tokens, 8 K/V heads, d =
-// 128, 189 MB): 70 us with the merge. Before probabilities went in as two
-// numbers (below) it was 69, where one cache is read again and again 65; of
-// those the copies alone took 37 and the products alone, on whatever the ring
-// holds, 53. A stage of 32 keys cost a warp about 640 instructions (with the
-// two numbers 40 more), nearly half of them on the integer pipe at two clocks
-// each, and 36 mma.sync at 8 clocks of the tensor pipe each; fixed latencies
-// between them kept the schedulers to 54% of their issue slots. 12, 16 or 20 warps an SM, 16-key
-// steps and scores one tile ahead of the output all measured within 5%, or
-// slower; so did 8-bit products over the nibbles as they are (a byte n is
-// e4m3's n 2^-9), which the compiler expands into conversions and 16-bit
-// products: 77 us.
+// 128, 189 MB): 70 us with the merge. A stage of 32 keys costs a warp about
+// 690 instructions, nearly half of them on the integer pipe at two clocks
+// each, and 36 mma.sync at 8 clocks of the tensor pipe each. No pipe is full
+// (integer 52%, tensor 19%, DRAM 38%): at 12 warps an SM the latencies between
+// dependent steps keep the schedulers to 46% of their issue slots. Before
+// probabilities went in as two numbers (below) the step took 69 us, and where
+// one cache is read again and again 65; of those the copies alone took 37 and
+// the products alone, on whatever the ring holds, 53. At that time 12, 16 or
+// 20 warps an SM, 16-key steps and scores one tile ahead of the output all
+// measured within 5%, or slower; so did 8-bit products over the nibbles as they
+// are (a byte n is e4m3's n 2^-9), which the compiler expands into conversions
+// and 16-bit products: 77 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -144,6 +144,8 @@ __device__ __forceinline__ uint32_t encode8(const float2* x, const Grid& g, floa
     const float2 y2 = make_float2(y, y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      // (A normed key's product with its weight reaches here through the
+      // rotation's branch, so it is rounded before this difference.)
       const float2 d = fsub2(x[e], z2), q = fmul2(d, y2);
       n[e] = ffma2(ffma2(q, s2, d), y2, q);
     }
