@@ -44,6 +44,9 @@ __all__ = [
     "append_paged_q4",
     "decode_paged_q4",
     "decode_q4_splits",
+    "extend_paged",
+    "extend_paged_q4",
+    "extend_workspace_bytes",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -98,6 +101,9 @@ EXPORTED_SYMBOLS = (
     "fa_append_paged_q4",
     "fa_decode_q4_splits",
     "fa_decode_paged_q4",
+    "fa_extend_workspace_bytes",
+    "fa_extend_paged",
+    "fa_extend_paged_q4",
 )
 
 
@@ -113,6 +119,7 @@ _NORM_ROPE_ARGS = struct.Struct("@" + 4 * _HEADS + "5P10if")
 _NORM_ROPE_GRADS = struct.Struct("@" + 2 * _HEADS + "3PN")
 _APPEND_ARGS = struct.Struct("@" + 4 * _TOKENS + "13P12if")
 _DECODE_Q4_ARGS = struct.Struct("@10PN8if")
+_EXTEND_ARGS = struct.Struct("@11PN10if")
 _ZERO_SKIPPED = 2  # FA_ZERO_SKIPPED
 
 
@@ -187,6 +194,12 @@ def lib() -> ctypes.CDLL:
         L.fa_decode_q4_splits.restype = i
         L.fa_decode_paged_q4.argtypes = [vp, vp]
         L.fa_decode_paged_q4.restype = i
+        L.fa_extend_workspace_bytes.argtypes = [i] * 7
+        L.fa_extend_workspace_bytes.restype = sz
+        L.fa_extend_paged.argtypes = [vp, vp]
+        L.fa_extend_paged.restype = i
+        L.fa_extend_paged_q4.argtypes = [vp, vp]
+        L.fa_extend_paged_q4.restype = i
         L.fa_last_device_error.argtypes = [vp]
         L.fa_last_device_error.restype = i
         L.fa_selftest_wait_limit.argtypes = [vp]
@@ -874,3 +887,85 @@ def decode_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens
         num_blocks, bs, max_blocks, n_splits, _scale(d, scale))
     _check(L.fa_decode_paged_q4(args, _stream(dev)), "fa_decode_paged_q4")
     return out, lse
+
+
+def extend_workspace_bytes(T, B, H, Hkv, d, block_size, max_blocks) -> int:
+    return int(lib().fa_extend_workspace_bytes(T, B, H, Hkv, d, block_size, max_blocks))
+
+
+def _extend(entry, q, caches, block_table, seq_lens, q_starts, causal, scale, workspace, out, lse):
+    """Check a chunk call's arguments (the caches' own by the caller) and call it."""
+    T, H, d = shape = q.shape
+    dev = q.device
+    _on_device(q, "q")
+    _expect(q, "q", shape, _BF16, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks] int32")
+    B, max_blocks = block_table.shape
+    _expect(block_table, "block_table", (B, max_blocks), _I32, dev)
+    _expect(seq_lens, "seq_lens", (B,), _I32, dev)
+    _expect(q_starts, "q_starts", (B + 1,), _I32, dev)
+    num_blocks, Hkv, bs, _ = caches[0].shape
+    L = lib()
+    if workspace is None:
+        ws_bytes = L.fa_extend_workspace_bytes(T, B, H, Hkv, d, bs, max_blocks)
+        workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
+    else:
+        _expect_workspace(workspace, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    zero = out is None and lse is None
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect(out, "out", shape, _BF16, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=_F32, device=dev)
+    else:
+        _expect(lse, "lse", (T, H), _F32, dev)
+    kc, ks, vc, vs = ((caches[0].data_ptr(), 0, caches[1].data_ptr(), 0) if len(caches) == 2
+                      else [t.data_ptr() for t in caches])
+    args = _EXTEND_ARGS.pack(
+        q.data_ptr(), kc, ks, vc, vs, block_table.data_ptr(), seq_lens.data_ptr(), q_starts.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), ws_bytes, T, B, H, Hkv, d, num_blocks, bs, max_blocks,
+        1 if causal else 0, 1 if zero else 0, _scale(d, scale))
+    _check(getattr(L, entry)(args, _stream(dev)), entry)
+    return out, lse
+
+
+def extend_paged(q, k_cache, v_cache, block_table, seq_lens, q_starts, causal=True, scale=None, workspace=None,
+                 out=None, lse=None):
+    """Attention of chunks of new tokens over a paged cache: q [T, H, d] bf16
+    (append_paged's queries), request after request; request b's tokens are
+    rows q_starts[b] .. q_starts[b + 1] - 1 (int32 [B + 1]) and the last of its
+    seq_lens[b] cached tokens (int32 [B], the new ones included). A token sees
+    the keys up to its own position, or with causal=False all of its request's.
+    Caches and block_table as in decode_paged; the workspace is
+    extend_workspace_bytes(...) bytes. Returns (o [T, H, d] bf16, lse [T, H]
+    fp32).
+
+    Rows of no request (before q_starts[0], from q_starts[B] on) are o = 0, lse
+    = -inf where both outputs are made here and stay as they were where either
+    is given. The lengths are read on the device: a captured call may be
+    replayed with others."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("expected q [T, H, d]")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
+    _expect_cache(k_cache, "k_cache", k_cache.shape[1], q.shape[2], _BF16, q.device)
+    _expect(v_cache, "v_cache", k_cache.shape, _BF16, q.device)
+    return _extend("fa_extend_paged", q, (k_cache, v_cache), block_table, seq_lens, q_starts, causal, scale, workspace,
+                   out, lse)
+
+
+def extend_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, q_starts, causal=True, scale=None,
+                    workspace=None, out=None, lse=None):
+    """extend_paged over a cache held in 4 bits (append_paged_q4's). Keys and
+    values are read back in bf16, rounded once: what append_paged_q4 hands out
+    as k_values and v_values."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("expected q [T, H, d]")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d/2] uint8")
+    _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, k_cache.shape[1], q.shape[2], q.device)
+    return _extend("fa_extend_paged_q4", q, (k_cache, k_scale, v_cache, v_scale), block_table, seq_lens, q_starts,
+                   causal, scale, workspace, out, lse)

@@ -482,13 +482,73 @@ int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream) {
   return map_cuda(fa::launch_decode_q4(p, d, S, static_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------- chunks over a paged cache
+
+// Checks the sizes of a chunk call and fills p's.
+static int extend_sizes_ok(fa::Extend* p, int T, int B, int H, int Hkv, int d, int block_size, int max_blocks) {
+  if (T < 1 || B < 1 || H < 1) return FA_ERR_INVALID_ARG;
+  int st = check_heads(H, Hkv);
+  if (st != FA_OK) return st;
+  if ((st = check_cache(Hkv, 1, block_size, max_blocks)) != FA_OK) return st;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  // rows and tokens are indexed in 32 bits
+  if (static_cast<long long>(T) * H > INT_MAX || T > (1 << 30) || B > (1 << 24) || H / Hkv > 16384)
+    return FA_ERR_UNSUPPORTED;
+  p->T = T, p->B = B, p->H = H, p->Hkv = Hkv, p->bs = block_size, p->max_blocks = max_blocks;
+  return FA_OK;
+}
+
+size_t fa_extend_workspace_bytes(int T, int B, int H, int Hkv, int d, int block_size, int max_blocks_per_seq) {
+  size_t most = 0;
+  for (int q4 = 0; q4 < 2; ++q4) {
+    fa::Extend p{};
+    if (extend_sizes_ok(&p, T, B, H, Hkv, d, block_size, max_blocks_per_seq) != FA_OK) return 0;
+    const size_t bytes = fa::extend_sizes(&p, d, q4 != 0);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
+static int extend(const fa_extend_args* a, bool q4, void* stream) {
+  if (!a || !a->q || !a->k_cache || !a->v_cache || !a->block_table || !a->seq_lens || !a->q_starts || !a->o || !a->lse)
+    return FA_ERR_INVALID_ARG;
+  if (q4 && (!a->k_scale || !a->v_scale)) return FA_ERR_INVALID_ARG;
+  fa::Extend p{};
+  int st = extend_sizes_ok(&p, a->T, a->B, a->H, a->Hkv, a->d, a->block_size, a->max_blocks_per_seq);
+  if (st != FA_OK) return st;
+  if ((st = check_scale(a->scale)) != FA_OK) return st;
+  if ((st = check_cache(a->Hkv, a->num_blocks, a->block_size, a->max_blocks_per_seq)) != FA_OK) return st;
+  // a block's K/V head is one coordinate of the copies' tensor
+  if (static_cast<long long>(a->num_blocks) * a->Hkv > INT_MAX - 1) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa::extend_sizes(&p, a->d, q4);
+  if (!a->workspace || a->ws_bytes < need) return FA_ERR_WORKSPACE;
+  if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->o) ||
+      !aligned16(a->workspace) || (q4 && (!aligned16(a->k_scale) || !aligned16(a->v_scale))) ||
+      ((reinterpret_cast<uintptr_t>(a->lse) | reinterpret_cast<uintptr_t>(a->block_table) |
+        reinterpret_cast<uintptr_t>(a->seq_lens) | reinterpret_cast<uintptr_t>(a->q_starts)) & 3u))
+    return FA_ERR_MISALIGNED;
+  p.k_cache = a->k_cache, p.v_cache = a->v_cache;
+  p.k_scale = static_cast<const uint32_t*>(a->k_scale), p.v_scale = static_cast<const uint32_t*>(a->v_scale);
+  p.block_table = a->block_table, p.seq_lens = a->seq_lens, p.q_starts = a->q_starts;
+  p.o = static_cast<__nv_bfloat16*>(a->o), p.lse = a->lse;
+  p.o_part = static_cast<float*>(a->workspace);
+  p.lse_part = p.o_part + static_cast<size_t>(p.n_slots) * 256 * a->d;
+  p.num_blocks = a->num_blocks;
+  p.causal = a->causal != 0, p.zero_skipped = a->zero_skipped != 0;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  return map_cuda(fa::launch_extend(p, a->q, a->d, q4, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_extend_paged(const fa_extend_args* a, void* stream) { return extend(a, false, stream); }
+int fa_extend_paged_q4(const fa_extend_args* a, void* stream) { return extend(a, true, stream); }
+
 int fa_selftest_wait_limit(void* stream) {
   return map_cuda(fa::launch_wait_limit_selftest(static_cast<cudaStream_t>(stream)));
 }
 
 int fa_last_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t ef = 0, eb = 0, ed = 0, et = 0, es = 0, er = 0, ea = 0, eq = 0;
+  uint32_t ef = 0, eb = 0, ed = 0, et = 0, es = 0, er = 0, ea = 0, eq = 0, ex = 0;
   if (fa::read_and_clear_fwd_error(&ef, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::read_and_clear_bwd_error(&eb, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::read_and_clear_decode_error(&ed, s) != cudaSuccess) return FA_ERR_CUDA;
@@ -497,10 +557,11 @@ int fa_last_device_error(void* stream) {
   if (fa::read_and_clear_rope_error(&er, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::read_and_clear_append_error(&ea, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::read_and_clear_decode_q4_error(&eq, s) != cudaSuccess) return FA_ERR_CUDA;
-  if (ef == 1 || eb == 1 || ed == 1 || et == 1 || eq == 1) return FA_ERR_TIMEOUT;
-  if (ef == 3 || eb == 3 || ed == 3 || es == 3 || er == 3 || ea == 3 || eq == 3) return FA_ERR_BOUNDS;
-  if (ed == 2 || er == 2 || ea == 2 || eq == 2) return FA_ERR_BAD_INDEX;
-  if (ef || eb || ed || et || es || er || ea || eq) return FA_ERR_TIMEOUT;
+  if (fa::read_and_clear_extend_error(&ex, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (ef == 1 || eb == 1 || ed == 1 || et == 1 || eq == 1 || ex == 1) return FA_ERR_TIMEOUT;
+  if (ef == 3 || eb == 3 || ed == 3 || es == 3 || er == 3 || ea == 3 || eq == 3 || ex == 3) return FA_ERR_BOUNDS;
+  if (ed == 2 || er == 2 || ea == 2 || eq == 2 || ex == 2) return FA_ERR_BAD_INDEX;
+  if (ef || eb || ed || et || es || er || ea || eq || ex) return FA_ERR_TIMEOUT;
   return FA_OK;
 }
 

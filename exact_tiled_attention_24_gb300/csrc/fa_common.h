@@ -145,6 +145,31 @@ struct DecodeQ4 {
 int decode_q4_splits(int B, int H, int Hkv, long long max_ctx);
 cudaError_t launch_decode_q4(const DecodeQ4& p, int d, int S, cudaStream_t stream);
 
+// ---- attention of chunks of new tokens over a paged cache (fa_extend.cu)
+struct Extend {
+  const void* k_cache;       // bf16 [num_blocks][Hkv][bs][d], or codes [...][d / 2]
+  const void* v_cache;
+  const uint32_t* k_scale;   // (s, z) pairs, [num_blocks][Hkv][bs][d / 64], 4-bit caches only
+  const uint32_t* v_scale;
+  const int* block_table;    // [B][max_blocks]
+  const int* seq_lens;       // [B]
+  const int* q_starts;       // [B + 1]
+  __nv_bfloat16* o;          // [T][H][d]
+  float* lse;                // [T][H]
+  float* o_part;             // [n_slots][d / 4][256][4]: normalised parts of cut items
+  float* lse_part;           // [n_slots][256]
+  int T, B, H, Hkv, num_blocks, bs, max_blocks;
+  int heads, hv;             // query heads a tile holds (at most 128), K/V heads times the parts its query heads are cut into
+  int tpt;                   // tokens a query tile holds: 128 / heads
+  int ctas, lc, may_chunk;   // see fa_extend_plan.cuh
+  int n_slots, n_long;       // workspace parts; long items there may be
+  bool causal, zero_skipped;
+  float scale_log2;
+};
+// Sets the fields from `heads` to `n_long` from the sizes and `causal`; returns the workspace's bytes.
+size_t extend_sizes(Extend* p, int d, bool q4);
+cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream);
+
 // The calling host thread's side stream on the current device (a
 // non-blocking stream the library creates on first use and keeps).
 cudaError_t side_stream(cudaStream_t* out);
@@ -159,5 +184,6 @@ cudaError_t read_and_clear_softmax_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_rope_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_append_error(uint32_t* out, cudaStream_t stream);
 cudaError_t read_and_clear_decode_q4_error(uint32_t* out, cudaStream_t stream);
+cudaError_t read_and_clear_extend_error(uint32_t* out, cudaStream_t stream);
 
 }  // namespace fa

@@ -1,0 +1,1089 @@
+// Attention of chunks of new tokens over a paged KV cache, in bf16 or in
+// 4-bit codes: a packed, ragged batch of any requests' tokens (whole prompts,
+// parts of prompts, a few tokens to be verified, single tokens).
+//
+//   o_i = Σ_j softmax_j(scale q_i·k_j) v_j,  lse_i = ln Σ_j e^(scale q_i·k_j)
+//
+// over the keys j that token i sees: those up to its own position (causal),
+// or all of its request's. Tile by tile with a running maximum and sum, as in
+// the forward (fa_fwd.cu), whose two tensor-core products, order of products
+// and threshold for rescaling are used here too.
+//
+// A query tile holds up to 128 rows: tpt tokens with the `heads` query heads
+// that share a K/V head (row = token · heads + head), so a K/V tile is read
+// once for all of them. A CTA works on items of two query tiles, a share of
+// all (item, key tile) units of the call (fa_extend_plan.cuh), one piece (the
+// part of an item in its share) after another without a pause: while the last
+// products of a piece run, the next one's keys are on their way.
+//
+// Roles:
+//   warp 0       the pieces of the CTA's share, into a ring of descriptors
+//   warp 1       TMEM owner and MMA issuer (warp-uniform, one elected lane)
+//   warp 2       K and V tiles as TMA boxes (block sizes that are a multiple of
+//                8 dividing 128), one box per cache block
+//   warp 3       Q tiles
+//   warps 4..7   softmax of the first query tile, one thread per row
+//   warps 8..11  softmax of the second
+//   warps 12..15 (other block sizes, 4-bit caches) K and V tiles: gathered row
+//                by row, or codes unpacked to bf16 into the products' layout
+// TMEM columns: S0 0.., S1 128.., O0 256.., O1 384... P overwrites S.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fa_common.h"
+#include "fa_extend_plan.cuh"
+#include "fa_ptx.cuh"
+#include "fa_tmap.h"
+
+namespace fa {
+
+static __device__ uint32_t g_extend_err;
+
+namespace ext {
+
+constexpr int BM = 128;     // rows a query tile
+constexpr int ROWS = 256;   // rows an item
+constexpr int RING = 16;    // piece descriptors in flight
+constexpr float RESCALE_LOG2 = 8.f;
+constexpr float LN2 = 0.69314718055994531f;
+
+// How K and V tiles reach shared memory.
+enum Load : int { BOXES = 0, GATHER = 1, CODES = 2 };
+
+template <int LOAD>
+struct Threads {
+  static constexpr int N = LOAD == BOXES ? 384 : 512;
+  // readers of a piece: boxes or four loaders, Q, products, eight softmax warps
+  static constexpr int READERS = (LOAD == BOXES ? 1 : 4) + 2 + 8;
+};
+
+struct Piece {
+  int n, kt0;            // key tiles, the first of them; n = 0: no more pieces
+  int b, kvh, head0, heads;
+  int tok0, ntok;        // first row of q, tokens of the item
+  int pos0, len;         // position of the first token; cached tokens
+  int slot;              // -1: the outputs
+  int n0, n1;            // key tiles that each query tile sees
+  int pad[3];
+};
+static_assert(sizeof(Piece) == 64, "");
+
+template <int D>
+struct Smem {
+  static constexpr int PANELS = D / 64;
+  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int TILE = BM * D * 2;
+  static constexpr int PANEL = BM * 128;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * TILE;
+  static constexpr int V_OFF = K_OFF + STAGES * TILE;
+  static constexpr int PIECE_OFF = V_OFF + STAGES * TILE;
+  static constexpr int BAR_OFF = PIECE_OFF + RING * static_cast<int>(sizeof(Piece));
+  // q_full, q_empty, k0_full, kv_full[], kv_empty[], s_full[2], p_lo[2], p_hi[2], pv_done[2], o_free[2], final,
+  // piece_full[], piece_empty[]
+  static constexpr int NBARS = 3 + 2 * STAGES + 10 + 1 + 2 * RING;
+  static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int PLAN_OFF = SLOT_OFF + 16;
+  static constexpr int BYTES = PLAN_OFF + static_cast<int>(sizeof(PlanSmem));
+  // One CTA an SM (one 512-column TMEM allocation), 1024 bytes to align.
+  static constexpr int ALLOC = BYTES + 1024 > 118784 ? BYTES + 1024 : 118784;
+  static_assert(ALLOC <= 232448, "");
+};
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The ring of piece descriptors, as one reader sees it: a warp that reads
+// every piece in order.
+struct Pieces {
+  Piece* ring;
+  uint64_t *full, *empty;
+  uint32_t* err;
+  int next = 0;
+  __device__ __forceinline__ Pieces(Piece* r, uint64_t* f, uint64_t* e, uint32_t* er)
+      : ring(r), full(f), empty(e), err(er) {}
+  __device__ __forceinline__ bool read(Piece* out) {
+    const int s = next % RING;
+    if (!mbar_wait_warp(&full[s], (next / RING) & 1, err)) return false;
+    *out = ring[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
+    ++next;
+    return true;
+  }
+};
+
+// Eight codes of one 32-bit word as bf16 values z + s (n − 8), one rounding
+// each: a code lands in the mantissa of bf16 128 (the odd ones three bits up:
+// 128 + 8 n), one subtraction leaves n − 8 (and 8 (n − 8)), exactly, and the
+// fused multiply-add in bf16 rounds the sum.
+__device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 z) {
+  const uint32_t v = w >> 1;
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xc308), __ushort_as_bfloat16(0xc340));  // -136, -192
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t = __byte_perm(w, v, i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
+    t = (t & 0x0078000fu) | 0x43004300u;
+    const __nv_bfloat162 n = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&t), off);
+    const __nv_bfloat162 x = __hfma2(n, s, z);
+    out[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int D, int LOAD>
+__global__ void __launch_bounds__(Threads<LOAD>::N, 1)
+    extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ Extend p) {
+  using L = Smem<D>;
+  constexpr int ST = L::STAGES, NT = Threads<LOAD>::N;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem + L::Q_OFF;
+  uint8_t* sK = smem + L::K_OFF;
+  uint8_t* sV = smem + L::V_OFF;
+  Piece* ring = reinterpret_cast<Piece*>(smem + L::PIECE_OFF);
+  // As in the forward, slot u % ST holds V of unit u and K of unit u + 1,
+  // loaded and released together; the first unit's K has its own barrier.
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k0_full = q_full + 2;
+  uint64_t* kv_full = q_full + 3;
+  uint64_t* kv_empty = kv_full + ST;
+  uint64_t* s_full = kv_empty + ST;    // [2], one per query tile
+  uint64_t* p_lo = s_full + 2;         // [2] keys 0..63 of P
+  uint64_t* p_hi = p_lo + 2;           // [2] keys 64..127
+  uint64_t* pv_done = p_hi + 2;        // [2]
+  uint64_t* o_free = pv_done + 2;      // [2] the epilogue has read O
+  uint64_t* final_bar = o_free + 2;
+  uint64_t* piece_full = final_bar + 1;
+  uint64_t* piece_empty = piece_full + RING;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
+  PlanSmem* plan = reinterpret_cast<PlanSmem*>(smem + L::PLAN_OFF);
+  uint32_t* err = &g_extend_err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(blockIdx.x);
+  launch_dependents();  // the merge may be set up; it waits for this grid's writes
+
+  // Rows of no request.
+  if (p.zero_skipped) {
+    const int first = min(max(p.q_starts[0], 0), p.T), last = min(max(p.q_starts[p.B], first), p.T);
+    const long long per = static_cast<long long>(p.H) * (D / 8);
+    const long long n = static_cast<long long>(first + p.T - last) * per;
+    for (long long i = static_cast<long long>(cta) * NT + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * NT) {
+      long long tok = i / per;
+      if (tok >= first) tok += last - first;
+      const long long at = tok * per + i % per;
+      if (in_range(at, 1, static_cast<long long>(p.T) * per, err))
+        reinterpret_cast<uint4*>(p.o)[at] = make_uint4(0u, 0u, 0u, 0u);
+      if (i % (D / 8) == 0 && in_range(at / (D / 8), 1, static_cast<long long>(p.T) * p.H, err))
+        p.lse[at / (D / 8)] = -INFINITY;
+    }
+  }
+
+  Shape sh{2 * p.tpt, p.causal, p.lc};
+  const Cut cut = cut_of<NT>(p, &sh, plan, err);
+  if (cut.units == 0 || cta >= cut.ctas) return;
+  const u64 u_begin = cut.start(cta), u_end = cut.start(cta + 1);
+  Place at;
+  u64 items0;
+  if (!find_request<NT, false>(p, sh, plan, u_begin, &at, &items0, err)) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(k0_full, LOAD == BOXES ? 1 : LOAD == GATHER ? 128 : 4);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&kv_full[s], LOAD == BOXES ? 1 : LOAD == GATHER ? 128 : 4);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_lo[g], 4);
+      mbar_init(&p_hi[g], 4);
+      mbar_init(&pv_done[g], 1);
+      mbar_init(&o_free[g], 4);
+    }
+    mbar_init(final_bar, 1);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], Threads<LOAD>::READERS);
+    }
+    fence_mbar_init();
+  }
+  // Rows of a query tile that no token fills (128 is no multiple of the heads)
+  // are zero for good: their scores then never ask for a rescaling.
+  const int filled = p.tpt * p.heads;
+  if (filled < BM)
+    for (int i = threadIdx.x; i < 2 * L::PANELS * (BM - filled) * 8; i += NT) {
+      const int panel = i / ((BM - filled) * 8), rest = i % ((BM - filled) * 8);
+      *reinterpret_cast<uint4*>(sQ + panel * L::PANEL + filled * 128 + rest * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  fence_async_smem();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Without boxes 16 warps share the registers: 128 a thread at the launch, then
+  // 128 · (80 + 2 · 168 + 96) = 65536 where they are needed.
+  if (warp < 4) {
+    if (LOAD != BOXES) regs_down<80>();
+    if (warp == 0) {
+      // --------------------------------------------------------------- pieces
+      locate(p, sh, u_begin, &at);
+      u64 left = u_end - u_begin;
+      const int G = p.H / p.Hkv, parts = p.hv / p.Hkv;
+      for (int idx = 0;; ++idx) {
+        const int s = idx % RING;
+        if (idx >= RING && !mbar_wait_warp(&piece_empty[s], ((idx / RING) - 1) & 1, err)) break;
+        if (left == 0) {
+          if (lane == 0) {
+            ring[s].n = 0;
+            mbar_arrive(&piece_full[s]);
+          }
+          break;
+        }
+        const Request& r = at.r;
+        const int whole = sh.length(r, at.c, at.i);
+        const int n = static_cast<int>(min(static_cast<u64>(whole - at.off), left));
+        if (lane == 0) {
+          Piece x;
+          x.n = n;
+          x.kt0 = at.c * (sh.chunked(r) ? sh.lc : 0) + at.off;
+          x.b = at.b;
+          x.kvh = at.hv / parts;
+          const int h0 = at.hv % parts * p.heads;
+          x.head0 = x.kvh * G + h0;
+          x.heads = min(p.heads, G - h0);
+          const int t0 = at.i * sh.span;
+          x.tok0 = r.row0 + t0;
+          x.ntok = min(sh.span, r.n - t0);
+          x.pos0 = r.base() + t0;
+          x.len = r.len;
+          x.slot = part_slot(p, sh, cut, at, cta, at.off > 0, at.off + n < whole);
+          if (x.slot >= p.n_slots) {  // the host's bound holds: never
+            atomicExch(err, DEV_BOUNDS);
+            x.slot = 2 * cta;
+          }
+          auto sees = [&](int g) {
+            const int t = min((g + 1) * p.tpt, x.ntok);
+            if (t <= g * p.tpt) return 0;
+            const int keys = p.causal ? max(x.pos0 + t, 0) : x.len;
+            return min(max((keys + TK - 1) / TK - x.kt0, 0), n);
+          };
+          x.n0 = sees(0), x.n1 = sees(1);
+          ring[s] = x;
+          mbar_arrive(&piece_full[s]);
+        }
+        __syncwarp();
+        left -= n;
+        if (left == 0 || at.off + n < whole) continue;
+        at.off = 0;
+        if (++at.i < r.items) continue;
+        if (++at.hv == p.hv) {
+          at.hv = 0;
+          if (++at.c == sh.chunks(r)) {
+            if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
+            at.c = 0;
+            do {
+              at.r = request_of(p, ++at.b, err);  // units are left, so there is a request with tokens
+            } while (at.r.n == 0 && at.b + 1 < p.B);
+          }
+        }
+        at.i = sh.chunked(at.r) ? sh.past(at.r, static_cast<long long>(at.c) * sh.lc) : 0;
+      }
+    } else if (warp == 1) {
+      // ----------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16(BM, TK, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16(BM, D, false, true);
+      const uint64_t dq = sdesc_kmajor(smem_u32(sQ), 0);
+      const uint64_t dk = sdesc_kmajor(smem_u32(sK), 0);
+      const uint64_t dv = sdesc_mnmajor(smem_u32(sV), 0, L::PANEL);
+      auto issue_s = [&](int g, int s) {  // S_g = Q_g Kᵀ, K in stage s
+        const uint64_t a = desc_add(dq, g * L::TILE), b = desc_add(dk, s * L::TILE);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + g * TK, desc_add(a, kmajor_step(ks, L::PANEL)), desc_add(b, kmajor_step(ks, L::PANEL)),
+                   idesc_s, ks > 0);
+          tc_commit(&s_full[g]);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int g, int s, int half, uint32_t acc0) {  // O_g += P_g V over 64 keys
+        const uint64_t b = desc_add(dv, s * L::TILE);
+        if (elect_one()) {
+#pragma unroll
+          for (int k4 = 0; k4 < TK / 32; ++k4) {
+            const int ks = half * (TK / 32) + k4;
+            mma_ts(tmem + 256 + g * 128, tmem + g * TK + ks * 8, desc_add(b, mnmajor_step(ks)), idesc_o,
+                   ks > 0 ? 1u : acc0);
+          }
+          if (half == 1) tc_commit(&pv_done[g]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      Pieces pieces(ring, piece_full, piece_empty, err);
+      Piece x;
+      bool ok = pieces.read(&x) && mbar_wait_warp(q_full, 0, err) && mbar_wait_warp(k0_full, 0, err);
+      int n[2] = {0, 0}, seen[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece; units, pieces so far of each query tile
+      int len = 0, idx = 0, u = 0;
+      if (ok) {
+        tc_fence_after();
+        if (LOAD == GATHER) fence_async_smem();
+        len = x.n, n[0] = x.n0, n[1] = x.n1;
+        if (n[0] > 0) issue_s(0, 0);
+        if (n[1] > 0) issue_s(1, 0);
+        commit(&kv_empty[ST - 1]);  // the first K is read: slot ST - 1 may load
+        if (len == 1) commit(q_empty);
+      }
+      while (ok && len > 0) {
+        int next = 0;
+        for (int j = 0; j < len && ok; ++j, ++u) {
+          const int s = u % ST, s1 = (u + 1) % ST;
+          const bool last = j + 1 == len;
+          ok = mbar_wait_warp(&kv_full[s], (u / ST) & 1, err);
+          if (!ok) break;
+          if (LOAD == GATHER) fence_async_smem();  // the lanes' copies, for the tensor core
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (j >= n[g]) continue;
+            if (j == 0 && done[g] > 0) {
+              ok = mbar_wait_warp(&o_free[g], (done[g] - 1) & 1, err);
+              if (!ok) break;
+            }
+            ok = mbar_wait_warp(&p_lo[g], seen[g] & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(g, s, 0, j > 0 ? 1u : 0u);
+            ok = mbar_wait_warp(&p_hi[g], seen[g] & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(g, s, 1, 1u);
+            ++seen[g];
+            if (j + 1 < n[g]) issue_s(g, s1);
+          }
+          if (!ok) break;
+          if (j + 2 == len) commit(q_empty);  // the piece's last scores are under way
+          if (last) {
+            if (n[0] > 0) ++done[0];
+            if (n[1] > 0) ++done[1];
+            ok = pieces.read(&x);
+            if (!ok) break;
+            next = x.n;
+            if (next > 0) {
+              ok = mbar_wait_warp(q_full, (idx + 1) & 1, err);
+              if (!ok) break;
+              tc_fence_after();
+              n[0] = x.n0, n[1] = x.n1;
+              if (n[0] > 0) issue_s(0, s1);
+              if (n[1] > 0) issue_s(1, s1);
+              if (next == 1) commit(q_empty);
+            }
+          }
+          commit(&kv_empty[s]);  // V of unit u and K of unit u + 1 are read
+        }
+        len = next;
+        ++idx;
+      }
+      commit(final_bar);
+      mbar_wait_warp(final_bar, 0, err);
+    } else if (warp == 3) {
+      // -------------------------------------------------------------- Q tiles
+      if (lane == 0) prefetch_tmap(&tq);
+      const int bytes = p.tpt * p.heads * 128 * L::PANELS;
+      Pieces pieces(ring, piece_full, piece_empty, err);
+      Piece x;
+      int idx = 0;
+      for (; pieces.read(&x) && x.n > 0; ++idx) {
+        if (idx > 0 && !mbar_wait_warp(q_empty, (idx - 1) & 1, err)) break;
+        if (lane == 0) {
+          const int tiles = (x.n0 > 0) + (x.n1 > 0);
+          if (tiles == 0) mbar_arrive(q_full);
+          else mbar_arrive_expect_tx(q_full, tiles * bytes);
+          for (int g = 0; g < 2; ++g)
+            if ((g ? x.n1 : x.n0) > 0)
+              for (int c = 0; c < L::PANELS; ++c)
+                tma_load_3d(sQ + g * L::TILE + c * L::PANEL, &tq, q_full, c * 64, x.head0, x.tok0 + g * p.tpt);
+        }
+        __syncwarp();
+      }
+      if (idx > 0) mbar_wait_warp(q_full, (idx - 1) & 1, err);  // no copy outlives the CTA
+    } else if (LOAD == BOXES) {
+      // --------------------------------------------------- K and V by TMA boxes
+      // Lane i issues the box of block i of a tile; a block past the context or
+      // outside the cache is asked for at an out-of-range coordinate, which
+      // reads zeros. Table entries are loaded two units ahead.
+      if (lane == 0) {
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+      }
+      const int bpt = TK / p.bs;
+      struct Unit {
+        bool any;
+        int entry, kvh;  // this lane's table entry (-2: none wanted)
+      };
+      Pieces pieces(ring, piece_full, piece_empty, err);
+      Piece x;
+      x.n = 0;
+      int j = 0;
+      bool more = true;
+      auto fetch = [&]() -> Unit {  // the next unit
+        Unit t{false, -2, 0};
+        if (more && ++j >= x.n) {
+          more = pieces.read(&x) && x.n > 0;
+          j = 0;
+        }
+        if (!more) return t;
+        t.any = true;
+        t.kvh = x.kvh;
+        const int bi = (x.kt0 + j) * bpt + lane;
+        if (lane < bpt && static_cast<long long>(bi) * p.bs < x.len) {
+          const long long ti = static_cast<long long>(x.b) * p.max_blocks + bi;
+          t.entry = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
+        }
+        return t;
+      };
+      auto place = [&](const Unit& t) {  // the box's outer coordinate
+        if (t.entry >= 0 && t.entry < p.num_blocks) return t.entry * p.Hkv + t.kvh;
+        if (t.entry != -2) atomicExch(err, DEV_BAD_INDEX);
+        return p.num_blocks * p.Hkv;
+      };
+      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int z) {
+        if (lane < bpt)
+          for (int c = 0; c < L::PANELS; ++c) tma_load_3d(dst + c * L::PANEL + lane * p.bs * 128, map, bar, c * 64, 0, z);
+      };
+      Unit cur = fetch(), nxt = fetch(), far = fetch();
+      int z = place(cur), u = 0;
+      if (lane == 0) mbar_arrive_expect_tx(k0_full, L::TILE);
+      __syncwarp();
+      load(&tk, sK, k0_full, z);
+      bool ok = true;
+      while (ok) {
+        const int s = u % ST, s1 = (u + 1) % ST;
+        const int z1 = nxt.any ? place(nxt) : 0;
+        if (u >= ST - 1) ok = mbar_wait_warp(&kv_empty[s], ((u - (ST - 1)) / ST) & 1, err);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], nxt.any ? 2 * L::TILE : L::TILE);
+        __syncwarp();
+        load(&tv, sV + s * L::TILE, &kv_full[s], z);
+        ++u;
+        if (!nxt.any) break;
+        load(&tk, sK + s1 * L::TILE, &kv_full[s], z1);
+        z = z1;
+        nxt = far;
+        far = fetch();
+      }
+      // no copy outlives the CTA
+      mbar_wait_warp(k0_full, 0, err);
+      for (int i = max(0, u - ST); i < u; ++i) mbar_wait_warp(&kv_full[i % ST], (i / ST) & 1, err);
+    }
+  } else if (warp < 12) {
+    if (LOAD != BOXES) regs_up<168>();
+    // -------------------------------------------------------------- softmax
+    const int g = (warp - 4) >> 2;  // query tile
+    const int quarter = warp & 3;   // TMEM lanes 32*quarter .. +31
+    const int r = quarter * 32 + lane;
+    const int tt = r / p.heads, hh = r - tt * p.heads;  // token and head of this row within the tile
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_addr + g * TK;
+    const uint32_t o_addr = tmem + lane_addr + 256 + g * 128;
+    const float scale_log2 = p.scale_log2;
+    int u0 = 0, seen = 0;  // units before the piece; units of this query tile so far
+    // The piece stays in the ring until this warp is through with it.
+    for (int idx = 0;; ++idx) {
+      if (!mbar_wait_warp(&piece_full[idx % RING], (idx / RING) & 1, err)) break;
+      const Piece& x = ring[idx % RING];
+      if (x.n == 0) break;
+      bool ok = true;
+      const int n = g ? x.n1 : x.n0, kt0 = x.kt0, len = x.len;
+      const int tok = g * p.tpt + tt;
+      const bool valid = r < filled && tok < x.ntok && hh < x.heads;
+      const int sight = valid ? (p.causal ? max(x.pos0 + tok + 1, 0) : x.len) : 0x7fffffff;  // keys this row sees
+      const int sight_lo = __reduce_min_sync(0xffffffffu, sight);
+      const bool live = sight_lo != 0x7fffffff;  // some row of the warp has a token
+      float m = -INFINITY;  // exponent reference (log2 units of scaled scores)
+      float nm = 0.f;       // -m, or 0 while there is none
+      float l = 0.f;        // running denominator relative to m
+      for (int j = 0; j < n; ++j, ++seen) {
+        const int k0 = (kt0 + j) * TK;
+        ok = mbar_wait(&s_full[g], seen & 1, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        // A box brings whole cache blocks: slots past the context may hold
+        // anything, and a NaN of theirs would outlive its zero probability.
+        // Their value rows are zeroed before the product reads them. (S of this
+        // unit is there, so the barrier is at this unit's phase at least: its
+        // parity wait is exact.)
+        if (LOAD == BOXES && k0 + TK > len) {
+          const int s = (u0 + j) % ST;
+          ok = mbar_wait_warp(&kv_full[s], ((u0 + j) / ST) & 1, err);
+          if (!ok) break;
+          if (k0 + r >= len)
+            for (int i = 0; i < L::PANELS * 8; ++i)
+              *reinterpret_cast<uint4*>(sV + s * L::TILE + (i >> 3) * L::PANEL + r * 128 + (i & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
+        }
+        auto release = [&](uint64_t* bar) {  // this half of P is in TMEM
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        if (!live) {  // no row to compute: what P holds for these rows reaches no other
+          release(&p_lo[g]);
+          release(&p_hi[g]);
+          continue;
+        }
+        uint32_t raw[4][32];
+        tmem_ld32(s_addr + 0, raw[0]);
+        tmem_ld32(s_addr + 32, raw[1]);
+        tmem_ld32(s_addr + 64, raw[2]);
+        tmem_ld32(s_addr + 96, raw[3]);
+        tmem_ld_wait();
+        float y[TK];
+#pragma unroll
+        for (int c = 0; c < TK; ++c) y[c] = __uint_as_float(raw[c / 32][c % 32]);
+        if (k0 + TK > sight_lo) {
+          const int mine = sight - k0;
+#pragma unroll
+          for (int c = 0; c < TK; ++c)
+            if (c >= mine) y[c] = -INFINITY;
+        }
+        float2 sum[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[q] = make_float2(0.f, 0.f);
+        const float2 sc2 = make_float2(scale_log2, scale_log2);
+        auto p_chunk = [&](int c, float2 nm2) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int t2 = 0; t2 < 16; ++t2) {
+            const float2 e = ffma2(make_float2(y[c + 2 * t2], y[c + 2 * t2 + 1]), sc2, nm2);
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            sum[t2 & 3] = fadd2(sum[t2 & 3], make_float2(p0, p1));
+            pk[t2] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(s_addr + c / 2, pk);
+        };
+        // The first half against the reference so far, before the tile's
+        // maximum is known; again if that outgrew it (as in the forward).
+        if (j > 0) {
+          p_chunk(0, make_float2(nm, nm));
+          p_chunk(32, make_float2(nm, nm));
+        }
+        float mx[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) mx[q] = fmaxf(y[q], y[8 + q]);
+#pragma unroll
+        for (int c = 16; c < TK; c += 16)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) mx[q] = fmax3(mx[q], y[c + q], y[c + 8 + q]);
+        const float tile_max = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale_log2;
+        const bool raise = __any_sync(0xffffffffu, tile_max > m + RESCALE_LOG2);
+        if (raise || j == 0) {
+          const float m_new = fmaxf(m, tile_max);
+          const float alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);  // 0 on a row's first key
+          m = m_new;
+          nm = m == -INFINITY ? 0.f : -m;  // a row that has seen no key: 2^-inf = 0 throughout
+          l *= alpha;
+          if (j > 0) {
+            ok = mbar_wait_warp(&pv_done[g], (seen - 1) & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + c, o);
+              tmem_ld_wait();
+              uint32_t a[16], b[16];
+#pragma unroll
+              for (int t2 = 0; t2 < 16; ++t2) {
+                a[t2] = __float_as_uint(__uint_as_float(o[t2]) * alpha);
+                b[t2] = __float_as_uint(__uint_as_float(o[16 + t2]) * alpha);
+              }
+              tmem_st16(o_addr + c, a);
+              tmem_st16(o_addr + c + 16, b);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[q] = make_float2(0.f, 0.f);
+          p_chunk(0, make_float2(nm, nm));
+          p_chunk(32, make_float2(nm, nm));
+        }
+        release(&p_lo[g]);
+        p_chunk(64, make_float2(nm, nm));
+        p_chunk(96, make_float2(nm, nm));
+        release(&p_hi[g]);
+        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ epilogue
+      if (n > 0) {
+        ok = mbar_wait_warp(&pv_done[g], (seen - 1) & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+      const bool none = l == 0.f;                  // no key: zeros, whatever O holds
+      const float lse = none ? -INFINITY : (m + __log2f(l)) * LN2;
+      const long long orow = static_cast<long long>(x.tok0 + tok) * p.H + x.head0 + hh;
+      const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (n > 0 && live) {
+          tmem_ld32(o_addr + c, o);
+          tmem_ld_wait();
+        }
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : __uint_as_float(o[i]) * inv;
+        if (valid && x.slot < 0) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            const float* v = f + ch * 8;
+            const long long off = orow * D + c + ch * 8;
+            if (in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
+              *reinterpret_cast<uint4*>(p.o + off) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            const long long off = ((static_cast<long long>(x.slot) * (D / 4) + c / 4 + ch) * ROWS + g * BM + r) * 4;
+            if (in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err))
+              *reinterpret_cast<float4*>(p.o_part + off) = make_float4(f[ch * 4], f[ch * 4 + 1], f[ch * 4 + 2], f[ch * 4 + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (x.slot < 0) {
+          if (in_range(orow, 1, static_cast<long long>(p.T) * p.H, err)) p.lse[orow] = lse;
+        } else if (in_range(prow, 1, static_cast<long long>(p.n_slots) * ROWS, err)) {
+          p.lse_part[prow] = lse;
+        }
+      }
+      if (n > 0) {  // O is read: the next piece's products may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[g]);
+      }
+      u0 += x.n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&piece_empty[idx % RING]);
+    }
+  } else if constexpr (LOAD != BOXES) {
+    regs_down<96>();
+    // ----------------------------------------- K and V row by row, or unpacked
+    // Each of four warps takes 32 rows of a tile, lane i the place of row i.
+    constexpr uint32_t NO_ROW = 0xffffffffu;  // zeros (the host keeps the cache below 2^32 - 1 rows)
+    const int w = warp - 12;
+    const long long rows_all = static_cast<long long>(p.num_blocks) * p.Hkv * p.bs;
+    struct Unit {
+      bool any;
+      uint32_t row;
+    };
+    struct Raw {  // a unit's row before its table entry is there
+      bool any, want;
+      int entry, kvh, slot;
+    };
+    Pieces pieces(ring, piece_full, piece_empty, err);
+    Piece x;
+    x.n = 0;
+    int j = 0;
+    bool more = true;
+    auto fetch = [&]() -> Raw {
+      Raw t{false, false, -1, 0, 0};
+      if (more && ++j >= x.n) {
+        more = pieces.read(&x) && x.n > 0;
+        j = 0;
+      }
+      if (!more) return t;
+      t.any = true;
+      const int key = (x.kt0 + j) * TK + w * 32 + lane;
+      if (key < x.len) {
+        const int bi = key / p.bs;
+        const long long ti = static_cast<long long>(x.b) * p.max_blocks + bi;
+        t.want = true;
+        t.kvh = x.kvh;
+        t.slot = key - bi * p.bs;
+        t.entry = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
+      }
+      return t;
+    };
+    auto resolve = [&](const Raw& t) -> Unit {
+      Unit y{t.any, NO_ROW};
+      if (t.want) {
+        if (t.entry >= 0 && t.entry < p.num_blocks)
+          y.row = (static_cast<uint32_t>(t.entry) * static_cast<uint32_t>(p.Hkv) + static_cast<uint32_t>(t.kvh)) *
+                      static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(t.slot);
+        else
+          atomicExch(err, DEV_BAD_INDEX);
+      }
+      return y;
+    };
+    int u = 0;
+    bool ok = true;
+    if constexpr (LOAD == GATHER) {
+      auto copy = [&](const void* cache, uint8_t* dst, uint32_t row) {
+        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks a row, rows a step
+        const int c = lane % CH, sub = lane / CH;
+#pragma unroll 4
+        for (int k = 0; k < CH; ++k) {
+          const int r = k * RPI + sub;
+          const uint32_t at_row = __shfl_sync(0xffffffffu, row, r);
+          const bool live = at_row != NO_ROW && in_range(at_row, 1, rows_all, err);
+          const char* src = static_cast<const char*>(cache) + static_cast<size_t>(live ? at_row : 0u) * (D * 2) + c * 16;
+          cp_async_16(dst + (c >> 3) * L::PANEL + (w * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4), src, live ? 16u : 0u);
+        }
+      };
+      Raw a = fetch(), b = fetch();
+      Unit cur = resolve(a);
+      copy(p.k_cache, sK, cur.row);
+      cp_async_arrive_noinc(k0_full);
+      a = b, b = fetch();
+      while (ok) {
+        const int s = u % ST, s1 = (u + 1) % ST;
+        const Unit nxt = resolve(a);
+        if (u >= ST - 1) ok = mbar_wait_warp(&kv_empty[s], ((u - (ST - 1)) / ST) & 1, err);
+        if (!ok) break;
+        copy(p.v_cache, sV + s * L::TILE, cur.row);
+        if (nxt.any) copy(p.k_cache, sK + s1 * L::TILE, nxt.row);
+        cp_async_arrive_noinc(&kv_full[s]);
+        ++u;
+        if (!nxt.any) break;
+        cur = nxt;
+        a = b, b = fetch();
+      }
+      cp_async_commit();
+      cp_async_wait<0>();  // no copy outlives the CTA
+    } else {
+      // A lane holds 32 codes (16 bytes) of a row and their group's pair; its
+      // loads for the next tile are under way while it unpacks this one.
+      constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte pieces a row, rows a step; CPR steps
+      const int quarter = lane % CPR, sub = lane / CPR;
+      struct Codes {
+        uint4 n[CPR];
+        uint32_t sz[CPR];
+      };
+      auto fetch_codes = [&](const void* cache, const uint32_t* scale, const Unit& t, Codes& y) {
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) {
+          const uint32_t row = __shfl_sync(0xffffffffu, t.row, k * RPI + sub);
+          y.n[k] = make_uint4(0u, 0u, 0u, 0u);
+          y.sz[k] = 0u;  // step and centre 0: zeros
+          if (row != NO_ROW && in_range(row, 1, rows_all, err)) {
+            y.n[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + static_cast<size_t>(row) * (D / 2)) + quarter);
+            y.sz[k] = __ldg(scale + static_cast<size_t>(row) * (D / 64) + quarter / 2);
+          }
+        }
+      };
+      // Rows r and r + 1 and both panels meet in one store: with the words of
+      // the second panel's lanes two places on, no two lanes share a bank.
+      auto unpack = [&](uint8_t* dst, const Codes& y) {
+        const bool swap = quarter & 2;
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) {
+          const int r = w * 32 + k * RPI + sub;
+          uint32_t sbits = __byte_perm(y.sz[k], 0, 0x1010);
+          const uint32_t zbits = __byte_perm(y.sz[k], 0, 0x3232);
+          const __nv_bfloat162 eighth = __halves2bfloat162(__ushort_as_bfloat16(0x3f80), __ushort_as_bfloat16(0x3e00));  // 1, 1/8
+          const __nv_bfloat162 s2 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&sbits), eighth);
+          const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162*>(&zbits);
+          const uint4 c = y.n[k];
+          const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+          uint8_t* base = dst + (quarter >> 1) * L::PANEL + r * 128;
+          const int c0 = (quarter & 1) * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int chunk = c0 + (e ^ (swap ? 2 : 0));
+            *reinterpret_cast<uint4*>(base + ((chunk ^ (r & 7)) << 4)) = values8(word[e], s2, z2);
+          }
+        }
+      };
+      auto publish = [&](uint64_t* bar) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
+      // K of unit u + 1 and V of unit u, loaded a step ahead.
+      Codes kc, vc;
+      Raw a = fetch(), b = fetch();
+      Unit cur = resolve(a);
+      fetch_codes(p.k_cache, p.k_scale, cur, kc);
+      fetch_codes(p.v_cache, p.v_scale, cur, vc);
+      Unit nxt = resolve(b);
+      Raw far = fetch();
+      unpack(sK, kc);
+      publish(k0_full);
+      fetch_codes(p.k_cache, p.k_scale, nxt, kc);
+      while (ok) {
+        const int s = u % ST, s1 = (u + 1) % ST;
+        const Unit after = resolve(far);
+        far = fetch();
+        if (u >= ST - 1) ok = mbar_wait_warp(&kv_empty[s], ((u - (ST - 1)) / ST) & 1, err);
+        if (!ok) break;
+        unpack(sV + s * L::TILE, vc);
+        fetch_codes(p.v_cache, p.v_scale, nxt, vc);
+        if (nxt.any) {
+          unpack(sK + s1 * L::TILE, kc);
+          fetch_codes(p.k_cache, p.k_scale, after, kc);
+        }
+        publish(&kv_full[s]);
+        ++u;
+        if (!nxt.any) break;
+        nxt = after;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- merge
+//
+// One output row from its parts: lse = ln Σ_s e^(lse_s), o = Σ_s e^(lse_s −
+// lse) o_s. The first ctas - 1 blocks in x take the items that share ends cut
+// (the first end inside an item is its block's), the others one long item
+// each; y is a slice of 32 rows. What each block merges follows from the
+// lengths alone and is worked out while the attention kernel still runs.
+constexpr int MERGE_THREADS = 256;
+constexpr int MAX_PARTS = (SHARE_CHUNKS + 1) * MAX_CTAS + 32;
+
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
+  __shared__ PlanSmem plan;
+  __shared__ int parts[MAX_PARTS];
+  __shared__ int n_parts, head, item;
+  uint32_t* err = &g_extend_err;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Shape sh{2 * p.tpt, p.causal, p.lc};
+  const Cut cut = cut_of<MERGE_THREADS>(p, &sh, &plan, err);
+  Place at;
+  u64 items0;
+  const int job = static_cast<int>(blockIdx.x);
+  if (threadIdx.x == 0) n_parts = head = item = 0;
+  at.r = Request{0, 0, 0, 0};
+  if (job < p.ctas - 1) {
+    const int k = job + 1;
+    const u64 u = cut.start(k);
+    if (k < cut.ctas && cut.units > 0 && find_request<MERGE_THREADS, false>(p, sh, &plan, u, &at, &items0, err) &&
+        warp == 0) {
+      locate(p, sh, u, &at);
+      const u64 begin = u - at.off;
+      int n = 0;
+      // cut here for the first time, and not one of the long ones
+      if (at.off > 0 && begin >= cut.start(k - 1) && !sh.is_long(at.r, at.i)) {
+        const int last = cut.owner(begin + sh.length(at.r, at.c, at.i) - 1);
+        n = last - k + 2;
+        for (int i = lane; i < n; i += 32) parts[i] = i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i);
+      }
+      if (lane == 0) n_parts = n, head = at.hv, item = at.i;
+    }
+  } else {
+    const u64 want = static_cast<u64>(job - (p.ctas - 1));
+    if (cut.units > 0 && find_request<MERGE_THREADS, true>(p, sh, &plan, want, &at, &items0, err) && warp == 0) {
+      const int first = sh.first_long(at.r, 0), each = at.r.items - first;
+      const int nth = static_cast<int>(want - items0);
+      at.hv = nth / each;
+      at.i = first + nth % each;
+      const int n_c = (sh.tiles(at.r, at.i) + sh.lc - 1) / sh.lc;
+      int n = 0;
+      for (int c0 = 0; c0 < n_c; c0 += 32) {
+        const int c = c0 + lane;
+        int mine = 0, k0 = 0;
+        if (c < n_c) {
+          const u64 row = sh.in_chunk_before(at.r, c, at.r.items);
+          const u64 begin = at.units0 + sh.chunks_before(at.r, c) * p.hv + row * at.hv + sh.in_chunk_before(at.r, c, at.i);
+          k0 = cut.owner(begin);
+          mine = cut.owner(begin + sh.length(at.r, c, at.i) - 1) - k0 + 1;
+        }
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += t;
+        }
+        at.c = c;
+        for (int i = 0; i < mine; ++i)
+          if (n + sum - mine + i < MAX_PARTS)
+            parts[n + sum - mine + i] = part_slot(p, sh, cut, at, k0 + i, i > 0, i == 0 && mine > 1);
+        n += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (lane == 0) n_parts = min(n, MAX_PARTS), head = at.hv, item = at.i;
+    }
+  }
+  __syncthreads();
+  wait_for_primary();
+  const int n = n_parts, hv = head;
+  const int row = static_cast<int>(blockIdx.y) * 32 + lane, g = row / BM, r = row % BM;
+  const int tt = r / p.heads, hh = r - tt * p.heads, per = p.hv / p.Hkv, h0 = hv % per * p.heads, G = p.H / p.Hkv;
+  const int t0 = item * sh.span, tok = g * p.tpt + tt;
+  const bool valid = r < p.tpt * p.heads && t0 + tok < at.r.n && h0 + hh < G;
+  if (n == 0 || !valid) return;
+  constexpr int PER = D / 4 / 8;  // 4-value groups a warp takes: consecutive ones
+  float m = -INFINITY;
+  for (int s = 0; s < n; ++s) {
+    const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
+    const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
+    m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
+  }
+  float l = 0.f;
+  float4 acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
+      const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
+      const float w = ex2((v - m) * 1.4426950408889634f);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + warp * PER + i) * ROWS + row) * 4;
+        if (!in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)) continue;
+        const float4 t = *reinterpret_cast<const float4*>(p.o_part + off);
+        acc[i].x = fmaf(w, t.x, acc[i].x), acc[i].y = fmaf(w, t.y, acc[i].y);
+        acc[i].z = fmaf(w, t.z, acc[i].z), acc[i].w = fmaf(w, t.w, acc[i].w);
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long orow = static_cast<long long>(at.r.row0 + t0 + tok) * p.H + hv / per * G + h0 + hh;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const long long off = orow * D + (warp * PER + i) * 4;
+    if (in_range(off, 4, static_cast<long long>(p.T) * p.H * D, err))
+      *reinterpret_cast<uint2*>(p.o + off) = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
+                                                        pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+  }
+  if (warp == 0 && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err))
+    p.lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
+}
+
+// ------------------------------------------------------------------ launch
+
+// TMA boxes serve a block size that is a multiple of 8 dividing 128 (each box
+// lands on whole 1024-byte swizzle groups); other sizes are gathered.
+static bool boxes(int bs) { return bs % 8 == 0 && TK % bs == 0; }
+
+// q [T][H][d]: box = 64 columns x `heads` heads x tpt tokens.
+static bool make_tmap_q(CUtensorMap* map, const void* q, int T, int H, int d, int heads, int tpt) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tpt};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int LOAD>
+static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_q(&tq, q, p.T, p.H, D, p.heads, p.tpt)) return cudaErrorInvalidValue;
+  if (LOAD == BOXES) {
+    if (!make_tmap_bf16(&tk, p.k_cache, p.num_blocks * p.Hkv, p.bs, D, p.bs) ||
+        !make_tmap_bf16(&tv, p.v_cache, p.num_blocks * p.Hkv, p.bs, D, p.bs))
+      return cudaErrorInvalidValue;
+  } else {
+    tk = tv = tq;  // unused
+  }
+  auto kern = extend_kernel<D, LOAD>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::ALLOC);
+  if (e != cudaSuccess) return e;
+  kern<<<p.ctas, Threads<LOAD>::N, Smem<D>::ALLOC, stream>>>(tq, tk, tv, p);
+  e = cudaGetLastError();
+  const int jobs = p.ctas - 1 + p.n_long;
+  if (e != cudaSuccess || jobs == 0) return e;  // one CTA: nothing is cut
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(jobs), ROWS / 32);
+  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, extend_merge_kernel<D>, p);
+}
+
+}  // namespace ext
+
+size_t extend_sizes(Extend* p, int d, bool q4) {
+  using namespace ext;
+  const int G = p->H / p->Hkv, parts = (G + BM - 1) / BM;
+  p->heads = (G + parts - 1) / parts;
+  p->hv = p->Hkv * parts;
+  p->tpt = BM / p->heads;
+  const long long span = 2 * p->tpt;
+  const long long tiles = (static_cast<long long>(p->max_blocks) * p->bs + TK - 1) / TK;
+  // A chunk's K and V, of all K/V heads, stay in L2 (read as they lie there).
+  const long long tile_bytes = 2ll * TK * p->Hkv * (q4 ? d / 2 + d / 16 : 2 * d);
+  long long lc = kL2GroupBytes / tile_bytes;
+  p->lc = static_cast<int>(lc < 8 ? 8 : lc > (1 << 20) ? 1 << 20 : lc);
+  const long long items = p->hv * (p->T / span + (p->T < p->B ? p->T : p->B));  // at most
+  const long long shares = items * tiles / MIN_SHARE;
+  p->ctas = static_cast<int>(shares < 1 ? 1 : shares > MAX_CTAS ? MAX_CTAS : shares);
+  p->may_chunk = p->T > span && tiles > p->lc;
+  p->n_long = 0;
+  long long whole = 0;
+  if (p->may_chunk) {
+    // Items of requests with two or more: at most 2 T / span. A chunk is at
+    // least 1/8 of a share, a long item passes at most twice its tiles / lc.
+    const long long long_items = p->hv * (2ll * p->T / span), by_share = 2ll * SHARE_CHUNKS * p->ctas;
+    p->n_long = static_cast<int>(long_items < by_share ? long_items : by_share);
+    whole = long_items * ((tiles + p->lc - 1) / p->lc);
+    if (whole > by_share) whole = by_share;
+  }
+  p->n_slots = static_cast<int>(2 * p->ctas + whole);
+  return static_cast<size_t>(p->n_slots) * ROWS * (d + 1) * sizeof(float);
+}
+
+cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream) {
+  using namespace ext;
+  if (q4) return d == 64 ? launch<64, CODES>(p, q, stream) : launch<128, CODES>(p, q, stream);
+  if (boxes(p.bs)) return d == 64 ? launch<64, BOXES>(p, q, stream) : launch<128, BOXES>(p, q, stream);
+  return d == 64 ? launch<64, GATHER>(p, q, stream) : launch<128, GATHER>(p, q, stream);
+}
+
+cudaError_t read_and_clear_extend_error(uint32_t* out, cudaStream_t stream) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_extend_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_extend_err, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+  if (e != cudaSuccess) return e;
+  return cudaStreamSynchronize(stream);
+}
+
+}  // namespace fa

@@ -568,6 +568,71 @@ typedef struct {
 int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
 
 /*
+ * Attention of chunks of new tokens over a paged cache: what lies between
+ * fa_append_paged (which writes any number of a request's tokens) and a decode
+ * step (one query row per request). Whole prompts, parts of prompts behind a
+ * cached prefix, a few tokens to be verified and single tokens, of any
+ * requests in one call.
+ *   q          [T][H][d] bf16: the new tokens' queries (fa_append_paged's
+ *              q_out), request after request.
+ *   q_starts   [B + 1] device int32: request b's tokens are rows q_starts[b] ..
+ *              q_starts[b + 1] - 1 of q, o and lse (none: nothing is read).
+ *              Not decreasing, in [0, T]. A request whose two numbers break
+ *              this is taken for empty and fa_last_device_error reports
+ *              FA_ERR_BAD_INDEX.
+ *   seq_lens   [B] device int32: cached tokens of each request, its new ones
+ *              included (they are the last; the caller has appended them),
+ *              clamped to [0, max_blocks_per_seq·block_size]. The i-th of n new
+ *              tokens is at position seq_len - n + i.
+ *   causal     non-zero: a token sees the keys up to its own position; else
+ *              all keys of its request. A token that sees none (a position
+ *              below 0, an empty context) gets o = 0, lse = -inf. Keys and
+ *              values of tokens that are cached and not seen have to be
+ *              finite; slots past a request's length may hold anything.
+ *   o, lse     [T][H][d] bf16 and [T][H] fp32. Rows of no request (before
+ *              q_starts[0], from q_starts[B] on) stay as they were; with
+ *              zero_skipped they get o = 0, lse = -inf.
+ *   workspace  fa_extend_workspace_bytes(...) bytes, 16-byte aligned, needed
+ *              always; contents on entry are ignored. Calls that run at the
+ *              same time need one each.
+ *   The cache, block_table and head sharing as in fa_decode_paged; a
+ *   block-table entry outside [0, num_blocks) is never dereferenced (zeros in
+ *   its place; FA_ERR_BAD_INDEX).
+ * fa_extend_paged_q4: the same over a cache in 4-bit codes (k_scale, v_scale:
+ * its pairs; NULL otherwise). Keys and values are read back as z + s (n - 8)
+ * rounded to bf16 once, as fa_append_paged_q4's k_values and v_values, where a
+ * decode step holds them exactly.
+ * The lengths are read on the device and the work is cut there: a captured
+ * call may be replayed with other lengths within the same T, B and table.
+ * Errors: a NULL struct or pointer it must hold, sizes < 1, Hkv not dividing
+ * H, bad scale -> FA_ERR_INVALID_ARG; d not 64/128, T·H past 2^31, T past
+ * 2^30, B past 2^24, H/Hkv past 16384, a cache past 2^32 token rows or 2^31 - 2
+ * (block, K/V head) pairs -> FA_ERR_UNSUPPORTED; FA_ERR_WORKSPACE;
+ * FA_ERR_MISALIGNED (int and lse arrays: 4 bytes).
+ */
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* k_scale;
+  const void* v_cache;
+  const void* v_scale;
+  const int* block_table; /* [B][max_blocks_per_seq] */
+  const int* seq_lens;    /* [B] */
+  const int* q_starts;    /* [B + 1] */
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int T, B, H, Hkv, d;
+  int num_blocks, block_size, max_blocks_per_seq;
+  int causal, zero_skipped;
+  float scale;
+} fa_extend_args;
+size_t fa_extend_workspace_bytes(int T, int B, int H, int Hkv, int d, int block_size, int max_blocks_per_seq);
+int fa_extend_paged(const fa_extend_args* a, void* stream);
+int fa_extend_paged_q4(const fa_extend_args* a, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word set by
  * any kernel of this library on the current device. Returns FA_OK,
  * FA_ERR_TIMEOUT (a pipeline wait gave up; outputs of the calls since the

@@ -24,6 +24,7 @@ from .attention import (  # noqa: F401
 )
 from .cached import (  # noqa: F401
     append_slots,
+    extend_paged,
     norm_rope,
     norm_rope_bwd,
     q4_encode,

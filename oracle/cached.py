@@ -104,3 +104,34 @@ def append_slots(block_table, positions, requests, block_size):
         if r >= 0 and pos >= 0:
             out.append((t, int(block_table[r, pos // block_size]), int(pos) % block_size))
     return out
+
+
+def extend_paged(q, k_cache, v_cache, block_table, seq_lens, q_starts, scale, causal=True):
+    """q [T, H, d] -> o [T, H, d], lse [T, H] and Σ_j p_j |v_j| [T, H, d] (what
+    a rounding of the weights acts on). Request b's tokens are rows q_starts[b]
+    .. q_starts[b+1] - 1, the last of its seq_lens[b] cached tokens; rows of no
+    request are zeros with lse = -inf."""
+    T, H, d = q.shape
+    Hkv, bs = k_cache.shape[1:3]
+    o, around = np.zeros((T, H, d)), np.zeros((T, H, d))
+    lse = np.full((T, H), -np.inf)
+    for b, L in enumerate(int(n) for n in seq_lens):
+        lo, hi = int(q_starts[b]), int(q_starts[b + 1])
+        t = np.arange(L)
+        blocks = np.asarray(block_table)[b][t // bs]
+        K, V = (c[blocks, :, t % bs] for c in (k_cache, v_cache))  # [L, Hkv, d]
+        sight = L - (hi - lo) + np.arange(hi - lo) if causal else np.full(hi - lo, L - 1)
+        for h in range(H):
+            x = scale * (q[lo:hi, h] @ K[:, h // (H // Hkv)].T)
+            x = np.where(t[None, :] <= sight[:, None], x, -np.inf)
+            some = sight >= 0
+            if L == 0 or not some.any():
+                continue
+            m = x[some].max(-1, keepdims=True)
+            p = np.exp(x[some] - m)
+            total = p.sum(-1, keepdims=True)
+            rows = np.arange(lo, hi)[some]
+            o[rows, h] = p @ V[:, h // (H // Hkv)] / total
+            around[rows, h] = p @ np.abs(V[:, h // (H // Hkv)]) / total
+            lse[rows, h] = (m + np.log(total))[:, 0]
+    return o, lse, around
