@@ -162,9 +162,17 @@ struct Extend {
   int heads, hv;             // query heads a tile holds (at most 128), K/V heads times the parts its query heads are cut into
   int tpt;                   // tokens a query tile holds: 128 / heads
   int ctas, lc, may_chunk;   // see fa_extend_plan.cuh
+  unsigned bs_inverse;       // 2^32 / bs, rounded up (bs = 1: 1)
   int n_slots, n_long;       // workspace parts; long items there may be
   bool causal, zero_skipped;
   float scale_log2;
+  // The block of a key below 2^30: the product is at most key / 2^32 < 1 too
+  // large, so one too many at most.
+  __host__ __device__ int block_of(int key) const {
+    if (bs == 1) return key;
+    const int q = static_cast<int>((static_cast<unsigned long long>(bs_inverse) * static_cast<unsigned>(key)) >> 32);
+    return q * bs > key ? q - 1 : q;
+  }
 };
 // Sets the fields from `heads` to `n_long` from the sizes and `causal`; returns the workspace's bytes.
 size_t extend_sizes(Extend* p, int d, bool q4);

@@ -68,7 +68,7 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 64, "");
 
-template <int D>
+template <int D, int LOAD>
 struct Smem {
   static constexpr int PANELS = D / 64;
   static constexpr int STAGES = D == 64 ? 4 : 2;
@@ -84,7 +84,9 @@ struct Smem {
   static constexpr int NBARS = 3 + 2 * STAGES + 10 + 1 + 2 * RING;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int PLAN_OFF = SLOT_OFF + 16;
-  static constexpr int BYTES = PLAN_OFF + static_cast<int>(sizeof(PlanSmem));
+  static constexpr int RAW_OFF = (PLAN_OFF + static_cast<int>(sizeof(PlanSmem)) + 15) / 16 * 16;
+  // 4-bit caches: a tile's codes and pairs of K and of V
+  static constexpr int BYTES = RAW_OFF + (LOAD == CODES ? 2 * TK * (D / 2 + D / 8) : 0);
   // One CTA an SM (one 512-column TMEM allocation), 1024 bytes to align.
   static constexpr int ALLOC = BYTES + 1024 > 118784 ? BYTES + 1024 : 118784;
   static_assert(ALLOC <= 232448, "");
@@ -97,6 +99,22 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Barriers by their shared-memory address: in the softmax warps one base
+// register serves them all.
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, uint32_t* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer();
+    while (!(ok = mbar_try_wait(bar, parity)) && globaltimer() - t0 <= kWaitLimitNs) {
+    }
+    if (!ok) atomicExch(err, DEV_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The ring of piece descriptors, as one reader sees it: a warp that reads
@@ -138,11 +156,19 @@ __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 s, __nv_bflo
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// A load that stays where it is written, a step before its value is used, and
+// never under a branch: what a branch loads is copied where its paths meet, and
+// the copy waits for the load.
+__device__ __forceinline__ int load_entry(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 template <int D, int LOAD>
 __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ Extend p) {
-  using L = Smem<D>;
+  using L = Smem<D, LOAD>;
   constexpr int ST = L::STAGES, NT = Threads<LOAD>::N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -238,10 +264,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Without boxes 16 warps share the registers: 128 a thread at the launch, then
-  // 128 · (80 + 2 · 168 + 96) = 65536 where they are needed.
+  // The launch's registers go where they are needed: 128 · (104 + 2 · 200) of
+  // 384 · 168 with boxes, else 128 · (72 + 2 · 168 + 104) = 512 · 128.
   if (warp < 4) {
-    if (LOAD != BOXES) regs_down<80>();
+    regs_down<LOAD == BOXES ? 104 : 72>();
     if (warp == 0) {
       // --------------------------------------------------------------- pieces
       locate(p, sh, u_begin, &at);
@@ -438,8 +464,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       }
       const int bpt = TK / p.bs;
       struct Unit {
-        bool any;
-        int entry, kvh;  // this lane's table entry (-2: none wanted)
+        bool any, want;  // a unit; this lane has a box of the context
+        int entry, kvh;  // this lane's table entry
       };
       Pieces pieces(ring, piece_full, piece_empty, err);
       Piece x;
@@ -447,24 +473,23 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       int j = 0;
       bool more = true;
       auto fetch = [&]() -> Unit {  // the next unit
-        Unit t{false, -2, 0};
         if (more && ++j >= x.n) {
           more = pieces.read(&x) && x.n > 0;
           j = 0;
         }
-        if (!more) return t;
-        t.any = true;
-        t.kvh = x.kvh;
         const int bi = (x.kt0 + j) * bpt + lane;
-        if (lane < bpt && static_cast<long long>(bi) * p.bs < x.len) {
-          const long long ti = static_cast<long long>(x.b) * p.max_blocks + bi;
-          t.entry = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
-        }
+        Unit t;
+        t.any = more;
+        t.want = more && lane < bpt && static_cast<long long>(bi) * p.bs < x.len;
+        t.kvh = x.kvh;
+        const long long ti = t.want ? static_cast<long long>(x.b) * p.max_blocks + bi : 0;
+        t.want = t.want && in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err);
+        t.entry = load_entry(p.block_table + (t.want ? ti : 0));
         return t;
       };
       auto place = [&](const Unit& t) {  // the box's outer coordinate
-        if (t.entry >= 0 && t.entry < p.num_blocks) return t.entry * p.Hkv + t.kvh;
-        if (t.entry != -2) atomicExch(err, DEV_BAD_INDEX);
+        if (t.want && t.entry >= 0 && t.entry < p.num_blocks) return t.entry * p.Hkv + t.kvh;
+        if (t.want) atomicExch(err, DEV_BAD_INDEX);
         return p.num_blocks * p.Hkv;
       };
       auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int z) {
@@ -497,36 +522,47 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       for (int i = max(0, u - ST); i < u; ++i) mbar_wait_warp(&kv_full[i % ST], (i / ST) & 1, err);
     }
   } else if (warp < 12) {
-    if (LOAD != BOXES) regs_up<168>();
+    regs_up<LOAD == BOXES ? 200 : 168>();
     // -------------------------------------------------------------- softmax
     const int g = (warp - 4) >> 2;  // query tile
     const int quarter = warp & 3;   // TMEM lanes 32*quarter .. +31
     const int r = quarter * 32 + lane;
-    const int tt = r / p.heads, hh = r - tt * p.heads;  // token and head of this row within the tile
-    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_addr + g * TK;
-    const uint32_t o_addr = tmem + lane_addr + 256 + g * 128;
+    const uint32_t s_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * TK;
+    const uint32_t bars = smem_u32(s_full + g);  // s_full[g]; p_lo, p_hi, pv_done and o_free follow, two by two
+    constexpr uint32_t P_LO = 16, P_HI = 32, PV_DONE = 48, O_FREE = 64;
+    const uint32_t o_addr = s_addr + 256;
     const float scale_log2 = p.scale_log2;
-    int u0 = 0, seen = 0;  // units before the piece; units of this query tile so far
-    // The piece stays in the ring until this warp is through with it.
+    // Registers are short here (a row's 128 scores are in them): what a row
+    // needs of its piece is read from the ring each time, where the piece stays
+    // until this warp is through with it.
+    struct Row {  // this thread's row
+      bool valid;
+      int tok, head;  // token of the item, head of the K/V head's
+    };
+    auto row_of = [&](const Piece& x) {
+      const int tt = r / p.heads;
+      Row y{false, g * p.tpt + tt, r - tt * p.heads};
+      y.valid = r < filled && y.tok < x.ntok && y.head < x.heads;
+      return y;
+    };
+    constexpr int ALL = 0x7fffffff;
+    auto sight_of = [&](const Piece& x) {  // keys this row sees (a row without a token: ALL)
+      const Row y = row_of(x);
+      return !y.valid ? ALL : p.causal ? max(x.pos0 + y.tok + 1, 0) : x.len;
+    };
+    int u = 0, seen = 0;  // units of the CTA; units of this query tile
     for (int idx = 0;; ++idx) {
       if (!mbar_wait_warp(&piece_full[idx % RING], (idx / RING) & 1, err)) break;
       const Piece& x = ring[idx % RING];
       if (x.n == 0) break;
       bool ok = true;
-      const int n = g ? x.n1 : x.n0, kt0 = x.kt0, len = x.len;
-      const int tok = g * p.tpt + tt;
-      const bool valid = r < filled && tok < x.ntok && hh < x.heads;
-      const int sight = valid ? (p.causal ? max(x.pos0 + tok + 1, 0) : x.len) : 0x7fffffff;  // keys this row sees
-      const int sight_lo = __reduce_min_sync(0xffffffffu, sight);
-      const bool live = sight_lo != 0x7fffffff;  // some row of the warp has a token
+      const int sight_lo = __reduce_min_sync(0xffffffffu, sight_of(x));  // ALL: no row of the warp has a token
       float m = -INFINITY;  // exponent reference (log2 units of scaled scores)
-      float nm = 0.f;       // -m, or 0 while there is none
       float l = 0.f;        // running denominator relative to m
-      for (int j = 0; j < n; ++j, ++seen) {
-        const int k0 = (kt0 + j) * TK;
-        ok = mbar_wait(&s_full[g], seen & 1, err);
-        ok = __all_sync(0xffffffffu, ok);
+      const int u_next = u + x.n;
+      for (int j = 0; j < (g ? x.n1 : x.n0); ++j, ++seen, ++u) {
+        const int k0 = (x.kt0 + j) * TK;
+        ok = wait_at(bars, seen & 1, err);
         if (!ok) break;
         tc_fence_after();
         // A box brings whole cache blocks: slots past the context may hold
@@ -534,25 +570,25 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         // Their value rows are zeroed before the product reads them. (S of this
         // unit is there, so the barrier is at this unit's phase at least: its
         // parity wait is exact.)
-        if (LOAD == BOXES && k0 + TK > len) {
-          const int s = (u0 + j) % ST;
-          ok = mbar_wait_warp(&kv_full[s], ((u0 + j) / ST) & 1, err);
+        if (LOAD == BOXES && k0 + TK > x.len) {
+          const int s = u % ST;
+          ok = mbar_wait_warp(&kv_full[s], (u / ST) & 1, err);
           if (!ok) break;
-          if (k0 + r >= len)
+          if (k0 + r >= x.len)
             for (int i = 0; i < L::PANELS * 8; ++i)
               *reinterpret_cast<uint4*>(sV + s * L::TILE + (i >> 3) * L::PANEL + r * 128 + (i & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
         }
-        auto release = [&](uint64_t* bar) {  // this half of P is in TMEM
+        auto release = [&](uint32_t bar) {  // this half of P is in TMEM
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
+          if (lane == 0) arrive_at(bars + bar);
         };
-        if (!live) {  // no row to compute: what P holds for these rows reaches no other
-          release(&p_lo[g]);
-          release(&p_hi[g]);
+        if (sight_lo == ALL) {  // no row to compute: what P holds for these rows reaches no other
+          release(P_LO);
+          release(P_HI);
           continue;
         }
         uint32_t raw[4][32];
@@ -565,7 +601,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 #pragma unroll
         for (int c = 0; c < TK; ++c) y[c] = __uint_as_float(raw[c / 32][c % 32]);
         if (k0 + TK > sight_lo) {
-          const int mine = sight - k0;
+          const int mine = sight_of(x) - k0;
 #pragma unroll
           for (int c = 0; c < TK; ++c)
             if (c >= mine) y[c] = -INFINITY;
@@ -587,9 +623,13 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         };
         // The first half against the reference so far, before the tile's
         // maximum is known; again if that outgrew it (as in the forward).
+        auto minus = [&]() {  // -m; 0 for a row that has seen no key: 2^-inf = 0 throughout
+          const float v = m == -INFINITY ? 0.f : -m;
+          return make_float2(v, v);
+        };
         if (j > 0) {
-          p_chunk(0, make_float2(nm, nm));
-          p_chunk(32, make_float2(nm, nm));
+          p_chunk(0, minus());
+          p_chunk(32, minus());
         }
         float mx[8];
 #pragma unroll
@@ -604,10 +644,9 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           const float m_new = fmaxf(m, tile_max);
           const float alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);  // 0 on a row's first key
           m = m_new;
-          nm = m == -INFINITY ? 0.f : -m;  // a row that has seen no key: 2^-inf = 0 throughout
           l *= alpha;
           if (j > 0) {
-            ok = mbar_wait_warp(&pv_done[g], (seen - 1) & 1, err);
+            ok = wait_at(bars + PV_DONE, (seen - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -627,33 +666,39 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[q] = make_float2(0.f, 0.f);
-          p_chunk(0, make_float2(nm, nm));
-          p_chunk(32, make_float2(nm, nm));
+          p_chunk(0, minus());
+          p_chunk(32, minus());
         }
-        release(&p_lo[g]);
-        p_chunk(64, make_float2(nm, nm));
-        p_chunk(96, make_float2(nm, nm));
-        release(&p_hi[g]);
+        release(P_LO);
+        p_chunk(64, minus());
+        p_chunk(96, minus());
+        release(P_HI);
         l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       }
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
-      if (n > 0) {
-        ok = mbar_wait_warp(&pv_done[g], (seen - 1) & 1, err);
+      const bool any = (g ? x.n1 : x.n0) > 0;
+      if (any) {
+        ok = wait_at(bars + PV_DONE, (seen - 1) & 1, err);
         if (!ok) break;
         tc_fence_after();
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
       const bool none = l == 0.f;                  // no key: zeros, whatever O holds
       const float lse = none ? -INFINITY : (m + __log2f(l)) * LN2;
-      const long long orow = static_cast<long long>(x.tok0 + tok) * p.H + x.head0 + hh;
+      const Row y = row_of(x);
+      const bool valid = y.valid;
+      const long long orow = static_cast<long long>(x.tok0 + y.tok) * p.H + x.head0 + y.head;
       const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        if (n > 0 && live) {
+        if (any && sight_lo != ALL) {
           tmem_ld32(o_addr + c, o);
           tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         float f[32];
 #pragma unroll
@@ -684,17 +729,17 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           p.lse_part[prow] = lse;
         }
       }
-      if (n > 0) {  // O is read: the next piece's products may overwrite it
+      if (any) {  // O is read: the next piece's products may overwrite it
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[g]);
+        if (lane == 0) arrive_at(bars + O_FREE);
       }
-      u0 += x.n;
+      u = u_next;
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_empty[idx % RING]);
     }
   } else if constexpr (LOAD != BOXES) {
-    regs_down<96>();
+    regs_down<104>();
     // ----------------------------------------- K and V row by row, or unpacked
     // Each of four warps takes 32 rows of a tile, lane i the place of row i.
     constexpr uint32_t NO_ROW = 0xffffffffu;  // zeros (the host keeps the cache below 2^32 - 1 rows)
@@ -714,22 +759,20 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     int j = 0;
     bool more = true;
     auto fetch = [&]() -> Raw {
-      Raw t{false, false, -1, 0, 0};
       if (more && ++j >= x.n) {
         more = pieces.read(&x) && x.n > 0;
         j = 0;
       }
-      if (!more) return t;
-      t.any = true;
       const int key = (x.kt0 + j) * TK + w * 32 + lane;
-      if (key < x.len) {
-        const int bi = key / p.bs;
-        const long long ti = static_cast<long long>(x.b) * p.max_blocks + bi;
-        t.want = true;
-        t.kvh = x.kvh;
-        t.slot = key - bi * p.bs;
-        t.entry = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
-      }
+      Raw t;
+      t.any = more;
+      t.want = more && key < x.len;
+      const int bi = p.block_of(t.want ? key : 0);
+      t.kvh = x.kvh;
+      t.slot = key - bi * p.bs;
+      const long long ti = static_cast<long long>(t.want ? x.b : 0) * p.max_blocks + bi;
+      t.want = t.want && in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err);
+      t.entry = load_entry(p.block_table + (t.want ? ti : 0));
       return t;
     };
     auto resolve = [&](const Raw& t) -> Unit {
@@ -779,47 +822,54 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       cp_async_commit();
       cp_async_wait<0>();  // no copy outlives the CTA
     } else {
-      // A lane holds 32 codes (16 bytes) of a row and their group's pair; its
-      // loads for the next tile are under way while it unpacks this one.
+      // A lane takes 32 codes (16 bytes) of a row and their group's pair. They
+      // wait in shared memory, in a place of the lane's own, for the step they
+      // are unpacked in: the copies of the next tile are under way meanwhile.
+      // (Held in registers instead, a tile took 6000 clocks: the compiler's waits
+      // for one load cover others.)
       constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte pieces a row, rows a step; CPR steps
       const int quarter = lane % CPR, sub = lane / CPR;
-      struct Codes {
-        uint4 n[CPR];
-        uint32_t sz[CPR];
-      };
-      auto fetch_codes = [&](const void* cache, const uint32_t* scale, const Unit& t, Codes& y) {
+      uint8_t* kraw = smem + L::RAW_OFF + w * (2 * CPR * 32 * 20) + lane * 16;
+      uint8_t* vraw = kraw + CPR * 32 * 20;
+      constexpr int PAIRS = CPR * 32 * 16;  // the pairs stand behind the codes, 4 bytes a lane
+      auto fetch_codes = [&](const void* cache, const uint32_t* scale, const Unit& t, uint8_t* raw) {
 #pragma unroll
         for (int k = 0; k < CPR; ++k) {
           const uint32_t row = __shfl_sync(0xffffffffu, t.row, k * RPI + sub);
-          y.n[k] = make_uint4(0u, 0u, 0u, 0u);
-          y.sz[k] = 0u;  // step and centre 0: zeros
-          if (row != NO_ROW && in_range(row, 1, rows_all, err)) {
-            y.n[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + static_cast<size_t>(row) * (D / 2)) + quarter);
-            y.sz[k] = __ldg(scale + static_cast<size_t>(row) * (D / 64) + quarter / 2);
-          }
+          const bool live = row != NO_ROW && in_range(row, 1, rows_all, err);  // else zeros: step and centre 0
+          const size_t at_row = live ? row : 0u;
+          cp_async_16(raw + k * 512, static_cast<const uint8_t*>(cache) + at_row * (D / 2) + quarter * 16, live ? 16u : 0u);
+          cp_async_4(raw + PAIRS + k * 128 - lane * 12, scale + at_row * (D / 64) + quarter / 2, live ? 4u : 0u);
         }
+        cp_async_commit();
       };
       // Rows r and r + 1 and both panels meet in one store: with the words of
       // the second panel's lanes two places on, no two lanes share a bank.
-      auto unpack = [&](uint8_t* dst, const Codes& y) {
-        const bool swap = quarter & 2;
+      const bool swap = quarter & 2;
+      uint32_t put[4];  // where a step's words go: row `sub` of it (rows a step on are RPI · 128 bytes on)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        put[e] = (quarter >> 1) * L::PANEL + (w * 32 + sub) * 128 +
+                 ((((quarter & 1) * 4 + (e ^ (swap ? 2 : 0))) ^ (sub & 7)) << 4);
+      auto unpack = [&](uint8_t* dst, const uint8_t* raw) {
+        uint4 code[CPR];
+        uint32_t pair[CPR];
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) {  // all loads first: what is stored may be what is loaded, for all the compiler knows
+          code[k] = *reinterpret_cast<const uint4*>(raw + k * 512);
+          pair[k] = *reinterpret_cast<const uint32_t*>(raw + PAIRS + k * 128 - lane * 12);
+        }
 #pragma unroll
         for (int k = 0; k < CPR; ++k) {
-          const int r = w * 32 + k * RPI + sub;
-          uint32_t sbits = __byte_perm(y.sz[k], 0, 0x1010);
-          const uint32_t zbits = __byte_perm(y.sz[k], 0, 0x3232);
+          const uint32_t sbits = __byte_perm(pair[k], 0, 0x1010), zbits = __byte_perm(pair[k], 0, 0x3232);
           const __nv_bfloat162 eighth = __halves2bfloat162(__ushort_as_bfloat16(0x3f80), __ushort_as_bfloat16(0x3e00));  // 1, 1/8
-          const __nv_bfloat162 s2 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&sbits), eighth);
+          const __nv_bfloat162 s2 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&sbits), eighth);
           const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162*>(&zbits);
-          const uint4 c = y.n[k];
+          const uint4 c = code[k];
           const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
-          uint8_t* base = dst + (quarter >> 1) * L::PANEL + r * 128;
-          const int c0 = (quarter & 1) * 4;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int chunk = c0 + (e ^ (swap ? 2 : 0));
-            *reinterpret_cast<uint4*>(base + ((chunk ^ (r & 7)) << 4)) = values8(word[e], s2, z2);
-          }
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(dst + put[e] + k * (RPI * 128)) = values8(word[e], s2, z2);
         }
       };
       auto publish = [&](uint64_t* bar) {
@@ -827,34 +877,35 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
-      // K of unit u + 1 and V of unit u, loaded a step ahead.
-      Codes kc, vc;
+      // K of unit u + 1 and V of unit u, copied a step ahead.
       Raw a = fetch(), b = fetch();
       Unit cur = resolve(a);
-      fetch_codes(p.k_cache, p.k_scale, cur, kc);
-      fetch_codes(p.v_cache, p.v_scale, cur, vc);
+      fetch_codes(p.k_cache, p.k_scale, cur, kraw);
+      fetch_codes(p.v_cache, p.v_scale, cur, vraw);
       Unit nxt = resolve(b);
       Raw far = fetch();
-      unpack(sK, kc);
+      cp_async_wait<1>();
+      unpack(sK, kraw);
       publish(k0_full);
-      fetch_codes(p.k_cache, p.k_scale, nxt, kc);
+      fetch_codes(p.k_cache, p.k_scale, nxt, kraw);
       while (ok) {
         const int s = u % ST, s1 = (u + 1) % ST;
         const Unit after = resolve(far);
         far = fetch();
         if (u >= ST - 1) ok = mbar_wait_warp(&kv_empty[s], ((u - (ST - 1)) / ST) & 1, err);
         if (!ok) break;
-        unpack(sV + s * L::TILE, vc);
-        fetch_codes(p.v_cache, p.v_scale, nxt, vc);
-        if (nxt.any) {
-          unpack(sK + s1 * L::TILE, kc);
-          fetch_codes(p.k_cache, p.k_scale, after, kc);
-        }
+        cp_async_wait<1>();
+        unpack(sV + s * L::TILE, vraw);
+        fetch_codes(p.v_cache, p.v_scale, nxt, vraw);
+        cp_async_wait<1>();
+        if (nxt.any) unpack(sK + s1 * L::TILE, kraw);
+        fetch_codes(p.k_cache, p.k_scale, after, kraw);
         publish(&kv_full[s]);
         ++u;
         if (!nxt.any) break;
         nxt = after;
       }
+      cp_async_wait<0>();  // no copy outlives the CTA
     }
   }
   tc_fence_before();
@@ -1018,9 +1069,9 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
     tk = tv = tq;  // unused
   }
   auto kern = extend_kernel<D, LOAD>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::ALLOC);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, LOAD>::ALLOC);
   if (e != cudaSuccess) return e;
-  kern<<<p.ctas, Threads<LOAD>::N, Smem<D>::ALLOC, stream>>>(tq, tk, tv, p);
+  kern<<<p.ctas, Threads<LOAD>::N, Smem<D, LOAD>::ALLOC, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   const int jobs = p.ctas - 1 + p.n_long;
   if (e != cudaSuccess || jobs == 0) return e;  // one CTA: nothing is cut
@@ -1040,6 +1091,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
 
 size_t extend_sizes(Extend* p, int d, bool q4) {
   using namespace ext;
+  p->bs_inverse = static_cast<unsigned>((1ull << 32) / p->bs + 1);
   const int G = p->H / p->Hkv, parts = (G + BM - 1) / BM;
   p->heads = (G + parts - 1) / parts;
   p->hv = p->Hkv * parts;

@@ -157,6 +157,12 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, uint32_t
                "l"(__cvta_generic_to_global(src)), "r"(src_bytes)
                : "memory");
 }
+// The same for 4 bytes.
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(src_bytes)
+               : "memory");
+}
 // Arrive on `bar` once every cp.async this thread issued before has landed.
 // The arrival is one of the barrier's expected count (noinc: the count is
 // not raised for it), so the thread goes on without waiting for its copies.
