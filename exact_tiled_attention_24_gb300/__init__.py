@@ -37,6 +37,7 @@ __all__ = [
     "fwd_bwd_host",
     "softmax_host",
     "rope_tables",
+    "rope_axes",
     "qk_norm_rope",
     "qk_norm_rope_bwd",
     "qk_norm_rope_bwd_workspace_bytes",
@@ -101,6 +102,10 @@ EXPORTED_SYMBOLS = (
     "fa_append_paged_q4",
     "fa_decode_q4_splits",
     "fa_decode_paged_q4",
+    "fa_qk_norm_rope_axes",
+    "fa_qk_norm_rope_axes_bwd",
+    "fa_append_paged_axes",
+    "fa_append_paged_q4_axes",
     "fa_extend_workspace_bytes",
     "fa_extend_paged",
     "fa_extend_paged_q4",
@@ -119,6 +124,7 @@ _NORM_ROPE_ARGS = struct.Struct("@" + 4 * _HEADS + "5P10if")
 _NORM_ROPE_GRADS = struct.Struct("@" + 2 * _HEADS + "3PN")
 _APPEND_ARGS = struct.Struct("@" + 4 * _TOKENS + "13P12if")
 _DECODE_Q4_ARGS = struct.Struct("@10PN8if")
+_ROPE_AXES = struct.Struct("@Pi64s")
 _EXTEND_ARGS = struct.Struct("@11PN10if")
 _ZERO_SKIPPED = 2  # FA_ZERO_SKIPPED
 
@@ -194,6 +200,14 @@ def lib() -> ctypes.CDLL:
         L.fa_decode_q4_splits.restype = i
         L.fa_decode_paged_q4.argtypes = [vp, vp]
         L.fa_decode_paged_q4.restype = i
+        L.fa_qk_norm_rope_axes.argtypes = [vp, vp, vp]
+        L.fa_qk_norm_rope_axes.restype = i
+        L.fa_qk_norm_rope_axes_bwd.argtypes = [vp, vp, vp, vp]
+        L.fa_qk_norm_rope_axes_bwd.restype = i
+        L.fa_append_paged_axes.argtypes = [vp, vp, vp]
+        L.fa_append_paged_axes.restype = i
+        L.fa_append_paged_q4_axes.argtypes = [vp, vp, vp]
+        L.fa_append_paged_q4_axes.restype = i
         L.fa_extend_workspace_bytes.argtypes = [i] * 7
         L.fa_extend_workspace_bytes.restype = sz
         L.fa_extend_paged.argtypes = [vp, vp]
@@ -584,6 +598,20 @@ def rope_tables(n_pos, rot, base=10000.0, device=None):
     return angle.cos().float(), angle.sin().float()
 
 
+def rope_axes(sections, in_turn=False) -> bytes:
+    """The axis of each rotated pair, for the `axes` of qk_norm_rope and the
+    appends: sections[a] pairs belong to axis a (up to four axes, rot/2 pairs in
+    all), one section after another, or with in_turn dealt 0, 1, 2, 0, 1, 2 ...
+    while an axis has pairs left. Any other assignment is a bytes of rot/2 axis
+    numbers."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections: one to four axes, numbers of pairs")
+    if not in_turn:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for turn in range(max(left)) for a, n in enumerate(left) if turn < n)
+
+
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -643,10 +671,18 @@ def _rope_args(cos, sin, q_weight, k_weight, d, device):
     return (cp, sp), (qp, kp), rot, n_pos, w32
 
 
-def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, interleaved, names, out):
+def _pack_axes(axes, positions, n_axes, rot):
+    """The packed fa_rope_axes of checked positions [n_axes, ...]."""
+    axes = bytes(axes)
+    if len(axes) != rot // 2:
+        raise ValueError("axes: one axis number for each of the rot/2 pairs")
+    return _ROPE_AXES.pack(positions.data_ptr(), n_axes, axes)
+
+
+def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, interleaved, names, out, axes):
     """Check qk_norm_rope's arguments; a and b are the tensors beside q and k
-    (the outputs, made here if None, or their gradients). Returns a, b and the
-    packed fa_norm_rope_args."""
+    (the outputs, made here if None, or their gradients). Returns a, b, the
+    packed fa_norm_rope_args and the packed fa_rope_axes (None without axes)."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise ValueError("expected [B, H, N, d] tensors")
     B, H, N, d = qs = q.shape
@@ -660,7 +696,14 @@ def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, in
         raise ValueError("neither weights (norm) nor cos and sin (rotation) given")
     tables, weights, rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
     per_batch = pp = 0
-    if positions is not None:
+    packed = None
+    if axes is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() < 2 or cos is None:
+            raise ValueError("axes need cos, sin and positions [axes, N] or [axes, B, N]")
+        per_batch = int(positions.dim() == 3)
+        _expect(positions, "positions", (positions.shape[0], B, N) if per_batch else (positions.shape[0], N), _I32, dev)
+        packed = _pack_axes(axes, positions, positions.shape[0], rot)
+    elif positions is not None:
         per_batch = int(isinstance(positions, torch.Tensor) and positions.dim() == 2)
         _expect(positions, "positions", (B, N) if per_batch else (N,), _I32, dev)
         pp = positions.data_ptr()
@@ -670,11 +713,11 @@ def _norm_rope_args(q, k, a, b, cos, sin, positions, q_weight, k_weight, eps, in
     a, ar = _made(qs, dev) if a is None else (a, _rows(a, names[0], qs, dev, out))
     b, br = _made(ks, dev) if b is None else (b, _rows(b, names[1], ks, dev, out))
     return a, b, _NORM_ROPE_ARGS.pack(*qr, *kr, *ar, *br, *tables, pp, *weights, B, H, Hkv, N, d, rot, n_pos,
-                                      per_batch, w32, 1 if interleaved else 0, eps)
+                                      per_batch, w32, 1 if interleaved else 0, eps), packed
 
 
 def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
-                 interleaved=False, q_out=None, k_out=None):
+                 interleaved=False, q_out=None, k_out=None, axes=None):
     """Per-head norm (with q_weight, k_weight [d], bf16 or fp32) and position
     rotation (with cos, sin [n_pos, rot/2] fp32) of q [B, H, N, d] and k
     [B, Hkv, N, d], in one pass. Returns (q_out, k_out), contiguous unless
@@ -684,10 +727,17 @@ def qk_norm_rope(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weig
     contiguous, such as those of a packed projection; an output may be its
     input. positions: int32 [N] or [B, N], the token's row of the tables
     (default: token n is at position n). interleaved pairs dimensions
-    (2i, 2i + 1), else (i, i + rot/2)."""
-    q_out, k_out, args = _norm_rope_args(q, k, q_out, k_out, cos, sin, positions, q_weight, k_weight, eps,
-                                         interleaved, ("q_out", "k_out"), True)
-    _check(lib().fa_qk_norm_rope(args, _stream(q.device)), "fa_qk_norm_rope")
+    (2i, 2i + 1), else (i, i + rot/2).
+
+    axes (rope_axes' bytes: the axis of each pair) gives tokens a position on
+    each of up to four axes, such as time, height and width: positions are then
+    int32 [axes, N] or [axes, B, N], and a pair turns by its own axis's."""
+    q_out, k_out, args, packed = _norm_rope_args(q, k, q_out, k_out, cos, sin, positions, q_weight, k_weight, eps,
+                                                 interleaved, ("q_out", "k_out"), True, axes)
+    if packed is None:
+        _check(lib().fa_qk_norm_rope(args, _stream(q.device)), "fa_qk_norm_rope")
+    else:
+        _check(lib().fa_qk_norm_rope_axes(args, packed, _stream(q.device)), "fa_qk_norm_rope_axes")
     return q_out, k_out
 
 
@@ -696,18 +746,19 @@ def qk_norm_rope_bwd_workspace_bytes(B, N, d) -> int:
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None,
-                     eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None):
+                     eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None, axes=None):
     """Gradient of qk_norm_rope for the output gradients dq_out, dk_out (bwd's
     dq and dk). Returns (dq, dk, dq_weight, dk_weight): dq and dk contiguous
     bf16 unless given (strided views are allowed, as in qk_norm_rope), the
     weight gradients fp32 [d] whatever the weights' type (None without
-    weights; q and k are then not read and may be None)."""
+    weights; q and k are then not read and may be None). axes as in
+    qk_norm_rope."""
     if q_weight is None and k_weight is None:
         q, k = dq_out, dk_out
     if dq_out is None or dk_out is None:
         raise ValueError("expected output gradients of both q and k")
-    _, _, args = _norm_rope_args(q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, eps, interleaved,
-                                 ("dq_out", "dk_out"), False)
+    _, _, args, packed = _norm_rope_args(q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, eps,
+                                         interleaved, ("dq_out", "dk_out"), False, axes)
     dev = q.device
     dq, dqr = _made(q.shape, dev) if dq is None else (dq, _rows(dq, "dq", q.shape, dev, True))
     dk, dkr = _made(k.shape, dev) if dk is None else (dk, _rows(dk, "dk", k.shape, dev, True))
@@ -725,12 +776,15 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos=None, sin=None, positions=None, q
         wp = workspace.data_ptr()
         qp, kp = dqw.data_ptr(), dkw.data_ptr()
     grads = _NORM_ROPE_GRADS.pack(*dqr, *dkr, qp, kp, wp, ws_bytes)
-    _check(lib().fa_qk_norm_rope_bwd(args, grads, _stream(dev)), "fa_qk_norm_rope_bwd")
+    if packed is None:
+        _check(lib().fa_qk_norm_rope_bwd(args, grads, _stream(dev)), "fa_qk_norm_rope_bwd")
+    else:
+        _check(lib().fa_qk_norm_rope_axes_bwd(args, packed, grads, _stream(dev)), "fa_qk_norm_rope_axes_bwd")
     return dq, dk, dqw, dkw
 
 
 def _append(entry, k, v, caches, values, block_table, positions, requests, cos, sin, q, q_weight, k_weight, eps,
-            interleaved, q_out):
+            interleaved, q_out, rope_positions, axes):
     """Check an append's arguments (the caches' own by the caller) and call it."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
@@ -765,13 +819,30 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
     elif T > B:
         raise ValueError("more tokens than requests: say which request each token belongs to")
     tables, weights, rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
+    packed = None
+    if rope_positions is not None:
+        if cos is None or not isinstance(rope_positions, torch.Tensor):
+            raise ValueError("rope_positions need cos and sin")
+        if axes is None:
+            _expect(rope_positions, "rope_positions", (T,), _I32, dev)
+            packed = _pack_axes(bytes(rot // 2), rope_positions, 1, rot)
+        else:
+            n_axes = rope_positions.shape[0] if rope_positions.dim() else 0
+            _expect(rope_positions, "rope_positions", (n_axes, T), _I32, dev)
+            packed = _pack_axes(axes, rope_positions, n_axes, rot)
+    elif axes is not None:
+        raise ValueError("axes need rope_positions [axes, T]")
     k_cache = caches[0]
     ks, vs, kv, vv = (caches[1].data_ptr(), caches[3].data_ptr(), *values) if len(caches) == 4 else (0, 0, 0, 0)
     args = _APPEND_ARGS.pack(
         *qr, *kr, *vr, *qor, k_cache.data_ptr(), caches[-1 if len(caches) == 2 else 2].data_ptr(), ks, vs, kv, vv,
         block_table.data_ptr(), positions.data_ptr(), rp, *tables, *weights, T, B, H, Hkv, d, k_cache.shape[0],
         k_cache.shape[2], max_blocks, rot, n_pos, w32 | zero, 1 if interleaved else 0, eps)
-    _check(getattr(lib(), entry)(args, _stream(dev)), entry)
+    if packed is None:
+        _check(getattr(lib(), entry)(args, _stream(dev)), entry)
+    else:
+        entry += "_axes"
+        _check(getattr(lib(), entry)(args, packed, _stream(dev)), entry)
     return q_out
 
 
@@ -784,7 +855,7 @@ def _expect_cache(t, name, Hkv, last, dtype, device):
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, cos=None, sin=None, q=None,
-                 q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None):
+                 q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None, rope_positions=None, axes=None):
     """Write new tokens' keys (after norm and rotation, as in qk_norm_rope)
     and values k, v [T, Hkv, d] into the paged cache k_cache, v_cache
     [num_blocks, Hkv, block_size, d] bf16, in place. Token t goes to position
@@ -796,13 +867,16 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
     returns them ([T, H, d]: decode_paged's q), else None. Rows of skipped
     tokens are zeros in a q_out made here and stay as they were in a given one.
     k, v, q and q_out may be strided views, such as those of a packed
-    projection."""
+    projection.
+
+    rope_positions turns keys and queries by positions of their own, apart from
+    the slots: int32 [T], or with axes (as in qk_norm_rope) [axes, T]."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k and v [T, Hkv, d]")
     _expect_cache(k_cache, "k_cache", k.shape[1], k.shape[2], _BF16, k.device)
     _expect(v_cache, "v_cache", k_cache.shape, _BF16, k.device)
     return _append("fa_append_paged", k, v, (k_cache, v_cache), None, block_table, positions, requests, cos, sin, q,
-                   q_weight, k_weight, eps, interleaved, q_out)
+                   q_weight, k_weight, eps, interleaved, q_out, rope_positions, axes)
 
 
 def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
@@ -816,7 +890,7 @@ def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
 
 def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, positions, requests=None, cos=None,
                     sin=None, q=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
-                    k_values=None, v_values=None):
+                    k_values=None, v_values=None, rope_positions=None, axes=None):
     """append_paged into a cache held in 4 bits: k_cache, v_cache
     [num_blocks, Hkv, block_size, d/2] uint8 codes and k_scale, v_scale
     [num_blocks, Hkv, block_size, d/64, 2] bf16 (step, centre) of each group
@@ -832,7 +906,7 @@ def append_paged_q4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, posit
         _expect(v_values, "v_values", k.shape, _BF16, k.device)
         values = (k_values.data_ptr(), v_values.data_ptr())
     return _append("fa_append_paged_q4", k, v, (k_cache, k_scale, v_cache, v_scale), values, block_table, positions,
-                   requests, cos, sin, q, q_weight, k_weight, eps, interleaved, q_out)
+                   requests, cos, sin, q, q_weight, k_weight, eps, interleaved, q_out, rope_positions, axes)
 
 
 def decode_q4_splits(B, H, Hkv, block_size, max_blocks) -> int:

@@ -302,8 +302,20 @@ static fa::HeadRows head_rows(const fa_heads* t, int B, int H, int N, int d) {
           t->stride_b * (B - 1) + t->stride_h * (H - 1) + t->stride_n * (N - 1) + d};
 }
 
-// Checks of the training form; on FA_OK fills p.
-static int norm_rope_args(fa::NormRope* p, const fa_norm_rope_args* a, const fa_heads* q, const fa_heads* k) {
+// Several position axes for rot / 2 pairs; on FA_OK fills out ([n_axes][stride] positions).
+static int check_axes(fa::Axes* out, const fa_rope_axes* x, int rot, long long stride) {
+  if (!x->positions || rot == 0 || x->n_axes < 1 || x->n_axes > FA_MAX_AXES) return FA_ERR_INVALID_ARG;
+  *out = fa::Axes{x->positions, stride, x->n_axes, {0, 0}};
+  for (int i = 0; i < rot / 2; ++i) {
+    if (x->pair_axis[i] >= x->n_axes) return FA_ERR_INVALID_ARG;
+    out->of_pair[i / 32] |= static_cast<unsigned long long>(x->pair_axis[i]) << (2 * (i % 32));
+  }
+  return (reinterpret_cast<uintptr_t>(x->positions) & 3u) ? FA_ERR_MISALIGNED : FA_OK;
+}
+
+// Checks of the training form; on FA_OK fills p. x: several axes, or NULL.
+static int norm_rope_args(fa::NormRope* p, const fa_norm_rope_args* a, const fa_rope_axes* x, const fa_heads* q,
+                          const fa_heads* k) {
   const fa_heads* ts[] = {q, k, &a->q_out, &a->k_out};
   for (const fa_heads* t : ts)
     if (!t->ptr || !heads_strides_ok(t)) return FA_ERR_INVALID_ARG;
@@ -315,7 +327,8 @@ static int norm_rope_args(fa::NormRope* p, const fa_norm_rope_args* a, const fa_
       FA_OK)
     return st;
   if (a->rot == 0 && !a->q_weight) return FA_ERR_INVALID_ARG;                     // nothing to do
-  if (a->rot > 0 && !a->positions && a->n_pos < a->N) return FA_ERR_INVALID_ARG;  // token n is at position n
+  if (x && a->positions) return FA_ERR_INVALID_ARG;  // x has them
+  if (!x && a->rot > 0 && !a->positions && a->n_pos < a->N) return FA_ERR_INVALID_ARG;  // token n is at position n
   if (a->H > 65536 || a->Hkv > 65536) return FA_ERR_UNSUPPORTED;
   for (const fa_heads* t : ts)
     if (!heads_aligned(t)) return FA_ERR_MISALIGNED;
@@ -334,15 +347,20 @@ static int norm_rope_args(fa::NormRope* p, const fa_norm_rope_args* a, const fa_
   p->w32 = a->weight_fp32 != 0, p->interleaved = a->interleaved != 0;
   p->B = a->B, p->H = a->H, p->Hkv = a->Hkv, p->N = a->N, p->rot = a->rot, p->n_pos = a->n_pos;
   p->eps = a->eps;
-  return FA_OK;
+  return x ? check_axes(&p->axes, x, a->rot, a->positions_per_batch ? static_cast<long long>(a->B) * a->N : a->N) : FA_OK;
 }
 
-int fa_qk_norm_rope(const fa_norm_rope_args* a, void* stream) {
+static int norm_rope(const fa_norm_rope_args* a, const fa_rope_axes* x, void* stream) {
   if (!a) return FA_ERR_INVALID_ARG;
   fa::NormRope p;
-  const int st = norm_rope_args(&p, a, &a->q, &a->k);
+  const int st = norm_rope_args(&p, a, x, &a->q, &a->k);
   if (st != FA_OK) return st;
   return map_cuda(fa::launch_norm_rope(p, a->d, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_qk_norm_rope(const fa_norm_rope_args* a, void* stream) { return norm_rope(a, nullptr, stream); }
+int fa_qk_norm_rope_axes(const fa_norm_rope_args* a, const fa_rope_axes* x, void* stream) {
+  return x ? norm_rope(a, x, stream) : FA_ERR_INVALID_ARG;
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d) {
@@ -350,12 +368,12 @@ size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d) {
   return fa::norm_rope_bwd_partial_bytes(d);
 }
 
-int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream) {
+static int norm_rope_bwd(const fa_norm_rope_args* a, const fa_rope_axes* x, const fa_norm_rope_grads* g, void* stream) {
   if (!a || !g) return FA_ERR_INVALID_ARG;
   const bool norm = a->q_weight || a->k_weight;
   fa::NormRope p;
   // no norm: q and k are not read
-  const int st = norm_rope_args(&p, a, norm ? &a->q : &a->q_out, norm ? &a->k : &a->k_out);
+  const int st = norm_rope_args(&p, a, x, norm ? &a->q : &a->q_out, norm ? &a->k : &a->k_out);
   if (st != FA_OK) return st;
   if (!g->dq.ptr || !g->dk.ptr || !heads_strides_ok(&g->dq) || !heads_strides_ok(&g->dk)) return FA_ERR_INVALID_ARG;
   if (norm && (!g->dq_weight || !g->dk_weight)) return FA_ERR_INVALID_ARG;
@@ -368,6 +386,14 @@ int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g,
   p.dk = head_rows(&g->dk, a->B, a->Hkv, a->N, a->d);
   return map_cuda(fa::launch_norm_rope_bwd(p, a->d, static_cast<float*>(g->workspace), g->dq_weight, g->dk_weight,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream) {
+  return norm_rope_bwd(a, nullptr, g, stream);
+}
+int fa_qk_norm_rope_axes_bwd(const fa_norm_rope_args* a, const fa_rope_axes* x, const fa_norm_rope_grads* g,
+                             void* stream) {
+  return x ? norm_rope_bwd(a, x, g, stream) : FA_ERR_INVALID_ARG;
 }
 
 // Sizes of a paged cache: its token rows are indexed in 32 bits.
@@ -388,7 +414,7 @@ static fa::TokenRows token_rows(const fa_tokens* t, int T, int H, int d) {
           t->stride_t * (T - 1) + t->stride_h * (H - 1) + d};
 }
 
-static int append(const fa_append_args* a, bool q4, void* stream) {
+static int append(const fa_append_args* a, const fa_rope_axes* x, bool q4, void* stream) {
   if (!a || !a->k.ptr || !a->v.ptr || !a->k_cache || !a->v_cache || !a->block_table || !a->positions)
     return FA_ERR_INVALID_ARG;
   if (!tokens_strides_ok(&a->k) || !tokens_strides_ok(&a->v)) return FA_ERR_INVALID_ARG;
@@ -434,11 +460,18 @@ static int append(const fa_append_args* a, bool q4, void* stream) {
   p.num_blocks = a->num_blocks, p.bs = a->block_size, p.max_blocks = a->max_blocks_per_seq;
   p.rot = a->rot, p.n_pos = a->n_pos;
   p.eps = a->eps;
+  if (x && (st = check_axes(&p.axes, x, a->rot, a->T)) != FA_OK) return st;
   return map_cuda(fa::launch_append(p, a->d, q4, static_cast<cudaStream_t>(stream)));
 }
 
-int fa_append_paged(const fa_append_args* a, void* stream) { return append(a, false, stream); }
-int fa_append_paged_q4(const fa_append_args* a, void* stream) { return append(a, true, stream); }
+int fa_append_paged(const fa_append_args* a, void* stream) { return append(a, nullptr, false, stream); }
+int fa_append_paged_q4(const fa_append_args* a, void* stream) { return append(a, nullptr, true, stream); }
+int fa_append_paged_axes(const fa_append_args* a, const fa_rope_axes* x, void* stream) {
+  return x ? append(a, x, false, stream) : FA_ERR_INVALID_ARG;
+}
+int fa_append_paged_q4_axes(const fa_append_args* a, const fa_rope_axes* x, void* stream) {
+  return x ? append(a, x, true, stream) : FA_ERR_INVALID_ARG;
+}
 
 int fa_decode_q4_splits(int B, int H, int Hkv, int block_size, int max_blocks_per_seq) {
   if (B < 1 || H < 1 || check_heads(H, Hkv) != FA_OK || check_cache(Hkv, 1, block_size, max_blocks_per_seq) != FA_OK)

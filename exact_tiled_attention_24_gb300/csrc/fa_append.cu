@@ -60,13 +60,14 @@ struct Slot {
   bool live;
   int pos, block;
 };
+template <bool AXES>
 __device__ __forceinline__ Slot slot_of(const Append& p, long long t, uint32_t* err) {
   Slot s{false, 0, 0};
   if (t >= p.T || !in_range(t, 1, p.T, err)) return s;
   const int req = p.requests ? p.requests[t] : static_cast<int>(t);
   const int pos = p.positions[t];
   if (req < 0 || pos < 0) return s;
-  if (req < p.B && pos / p.bs < p.max_blocks && (p.rot == 0 || pos < p.n_pos)) {
+  if (req < p.B && pos / p.bs < p.max_blocks && (AXES || p.rot == 0 || pos < p.n_pos)) {
     const long long ti = static_cast<long long>(req) * p.max_blocks + pos / p.bs;
     const int blk = in_range(ti, 1, static_cast<long long>(p.B) * p.max_blocks, err) ? p.block_table[ti] : -1;
     if (blk >= 0 && blk < p.num_blocks) return Slot{true, pos, blk};
@@ -79,7 +80,7 @@ __device__ __forceinline__ Slot slot_of(const Append& p, long long t, uint32_t* 
 // keys or values (blockIdx.y says which), two heads at a time with the next
 // two on their way.
 constexpr int STEP = 2;
-template <int D, bool Q4, bool INTER>
+template <int D, bool Q4, bool INTER, bool AXES>
 __global__ void __launch_bounds__(THREADS, 5) append_kernel(const Append p) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR, NG = D / 64;
   uint32_t* err = &g_append_err;
@@ -100,10 +101,19 @@ __global__ void __launch_bounds__(THREADS, 5) append_kernel(const Append p) {
   };
   Raw cur[STEP], next[STEP];
   load(h0, cur);
-  const Slot slot = slot_of(p, t, err);
+  Slot slot = slot_of<AXES>(p, t, err);
   Angles ang;
-  const bool turned = part != VALUES && ln.turned && slot.live;
-  if (turned) ang.load(p.cos, p.sin, slot.pos, p.rot, ln, INTER);
+  bool turned = part != VALUES && ln.turned && slot.live;
+  if constexpr (AXES) {  // the rotary positions are apart from the slot, and as much as the slot what makes a token live
+    const rope::AxisRows rows(p.axes, slot.live ? t : 0, p.n_pos, err);
+    if (slot.live && !rows.ok) {
+      atomicExch(err, DEV_BAD_INDEX);
+      slot.live = turned = false;
+    }
+    if (turned) ang.load(p.cos, p.sin, rows, p.axes, p.rot, ln, INTER);
+  } else if (turned) {
+    ang.load(p.cos, p.sin, slot.pos, p.rot, ln, INTER);
+  }
   const void* w = part == QUERIES ? p.q_weight : part == KEYS ? p.k_weight : nullptr;
   Row wt;
   if (w) {
@@ -174,8 +184,9 @@ static cudaError_t launch(Append p, cudaStream_t stream) {
     if (tiles * (p.q_sections + 2 * p.kv_sections) >= 152 * 5) break;
   }
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.q_sections + 2 * p.kv_sections));
-  if (p.interleaved) append_kernel<D, Q4, true><<<grid, THREADS, 0, stream>>>(p);
-  else append_kernel<D, Q4, false><<<grid, THREADS, 0, stream>>>(p);
+  const auto kern = p.axes.n > 0 ? (p.interleaved ? append_kernel<D, Q4, true, true> : append_kernel<D, Q4, false, true>)
+                                 : (p.interleaved ? append_kernel<D, Q4, true, false> : append_kernel<D, Q4, false, false>);
+  kern<<<grid, THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -76,6 +76,14 @@ struct HeadRows {
   long long sb, sh, sn;
   long long extent;
 };
+// Rotations with several position axes: pair i of a token's rotated dimensions
+// turns by its position on one axis. n = 0: one position a token.
+struct Axes {
+  const int* positions;  // [n][stride]
+  long long stride;
+  int n;
+  unsigned long long of_pair[2];  // two bits a pair: its axis
+};
 // Arguments of the norm and rotation kernels. No norm: the weights are null.
 // No rotation: rot = 0. The backward takes dy in q_out and k_out.
 struct NormRope {
@@ -89,6 +97,7 @@ struct NormRope {
   bool w32, interleaved;
   int B, H, Hkv, N, rot, n_pos;
   float eps;
+  Axes axes;  // with n > 0: positions as [n][B][N] (pos_sb = N) or [n][N] in place of `positions`
   int q_sections, k_sections;  // set by the launcher: parts that the heads are cut into
 };
 cudaError_t launch_norm_rope(const NormRope& p, int d, cudaStream_t stream);
@@ -122,6 +131,7 @@ struct Append {
   bool w32, interleaved, zero_skipped;
   int T, B, H, Hkv, num_blocks, bs, max_blocks, rot, n_pos;
   float eps;
+  Axes axes;  // with n > 0: the tokens' rotary positions, [n][T]; `positions` are slots only
   int q_sections, kv_sections;  // set by the launcher: parts that the heads are cut into
 };
 cudaError_t launch_append(const Append& p, int d, bool q4, cudaStream_t stream);

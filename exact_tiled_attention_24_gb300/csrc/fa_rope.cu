@@ -67,6 +67,23 @@ __device__ __forceinline__ int position_of(const NormRope& p, int b, int n, uint
   return -1;
 }
 
+// The token's angles, and whether it has any (false: reported). AXES: of its
+// positions on several axes.
+template <bool AXES>
+__device__ __forceinline__ bool angles_of(const NormRope& p, int b, int n, const Lane& ln, bool inter, Angles* t,
+                                          uint32_t* err) {
+  if constexpr (AXES) {
+    const AxisRows rows(p.axes, b * p.pos_sb + n, p.n_pos, err);
+    if (!rows.ok) atomicExch(err, DEV_BAD_INDEX);
+    else if (ln.turned) t->load(p.cos, p.sin, rows, p.axes, p.rot, ln, inter);
+    return rows.ok;
+  } else {
+    const int pos = position_of(p, b, n, err);
+    if (ln.turned && pos >= 0) t->load(p.cos, p.sin, pos, p.rot, ln, inter);
+    return pos >= 0;
+  }
+}
+
 // Token `tok` of all B·N, split into batch and position in it.
 struct Token {
   bool live;
@@ -90,7 +107,7 @@ __device__ __forceinline__ int section_start(int i, int n, int heads) {
 // section. The rows of a warp are consecutive tokens, contiguous in the
 // output. Five CTAs an SM (the case above: 58 us; four 62, six, with spilled
 // registers, 68).
-template <int D, bool INTER>
+template <int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR;
   uint32_t* err = &g_rope_err;
@@ -112,9 +129,8 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
   };
   Raw cur[2], next[2];
   load2(h0, cur);
-  const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : 0;
   Angles t;
-  if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
+  const bool placed = tk.live && angles_of<AXES>(p, tk.b, tk.n, ln, INTER, &t, err);
   Row wt;
   const void* w = is_k ? p.k_weight : p.q_weight;
   if (w) {
@@ -127,8 +143,8 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
     for (int j = 0; j < 2; ++j) {
       Row x = unpack(cur[j]);
       if (w) x = times(times(x, inv_rms<LPR>(x, p.eps)), wt);
-      if (ln.turned && pos >= 0) turn<false>(x, t, INTER);
-      if (pos < 0) x = Row{};  // no angle to turn by: a zero row
+      if (ln.turned && placed) turn<false>(x, t, INTER);
+      if (!placed) x = Row{};  // no angle to turn by: a zero row
       if (tk.live && h + j < h1) out.store(x, err);
       out.at += out.step;
       cur[j] = next[j];
@@ -143,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRope p)
 // Five CTAs an SM leave 96 registers a thread, and with a norm 72 to 104 bytes
 // a thread are spilled; still 95 us (four CTAs and 608 parts: 103).
 constexpr int MAX_PARTS = 760;
-template <int D, bool NORM, bool INTER>
+template <int D, bool NORM, bool INTER, bool AXES>
 __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRope p, int parts_q,
                                                                    float* __restrict__ partial) {
   constexpr int LPR = D / 16, ROWS = THREADS / LPR, WARPS = THREADS / 32;
@@ -191,19 +207,18 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_bwd_kernel(const NormRop
     };
     Raw dy, x, dy_next, x_next;
     load(h0, dy, x);
-    const int pos = tk.live ? position_of(p, tk.b, tk.n, err) : -1;
     Angles t;
-    if (ln.turned && pos >= 0) t.load(p.cos, p.sin, pos, p.rot, ln, INTER);
+    const bool placed = tk.live && angles_of<AXES>(p, tk.b, tk.n, ln, INTER, &t, err);
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
       load(h + 1, dy_next, x_next);
       Row g = unpack(dy);
-      if (ln.turned && pos >= 0) turn<true>(g, t, INTER);
+      if (ln.turned && placed) turn<true>(g, t, INTER);
       // A row past the last token, or whose position the tables do not have
       // (the forward wrote zeros), adds nothing to dw and has no gradient. Ones
       // in place of x: a row of zeros has no finite r at eps = 0, and what the
       // input holds there may be NaN.
-      if (pos < 0) {
+      if (!placed) {
         g = Row{};
         x.a = x.b = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
       }
@@ -314,8 +329,9 @@ static cudaError_t fwd(NormRope p, cudaStream_t stream) {
   set_sections(&p, 16);
   for (int hs = 8; hs > 1 && tiles * (p.q_sections + p.k_sections) < 152 * 5; hs /= 2) set_sections(&p, hs);
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.q_sections + p.k_sections));
-  if (p.interleaved) norm_rope_kernel<D, true><<<grid, THREADS, 0, stream>>>(p);
-  else norm_rope_kernel<D, false><<<grid, THREADS, 0, stream>>>(p);
+  const auto kern = p.axes.n > 0 ? (p.interleaved ? norm_rope_kernel<D, true, true> : norm_rope_kernel<D, false, true>)
+                                 : (p.interleaved ? norm_rope_kernel<D, true, false> : norm_rope_kernel<D, false, false>);
+  kern<<<grid, THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -340,15 +356,17 @@ static cudaError_t bwd(NormRope p, float* partial, float* dqw, float* dkw, cudaS
   parts_q = parts_q > items_q ? items_q : parts_q;
   if (items_q + items_k <= MAX_PARTS) parts_q = items_q, parts_k = items_k;
   const unsigned grid = static_cast<unsigned>(parts_q + parts_k);
-  if (!p.q_weight) {
-    if (p.interleaved) norm_rope_bwd_kernel<D, false, true><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), nullptr);
-    else norm_rope_bwd_kernel<D, false, false><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), nullptr);
-    return cudaGetLastError();
+  const bool norm = p.q_weight != nullptr;
+  auto rows = [&](auto kern) { kern<<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), norm ? partial : nullptr); };
+  if (p.axes.n > 0) {
+    if (norm) rows(p.interleaved ? norm_rope_bwd_kernel<D, true, true, true> : norm_rope_bwd_kernel<D, true, false, true>);
+    else rows(p.interleaved ? norm_rope_bwd_kernel<D, false, true, true> : norm_rope_bwd_kernel<D, false, false, true>);
+  } else {
+    if (norm) rows(p.interleaved ? norm_rope_bwd_kernel<D, true, true, false> : norm_rope_bwd_kernel<D, true, false, false>);
+    else rows(p.interleaved ? norm_rope_bwd_kernel<D, false, true, false> : norm_rope_bwd_kernel<D, false, false, false>);
   }
-  if (p.interleaved) norm_rope_bwd_kernel<D, true, true><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), partial);
-  else norm_rope_bwd_kernel<D, true, false><<<grid, THREADS, 0, stream>>>(p, static_cast<int>(parts_q), partial);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !norm) return e;
   // Launched while the rows' kernel drains (4112 tokens of 12 + 12 heads, d =
   // 64: 16.7 us instead of 18.5).
   cudaLaunchAttribute early{};

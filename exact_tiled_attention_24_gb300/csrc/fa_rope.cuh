@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "fa_common.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -149,6 +150,25 @@ __device__ __forceinline__ float inv_rms(const Row& x, float eps) {
   return rsqrtf(row_sum<LPR>(dot(x, x)) * (1.f / (16 * LPR)) + eps);
 }
 
+// A token's positions on the axes; ok: all of them are rows of the tables.
+struct AxisRows {
+  int at[4];
+  bool ok;
+  __device__ __forceinline__ AxisRows(const Axes& x, long long i, int n_pos, uint32_t* err) : ok(true) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      at[a] = 0;
+      if (a < x.n) {
+        at[a] = in_range(a * x.stride + i, 1, x.n * x.stride, err) ? x.positions[a * x.stride + i] : -1;
+        ok = ok && at[a] >= 0 && at[a] < n_pos;
+      }
+    }
+  }
+  __device__ __forceinline__ long long row(uint32_t axis) const {
+    return axis == 0 ? at[0] : axis == 1 ? at[1] : axis == 2 ? at[2] : at[3];
+  }
+};
+
 // The cosines and sines a lane needs, from row `pos` of the tables
 // ([n_pos][rot/2] fp32). Split: angles 8·ca .. 8·ca + 7 for its eight pairs.
 // Interleaved: angles 4·ca .. 4·ca + 3, then 4·cb .. 4·cb + 3.
@@ -167,6 +187,31 @@ struct Angles {
     c[2] = make_float2(c1.x, c1.y), c[3] = make_float2(c1.z, c1.w);
     s[0] = make_float2(s0.x, s0.y), s[1] = make_float2(s0.z, s0.w);
     s[2] = make_float2(s1.x, s1.y), s[3] = make_float2(s1.z, s1.w);
+  }
+  // The same with each pair's row of its own axis: four at once where four
+  // neighbours share one (sections of multiples of 4), else one by one.
+  __device__ __forceinline__ void load(const float* cos, const float* sin, const AxisRows& rows, const Axes& axes,
+                                       int rot, const Lane& ln, bool interleaved) {
+    const int half = rot >> 1;
+    const int first[2] = {interleaved ? 4 * ln.ca : 8 * ln.ca, interleaved ? 4 * ln.cb : 8 * ln.ca + 4};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = first[q];
+      const uint32_t bits = static_cast<uint32_t>((i < 32 ? axes.of_pair[0] : axes.of_pair[1]) >> (2 * (i & 31))) & 0xffu;
+      float4 c4, s4;
+      if (bits == (bits & 3u) * 0x55u) {
+        const long long base = rows.row(bits & 3u) * half + i;
+        c4 = *reinterpret_cast<const float4*>(cos + base);
+        s4 = *reinterpret_cast<const float4*>(sin + base);
+      } else {
+        const long long b0 = rows.row(bits & 3u) * half + i, b1 = rows.row(bits >> 2 & 3u) * half + i + 1;
+        const long long b2 = rows.row(bits >> 4 & 3u) * half + i + 2, b3 = rows.row(bits >> 6) * half + i + 3;
+        c4 = make_float4(cos[b0], cos[b1], cos[b2], cos[b3]);
+        s4 = make_float4(sin[b0], sin[b1], sin[b2], sin[b3]);
+      }
+      c[2 * q] = make_float2(c4.x, c4.y), c[2 * q + 1] = make_float2(c4.z, c4.w);
+      s[2 * q] = make_float2(s4.x, s4.y), s[2 * q + 1] = make_float2(s4.z, s4.w);
+    }
   }
 };
 

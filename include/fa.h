@@ -455,6 +455,31 @@ typedef struct {
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int d);
 int fa_qk_norm_rope_bwd(const fa_norm_rope_args* a, const fa_norm_rope_grads* g, void* stream);
 
+/*
+ * Several position axes, for tokens of images and video (time, height, width):
+ * pair i of the rotated dimensions turns by the angle of the token's position
+ * on axis pair_axis[i], the entry of that position's row of the tables. Any
+ * assignment of pairs to axes: sections one after another, or dealt in turn.
+ *   positions  device int32, [n_axes][N], or [n_axes][B][N] with
+ *              positions_per_batch = 1; for appends [n_axes][T]. A token with a
+ *              position outside [0, n_pos) on any axis is treated as one whose
+ *              only position is outside.
+ * fa_qk_norm_rope_axes and _axes_bwd: fa_qk_norm_rope and _bwd with these in
+ * place of a->positions, which has to be NULL.
+ * Errors: as theirs, and x or x->positions NULL, rot = 0, n_axes outside
+ * 1..FA_MAX_AXES, a pair's axis >= n_axes -> FA_ERR_INVALID_ARG; positions not
+ * 4-byte aligned -> FA_ERR_MISALIGNED.
+ */
+#define FA_MAX_AXES 4
+typedef struct {
+  const int* positions;
+  int n_axes;
+  unsigned char pair_axis[64]; /* the first rot/2 are used */
+} fa_rope_axes;
+int fa_qk_norm_rope_axes(const fa_norm_rope_args* a, const fa_rope_axes* x, void* stream);
+int fa_qk_norm_rope_axes_bwd(const fa_norm_rope_args* a, const fa_rope_axes* x, const fa_norm_rope_grads* g,
+                             void* stream);
+
 /* Arguments of an append to a paged cache. Unused ones are 0. */
 #define FA_ZERO_SKIPPED 2
 typedef struct {
@@ -533,6 +558,17 @@ int fa_append_paged(const fa_append_args* a, void* stream);
  *                       Rows of skipped tokens stay as they were.
  */
 int fa_append_paged_q4(const fa_append_args* a, void* stream);
+
+/*
+ * Appends whose rotary positions are not the slots: with several axes
+ * (fa_rope_axes), or with one (n_axes = 1, pair_axis all 0). a->positions says
+ * where a token is written and may be any the table holds; x->positions,
+ * [n_axes][T], by what its key and query are turned. A token that is written
+ * and has a position outside [0, n_pos) on an axis is skipped and
+ * fa_last_device_error reports FA_ERR_BAD_INDEX; those of padding are not used.
+ */
+int fa_append_paged_axes(const fa_append_args* a, const fa_rope_axes* x, void* stream);
+int fa_append_paged_q4_axes(const fa_append_args* a, const fa_rope_axes* x, void* stream);
 
 /*
  * Decode step over a 4-bit cache: fa_decode_paged's arguments, conventions
