@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   uint64_t* piece_full = final_bar + 1;
   uint64_t* piece_empty = piece_full + RING;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
-  PlanSmem* plan = reinterpret_cast<PlanSmem*>(smem + L::PLAN_OFF);
+  PlanSmem* plan_smem = reinterpret_cast<PlanSmem*>(smem + L::PLAN_OFF);
   uint32_t* err = &g_extend_err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,12 +217,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   }
 
   Shape sh{2 * p.tpt, p.causal, p.lc};
-  const Cut cut = cut_of<NT>(p, &sh, plan, err);
-  if (cut.units == 0 || cta >= cut.ctas) return;
-  const u64 u_begin = cut.start(cta), u_end = cut.start(cta + 1);
+  Cut cut;
   Place at;
-  u64 items0;
-  if (!find_request<NT, false>(p, sh, plan, u_begin, &at, &items0, err)) return;
+  i64 items0;
+  if (!plan<NT, false>(p, &sh, plan_smem, cta, &cut, &at, &items0, err)) return;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -270,26 +268,31 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     regs_down<LOAD == BOXES ? 104 : 72>();
     if (warp == 0) {
       // --------------------------------------------------------------- pieces
-      locate(p, sh, u_begin, &at);
-      u64 left = u_end - u_begin;
+      const i64 begin = cut.start(cta), end = cut.start(cta + 1);
+      locate(p, sh, begin, &at);
+      int lo = begin > at.item0 ? Shape::tile_at(begin - at.item0) : 0;
       const int G = p.H / p.Hkv, parts = p.hv / p.Hkv;
-      for (int idx = 0;; ++idx) {
+      int idx = 0;
+      auto emit = [&](const Piece& x) {
         const int s = idx % RING;
-        if (idx >= RING && !mbar_wait_warp(&piece_empty[s], ((idx / RING) - 1) & 1, err)) break;
-        if (left == 0) {
-          if (lane == 0) {
-            ring[s].n = 0;
-            mbar_arrive(&piece_full[s]);
-          }
-          break;
-        }
-        const Request& r = at.r;
-        const int whole = sh.length(r, at.c, at.i);
-        const int n = static_cast<int>(min(static_cast<u64>(whole - at.off), left));
+        if (idx >= RING && !mbar_wait_warp(&piece_empty[s], ((idx / RING) - 1) & 1, err)) return false;
         if (lane == 0) {
-          Piece x;
-          x.n = n;
-          x.kt0 = at.c * (sh.chunked(r) ? sh.lc : 0) + at.off;
+          ring[s] = x;
+          mbar_arrive(&piece_full[s]);
+        }
+        __syncwarp();
+        ++idx;
+        return true;
+      };
+      Piece x{};
+      while (true) {
+        const Request& r = at.r;
+        const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
+        const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
+        const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
+        if (hi > lo) {
+          x.n = hi - lo;
+          x.kt0 = at.c * (sh.lc / TK) + lo;
           x.b = at.b;
           x.kvh = at.hv / parts;
           const int h0 = at.hv % parts * p.heads;
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           x.ntok = min(sh.span, r.n - t0);
           x.pos0 = r.base() + t0;
           x.len = r.len;
-          x.slot = part_slot(p, sh, cut, at, cta, at.off > 0, at.off + n < whole);
+          x.slot = part_slot(p, sh, at, cta, lo > 0, hi < tiles);
           if (x.slot >= p.n_slots) {  // the host's bound holds: never
             atomicExch(err, DEV_BOUNDS);
             x.slot = 2 * cta;
@@ -309,16 +312,18 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
             const int t = min((g + 1) * p.tpt, x.ntok);
             if (t <= g * p.tpt) return 0;
             const int keys = p.causal ? max(x.pos0 + t, 0) : x.len;
-            return min(max((keys + TK - 1) / TK - x.kt0, 0), n);
+            return min(max((keys + TK - 1) / TK - x.kt0, 0), x.n);
           };
           x.n0 = sees(0), x.n1 = sees(1);
-          ring[s] = x;
-          mbar_arrive(&piece_full[s]);
+          if (!emit(x)) break;
         }
-        __syncwarp();
-        left -= n;
-        if (left == 0 || at.off + n < whole) continue;
-        at.off = 0;
+        if (item_end >= end) {
+          x.n = 0;
+          emit(x);
+          break;
+        }
+        at.item0 = item_end;
+        lo = 0;
         if (++at.i < r.items) continue;
         if (++at.hv == p.hv) {
           at.hv = 0;
@@ -326,11 +331,11 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
             if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
             at.c = 0;
             do {
-              at.r = request_of(p, ++at.b, err);  // units are left, so there is a request with tokens
+              at.r = request_of(p, ++at.b, err);  // costs are left, so there is a request with tokens
             } while (at.r.n == 0 && at.b + 1 < p.B);
           }
         }
-        at.i = sh.chunked(at.r) ? sh.past(at.r, static_cast<long long>(at.c) * sh.lc) : 0;
+        at.i = sh.reach(at.r, at.c);
       }
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issuer
@@ -369,7 +374,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       };
       Pieces pieces(ring, piece_full, piece_empty, err);
       Piece x;
-      bool ok = pieces.read(&x) && mbar_wait_warp(q_full, 0, err) && mbar_wait_warp(k0_full, 0, err);
+      // (A share may lie within one tile: then there is no piece.)
+      bool ok = pieces.read(&x) && x.n > 0 && mbar_wait_warp(q_full, 0, err) && mbar_wait_warp(k0_full, 0, err);
       int n[2] = {0, 0}, seen[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece; units, pieces so far of each query tile
       int len = 0, idx = 0, u = 0;
       if (ok) {
@@ -498,10 +504,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       };
       Unit cur = fetch(), nxt = fetch(), far = fetch();
       int z = place(cur), u = 0;
-      if (lane == 0) mbar_arrive_expect_tx(k0_full, L::TILE);
-      __syncwarp();
-      load(&tk, sK, k0_full, z);
-      bool ok = true;
+      bool ok = cur.any;
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(k0_full, L::TILE);
+        __syncwarp();
+        load(&tk, sK, k0_full, z);
+      }
       while (ok) {
         const int s = u % ST, s1 = (u + 1) % ST;
         const int z1 = nxt.any ? place(nxt) : 0;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         far = fetch();
       }
       // no copy outlives the CTA
-      mbar_wait_warp(k0_full, 0, err);
+      if (cur.any) mbar_wait_warp(k0_full, 0, err);
       for (int i = max(0, u - ST); i < u; ++i) mbar_wait_warp(&kv_full[i % ST], (i / ST) & 1, err);
     }
   } else if (warp < 12) {
@@ -787,7 +795,6 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       return y;
     };
     int u = 0;
-    bool ok = true;
     if constexpr (LOAD == GATHER) {
       auto copy = [&](const void* cache, uint8_t* dst, uint32_t row) {
         constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks a row, rows a step
@@ -803,8 +810,11 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       };
       Raw a = fetch(), b = fetch();
       Unit cur = resolve(a);
-      copy(p.k_cache, sK, cur.row);
-      cp_async_arrive_noinc(k0_full);
+      bool ok = cur.any;
+      if (ok) {
+        copy(p.k_cache, sK, cur.row);
+        cp_async_arrive_noinc(k0_full);
+      }
       a = b, b = fetch();
       while (ok) {
         const int s = u % ST, s1 = (u + 1) % ST;
@@ -884,9 +894,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       fetch_codes(p.v_cache, p.v_scale, cur, vraw);
       Unit nxt = resolve(b);
       Raw far = fetch();
+      bool ok = cur.any;
       cp_async_wait<1>();
-      unpack(sK, kraw);
-      publish(k0_full);
+      if (ok) {
+        unpack(sK, kraw);
+        publish(k0_full);
+      }
       fetch_codes(p.k_cache, p.k_scale, nxt, kraw);
       while (ok) {
         const int s = u % ST, s1 = (u + 1) % ST;
@@ -928,51 +941,45 @@ constexpr int MAX_PARTS = (SHARE_CHUNKS + 1) * MAX_CTAS + 32;
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
-  __shared__ PlanSmem plan;
+  __shared__ PlanSmem plan_smem;
   __shared__ int parts[MAX_PARTS];
   __shared__ int n_parts, head, item;
   uint32_t* err = &g_extend_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Shape sh{2 * p.tpt, p.causal, p.lc};
-  const Cut cut = cut_of<MERGE_THREADS>(p, &sh, &plan, err);
+  Cut cut;
   Place at;
-  u64 items0;
+  i64 items0;
   const int job = static_cast<int>(blockIdx.x);
   if (threadIdx.x == 0) n_parts = head = item = 0;
   at.r = Request{0, 0, 0, 0};
   if (job < p.ctas - 1) {
     const int k = job + 1;
-    const u64 u = cut.start(k);
-    if (k < cut.ctas && cut.units > 0 && find_request<MERGE_THREADS, false>(p, sh, &plan, u, &at, &items0, err) &&
-        warp == 0) {
-      locate(p, sh, u, &at);
-      const u64 begin = u - at.off;
-      int n = 0;
-      // cut here for the first time, and not one of the long ones
-      if (at.off > 0 && begin >= cut.start(k - 1) && !sh.is_long(at.r, at.i)) {
-        const int last = cut.owner(begin + sh.length(at.r, at.c, at.i) - 1);
-        n = last - k + 2;
-        for (int i = lane; i < n; i += 32) parts[i] = i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i);
+    if (plan<MERGE_THREADS, false>(p, &sh, &plan_smem, k, &cut, &at, &items0, err) && warp == 0) {
+      locate(p, sh, cut.start(k), &at);
+      // the first end within this item, and not one of the long ones
+      if (cut.start(k) > at.item0 && cut.start(k - 1) <= at.item0 && !sh.is_long(at.r, at.i) && lane == 0) {
+        const int n = parts_of(p, sh, cut, at, k - 1, [&](int i, int slot) { parts[i] = slot; });
+        n_parts = n > 1 ? n : 0, head = at.hv, item = at.i;  // one part: the outputs
       }
-      if (lane == 0) n_parts = n, head = at.hv, item = at.i;
     }
   } else {
-    const u64 want = static_cast<u64>(job - (p.ctas - 1));
-    if (cut.units > 0 && find_request<MERGE_THREADS, true>(p, sh, &plan, want, &at, &items0, err) && warp == 0) {
+    const int want = job - (p.ctas - 1);
+    if (plan<MERGE_THREADS, true>(p, &sh, &plan_smem, want, &cut, &at, &items0, err) && warp == 0) {
       const int first = sh.first_long(at.r, 0), each = at.r.items - first;
       const int nth = static_cast<int>(want - items0);
       at.hv = nth / each;
       at.i = first + nth % each;
-      const int n_c = (sh.tiles(at.r, at.i) + sh.lc - 1) / sh.lc;
+      const int n_c = (sh.keys(at.r, at.i) + sh.lc - 1) / sh.lc;
       int n = 0;
       for (int c0 = 0; c0 < n_c; c0 += 32) {
-        const int c = c0 + lane;
-        int mine = 0, k0 = 0;
-        if (c < n_c) {
-          const u64 row = sh.in_chunk_before(at.r, c, at.r.items);
-          const u64 begin = at.units0 + sh.chunks_before(at.r, c) * p.hv + row * at.hv + sh.in_chunk_before(at.r, c, at.i);
-          k0 = cut.owner(begin);
-          mine = cut.owner(begin + sh.length(at.r, c, at.i) - 1) - k0 + 1;
+        at.c = c0 + lane;
+        int mine = 0, k = 0;
+        if (at.c < n_c) {
+          const i64 row = sh.costs_before(at.r, at.c, at.r.items);
+          at.item0 = at.request0 + sh.chunks_before(at.r, at.c) * p.hv + row * at.hv + sh.costs_before(at.r, at.c, at.i);
+          k = cut.owner(at.item0);
+          mine = parts_of(p, sh, cut, at, k, [](int, int) {});
         }
         int sum = mine;
 #pragma unroll
@@ -980,10 +987,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
           const int t = __shfl_up_sync(0xffffffffu, sum, o);
           if (lane >= o) sum += t;
         }
-        at.c = c;
-        for (int i = 0; i < mine; ++i)
-          if (n + sum - mine + i < MAX_PARTS)
-            parts[n + sum - mine + i] = part_slot(p, sh, cut, at, k0 + i, i > 0, i == 0 && mine > 1);
+        const int at0 = n + sum - mine;
+        if (mine > 0)
+          parts_of(p, sh, cut, at, k, [&](int i, int slot) {
+            if (at0 + i < MAX_PARTS) parts[at0 + i] = slot;
+          });
         n += __shfl_sync(0xffffffffu, sum, 31);
       }
       if (lane == 0) n_parts = min(n, MAX_PARTS), head = at.hv, item = at.i;
@@ -1097,23 +1105,23 @@ size_t extend_sizes(Extend* p, int d, bool q4) {
   p->hv = p->Hkv * parts;
   p->tpt = BM / p->heads;
   const long long span = 2 * p->tpt;
-  const long long tiles = (static_cast<long long>(p->max_blocks) * p->bs + TK - 1) / TK;
+  const long long ctx = static_cast<long long>(p->max_blocks) * p->bs;
   // A chunk's K and V, of all K/V heads, stay in L2 (read as they lie there).
-  const long long tile_bytes = 2ll * TK * p->Hkv * (q4 ? d / 2 + d / 16 : 2 * d);
-  long long lc = kL2GroupBytes / tile_bytes;
-  p->lc = static_cast<int>(lc < 8 ? 8 : lc > (1 << 20) ? 1 << 20 : lc);
+  const long long key_bytes = 2ll * p->Hkv * (q4 ? d / 2 + d / 16 : 2 * d);
+  const long long lc = kL2GroupBytes / key_bytes / TK * TK;
+  p->lc = static_cast<int>(lc < 8 * TK ? 8 * TK : lc > (1 << 29) ? 1 << 29 : lc);
   const long long items = p->hv * (p->T / span + (p->T < p->B ? p->T : p->B));  // at most
-  const long long shares = items * tiles / MIN_SHARE;
+  const long long shares = items * (ctx + PIECE) / MIN_SHARE;
   p->ctas = static_cast<int>(shares < 1 ? 1 : shares > MAX_CTAS ? MAX_CTAS : shares);
-  p->may_chunk = p->T > span && tiles > p->lc;
+  p->may_chunk = p->T > span && ctx > p->lc;
   p->n_long = 0;
   long long whole = 0;
   if (p->may_chunk) {
     // Items of requests with two or more: at most 2 T / span. A chunk is at
-    // least 1/8 of a share, a long item passes at most twice its tiles / lc.
+    // least 1/8 of a share long, a long item passes at most twice its keys / lc.
     const long long long_items = p->hv * (2ll * p->T / span), by_share = 2ll * SHARE_CHUNKS * p->ctas;
     p->n_long = static_cast<int>(long_items < by_share ? long_items : by_share);
-    whole = long_items * ((tiles + p->lc - 1) / p->lc);
+    whole = long_items * ((ctx + p->lc - 1) / p->lc);
     if (whole > by_share) whole = by_share;
   }
   p->n_slots = static_cast<int>(2 * p->ctas + whole);

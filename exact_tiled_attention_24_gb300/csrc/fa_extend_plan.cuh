@@ -4,17 +4,20 @@
 //
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
-//   unit    one 128-key tile of one item, the work of one step of a CTA
-//   order   request by request, (chunk,) K/V head, item, key tile. The units
-//           in this order are cut into C equal shares, one a CTA: the lengths
-//           are on the device only, and equal shares need no rule for uneven
-//           ones. An item that crosses from one share to the next is finished
-//           by a merge of its parts.
+//   cost    of an item: the keys it sees, and PIECE for its start and end
+//           (measured: 1.5 key tiles' time). Keys and not key tiles, because
+//           their sums over items have a closed form without a division
+//           (counting tiles, the start of a CTA took 14 us, now 4)
+//   order   request by request, (chunk,) K/V head, item, key. The costs in this
+//           order are cut into C equal shares, one a CTA, each end rounded down
+//           to a key tile of its item: the lengths are on the device only, and
+//           equal shares need no rule for uneven ones. An item that crosses
+//           from one share to the next is finished by a merge of its parts.
 //   chunk   a request with several items reads its keys once an item. CTAs
 //           with equal shares stand at different keys of it, so what one reads
 //           has left L2 before another needs it. The keys are therefore cut
-//           into chunks of `lc` tiles (their K and V fit L2), and all items
-//           pass one chunk before any passes the next.
+//           into chunks of `lc` (their K and V fit L2), and all items pass one
+//           chunk before any passes the next.
 #pragma once
 
 #include <cstdint>
@@ -27,12 +30,13 @@
 namespace fa {
 namespace ext {
 
-constexpr int TK = 128;          // keys a tile
-constexpr int MIN_SHARE = 4;     // units a CTA has at least
+constexpr int TK = 128;             // keys a tile
+constexpr int PIECE = 192;          // an item's start and end, in keys
+constexpr int MIN_SHARE = 5 * TK;   // a CTA's share is at least that
 constexpr int MAX_CTAS = 152;
-constexpr int SHARE_CHUNKS = 8;  // chunks are at least 1/8 of a share long
+constexpr int SHARE_CHUNKS = 8;     // chunks are at least 1/8 of a share long
 
-typedef unsigned long long u64;
+typedef long long i64;
 
 // One request: its first row of q, new tokens, cached tokens, items.
 struct Request {
@@ -43,134 +47,126 @@ struct Request {
 __device__ __forceinline__ Request request_of(const Extend& p, int b, uint32_t* err) {
   Request r{0, 0, 0, 0};
   const int s = p.q_starts[b], e = p.q_starts[b + 1];
+  const int len = p.seq_lens[b];
   if (s < 0 || e > p.T || e < s) {
     atomicExch(err, DEV_BAD_INDEX);
     return r;
   }
   r.row0 = s, r.n = e - s;
-  r.len = min(max(p.seq_lens[b], 0), p.max_blocks * p.bs);
+  r.len = min(max(len, 0), p.max_blocks * p.bs);
   r.items = (r.n + 2 * p.tpt - 1) / (2 * p.tpt);
   return r;
-}
-
-// Σ_{i < n} floor((a i + b) / m), by Euclid's steps (a and m below 2^9).
-FA_HD u64 floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  u64 s = 0;
-  while (n > 0) {
-    if (a >= m) s += static_cast<u64>(n) * (n - 1) / 2 * (a / m), a %= m;
-    if (b >= m) s += static_cast<u64>(n) * (b / m), b %= m;
-    const uint32_t top = a * n + b;
-    if (top < m) break;
-    n = top / m, b = top % m;
-    const uint32_t t = a;
-    a = m, m = t;
-  }
-  return s;
 }
 
 struct Shape {
   int span;  // tokens an item: 2·tpt
   bool causal;
-  int lc;    // key tiles a chunk
+  int lc;    // keys a chunk, a multiple of TK
 
-  FA_HD static int tiles_to(int keys) { return max(1, (max(keys, 0) + TK - 1) / TK); }
-  // key tiles item i sees (one at least, so that its rows are written)
-  FA_HD int tiles(const Request& r, int i) const {
-    return tiles_to(causal ? r.base() + min((i + 1) * span, r.n) : r.len);
+  // key tiles of `keys` (one at least, so that rows that see nothing are written)
+  FA_HD static int tiles_of(int keys) { return max(1, (keys + TK - 1) / TK); }
+  // keys item i sees: not decreasing in i
+  FA_HD int keys(const Request& r, int i) const {
+    return causal ? max(0, r.base() + min((i + 1) * span, r.n)) : r.len;
   }
-  // Σ_{i' < i} tiles(i')
-  FA_HD u64 before(const Request& r, int i) const {
-    if (!causal) return static_cast<u64>(i) * tiles_to(r.len);
-    const int full = min(i, r.items - 1);  // the last item may be shorter
-    const int ones = min(full, r.base() >= TK ? 0 : (TK - r.base()) / span);
-    u64 s = ones;
-    if (full > ones) s += floor_sum(full - ones, TK, span, r.base() + (ones + 1) * span + TK - 1);
-    return i > full ? s + tiles(r, i - 1) : s;
+  // Σ_{i' < i} keys(i')
+  FA_HD i64 keys_before(const Request& r, int i) const {
+    if (!causal) return static_cast<i64>(i) * r.len;
+    const i64 full = min(i, r.items - 1);  // the last item may be shorter
+    const i64 none = r.base() >= 0 ? 0 : min(static_cast<int>(full), -r.base() / span);
+    const i64 s = (full - none) * r.base() + span * ((full * (full + 1) - none * (none + 1)) / 2);
+    return i > full ? s + keys(r, r.items - 1) : s;
   }
-  // the first item that sees more than x tiles
-  FA_HD int past(const Request& r, long long x) const {
-    if (x <= 0) return 0;
-    if (static_cast<long long>(r.len) <= x * TK) return r.items;
+  // the first item that sees more than x keys
+  FA_HD int past(const Request& r, i64 x) const {
+    if (r.len <= x) return r.items;
     if (!causal) return 0;
-    const long long d = x * TK - r.base();
-    return d < 0 ? 0 : static_cast<int>(min(d / span, static_cast<long long>(r.items - 1)));
+    const int d = static_cast<int>(x) - r.base();
+    return d < 0 ? 0 : min(d / span, r.items - 1);
   }
-  FA_HD bool chunked(const Request& r) const {
-    return r.items > 1 && tiles(r, r.items - 1) > lc;
+  FA_HD bool chunked(const Request& r) const { return r.items > 1 && r.len > lc; }
+  FA_HD int chunks(const Request& r) const { return chunked(r) ? (r.len + lc - 1) / lc : 1; }
+  // the first item that reaches chunk c
+  FA_HD int reach(const Request& r, int c) const { return c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
+  // keys of item i in chunk c, which it reaches
+  FA_HD int part(const Request& r, int c, int i) const {
+    const int k = keys(r, i);
+    return chunked(r) ? min(k - c * lc, lc) : k;
   }
-  FA_HD int chunks(const Request& r) const {
-    return chunked(r) ? (tiles(r, r.items - 1) + lc - 1) / lc : 1;
-  }
-  // tiles of item i in chunk c
-  FA_HD int length(const Request& r, int c, int i) const {
-    const int t = tiles(r, i);
-    return chunked(r) ? min(max(t - c * lc, 0), lc) : t;
-  }
-  // Σ_{c' < c} of the tiles of one head in chunk c'
-  FA_HD u64 chunks_before(const Request& r, int c) const {
-    if (c == 0) return 0;
-    const int i = past(r, static_cast<long long>(c) * lc);
-    return before(r, i) + static_cast<u64>(r.items - i) * (static_cast<u64>(c) * lc);
-  }
-  // Σ_{i' < i} length(c, i')
-  FA_HD u64 in_chunk_before(const Request& r, int c, int i) const {
-    if (!chunked(r)) return before(r, i);
-    const int i0 = past(r, static_cast<long long>(c) * lc), i1 = past(r, static_cast<long long>(c + 1) * lc);
+  FA_HD int cost(const Request& r, int c, int i) const { return PIECE + part(r, c, i); }
+  // Σ of the costs in chunk c of the items before i
+  FA_HD i64 costs_before(const Request& r, int c, int i) const {
+    if (!chunked(r)) return keys_before(r, i) + static_cast<i64>(i) * PIECE;
+    const int i0 = reach(r, c), i1 = past(r, static_cast<i64>(c + 1) * lc);
     if (i <= i0) return 0;
-    const int j = max(i0, min(i, i1));
-    u64 s = before(r, j) - before(r, i0) - static_cast<u64>(j - i0) * (static_cast<u64>(c) * lc);
-    if (i > j) s += static_cast<u64>(i - j) * lc;
+    const int j = min(i, i1);  // from i1 on a whole chunk each
+    return static_cast<i64>(i - i0) * PIECE + keys_before(r, j) - keys_before(r, i0) -
+           static_cast<i64>(j - i0) * (static_cast<i64>(c) * lc) + static_cast<i64>(i - j) * lc;
+  }
+  // Σ_{1 <= c' < c} of the items that reach chunk c'
+  FA_HD i64 reaches(const Request& r, int c) const {
+    i64 s = 0;
+    for (int x = 1; x < c; ++x) s += r.items - reach(r, x);
     return s;
+  }
+  // Σ of one head's costs in the chunks before c
+  FA_HD i64 chunks_before(const Request& r, int c) const {
+    if (c == 0) return 0;
+    const int i = past(r, static_cast<i64>(c) * lc);
+    return keys_before(r, i) + static_cast<i64>(r.items - i) * (static_cast<i64>(c) * lc) + (r.items + reaches(r, c)) * PIECE;
+  }
+  // a request's costs
+  FA_HD i64 total(const Request& r, int heads) const {
+    if (r.n == 0) return 0;
+    return (chunked(r) ? chunks_before(r, chunks(r)) : costs_before(r, 0, r.items)) * heads;
   }
   // Items that pass more than one chunk are "long"; each of their chunks has a
-  // part of its own. The first long item that reaches chunk c:
-  FA_HD int first_long(const Request& r, int c) const {
-    return past(r, static_cast<long long>(max(c, 1)) * lc);
-  }
-  FA_HD bool is_long(const Request& r, int i) const { return chunked(r) && tiles(r, i) > lc; }
-  // parts of one head's long items in the chunks before c
+  // part of its own: the first long item of chunk c, and one head's parts in
+  // the chunks before c.
+  FA_HD int first_long(const Request& r, int c) const { return past(r, static_cast<i64>(max(c, 1)) * lc); }
+  FA_HD bool is_long(const Request& r, int i) const { return chunked(r) && keys(r, i) > lc; }
   FA_HD int long_before(const Request& r, int c) const {
-    int s = 0;
-    for (int x = 0; x < c; ++x) s += r.items - first_long(r, x);
-    return s;
+    return c == 0 ? 0 : r.items - first_long(r, 0) + static_cast<int>(reaches(r, c));
   }
+  // the tile at which a share's end x into an item's cost cuts it
+  FA_HD static int tile_at(i64 x) { return x <= PIECE ? 0 : static_cast<int>((x - PIECE) / TK); }
 };
 
-// The whole call's cut. C shares of U units: share k is [start(k), start(k + 1)).
+// The whole call's cut. C shares of `cost`: share k is [start(k), start(k + 1)).
 struct Cut {
-  u64 units;
+  i64 cost;
   int ctas;
-  FA_HD u64 start(int k) const { return units * static_cast<u64>(k) / ctas; }
-  FA_HD int owner(u64 u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+  FA_HD i64 start(int k) const { return cost * k / ctas; }
+  FA_HD int owner(i64 x) const { return static_cast<int>(((x + 1) * ctas - 1) / cost); }
 };
 
-// Where a unit lies, with what lies before its request.
+// An item of one chunk, with what lies before it.
 struct Place {
   Request r;
   int b;
-  u64 units0;  // units before the request
-  int longs0;  // parts of long items before the request
+  i64 request0;  // costs before the request
+  int longs0;    // parts of long items before the request
   int c, hv, i;
-  int off;     // tile of the item within the chunk
+  i64 item0;     // costs before the item
 };
 
 // Block-wide exclusive scan of one value a thread.
 template <int NT>
-__device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
+__device__ __forceinline__ i64 block_scan(i64 v, i64* scratch, i64* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 s = v;
+  i64 s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const u64 t = __shfl_up_sync(0xffffffffu, s, o);
+    const i64 t = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += t;
   }
   __syncthreads();  // the scratch may be in use
   if (lane == 31) scratch[warp] = s;
   __syncthreads();
-  u64 below = 0, all = 0;
+  i64 below = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const u64 t = scratch[w];
+    const i64 t = scratch[w];
     if (w < warp) below += t;
     all += t;
   }
@@ -179,109 +175,133 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
 }
 
 struct PlanSmem {
-  u64 scan[16];
-  u64 units0, items0;
+  i64 scan[16];
+  i64 request0, items0;
   int b, longs0;
 };
 
-__device__ __forceinline__ u64 units_of(const Extend& p, const Shape& sh, const Request& r) {
-  return r.n > 0 ? sh.before(r, r.items) * p.hv : 0;
-}
-
-// The cut of the whole call (the shape's chunk length is set on the way).
-template <int NT>
-__device__ __forceinline__ Cut cut_of(const Extend& p, Shape* sh, PlanSmem* sm, uint32_t* err) {
-  u64 mine = 0, total;
-  for (int b = threadIdx.x; b < p.B; b += NT) mine += units_of(p, *sh, request_of(p, b, err));
-  block_scan<NT>(mine, sm->scan, &total);
-  Cut cut;
-  cut.units = total;
-  const u64 most = total / MIN_SHARE;
-  cut.ctas = static_cast<int>(most < 1 ? 1 : most > static_cast<u64>(p.ctas) ? p.ctas : most);
-  const u64 least = (total + SHARE_CHUNKS * cut.ctas - 1) / (SHARE_CHUNKS * cut.ctas);
-  sh->lc = least > static_cast<u64>(p.lc) ? static_cast<int>(least) : p.lc;
-  return cut;
-}
-
-// The request that holds unit `target` (LONG = false), or the target-th long
-// item (LONG = true); found by one thread, known to all afterwards. Returns
-// false if there is none.
+// The call's cut, and the place of one of its items: with LONG = false of the
+// one that share `want` begins in, with LONG = true of the want-th long item
+// (its request and, in *items0, the long items before that). False: there is
+// none. Run by a whole block; every thread knows the result, up to the request
+// (locate has the rest). Sets sh->lc.
 template <int NT, bool LONG>
-__device__ __forceinline__ bool find_request(const Extend& p, const Shape& sh, PlanSmem* sm, u64 target, Place* at,
-                                             u64* items0, uint32_t* err) {
-  if (threadIdx.x == 0) sm->b = -1;
-  u64 units = 0, longs = 0, items = 0;
+__device__ __forceinline__ bool plan(const Extend& p, Shape* sh, PlanSmem* sm, int want, Cut* cut, Place* at,
+                                     i64* items0, uint32_t* err) {
+  const int tid = static_cast<int>(threadIdx.x);
+  sh->lc = p.lc;
+  const Request none{0, 0, 0, 0};
+  const Request mine = tid < p.B ? request_of(p, tid, err) : none;  // all there are, mostly
+  if (p.may_chunk) {
+    i64 k = 0, all;
+    for (int b = tid; b < p.B; b += NT) {
+      const Request r = b == tid ? mine : request_of(p, b, err);
+      if (r.n > 0) k += sh->keys_before(r, r.items) * p.hv;
+    }
+    block_scan<NT>(k, sm->scan, &all);
+    const i64 least = (all / (SHARE_CHUNKS * p.ctas) + TK) / TK * TK;
+    if (least > sh->lc) sh->lc = least < (1 << 29) ? static_cast<int>(least) : 1 << 29;
+  }
+  // costs before each thread's request; with more requests than threads, the total first
+  i64 c = 0;
+  for (int b = tid; b < p.B; b += NT) c += sh->total(b == tid ? mine : request_of(p, b, err), p.hv);
+  const i64 before = block_scan<NT>(c, sm->scan, &cut->cost);
+  const i64 most = cut->cost / MIN_SHARE;
+  cut->ctas = static_cast<int>(most < 1 ? 1 : most > p.ctas ? p.ctas : most);
+  if (tid == 0) sm->b = -1;
+  const bool there = cut->cost > 0 && (LONG || want < cut->ctas);
+  const i64 target = LONG || !there ? want : cut->start(want);
+  i64 costs = 0, longs = 0, items = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    Request r{0, 0, 0, 0};
-    if (b < p.B) r = request_of(p, b, err);
-    const u64 u = units_of(p, sh, r);
-    u64 l = 0, it = 0;
-    if (p.may_chunk && r.n > 0 && sh.chunked(r)) {
-      l = static_cast<u64>(sh.long_before(r, sh.chunks(r))) * p.hv;
-      it = static_cast<u64>(r.items - sh.first_long(r, 0)) * p.hv;
-    }
-    u64 tu, tl = 0, ti = 0;
-    const u64 eu = units + block_scan<NT>(u, sm->scan, &tu);
-    u64 el = longs, ei = items;
+    const int b = b0 + tid;
+    const Request r = b0 == 0 ? mine : b < p.B ? request_of(p, b, err) : none;
+    const i64 cost = p.B <= NT ? c : sh->total(r, p.hv);
+    i64 sum = 0, sum_l = 0, sum_i = 0, l = 0, it = 0, e_l = 0, e_i = 0;
+    const i64 e = p.B <= NT ? before : costs + block_scan<NT>(cost, sm->scan, &sum);
     if (p.may_chunk) {
-      el += block_scan<NT>(l, sm->scan, &tl);
-      ei += block_scan<NT>(it, sm->scan, &ti);
+      if (r.n > 0 && sh->chunked(r)) {
+        l = static_cast<i64>(sh->long_before(r, sh->chunks(r))) * p.hv;
+        it = static_cast<i64>(r.items - sh->first_long(r, 0)) * p.hv;
+      }
+      e_l = longs + block_scan<NT>(l, sm->scan, &sum_l);
+      e_i = items + block_scan<NT>(it, sm->scan, &sum_i);
+    } else {
+      __syncthreads();  // sm->b is set
     }
-    const u64 key = LONG ? ei : eu, size = LONG ? it : u;
-    if (target >= key && target - key < size) sm->b = b, sm->units0 = eu, sm->longs0 = static_cast<int>(el), sm->items0 = ei;
-    units += tu, longs += tl, items += ti;
+    const i64 key = LONG ? e_i : e, size = LONG ? it : cost;
+    if (there && target >= key && target - key < size)
+      sm->b = b, sm->request0 = e, sm->longs0 = static_cast<int>(e_l), sm->items0 = e_i;
+    costs += sum, longs += sum_l, items += sum_i;
   }
   __syncthreads();
   at->b = sm->b;
   if (at->b < 0) return false;
   at->r = request_of(p, at->b, err);
-  at->units0 = sm->units0;
+  at->request0 = sm->request0;
   at->longs0 = sm->longs0;
   *items0 = sm->items0;
   return true;
 }
 
-// The rest of a unit's place within its request; run by a whole warp.
-__device__ __forceinline__ void locate(const Extend& p, const Shape& sh, u64 u, Place* at) {
+// The item that holds cost `x` of a request's; run by a whole warp.
+__device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, Place* at) {
   const int lane = threadIdx.x & 31;
   const Request& r = at->r;
-  u64 rem = u - at->units0;
-  const int n_c = sh.chunks(r);
+  i64 rem = x - at->request0;
   int c = 0;
-  for (int c0 = 0; c0 < n_c; c0 += 32) {
-    const bool ok = c0 + lane < n_c && sh.chunks_before(r, c0 + lane) * p.hv <= rem;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
-    if (cnt > 0) c = c0 + cnt - 1;
-    if (cnt < 32) break;
+  if (sh.chunked(r)) {
+    const int n_c = sh.chunks(r);
+    for (int c0 = 0; c0 < n_c; c0 += 32) {
+      const bool ok = c0 + lane < n_c && sh.chunks_before(r, c0 + lane) * p.hv <= rem;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
+      if (cnt > 0) c = c0 + cnt - 1;
+      if (cnt < 32) break;
+    }
+    rem -= sh.chunks_before(r, c) * p.hv;
   }
-  rem -= sh.chunks_before(r, c) * p.hv;
-  const u64 row = sh.in_chunk_before(r, c, r.items);
+  const i64 row = sh.costs_before(r, c, r.items);
   at->c = c;
   at->hv = static_cast<int>(rem / row);
   rem -= row * at->hv;
-  int lo = sh.chunked(r) ? sh.past(r, static_cast<long long>(c) * sh.lc) : 0, hi = r.items;
+  int lo = sh.reach(r, c), hi = r.items;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
-    const bool ok = probe < hi && sh.in_chunk_before(r, c, probe) <= rem;
+    const bool ok = probe < hi && sh.costs_before(r, c, probe) <= rem;
     const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
     lo += (cnt - 1) * step;
     hi = min(hi, lo + step);
   }
   at->i = lo;
-  at->off = static_cast<int>(rem - sh.in_chunk_before(r, c, lo));
+  at->item0 = x - (rem - sh.costs_before(r, c, lo));
 }
 
 // Where a piece's result goes: slots 2k and 2k + 1 are CTA k's first and last
 // piece where its share cuts an item, the others hold whole chunks of long
 // items; -1: the outputs themselves.
-__device__ __forceinline__ int part_slot(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k,
-                                         bool start_cut, bool end_cut) {
+__device__ __forceinline__ int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bool start_cut,
+                                         bool end_cut) {
   if (start_cut) return 2 * k;
   if (end_cut) return 2 * k + 1;
   if (!sh.is_long(at.r, at.i)) return -1;
   const int in_c = at.r.items - sh.first_long(at.r, at.c);
   return 2 * p.ctas + at.longs0 + p.hv * sh.long_before(at.r, at.c) + at.hv * in_c + at.i - sh.first_long(at.r, at.c);
+}
+
+// The parts that the shares make of one item of one chunk, in order: calls
+// f(slot) for each; k: the share in which it begins.
+template <class F>
+__device__ __forceinline__ int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
+  const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape::tiles_of(sh.part(at.r, at.c, at.i));
+  const i64 end = at.item0 + cost;
+  int n = 0;
+  for (int lo = 0; lo < tiles; ++k) {
+    const i64 e = cut.start(k + 1);
+    const int hi = e >= end ? tiles : Shape::tile_at(e - at.item0);
+    if (hi <= lo) continue;
+    f(n++, part_slot(p, sh, at, k, lo > 0, hi < tiles));
+    lo = hi;
+  }
+  return n;
 }
 
 }  // namespace ext
