@@ -566,6 +566,7 @@ static int extend(const fa_extend_args* a, bool q4, void* stream) {
   p.o = static_cast<__nv_bfloat16*>(a->o), p.lse = a->lse;
   p.o_part = static_cast<float*>(a->workspace);
   p.lse_part = p.o_part + static_cast<size_t>(p.n_slots) * 256 * a->d;
+  p.cuts = reinterpret_cast<fa::ItemCut*>(p.lse_part + static_cast<size_t>(p.n_slots) * 256);
   p.num_blocks = a->num_blocks;
   p.causal = a->causal != 0, p.zero_skipped = a->zero_skipped != 0;
   p.scale_log2 = a->scale * 1.4426950408889634f;

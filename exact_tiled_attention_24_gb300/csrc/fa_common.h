@@ -156,6 +156,11 @@ int decode_q4_splits(int B, int H, int Hkv, long long max_ctx);
 cudaError_t launch_decode_q4(const DecodeQ4& p, int d, int S, cudaStream_t stream);
 
 // ---- attention of chunks of new tokens over a paged cache (fa_extend.cu)
+// An item of work whose first tile is a CTA's and that goes on into others' shares.
+struct ItemCut {
+  int parts;  // 0: none
+  int tok0, ntok, head0, heads;
+};
 struct Extend {
   const void* k_cache;       // bf16 [num_blocks][Hkv][bs][d], or codes [...][d / 2]
   const void* v_cache;
@@ -168,6 +173,7 @@ struct Extend {
   float* lse;                // [T][H]
   float* o_part;             // [n_slots][d / 4][256][4]: normalised parts of cut items
   float* lse_part;           // [n_slots][256]
+  ItemCut* cuts;             // [ctas]
   int T, B, H, Hkv, num_blocks, bs, max_blocks;
   int heads, hv;             // query heads a tile holds (at most 128), K/V heads times the parts its query heads are cut into
   int tpt;                   // tokens a query tile holds: 128 / heads

@@ -43,7 +43,7 @@ namespace ext {
 
 constexpr int BM = 128;     // rows a query tile
 constexpr int ROWS = 256;   // rows an item
-constexpr int RING = 16;    // piece descriptors in flight
+constexpr int RING = 8;     // piece descriptors in flight: K and V run at most three units ahead of what is issued
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -64,7 +64,10 @@ struct Piece {
   int pos0, len;         // position of the first token; cached tokens
   int slot;              // -1: the outputs
   int n0, n1;            // key tiles that each query tile sees
-  int pad[3];
+  // One query tile and two key tiles at least: both softmax groups work on it,
+  // on every other key tile, and the first joins the two results.
+  int halves;
+  int unit0, joined;     // the CTA's units, and its pieces in halves, before this one
 };
 static_assert(sizeof(Piece) == 64, "");
 
@@ -79,14 +82,20 @@ struct Smem {
   static constexpr int V_OFF = K_OFF + STAGES * TILE;
   static constexpr int PIECE_OFF = V_OFF + STAGES * TILE;
   static constexpr int BAR_OFF = PIECE_OFF + RING * static_cast<int>(sizeof(Piece));
-  // q_full, q_empty, k0_full, kv_full[], kv_empty[], s_full[2], p_lo[2], p_hi[2], pv_done[2], o_free[2], final,
+  // q_full, q_empty, k0_full, kv_full[], kv_empty[], s_full[2], p_lo[2], p_hi[2], pv_done[2], o_free[2], half, final,
   // piece_full[], piece_empty[]
-  static constexpr int NBARS = 3 + 2 * STAGES + 10 + 1 + 2 * RING;
+  static constexpr int NBARS = 3 + 2 * STAGES + 10 + 2 + 2 * RING;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int PLAN_OFF = SLOT_OFF + 16;
   static constexpr int RAW_OFF = (PLAN_OFF + static_cast<int>(sizeof(PlanSmem)) + 15) / 16 * 16;
   // 4-bit caches: a tile's codes and pairs of K and of V
-  static constexpr int BYTES = RAW_OFF + (LOAD == CODES ? 2 * TK * (D / 2 + D / 8) : 0);
+  static constexpr int STATS_OFF = RAW_OFF + (LOAD == CODES ? 2 * TK * (D / 2 + D / 8) : 0);  // [128] (m, l)
+  // Results pass through shared memory on their way out, OUT columns of a
+  // warp's 32 rows at a time (as much as fits): rows of 16-byte pieces a thread
+  // each, 32 rows to an instruction, took 2 us a piece.
+  static constexpr int OUT_OFF = STATS_OFF + BM * 8;
+  static constexpr int OUT = LOAD == CODES && D == 128 ? 16 : 64;
+  static constexpr int BYTES = OUT_OFF + 8 * 32 * OUT * 2;
   // One CTA an SM (one 512-column TMEM allocation), 1024 bytes to align.
   static constexpr int ALLOC = BYTES + 1024 > 118784 ? BYTES + 1024 : 118784;
   static_assert(ALLOC <= 232448, "");
@@ -189,7 +198,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   uint64_t* p_hi = p_lo + 2;           // [2] keys 64..127
   uint64_t* pv_done = p_hi + 2;        // [2]
   uint64_t* o_free = pv_done + 2;      // [2] the epilogue has read O
-  uint64_t* final_bar = o_free + 2;
+  uint64_t* half = o_free + 2;         // the second group's half of a piece is there
+  uint64_t* final_bar = half + 1;
   uint64_t* piece_full = final_bar + 1;
   uint64_t* piece_empty = piece_full + RING;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
@@ -220,7 +230,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   Cut cut;
   Place at;
   i64 items0;
-  if (!plan<NT, false>(p, &sh, plan_smem, cta, &cut, &at, &items0, err)) return;
+  if (!plan<NT, false>(p, &sh, plan_smem, cta, &cut, &at, &items0, err)) {
+    if (threadIdx.x == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta].parts = 0;
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       mbar_init(&pv_done[g], 1);
       mbar_init(&o_free[g], 4);
     }
+    mbar_init(half, 4);
     mbar_init(final_bar, 1);
     for (int i = 0; i < RING; ++i) {
       mbar_init(&piece_full[i], 1);
@@ -284,13 +298,15 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         ++idx;
         return true;
       };
-      Piece x{};
+      Piece x{};  // n = 0
+      ItemCut last{0, 0, 0, 0, 0};
       while (true) {
         const Request& r = at.r;
         const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
         const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
         const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
         if (hi > lo) {
+          x.unit0 += x.n, x.joined += x.halves;
           x.n = hi - lo;
           x.kt0 = at.c * (sh.lc / TK) + lo;
           x.b = at.b;
@@ -315,7 +331,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
             return min(max((keys + TK - 1) / TK - x.kt0, 0), x.n);
           };
           x.n0 = sees(0), x.n1 = sees(1);
+          x.halves = x.ntok <= p.tpt && x.n0 > 1;
           if (!emit(x)) break;
+          if (lo == 0 && hi < tiles && !sh.is_long(r, at.i))
+            last = ItemCut{cut.owner(item_end - 1) - cta + 1, x.tok0, x.ntok, x.head0, x.heads};
         }
         if (item_end >= end) {
           x.n = 0;
@@ -337,6 +356,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         }
         at.i = sh.reach(at.r, at.c);
       }
+      if (lane == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta] = last;
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16(BM, TK, false, false);
@@ -344,8 +364,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       const uint64_t dq = sdesc_kmajor(smem_u32(sQ), 0);
       const uint64_t dk = sdesc_kmajor(smem_u32(sK), 0);
       const uint64_t dv = sdesc_mnmajor(smem_u32(sV), 0, L::PANEL);
-      auto issue_s = [&](int g, int s) {  // S_g = Q_g Kᵀ, K in stage s
-        const uint64_t a = desc_add(dq, g * L::TILE), b = desc_add(dk, s * L::TILE);
+      auto issue_s = [&](int g, int s, int tile) {  // S_g = Q Kᵀ, Q's tile, K in stage s
+        const uint64_t a = desc_add(dq, tile * L::TILE), b = desc_add(dk, s * L::TILE);
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -378,12 +398,17 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       bool ok = pieces.read(&x) && x.n > 0 && mbar_wait_warp(q_full, 0, err) && mbar_wait_warp(k0_full, 0, err);
       int n[2] = {0, 0}, seen[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece; units, pieces so far of each query tile
       int len = 0, idx = 0, u = 0;
+      bool halves = false;
+      auto first_s = [&](int s) {  // the scores of a piece's first unit
+        n[0] = x.n0, n[1] = x.n1, halves = x.halves != 0;
+        if (n[0] > 0) issue_s(0, s, 0);
+        if (n[1] > 0) issue_s(1, s, 1);
+      };
       if (ok) {
         tc_fence_after();
         if (LOAD == GATHER) fence_async_smem();
-        len = x.n, n[0] = x.n0, n[1] = x.n1;
-        if (n[0] > 0) issue_s(0, 0);
-        if (n[1] > 0) issue_s(1, 0);
+        len = x.n;
+        first_s(0);
         commit(&kv_empty[ST - 1]);  // the first K is read: slot ST - 1 may load
         if (len == 1) commit(q_empty);
       }
@@ -395,29 +420,36 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           ok = mbar_wait_warp(&kv_full[s], (u / ST) & 1, err);
           if (!ok) break;
           if (LOAD == GATHER) fence_async_smem();  // the lanes' copies, for the tensor core
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (j >= n[g]) continue;
-            if (j == 0 && done[g] > 0) {
-              ok = mbar_wait_warp(&o_free[g], (done[g] - 1) & 1, err);
-              if (!ok) break;
-            }
-            ok = mbar_wait_warp(&p_lo[g], seen[g] & 1, err);
-            if (!ok) break;
+          auto pv = [&](int g, bool begun) {  // O_g (+)= P_g V, half by half as P arrives
+            if (!begun && done[g] > 0 && !mbar_wait_warp(&o_free[g], (done[g] - 1) & 1, err)) return false;
+            if (!mbar_wait_warp(&p_lo[g], seen[g] & 1, err)) return false;
             tc_fence_after();
-            issue_pv(g, s, 0, j > 0 ? 1u : 0u);
-            ok = mbar_wait_warp(&p_hi[g], seen[g] & 1, err);
-            if (!ok) break;
+            issue_pv(g, s, 0, begun ? 1u : 0u);
+            if (!mbar_wait_warp(&p_hi[g], seen[g] & 1, err)) return false;
             tc_fence_after();
             issue_pv(g, s, 1, 1u);
             ++seen[g];
-            if (j + 1 < n[g]) issue_s(g, s1);
+            return true;
+          };
+          if (halves) {
+            // The next unit's scores go to the other group's columns, whose P was
+            // read a unit ago, so they need not wait for this unit's P.
+            if (!last) issue_s((j + 1) & 1, s1, 0);
+            ok = j & 1 ? pv(1, j > 1) : pv(0, j > 0);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (j >= n[g]) continue;
+              ok = pv(g, j > 0);
+              if (!ok) break;
+              if (j + 1 < n[g]) issue_s(g, s1, g);
+            }
           }
           if (!ok) break;
           if (j + 2 == len) commit(q_empty);  // the piece's last scores are under way
           if (last) {
             if (n[0] > 0) ++done[0];
-            if (n[1] > 0) ++done[1];
+            if (n[1] > 0 || halves) ++done[1];
             ok = pieces.read(&x);
             if (!ok) break;
             next = x.n;
@@ -425,9 +457,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
               ok = mbar_wait_warp(q_full, (idx + 1) & 1, err);
               if (!ok) break;
               tc_fence_after();
-              n[0] = x.n0, n[1] = x.n1;
-              if (n[0] > 0) issue_s(0, s1);
-              if (n[1] > 0) issue_s(1, s1);
+              first_s(s1);
               if (next == 1) commit(q_empty);
             }
           }
@@ -502,7 +532,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         if (lane < bpt)
           for (int c = 0; c < L::PANELS; ++c) tma_load_3d(dst + c * L::PANEL + lane * p.bs * 128, map, bar, c * 64, 0, z);
       };
-      Unit cur = fetch(), nxt = fetch(), far = fetch();
+      Unit cur = fetch();
       int z = place(cur), u = 0;
       bool ok = cur.any;
       if (ok) {
@@ -510,6 +540,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         __syncwarp();
         load(&tk, sK, k0_full, z);
       }
+      Unit nxt = fetch(), far = fetch();
       while (ok) {
         const int s = u % ST, s1 = (u + 1) % ST;
         const int z1 = nxt.any ? place(nxt) : 0;
@@ -536,8 +567,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     const int quarter = warp & 3;   // TMEM lanes 32*quarter .. +31
     const int r = quarter * 32 + lane;
     const uint32_t s_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * TK;
-    const uint32_t bars = smem_u32(s_full + g);  // s_full[g]; p_lo, p_hi, pv_done and o_free follow, two by two
-    constexpr uint32_t P_LO = 16, P_HI = 32, PV_DONE = 48, O_FREE = 64;
+    const uint32_t bars = smem_u32(s_full + g);  // s_full[g]; p_lo, p_hi, pv_done and o_free follow, two by two, then half
+    constexpr uint32_t P_LO = 16, P_HI = 32, PV_DONE = 48, O_FREE = 64, HALF = 80;
     const uint32_t o_addr = s_addr + 256;
     const float scale_log2 = p.scale_log2;
     // Registers are short here (a row's 128 scores are in them): what a row
@@ -549,7 +580,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     };
     auto row_of = [&](const Piece& x) {
       const int tt = r / p.heads;
-      Row y{false, g * p.tpt + tt, r - tt * p.heads};
+      Row y{false, (x.halves ? 0 : g * p.tpt) + tt, r - tt * p.heads};
       y.valid = r < filled && y.tok < x.ntok && y.head < x.heads;
       return y;
     };
@@ -558,7 +589,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       const Row y = row_of(x);
       return !y.valid ? ALL : p.causal ? max(x.pos0 + y.tok + 1, 0) : x.len;
     };
-    int u = 0, seen = 0;  // units of the CTA; units of this query tile
+    int seen = 0;  // units of this group
     for (int idx = 0;; ++idx) {
       if (!mbar_wait_warp(&piece_full[idx % RING], (idx / RING) & 1, err)) break;
       const Piece& x = ring[idx % RING];
@@ -567,9 +598,11 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       const int sight_lo = __reduce_min_sync(0xffffffffu, sight_of(x));  // ALL: no row of the warp has a token
       float m = -INFINITY;  // exponent reference (log2 units of scaled scores)
       float l = 0.f;        // running denominator relative to m
-      const int u_next = u + x.n;
-      for (int j = 0; j < (g ? x.n1 : x.n0); ++j, ++seen, ++u) {
-        const int k0 = (x.kt0 + j) * TK;
+      const bool live = sight_lo != ALL;
+      const int edge = min(sight_lo, x.len);  // keys below it need no mask and no zeroed values
+      const int k_end = (x.kt0 + (g && !x.halves ? x.n1 : x.n0)) * TK, step = TK << x.halves;
+      bool begun = false;
+      for (int k0 = (x.kt0 + (x.halves & g)) * TK; k0 < k_end; k0 += step, ++seen) {
         ok = wait_at(bars, seen & 1, err);
         if (!ok) break;
         tc_fence_after();
@@ -578,8 +611,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         // Their value rows are zeroed before the product reads them. (S of this
         // unit is there, so the barrier is at this unit's phase at least: its
         // parity wait is exact.)
-        if (LOAD == BOXES && k0 + TK > x.len) {
-          const int s = u % ST;
+        if (LOAD == BOXES && k0 + TK > edge && k0 + TK > x.len) {
+          const int u = x.unit0 + k0 / TK - x.kt0, s = u % ST;
           ok = mbar_wait_warp(&kv_full[s], (u / ST) & 1, err);
           if (!ok) break;
           if (k0 + r >= x.len)
@@ -594,7 +627,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           __syncwarp();
           if (lane == 0) arrive_at(bars + bar);
         };
-        if (sight_lo == ALL) {  // no row to compute: what P holds for these rows reaches no other
+        if (!live) {  // no row to compute: what P holds for these rows reaches no other
           release(P_LO);
           release(P_HI);
           continue;
@@ -608,7 +641,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         float y[TK];
 #pragma unroll
         for (int c = 0; c < TK; ++c) y[c] = __uint_as_float(raw[c / 32][c % 32]);
-        if (k0 + TK > sight_lo) {
+        if (k0 + TK > edge) {
           const int mine = sight_of(x) - k0;
 #pragma unroll
           for (int c = 0; c < TK; ++c)
@@ -635,7 +668,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           const float v = m == -INFINITY ? 0.f : -m;
           return make_float2(v, v);
         };
-        if (j > 0) {
+        if (begun) {
           p_chunk(0, minus());
           p_chunk(32, minus());
         }
@@ -648,12 +681,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           for (int q = 0; q < 8; ++q) mx[q] = fmax3(mx[q], y[c + q], y[c + 8 + q]);
         const float tile_max = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * scale_log2;
         const bool raise = __any_sync(0xffffffffu, tile_max > m + RESCALE_LOG2);
-        if (raise || j == 0) {
+        if (raise || !begun) {
           const float m_new = fmaxf(m, tile_max);
           const float alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);  // 0 on a row's first key
           m = m_new;
           l *= alpha;
-          if (j > 0) {
+          if (begun) {
             ok = wait_at(bars + PV_DONE, (seen - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
@@ -681,68 +714,128 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         p_chunk(64, minus());
         p_chunk(96, minus());
         release(P_HI);
+        begun = true;
         l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       }
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
-      const bool any = (g ? x.n1 : x.n0) > 0;
+      const bool any = x.halves || (g ? x.n1 : x.n0) > 0;
       if (any) {
         ok = wait_at(bars + PV_DONE, (seen - 1) & 1, err);
         if (!ok) break;
         tc_fence_after();
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
-      const bool none = l == 0.f;                  // no key: zeros, whatever O holds
-      const float lse = none ? -INFINITY : (m + __log2f(l)) * LN2;
-      const Row y = row_of(x);
-      const bool valid = y.valid;
-      const long long orow = static_cast<long long>(x.tok0 + y.tok) * p.H + x.head0 + y.head;
-      const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (any && sight_lo != ALL) {
-          tmem_ld32(o_addr + c, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-        float f[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : __uint_as_float(o[i]) * inv;
-        if (valid && x.slot < 0) {
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const float* v = f + ch * 8;
-            const long long off = orow * D + c + ch * 8;
-            if (in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
-              *reinterpret_cast<uint4*>(p.o + off) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          }
-        } else if (valid) {
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const long long off = ((static_cast<long long>(x.slot) * (D / 4) + c / 4 + ch) * ROWS + g * BM + r) * 4;
-            if (in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err))
-              *reinterpret_cast<float4*>(p.o_part + off) = make_float4(f[ch * 4], f[ch * 4 + 1], f[ch * 4 + 2], f[ch * 4 + 3]);
-          }
-        }
-        __syncwarp();
-      }
-      if (valid) {
-        if (x.slot < 0) {
-          if (in_range(orow, 1, static_cast<long long>(p.T) * p.H, err)) p.lse[orow] = lse;
-        } else if (in_range(prow, 1, static_cast<long long>(p.n_slots) * ROWS, err)) {
-          p.lse_part[prow] = lse;
-        }
-      }
-      if (any) {  // O is read: the next piece's products may overwrite it
+      // Halves: the second group leaves m and l, and its O in tensor memory (a
+      // row's two halves lie in one lane), to the first, which joins them.
+      const bool join = x.halves && g == 0, leave = x.halves && g == 1;
+      float l1 = 0.f, w0 = 1.f, w1 = 0.f;  // the other half's denominator; both halves' weights
+      if (leave) {
+        reinterpret_cast<float2*>(smem + L::STATS_OFF)[r] = make_float2(m, l);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at(bars + O_FREE);
+        if (lane == 0) arrive_at(bars + HALF - 8);  // bars: of group 1
       }
-      u = u_next;
+      if (join) {
+        ok = wait_at(bars + HALF, x.joined & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        const float2 other = reinterpret_cast<const float2*>(smem + L::STATS_OFF)[r];
+        l1 = other.y;
+        const float top = fmaxf(m, other.x);
+        w0 = m == -INFINITY ? 0.f : ex2(m - top);
+        w1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
+        if (l != l || l1 != l1) w0 = w1 = NAN;  // a NaN score: a NaN row
+        m = top;
+      }
+      if (!leave) {
+        const bool none0 = l == 0.f, none1 = l1 == 0.f;  // no key: nothing of O, whatever it holds
+        l = w0 * l + w1 * l1;
+        const float inv = none0 && none1 ? 0.f : 1.f / l;  // NaN stays NaN
+        const float lse = none0 && none1 ? -INFINITY : (m + __log2f(l)) * LN2;
+        w0 = none0 ? 0.f : w0 * inv, w1 = none1 ? 0.f : w1 * inv;
+        const Row y = row_of(x);
+        const bool valid = y.valid;
+        const int orow = (x.tok0 + y.tok) * p.H + x.head0 + y.head;  // below T·H, if valid
+        const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
+        constexpr int CW = 16;  // columns at a time
+        float f[CW];
+        auto columns = [&](int c) {  // this row's results c .. c + CW - 1
+#pragma unroll
+          for (int i = 0; i < CW; ++i) f[i] = 0.f;
+          if (!any || !live) return;
+          uint32_t o[CW];
+          tmem_ld16(o_addr + c, o);
+          tmem_ld_wait();
+          if (!none0) {
+#pragma unroll
+            for (int i = 0; i < CW; ++i) f[i] = __uint_as_float(o[i]) * w0;
+          }
+          __syncwarp();
+          if (join) {
+            tmem_ld16(o_addr + 128 + c, o);
+            tmem_ld_wait();
+            if (!none1) {
+#pragma unroll
+              for (int i = 0; i < CW; ++i) f[i] = fmaf(__uint_as_float(o[i]), w1, f[i]);
+            }
+            __syncwarp();
+          }
+        };
+        if (x.slot < 0) {
+          uint8_t* out = smem + L::OUT_OFF + (warp - 4) * (32 * L::OUT * 2);
+          constexpr int CH = L::OUT / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows to an instruction
+          const int at_row = valid ? orow : -1;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += L::OUT) {
+#pragma unroll 1
+            for (int c = 0; c < L::OUT; c += CW) {
+              columns(c0 + c);
+#pragma unroll
+              for (int e = 0; e < CW / 8; ++e) {
+                const float* v = f + e * 8;
+                *reinterpret_cast<uint4*>(out + lane * (L::OUT * 2) + (((c / 8 + e) ^ (lane & (CH - 1))) << 4)) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+              const int rr = k * RPI + lane / CH, ch = lane % CH;
+              const int to = __shfl_sync(0xffffffffu, at_row, rr);
+              const uint4 v = *reinterpret_cast<const uint4*>(out + rr * (L::OUT * 2) + ((ch ^ (rr & (CH - 1))) << 4));
+              const long long off = static_cast<long long>(to) * D + c0 + ch * 8;
+              if (to >= 0 && in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
+                *reinterpret_cast<uint4*>(p.o + off) = v;
+            }
+            __syncwarp();
+          }
+          if (valid && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err)) p.lse[orow] = lse;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D; c += CW) {
+            columns(c);
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < CW / 4; ++e) {
+                const long long off = ((static_cast<long long>(x.slot) * (D / 4) + c / 4 + e) * ROWS + g * BM + r) * 4;
+                if (in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err))
+                  *reinterpret_cast<float4*>(p.o_part + off) = make_float4(f[e * 4], f[e * 4 + 1], f[e * 4 + 2], f[e * 4 + 3]);
+              }
+            }
+            __syncwarp();
+          }
+          if (valid && in_range(prow, 1, static_cast<long long>(p.n_slots) * ROWS, err)) p.lse_part[prow] = lse;
+        }
+        if (any) {  // O is read: the next piece's products may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            arrive_at(bars + O_FREE);
+            if (join) arrive_at(bars + O_FREE + 8);
+          }
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_empty[idx % RING]);
     }
@@ -932,39 +1025,32 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 // ------------------------------------------------------------------- merge
 //
 // One output row from its parts: lse = ln Σ_s e^(lse_s), o = Σ_s e^(lse_s −
-// lse) o_s. The first ctas - 1 blocks in x take the items that share ends cut
-// (the first end inside an item is its block's), the others one long item
-// each; y is a slice of 32 rows. What each block merges follows from the
-// lengths alone and is worked out while the attention kernel still runs.
-constexpr int MERGE_THREADS = 256;
-constexpr int MAX_PARTS = (SHARE_CHUNKS + 1) * MAX_CTAS + 32;
+// lse) o_s. The first ctas - 1 blocks take the items that shares cut, as the
+// CTA with an item's first tile noted them (worked out from the lengths again
+// they took 6 us more), the others one long item each.
+constexpr int MERGE_THREADS = 512;
+constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
   __shared__ PlanSmem plan_smem;
   __shared__ int parts[MAX_PARTS];
-  __shared__ int n_parts, head, item;
+  __shared__ ItemCut shared_item;
   uint32_t* err = &g_extend_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Shape sh{2 * p.tpt, p.causal, p.lc};
-  Cut cut;
-  Place at;
-  i64 items0;
   const int job = static_cast<int>(blockIdx.x);
-  if (threadIdx.x == 0) n_parts = head = item = 0;
-  at.r = Request{0, 0, 0, 0};
   if (job < p.ctas - 1) {
-    const int k = job + 1;
-    if (plan<MERGE_THREADS, false>(p, &sh, &plan_smem, k, &cut, &at, &items0, err) && warp == 0) {
-      locate(p, sh, cut.start(k), &at);
-      // the first end within this item, and not one of the long ones
-      if (cut.start(k) > at.item0 && cut.start(k - 1) <= at.item0 && !sh.is_long(at.r, at.i) && lane == 0) {
-        const int n = parts_of(p, sh, cut, at, k - 1, [&](int i, int slot) { parts[i] = slot; });
-        n_parts = n > 1 ? n : 0, head = at.hv, item = at.i;  // one part: the outputs
-      }
-    }
+    wait_for_primary();
+    if (threadIdx.x == 0) shared_item = in_range(job, 1, p.ctas, err) ? p.cuts[job] : ItemCut{0, 0, 0, 0, 0};
+    __syncthreads();
+    for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * job + 1 : 2 * (job + i);
   } else {
+    Shape sh{2 * p.tpt, p.causal, p.lc};
+    Cut cut;
+    Place at;
+    i64 items0;
     const int want = job - (p.ctas - 1);
+    if (threadIdx.x == 0) shared_item = ItemCut{0, 0, 0, 0, 0};
     if (plan<MERGE_THREADS, true>(p, &sh, &plan_smem, want, &cut, &at, &items0, err) && warp == 0) {
       const int first = sh.first_long(at.r, 0), each = at.r.items - first;
       const int nth = static_cast<int>(want - items0);
@@ -994,56 +1080,67 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
           });
         n += __shfl_sync(0xffffffffu, sum, 31);
       }
-      if (lane == 0) n_parts = min(n, MAX_PARTS), head = at.hv, item = at.i;
+      const int per = p.hv / p.Hkv, h0 = at.hv % per * p.heads, G = p.H / p.Hkv, t0 = at.i * sh.span;
+      if (lane == 0)
+        shared_item = ItemCut{min(n, MAX_PARTS), at.r.row0 + t0, min(sh.span, at.r.n - t0), at.hv / per * G + h0,
+                              min(p.heads, G - h0)};
     }
+    wait_for_primary();
   }
   __syncthreads();
-  wait_for_primary();
-  const int n = n_parts, hv = head;
-  const int row = static_cast<int>(blockIdx.y) * 32 + lane, g = row / BM, r = row % BM;
-  const int tt = r / p.heads, hh = r - tt * p.heads, per = p.hv / p.Hkv, h0 = hv % per * p.heads, G = p.H / p.Hkv;
-  const int t0 = item * sh.span, tok = g * p.tpt + tt;
-  const bool valid = r < p.tpt * p.heads && t0 + tok < at.r.n && h0 + hh < G;
-  if (n == 0 || !valid) return;
-  constexpr int PER = D / 4 / 8;  // 4-value groups a warp takes: consecutive ones
-  float m = -INFINITY;
-  for (int s = 0; s < n; ++s) {
-    const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
-    const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
-    m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
-  }
-  float l = 0.f;
-  float4 acc[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m != -INFINITY) {
-#pragma unroll 4
+  const ItemCut it = shared_item;
+  const int n = it.parts;
+  // A warp takes 32 rows and a quarter of the columns at a time.
+  constexpr int PER = D / 16, TASKS = ROWS / 32 * 4;  // 4-value groups a quarter
+  if (n == 0) return;
+  for (int task = warp; task < TASKS; task += MERGE_THREADS / 32) {
+    const int row = task / 4 * 32 + lane, quarter = task % 4, g = row / BM, r = row % BM;
+    const int tt = r / p.heads, hh = r - tt * p.heads, tok = g * p.tpt + tt;
+    if (r >= p.tpt * p.heads || tok >= it.ntok || hh >= it.heads) continue;
+    float m = -INFINITY;
     for (int s = 0; s < n; ++s) {
       const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
       const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
-      const float w = ex2((v - m) * 1.4426950408889634f);
-      l += w;
+      m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
+    }
+    float l = 0.f;
+    float4 acc[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + warp * PER + i) * ROWS + row) * 4;
-        if (!in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)) continue;
-        const float4 t = *reinterpret_cast<const float4*>(p.o_part + off);
-        acc[i].x = fmaf(w, t.x, acc[i].x), acc[i].y = fmaf(w, t.y, acc[i].y);
-        acc[i].z = fmaf(w, t.z, acc[i].z), acc[i].w = fmaf(w, t.w, acc[i].w);
+    for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m != -INFINITY) {
+#pragma unroll 2
+      for (int s = 0; s < n; ++s) {
+        const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
+        const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
+        const float w = ex2((v - m) * 1.4426950408889634f);
+        l += w;
+        float4 t[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + quarter * PER + i) * ROWS + row) * 4;
+          t[i] = in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)
+                     ? *reinterpret_cast<const float4*>(p.o_part + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          acc[i].x = fmaf(w, t[i].x, acc[i].x), acc[i].y = fmaf(w, t[i].y, acc[i].y);
+          acc[i].z = fmaf(w, t[i].z, acc[i].z), acc[i].w = fmaf(w, t[i].w, acc[i].w);
+        }
       }
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long orow = static_cast<long long>(at.r.row0 + t0 + tok) * p.H + hv / per * G + h0 + hh;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long orow = static_cast<long long>(it.tok0 + tok) * p.H + it.head0 + hh;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const long long off = orow * D + (warp * PER + i) * 4;
-    if (in_range(off, 4, static_cast<long long>(p.T) * p.H * D, err))
-      *reinterpret_cast<uint2*>(p.o + off) = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
-                                                        pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    for (int i = 0; i < PER; i += 2) {
+      const long long off = orow * D + (quarter * PER + i) * 4;
+      if (in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
+        *reinterpret_cast<uint4*>(p.o + off) =
+            make_uint4(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv),
+                       pack_bf16x2(acc[i + 1].x * inv, acc[i + 1].y * inv), pack_bf16x2(acc[i + 1].z * inv, acc[i + 1].w * inv));
+    }
+    if (quarter == 0 && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err))
+      p.lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
   }
-  if (warp == 0 && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err))
-    p.lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
 }
 
 // ------------------------------------------------------------------ launch
@@ -1087,7 +1184,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(jobs), ROWS / 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(jobs));
   cfg.blockDim = dim3(MERGE_THREADS);
   cfg.stream = stream;
   cfg.attrs = &early;
@@ -1113,19 +1210,19 @@ size_t extend_sizes(Extend* p, int d, bool q4) {
   const long long items = p->hv * (p->T / span + (p->T < p->B ? p->T : p->B));  // at most
   const long long shares = items * (ctx + PIECE) / MIN_SHARE;
   p->ctas = static_cast<int>(shares < 1 ? 1 : shares > MAX_CTAS ? MAX_CTAS : shares);
-  p->may_chunk = p->T > span && ctx > p->lc;
+  p->may_chunk = p->T > (CHUNK_ITEMS - 1) * span && ctx > p->lc;
   p->n_long = 0;
   long long whole = 0;
   if (p->may_chunk) {
     // Items of requests with two or more: at most 2 T / span. A chunk is at
-    // least 1/8 of a share long, a long item passes at most twice its keys / lc.
-    const long long long_items = p->hv * (2ll * p->T / span), by_share = 2ll * SHARE_CHUNKS * p->ctas;
+    // least a share long, and a long item passes at most twice its keys / lc.
+    const long long long_items = p->hv * (2ll * p->T / span), by_share = 2ll * p->ctas;
     p->n_long = static_cast<int>(long_items < by_share ? long_items : by_share);
     whole = long_items * ((ctx + p->lc - 1) / p->lc);
     if (whole > by_share) whole = by_share;
   }
   p->n_slots = static_cast<int>(2 * p->ctas + whole);
-  return static_cast<size_t>(p->n_slots) * ROWS * (d + 1) * sizeof(float);
+  return static_cast<size_t>(p->n_slots) * ROWS * (d + 1) * sizeof(float) + p->ctas * sizeof(ItemCut);
 }
 
 cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream) {

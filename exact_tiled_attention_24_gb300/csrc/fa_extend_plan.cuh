@@ -5,7 +5,8 @@
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
 //   cost    of an item: the keys it sees, and PIECE for its start and end
-//           (measured: 1.5 key tiles' time). Keys and not key tiles, because
+//           (3 key tiles' time; 192, 320, 480 and 704 keys: a prompt of 8192
+//           tokens 435, 421, 427 and 436 us). Keys and not key tiles, because
 //           their sums over items have a closed form without a division
 //           (counting tiles, the start of a CTA took 14 us, now 4)
 //   order   request by request, (chunk,) K/V head, item, key. The costs in this
@@ -13,11 +14,15 @@
 //           to a key tile of its item: the lengths are on the device only, and
 //           equal shares need no rule for uneven ones. An item that crosses
 //           from one share to the next is finished by a merge of its parts.
-//   chunk   a request with several items reads its keys once an item. CTAs
-//           with equal shares stand at different keys of it, so what one reads
-//           has left L2 before another needs it. The keys are therefore cut
-//           into chunks of `lc` (their K and V fit L2), and all items pass one
-//           chunk before any passes the next.
+//   chunk   a request with many items reads its keys once an item. CTAs with
+//           equal shares stand at different keys of it, so what one reads has
+//           left L2 before another needs it. Such a request's keys are
+//           therefore cut into chunks of a share's length (or of what fits L2,
+//           if that is more), and all items pass one chunk before any passes
+//           the next: most shares are then one chunk of one item, and the CTAs
+//           walk along the keys together. 131072 keys, 8 K/V heads: 8 items a
+//           head 744 us, else 793; 16 items 1408 and 1532; but 4 items 441 and
+//           423, 2 items 320 and 252.
 #pragma once
 
 #include <cstdint>
@@ -31,10 +36,12 @@ namespace fa {
 namespace ext {
 
 constexpr int TK = 128;             // keys a tile
-constexpr int PIECE = 192;          // an item's start and end, in keys
-constexpr int MIN_SHARE = 5 * TK;   // a CTA's share is at least that
+constexpr int PIECE = 384;         // an item's start and end, in keys
+constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than PIECE + TK, so that the ends of two
+                                   // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
-constexpr int SHARE_CHUNKS = 8;     // chunks are at least 1/8 of a share long
+constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks
+static_assert(MIN_SHARE >= PIECE + 2 * TK, "");
 
 typedef long long i64;
 
@@ -84,7 +91,7 @@ struct Shape {
     const int d = static_cast<int>(x) - r.base();
     return d < 0 ? 0 : min(d / span, r.items - 1);
   }
-  FA_HD bool chunked(const Request& r) const { return r.items > 1 && r.len > lc; }
+  FA_HD bool chunked(const Request& r) const { return r.items >= CHUNK_ITEMS && r.len > lc; }
   FA_HD int chunks(const Request& r) const { return chunked(r) ? (r.len + lc - 1) / lc : 1; }
   // the first item that reaches chunk c
   FA_HD int reach(const Request& r, int c) const { return c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
@@ -132,12 +139,22 @@ struct Shape {
   FA_HD static int tile_at(i64 x) { return x <= PIECE ? 0 : static_cast<int>((x - PIECE) / TK); }
 };
 
-// The whole call's cut. C shares of `cost`: share k is [start(k), start(k + 1)).
+// The whole call's cut into `ctas` shares: share k is [start(k), start(k + 1)),
+// the first `extra` one longer than the others.
 struct Cut {
-  i64 cost;
-  int ctas;
-  FA_HD i64 start(int k) const { return cost * k / ctas; }
-  FA_HD int owner(i64 x) const { return static_cast<int>(((x + 1) * ctas - 1) / cost); }
+  i64 per;
+  int ctas, extra;
+  FA_HD Cut() : per(0), ctas(0), extra(0) {}
+  FA_HD Cut(i64 cost, int most) {
+    const i64 fit = cost / MIN_SHARE;
+    ctas = fit < 1 ? 1 : fit > most ? most : static_cast<int>(fit);
+    per = cost / ctas, extra = static_cast<int>(cost - per * ctas);
+  }
+  FA_HD i64 start(int k) const { return per * k + min(k, extra); }
+  FA_HD int owner(i64 x) const {
+    const i64 longer = (per + 1) * extra;
+    return static_cast<int>(x < longer ? x / (per + 1) : extra + (x - longer) / per);
+  }
 };
 
 // An item of one chunk, with what lies before it.
@@ -199,17 +216,17 @@ __device__ __forceinline__ bool plan(const Extend& p, Shape* sh, PlanSmem* sm, i
       if (r.n > 0) k += sh->keys_before(r, r.items) * p.hv;
     }
     block_scan<NT>(k, sm->scan, &all);
-    const i64 least = (all / (SHARE_CHUNKS * p.ctas) + TK) / TK * TK;
+    const i64 least = (all / p.ctas + TK) / TK * TK;
     if (least > sh->lc) sh->lc = least < (1 << 29) ? static_cast<int>(least) : 1 << 29;
   }
   // costs before each thread's request; with more requests than threads, the total first
   i64 c = 0;
   for (int b = tid; b < p.B; b += NT) c += sh->total(b == tid ? mine : request_of(p, b, err), p.hv);
-  const i64 before = block_scan<NT>(c, sm->scan, &cut->cost);
-  const i64 most = cut->cost / MIN_SHARE;
-  cut->ctas = static_cast<int>(most < 1 ? 1 : most > p.ctas ? p.ctas : most);
+  i64 total;
+  const i64 before = block_scan<NT>(c, sm->scan, &total);
+  *cut = Cut(total, p.ctas);
   if (tid == 0) sm->b = -1;
-  const bool there = cut->cost > 0 && (LONG || want < cut->ctas);
+  const bool there = total > 0 && (LONG || want < cut->ctas);
   const i64 target = LONG || !there ? want : cut->start(want);
   i64 costs = 0, longs = 0, items = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
@@ -261,7 +278,12 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
   }
   const i64 row = sh.costs_before(r, c, r.items);
   at->c = c;
-  at->hv = static_cast<int>(rem / row);
+  at->hv = 0;
+  for (int h0 = 0; h0 < p.hv; h0 += 32) {  // rem / row
+    const int cnt = __popc(__ballot_sync(0xffffffffu, h0 + lane < p.hv && row * (h0 + lane) <= rem));
+    if (cnt > 0) at->hv = h0 + cnt - 1;
+    if (cnt < 32) break;
+  }
   rem -= row * at->hv;
   int lo = sh.reach(r, c), hi = r.items;
   while (hi - lo > 1) {
@@ -288,7 +310,9 @@ __device__ __forceinline__ int part_slot(const Extend& p, const Shape& sh, const
 }
 
 // The parts that the shares make of one item of one chunk, in order: calls
-// f(slot) for each; k: the share in which it begins.
+// f(i, slot) for each; k: the share in which it begins. (An item cut once or
+// more, and not a long one: slot 2k + 1 of the share k in which its first tile
+// lies, then 2 (k + 1), 2 (k + 2) and so on.)
 template <class F>
 __device__ __forceinline__ int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
   const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape::tiles_of(sh.part(at.r, at.c, at.i));

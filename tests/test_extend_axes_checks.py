@@ -57,9 +57,9 @@ def test_extend_workspace(L):
                 (4, 1, 8, 2, 128, 0, 8), (4, 1, 8, 2, 128, 16, 0)):
         assert f(*bad) == 0, bad
     part = 256 * 129 * 4
-    assert f(1, 1, 8, 2, 128, 16, 1) % part == 0                       # one tile: one CTA
-    assert f(32, 32, 32, 8, 128, 16, 512) <= 2 * 152 * part            # one item a head: two parts a CTA
-    assert f(1 << 17, 1, 32, 8, 128, 16, 1 << 13) <= 20 * 152 * part   # however long the prompt and its prefix
+    assert f(1, 1, 8, 2, 128, 16, 1) < 3 * part                              # one tile: one CTA, two parts at most
+    assert f(32, 32, 32, 8, 128, 16, 512) <= 2 * 152 * (part + 64)           # one item a head: two parts a CTA
+    assert f(1 << 17, 1, 32, 8, 128, 16, 1 << 13) <= 20 * 152 * (part + 64)  # however long the prompt and its prefix
 
 
 def axes(pairs=(0,) * 64, n=3, positions=FAKE):

@@ -99,14 +99,17 @@ def test_q4_every_code_reads_back_rounded_once(fa):
     assert torch.equal(o[:, 0].float().cpu(), want[:, 0, 0])
 
 
-@pytest.mark.parametrize("H,Hkv,d,new,lens", [(64, 64, 128, [300, 2], [3000, 700]), (128, 128, 64, [600], [4500]),
-                                              (64, 64, 128, [2000], [2000])])
+@pytest.mark.parametrize("H,Hkv,d,new,lens", [(64, 64, 128, [300, 2], [3000, 700]), (128, 128, 64, [1500, 3], [4500, 4000]),
+                                              (64, 64, 128, [2000], [2000]), (64, 64, 128, [700, 1600], [1500, 6000]),
+                                              (240, 8, 128, [90], [24000])])
 def test_keys_in_chunks(fa, H, Hkv, d, new, lens):
-    """So many K/V heads that a chunk of keys is shorter than the context."""
+    """So many K/V heads, or so long a context, that a chunk of keys is shorter
+    than the context, with a few items a head and many."""
     q, (kc, vc), table, L, starts = extend_case(H, Hkv, d, 16, new, lens, seed=77)
     o, lse = run(fa, q, (kc, vc), table, L, starts)
-    pick = list(range(0, H, H // 4))  # the oracle on some heads
-    check(q[:, pick], to_f64(kc[:, pick]), to_f64(vc[:, pick]), table, L, starts, o[:, pick], lse[:, pick])
+    kv = list(range(0, Hkv, Hkv // 4))  # the oracle on some heads
+    pick = [h * (H // Hkv) + h % (H // Hkv) for h in kv]
+    check(q[:, pick], to_f64(kc[:, kv]), to_f64(vc[:, kv]), table, L, starts, o[:, pick], lse[:, pick])
 
 
 def test_one_token_is_a_decode_step(fa):
