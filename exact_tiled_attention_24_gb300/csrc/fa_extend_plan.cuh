@@ -276,25 +276,34 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
     }
     rem -= sh.chunks_before(r, c) * p.hv;
   }
-  const i64 row = sh.costs_before(r, c, r.items);
   at->c = c;
   at->hv = 0;
-  for (int h0 = 0; h0 < p.hv; h0 += 32) {  // rem / row
-    const int cnt = __popc(__ballot_sync(0xffffffffu, h0 + lane < p.hv && row * (h0 + lane) <= rem));
-    if (cnt > 0) at->hv = h0 + cnt - 1;
-    if (cnt < 32) break;
-  }
-  rem -= row * at->hv;
+  // First the head, from one head's costs, then the item, by 32 probes at a
+  // time; one copy of the code for both (it runs once, from a cold cache).
   int lo = sh.reach(r, c), hi = r.items;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
-    const bool ok = probe < hi && sh.costs_before(r, c, probe) <= rem;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
-    lo += (cnt - 1) * step;
-    hi = min(hi, lo + step);
+  i64 found = 0;
+  bool head = true;
+#pragma unroll 1
+  while (head || hi - lo > 1) {
+    const int step = head ? 0 : (hi - lo + 31) / 32, probe = head ? hi : lo + lane * step;
+    const i64 v = sh.costs_before(r, c, min(probe, hi));
+    if (head) {
+      for (int h0 = 0; h0 < p.hv; h0 += 32) {  // rem / v
+        const int cnt = __popc(__ballot_sync(0xffffffffu, h0 + lane < p.hv && v * (h0 + lane) <= rem));
+        if (cnt > 0) at->hv = h0 + cnt - 1;
+        if (cnt < 32) break;
+      }
+      rem -= v * at->hv;
+      head = false;
+    } else {
+      const int cnt = __popc(__ballot_sync(0xffffffffu, probe < hi && v <= rem));
+      found = __shfl_sync(0xffffffffu, v, cnt - 1);
+      lo += (cnt - 1) * step;
+      hi = min(hi, lo + step);
+    }
   }
   at->i = lo;
-  at->item0 = x - (rem - sh.costs_before(r, c, lo));
+  at->item0 = x - (rem - found);  // found: the costs before item lo (0 if it is the first and only one)
 }
 
 // Where a piece's result goes: slots 2k and 2k + 1 are CTA k's first and last
