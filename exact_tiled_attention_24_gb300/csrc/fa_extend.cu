@@ -64,10 +64,8 @@ struct Piece {
   int pos0, len;         // position of the first token; cached tokens
   int slot;              // -1: the outputs
   int n0, n1;            // key tiles that each query tile sees
-  // One query tile and two key tiles at least: both softmax groups work on it,
-  // on every other key tile, and the first joins the two results.
-  int halves;
-  int unit0, joined;     // the CTA's units, and its pieces in halves, before this one
+  int unit0;             // the CTA's units before this piece
+  int pad[2];
 };
 static_assert(sizeof(Piece) == 64, "");
 
@@ -82,18 +80,17 @@ struct Smem {
   static constexpr int V_OFF = K_OFF + STAGES * TILE;
   static constexpr int PIECE_OFF = V_OFF + STAGES * TILE;
   static constexpr int BAR_OFF = PIECE_OFF + RING * static_cast<int>(sizeof(Piece));
-  // q_full, q_empty, k0_full, kv_full[], kv_empty[], s_full[2], p_lo[2], p_hi[2], pv_done[2], o_free[2], half, final,
+  // q_full, q_empty, k0_full, kv_full[], kv_empty[], s_full[2], p_lo[2], p_hi[2], pv_done[2], o_free[2], final,
   // piece_full[], piece_empty[]
-  static constexpr int NBARS = 3 + 2 * STAGES + 10 + 2 + 2 * RING;
+  static constexpr int NBARS = 3 + 2 * STAGES + 10 + 1 + 2 * RING;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int PLAN_OFF = SLOT_OFF + 16;
-  static constexpr int RAW_OFF = (PLAN_OFF + static_cast<int>(sizeof(PlanSmem)) + 15) / 16 * 16;
+  static constexpr int PLAN_OFF = K_OFF;  // the plan is made before any K arrives
+  static constexpr int RAW_OFF = (SLOT_OFF + 16 + 15) / 16 * 16;
   // 4-bit caches: a tile's codes and pairs of K and of V
-  static constexpr int STATS_OFF = RAW_OFF + (LOAD == CODES ? 2 * TK * (D / 2 + D / 8) : 0);  // [128] (m, l)
   // Results pass through shared memory on their way out, OUT columns of a
   // warp's 32 rows at a time (as much as fits): rows of 16-byte pieces a thread
   // each, 32 rows to an instruction, took 2 us a piece.
-  static constexpr int OUT_OFF = STATS_OFF + BM * 8;
+  static constexpr int OUT_OFF = RAW_OFF + (LOAD == CODES ? 2 * TK * (D / 2 + D / 8) : 0);
   static constexpr int OUT = LOAD == CODES && D == 128 ? 16 : 64;
   static constexpr int BYTES = OUT_OFF + 8 * 32 * OUT * 2;
   // One CTA an SM (one 512-column TMEM allocation), 1024 bytes to align.
@@ -198,8 +195,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   uint64_t* p_hi = p_lo + 2;           // [2] keys 64..127
   uint64_t* pv_done = p_hi + 2;        // [2]
   uint64_t* o_free = pv_done + 2;      // [2] the epilogue has read O
-  uint64_t* half = o_free + 2;         // the second group's half of a piece is there
-  uint64_t* final_bar = half + 1;
+  uint64_t* final_bar = o_free + 2;
   uint64_t* piece_full = final_bar + 1;
   uint64_t* piece_empty = piece_full + RING;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
@@ -250,7 +246,6 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       mbar_init(&pv_done[g], 1);
       mbar_init(&o_free[g], 4);
     }
-    mbar_init(half, 4);
     mbar_init(final_bar, 1);
     for (int i = 0; i < RING; ++i) {
       mbar_init(&piece_full[i], 1);
@@ -277,7 +272,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   const uint32_t tmem = *tmem_slot;
 
   // The launch's registers go where they are needed: 128 · (104 + 2 · 200) of
-  // 384 · 168 with boxes, else 128 · (72 + 2 · 168 + 104) = 512 · 128.
+  // 384 · 168 with boxes, else 128 · (72 + 2 · 176 + 88) = 512 · 128.
   if (warp < 4) {
     regs_down<LOAD == BOXES ? 104 : 72>();
     if (warp == 0) {
@@ -306,7 +301,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
         const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
         if (hi > lo) {
-          x.unit0 += x.n, x.joined += x.halves;
+          x.unit0 += x.n;
           x.n = hi - lo;
           x.kt0 = at.c * (sh.lc / TK) + lo;
           x.b = at.b;
@@ -331,7 +326,6 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
             return min(max((keys + TK - 1) / TK - x.kt0, 0), x.n);
           };
           x.n0 = sees(0), x.n1 = sees(1);
-          x.halves = x.ntok <= p.tpt && x.n0 > 1;
           if (!emit(x)) break;
           if (lo == 0 && hi < tiles && !sh.is_long(r, at.i))
             last = ItemCut{cut.owner(item_end - 1) - cta + 1, x.tok0, x.ntok, x.head0, x.heads};
@@ -364,8 +358,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       const uint64_t dq = sdesc_kmajor(smem_u32(sQ), 0);
       const uint64_t dk = sdesc_kmajor(smem_u32(sK), 0);
       const uint64_t dv = sdesc_mnmajor(smem_u32(sV), 0, L::PANEL);
-      auto issue_s = [&](int g, int s, int tile) {  // S_g = Q Kᵀ, Q's tile, K in stage s
-        const uint64_t a = desc_add(dq, tile * L::TILE), b = desc_add(dk, s * L::TILE);
+      auto issue_s = [&](int g, int s) {  // S_g = Q_g Kᵀ, K in stage s
+        const uint64_t a = desc_add(dq, g * L::TILE), b = desc_add(dk, s * L::TILE);
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -398,11 +392,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       bool ok = pieces.read(&x) && x.n > 0 && mbar_wait_warp(q_full, 0, err) && mbar_wait_warp(k0_full, 0, err);
       int n[2] = {0, 0}, seen[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece; units, pieces so far of each query tile
       int len = 0, idx = 0, u = 0;
-      bool halves = false;
       auto first_s = [&](int s) {  // the scores of a piece's first unit
-        n[0] = x.n0, n[1] = x.n1, halves = x.halves != 0;
-        if (n[0] > 0) issue_s(0, s, 0);
-        if (n[1] > 0) issue_s(1, s, 1);
+        n[0] = x.n0, n[1] = x.n1;
+        if (n[0] > 0) issue_s(0, s);
+        if (n[1] > 0) issue_s(1, s);
       };
       if (ok) {
         tc_fence_after();
@@ -431,25 +424,18 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
             ++seen[g];
             return true;
           };
-          if (halves) {
-            // The next unit's scores go to the other group's columns, whose P was
-            // read a unit ago, so they need not wait for this unit's P.
-            if (!last) issue_s((j + 1) & 1, s1, 0);
-            ok = j & 1 ? pv(1, j > 1) : pv(0, j > 0);
-          } else {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (j >= n[g]) continue;
-              ok = pv(g, j > 0);
-              if (!ok) break;
-              if (j + 1 < n[g]) issue_s(g, s1, g);
-            }
+          for (int g = 0; g < 2; ++g) {
+            if (j >= n[g]) continue;
+            ok = pv(g, j > 0);
+            if (!ok) break;
+            if (j + 1 < n[g]) issue_s(g, s1);
           }
           if (!ok) break;
           if (j + 2 == len) commit(q_empty);  // the piece's last scores are under way
           if (last) {
             if (n[0] > 0) ++done[0];
-            if (n[1] > 0 || halves) ++done[1];
+            if (n[1] > 0) ++done[1];
             ok = pieces.read(&x);
             if (!ok) break;
             next = x.n;
@@ -561,14 +547,14 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       for (int i = max(0, u - ST); i < u; ++i) mbar_wait_warp(&kv_full[i % ST], (i / ST) & 1, err);
     }
   } else if (warp < 12) {
-    regs_up<LOAD == BOXES ? 200 : 168>();
+    regs_up<LOAD == BOXES ? 200 : 176>();
     // -------------------------------------------------------------- softmax
     const int g = (warp - 4) >> 2;  // query tile
     const int quarter = warp & 3;   // TMEM lanes 32*quarter .. +31
     const int r = quarter * 32 + lane;
     const uint32_t s_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * TK;
-    const uint32_t bars = smem_u32(s_full + g);  // s_full[g]; p_lo, p_hi, pv_done and o_free follow, two by two, then half
-    constexpr uint32_t P_LO = 16, P_HI = 32, PV_DONE = 48, O_FREE = 64, HALF = 80;
+    const uint32_t bars = smem_u32(s_full + g);  // s_full[g]; p_lo, p_hi, pv_done and o_free follow, two by two
+    constexpr uint32_t P_LO = 16, P_HI = 32, PV_DONE = 48, O_FREE = 64;
     const uint32_t o_addr = s_addr + 256;
     const float scale_log2 = p.scale_log2;
     // Registers are short here (a row's 128 scores are in them): what a row
@@ -580,7 +566,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     };
     auto row_of = [&](const Piece& x) {
       const int tt = r / p.heads;
-      Row y{false, (x.halves ? 0 : g * p.tpt) + tt, r - tt * p.heads};
+      Row y{false, g * p.tpt + tt, r - tt * p.heads};
       y.valid = r < filled && y.tok < x.ntok && y.head < x.heads;
       return y;
     };
@@ -600,9 +586,9 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       float l = 0.f;        // running denominator relative to m
       const bool live = sight_lo != ALL;
       const int edge = min(sight_lo, x.len);  // keys below it need no mask and no zeroed values
-      const int k_end = (x.kt0 + (g && !x.halves ? x.n1 : x.n0)) * TK, step = TK << x.halves;
+      const int k_end = (x.kt0 + (g ? x.n1 : x.n0)) * TK;
       bool begun = false;
-      for (int k0 = (x.kt0 + (x.halves & g)) * TK; k0 < k_end; k0 += step, ++seen) {
+      for (int k0 = x.kt0 * TK; k0 < k_end; k0 += TK, ++seen) {
         ok = wait_at(bars, seen & 1, err);
         if (!ok) break;
         tc_fence_after();
@@ -720,128 +706,91 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       }
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
-      const bool any = x.halves || (g ? x.n1 : x.n0) > 0;
+      const bool any = (g ? x.n1 : x.n0) > 0;
       if (any) {
         ok = wait_at(bars + PV_DONE, (seen - 1) & 1, err);
         if (!ok) break;
         tc_fence_after();
       }
-      // Halves: the second group leaves m and l, and its O in tensor memory (a
-      // row's two halves lie in one lane), to the first, which joins them.
-      const bool join = x.halves && g == 0, leave = x.halves && g == 1;
-      float l1 = 0.f, w0 = 1.f, w1 = 0.f;  // the other half's denominator; both halves' weights
-      if (leave) {
-        reinterpret_cast<float2*>(smem + L::STATS_OFF)[r] = make_float2(m, l);
+      const bool none = l == 0.f;               // no key: nothing of O, whatever it holds
+      const float inv = none ? 0.f : 1.f / l;   // NaN stays NaN
+      const float lse = none ? -INFINITY : (m + __log2f(l)) * LN2;
+      const Row y = row_of(x);
+      const bool valid = y.valid;
+      const int orow = (x.tok0 + y.tok) * p.H + x.head0 + y.head;  // below T·H, if valid
+      const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
+      constexpr int CW = 16;  // columns at a time
+      float f[CW];
+      auto columns = [&](int c) {  // this row's results c .. c + CW - 1
+#pragma unroll
+        for (int i = 0; i < CW; ++i) f[i] = 0.f;
+        if (!any) return;
+        uint32_t o[CW];
+        tmem_ld16(o_addr + c, o);
+        tmem_ld_wait();
+        if (!none) {
+#pragma unroll
+          for (int i = 0; i < CW; ++i) f[i] = __uint_as_float(o[i]) * inv;
+        }
+        __syncwarp();
+      };
+      if (!live) {  // no row of a token
+      } else if (x.slot < 0) {
+        uint8_t* out = smem + L::OUT_OFF + (warp - 4) * (32 * L::OUT * 2);
+        constexpr int CH = L::OUT / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows to an instruction
+        const int at_row = valid ? orow : -1;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += L::OUT) {
+#pragma unroll 1
+          for (int c = 0; c < L::OUT; c += CW) {
+            columns(c0 + c);
+#pragma unroll
+            for (int e = 0; e < CW / 8; ++e) {
+              const float* v = f + e * 8;
+              *reinterpret_cast<uint4*>(out + lane * (L::OUT * 2) + (((c / 8 + e) ^ (lane & (CH - 1))) << 4)) =
+                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7]));
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < CH; ++k) {
+            const int rr = k * RPI + lane / CH, ch = lane % CH;
+            const int to = __shfl_sync(0xffffffffu, at_row, rr);
+            const uint4 v = *reinterpret_cast<const uint4*>(out + rr * (L::OUT * 2) + ((ch ^ (rr & (CH - 1))) << 4));
+            const long long off = static_cast<long long>(to) * D + c0 + ch * 8;
+            if (to >= 0 && in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
+              *reinterpret_cast<uint4*>(p.o + off) = v;
+          }
+          __syncwarp();
+        }
+        if (valid && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err)) p.lse[orow] = lse;
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += CW) {
+          columns(c);
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < CW / 4; ++e) {
+              const long long off = ((static_cast<long long>(x.slot) * (D / 4) + c / 4 + e) * ROWS + g * BM + r) * 4;
+              if (in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err))
+                *reinterpret_cast<float4*>(p.o_part + off) = make_float4(f[e * 4], f[e * 4 + 1], f[e * 4 + 2], f[e * 4 + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (valid && in_range(prow, 1, static_cast<long long>(p.n_slots) * ROWS, err)) p.lse_part[prow] = lse;
+      }
+      if (any) {  // O is read: the next piece's products may overwrite it
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at(bars + HALF - 8);  // bars: of group 1
-      }
-      if (join) {
-        ok = wait_at(bars + HALF, x.joined & 1, err);
-        if (!ok) break;
-        tc_fence_after();
-        const float2 other = reinterpret_cast<const float2*>(smem + L::STATS_OFF)[r];
-        l1 = other.y;
-        const float top = fmaxf(m, other.x);
-        w0 = m == -INFINITY ? 0.f : ex2(m - top);
-        w1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
-        if (l != l || l1 != l1) w0 = w1 = NAN;  // a NaN score: a NaN row
-        m = top;
-      }
-      if (!leave) {
-        const bool none0 = l == 0.f, none1 = l1 == 0.f;  // no key: nothing of O, whatever it holds
-        l = w0 * l + w1 * l1;
-        const float inv = none0 && none1 ? 0.f : 1.f / l;  // NaN stays NaN
-        const float lse = none0 && none1 ? -INFINITY : (m + __log2f(l)) * LN2;
-        w0 = none0 ? 0.f : w0 * inv, w1 = none1 ? 0.f : w1 * inv;
-        const Row y = row_of(x);
-        const bool valid = y.valid;
-        const int orow = (x.tok0 + y.tok) * p.H + x.head0 + y.head;  // below T·H, if valid
-        const long long prow = static_cast<long long>(x.slot) * ROWS + g * BM + r;
-        constexpr int CW = 16;  // columns at a time
-        float f[CW];
-        auto columns = [&](int c) {  // this row's results c .. c + CW - 1
-#pragma unroll
-          for (int i = 0; i < CW; ++i) f[i] = 0.f;
-          if (!any || !live) return;
-          uint32_t o[CW];
-          tmem_ld16(o_addr + c, o);
-          tmem_ld_wait();
-          if (!none0) {
-#pragma unroll
-            for (int i = 0; i < CW; ++i) f[i] = __uint_as_float(o[i]) * w0;
-          }
-          __syncwarp();
-          if (join) {
-            tmem_ld16(o_addr + 128 + c, o);
-            tmem_ld_wait();
-            if (!none1) {
-#pragma unroll
-              for (int i = 0; i < CW; ++i) f[i] = fmaf(__uint_as_float(o[i]), w1, f[i]);
-            }
-            __syncwarp();
-          }
-        };
-        if (x.slot < 0) {
-          uint8_t* out = smem + L::OUT_OFF + (warp - 4) * (32 * L::OUT * 2);
-          constexpr int CH = L::OUT / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows to an instruction
-          const int at_row = valid ? orow : -1;
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += L::OUT) {
-#pragma unroll 1
-            for (int c = 0; c < L::OUT; c += CW) {
-              columns(c0 + c);
-#pragma unroll
-              for (int e = 0; e < CW / 8; ++e) {
-                const float* v = f + e * 8;
-                *reinterpret_cast<uint4*>(out + lane * (L::OUT * 2) + (((c / 8 + e) ^ (lane & (CH - 1))) << 4)) =
-                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                               pack_bf16x2(v[6], v[7]));
-              }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < CH; ++k) {
-              const int rr = k * RPI + lane / CH, ch = lane % CH;
-              const int to = __shfl_sync(0xffffffffu, at_row, rr);
-              const uint4 v = *reinterpret_cast<const uint4*>(out + rr * (L::OUT * 2) + ((ch ^ (rr & (CH - 1))) << 4));
-              const long long off = static_cast<long long>(to) * D + c0 + ch * 8;
-              if (to >= 0 && in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
-                *reinterpret_cast<uint4*>(p.o + off) = v;
-            }
-            __syncwarp();
-          }
-          if (valid && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err)) p.lse[orow] = lse;
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < D; c += CW) {
-            columns(c);
-            if (valid) {
-#pragma unroll
-              for (int e = 0; e < CW / 4; ++e) {
-                const long long off = ((static_cast<long long>(x.slot) * (D / 4) + c / 4 + e) * ROWS + g * BM + r) * 4;
-                if (in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err))
-                  *reinterpret_cast<float4*>(p.o_part + off) = make_float4(f[e * 4], f[e * 4 + 1], f[e * 4 + 2], f[e * 4 + 3]);
-              }
-            }
-            __syncwarp();
-          }
-          if (valid && in_range(prow, 1, static_cast<long long>(p.n_slots) * ROWS, err)) p.lse_part[prow] = lse;
-        }
-        if (any) {  // O is read: the next piece's products may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            arrive_at(bars + O_FREE);
-            if (join) arrive_at(bars + O_FREE + 8);
-          }
-        }
+        if (lane == 0) arrive_at(bars + O_FREE);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_empty[idx % RING]);
     }
   } else if constexpr (LOAD != BOXES) {
-    regs_down<104>();
+    regs_down<88>();
     // ----------------------------------------- K and V row by row, or unpacked
     // Each of four warps takes 32 rows of a tile, lane i the place of row i.
     constexpr uint32_t NO_ROW = 0xffffffffu;  // zeros (the host keeps the cache below 2^32 - 1 rows)
@@ -940,7 +889,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       // does not stay in the instruction cache beside the softmax. 306 -> 267 us
       // for 2777 tokens of 12 requests.)
       auto fetch_codes = [&](const void* cache, const uint32_t* scale, const Unit& t, uint8_t* raw) {
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < CPR; ++k) {
           const uint32_t row = __shfl_sync(0xffffffffu, t.row, k * RPI + sub);
           const bool live = row != NO_ROW && in_range(row, 1, rows_all, err);  // else zeros: step and centre 0
@@ -961,7 +910,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       auto unpack = [&](uint8_t* dst, const uint8_t* raw) {
         uint4 c = *reinterpret_cast<const uint4*>(raw);
         uint32_t pair = *reinterpret_cast<const uint32_t*>(raw + PAIRS - lane * 12);
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < CPR; ++k) {
           const uint32_t sbits = __byte_perm(pair, 0, 0x1010), zbits = __byte_perm(pair, 0, 0x3232);
           const __nv_bfloat162 eighth = __halves2bfloat162(__ushort_as_bfloat16(0x3f80), __ushort_as_bfloat16(0x3e00));  // 1, 1/8
@@ -1002,12 +951,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         far = fetch();
         if (u >= ST - 1) ok = mbar_wait_warp(&kv_empty[s], ((u - (ST - 1)) / ST) & 1, err);
         if (!ok) break;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {  // V of unit u, then K of unit u + 1
-          cp_async_wait<1>();
-          if (kv == 0 || nxt.any) unpack(kv ? sK + s1 * L::TILE : sV + s * L::TILE, kv ? kraw : vraw);
-          fetch_codes(kv ? p.k_cache : p.v_cache, kv ? p.k_scale : p.v_scale, kv ? after : nxt, kv ? kraw : vraw);
-        }
+        cp_async_wait<1>();
+        unpack(sV + s * L::TILE, vraw);
+        fetch_codes(p.v_cache, p.v_scale, nxt, vraw);
+        cp_async_wait<1>();
+        if (nxt.any) unpack(sK + s1 * L::TILE, kraw);
+        fetch_codes(p.k_cache, p.k_scale, after, kraw);
         publish(&kv_full[s]);
         ++u;
         if (!nxt.any) break;

@@ -192,7 +192,7 @@ __device__ __forceinline__ i64 block_scan(i64 v, i64* scratch, i64* total) {
 }
 
 struct PlanSmem {
-  i64 scan[16];
+  i64 scan[32];
   i64 request0, items0;
   int b, longs0;
 };
