@@ -27,6 +27,14 @@
 //   warps 12..15 (other block sizes, 4-bit caches) K and V tiles: gathered row
 //                by row, or codes unpacked to bf16 into the products' layout
 // TMEM columns: S0 0.., S1 128.., O0 256.., O1 384... P overwrites S.
+//
+// What bounds it (32 + 8 heads, d = 128, 2070 MHz): with full tiles the tensor
+// pipe, as in the forward: 2048 clocks of products in 3300 a unit (a prompt of
+// 8192 tokens 418 us, 1024 tokens at 131072 keys 1.38 to 1.45 ms, 1510 to 1590
+// TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
+// requests of 5 tokens over 2k to 8k keys: 136 us, 110 of them). Over codes the
+// unpacking: 155 us for the same. About 10 us pass until a CTA's first product
+// and 4 us with each piece's start and end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -879,15 +887,13 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       // wait in shared memory, in a place of the lane's own, for the step they
       // are unpacked in: the copies of the next tile are under way meanwhile.
       // (Held in registers instead, a tile took 6000 clocks: the compiler's waits
-      // for one load cover others.)
+      // for one load cover others. Now 3600 to 4200, 1100 to 1400 of them for
+      // each of keys and values: 4.25 instructions a pair of values, at half rate.)
       constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte pieces a row, rows a step; CPR steps
       const int quarter = lane % CPR, sub = lane / CPR;
       uint8_t* kraw = smem + L::RAW_OFF + w * (2 * CPR * 32 * 20) + lane * 16;
       uint8_t* vraw = kraw + CPR * 32 * 20;
       constexpr int PAIRS = CPR * 32 * 16;  // the pairs stand behind the codes, 4 bytes a lane
-      // (Loops and not straight lines, here and below: a tile's unpacking unrolled
-      // does not stay in the instruction cache beside the softmax. 306 -> 267 us
-      // for 2777 tokens of 12 requests.)
       auto fetch_codes = [&](const void* cache, const uint32_t* scale, const Unit& t, uint8_t* raw) {
 #pragma unroll
         for (int k = 0; k < CPR; ++k) {
@@ -910,6 +916,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       auto unpack = [&](uint8_t* dst, const uint8_t* raw) {
         uint4 c = *reinterpret_cast<const uint4*>(raw);
         uint32_t pair = *reinterpret_cast<const uint32_t*>(raw + PAIRS - lane * 12);
+        // Two steps at a time: four do not stay in the instruction cache beside the
+        // softmax (2777 tokens of 12 requests: one 265 us, two 258, four 306).
 #pragma unroll 2
         for (int k = 0; k < CPR; ++k) {
           const uint32_t sbits = __byte_perm(pair, 0, 0x1010), zbits = __byte_perm(pair, 0, 0x3232);
