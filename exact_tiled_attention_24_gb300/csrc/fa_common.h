@@ -156,9 +156,10 @@ int decode_q4_splits(int B, int H, int Hkv, long long max_ctx);
 cudaError_t launch_decode_q4(const DecodeQ4& p, int d, int S, cudaStream_t stream);
 
 // ---- attention of chunks of new tokens over a paged cache (fa_extend.cu)
-// An item of work whose first tile is a CTA's and that goes on into others' shares.
+// An item of work that a CTA's share begins within.
 struct ItemCut {
   int parts;  // 0: none
+  int nth;    // the CTA's place among those that share it (0 has its first tile)
   int tok0, ntok, head0, heads;
 };
 struct Extend {

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         return true;
       };
       Piece x{};  // n = 0
-      ItemCut last{0, 0, 0, 0, 0};
+      ItemCut entered{};
       while (true) {
         const Request& r = at.r;
         const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
@@ -335,8 +335,11 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
           };
           x.n0 = sees(0), x.n1 = sees(1);
           if (!emit(x)) break;
-          if (lo == 0 && hi < tiles && !sh.is_long(r, at.i))
-            last = ItemCut{cut.owner(item_end - 1) - cta + 1, x.tok0, x.ntok, x.head0, x.heads};
+          if (lo > 0 && !sh.is_long(r, at.i)) {  // the share's first piece at most
+            int first = cut.owner(at.item0);
+            if (Shape::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
+            entered = ItemCut{cut.owner(item_end - 1) - first + 1, cta - first, x.tok0, x.ntok, x.head0, x.heads};
+          }
         }
         if (item_end >= end) {
           x.n = 0;
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         }
         at.i = sh.reach(at.r, at.c);
       }
-      if (lane == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta] = last;
+      if (lane == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta] = entered;
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16(BM, TK, false, false);
@@ -984,11 +987,71 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 // ------------------------------------------------------------------- merge
 //
 // One output row from its parts: lse = ln Σ_s e^(lse_s), o = Σ_s e^(lse_s −
-// lse) o_s. The first ctas - 1 blocks take the items that shares cut, as the
-// CTA with an item's first tile noted them (worked out from the lengths again
-// they took 6 us more), the others one long item each.
+// lse) o_s. The first ctas - 1 blocks take the items that shares cut: a CTA
+// whose share begins within an item has noted it (worked out from the lengths
+// again they took 6 us more), and the blocks of an item's CTAs but the first
+// deal its rows out among them. (All by one block: 152 us for 64 tokens at
+// 131072 keys, 8 items of 19 parts each; now 121.) The others take one long item
+// each.
 constexpr int MERGE_THREADS = 512;
 constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
+
+// An item's rows: 32 rows and W 4-value groups of columns a task, UNROLL parts at a time.
+template <int D, int W, int UNROLL>
+__device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, const int* parts, int first, int step,
+                                           uint32_t* err) {
+  const int lane = threadIdx.x & 31, n = it.parts;
+  constexpr int ACROSS = D / 4 / W, TASKS = ROWS / 32 * ACROSS;
+  for (int task = first; task < TASKS; task += step) {
+    const int row = task / ACROSS * 32 + lane, c0 = task % ACROSS * W, g = row / BM, r = row % BM;
+    const int tt = r / p.heads, hh = r - tt * p.heads, tok = g * p.tpt + tt;
+    if (r >= p.tpt * p.heads || tok >= it.ntok || hh >= it.heads) continue;
+    float m = -INFINITY;
+#pragma unroll UNROLL
+    for (int s = 0; s < n; ++s) {
+      const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
+      const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
+      m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
+    }
+    float l = 0.f;
+    float4 acc[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m != -INFINITY) {
+#pragma unroll UNROLL
+      for (int s = 0; s < n; ++s) {
+        const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
+        const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
+        const float w = ex2((v - m) * 1.4426950408889634f);
+        l += w;
+        float4 t[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + c0 + i) * ROWS + row) * 4;
+          t[i] = in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)
+                     ? *reinterpret_cast<const float4*>(p.o_part + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          acc[i].x = fmaf(w, t[i].x, acc[i].x), acc[i].y = fmaf(w, t[i].y, acc[i].y);
+          acc[i].z = fmaf(w, t[i].z, acc[i].z), acc[i].w = fmaf(w, t[i].w, acc[i].w);
+        }
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long orow = static_cast<long long>(it.tok0 + tok) * p.H + it.head0 + hh;
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const long long off = orow * D + (c0 + i) * 4;
+      if (in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
+        *reinterpret_cast<uint4*>(p.o + off) =
+            make_uint4(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv),
+                       pack_bf16x2(acc[i + 1].x * inv, acc[i + 1].y * inv), pack_bf16x2(acc[i + 1].z * inv, acc[i + 1].w * inv));
+    }
+    if (c0 == 0 && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err))
+      p.lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
@@ -1000,16 +1063,17 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
   const int job = static_cast<int>(blockIdx.x);
   if (job < p.ctas - 1) {
     wait_for_primary();
-    if (threadIdx.x == 0) shared_item = in_range(job, 1, p.ctas, err) ? p.cuts[job] : ItemCut{0, 0, 0, 0, 0};
+    if (threadIdx.x == 0) shared_item = in_range(job + 1, 1, p.ctas, err) ? p.cuts[job + 1] : ItemCut{};
     __syncthreads();
-    for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * job + 1 : 2 * (job + i);
+    const int first = job + 1 - shared_item.nth;
+    for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * first + 1 : 2 * (first + i);
   } else {
     Shape sh{2 * p.tpt, p.causal, p.lc};
     Cut cut;
     Place at;
     i64 items0;
     const int want = job - (p.ctas - 1);
-    if (threadIdx.x == 0) shared_item = ItemCut{0, 0, 0, 0, 0};
+    if (threadIdx.x == 0) shared_item = ItemCut{};
     if (plan<MERGE_THREADS, true>(p, &sh, &plan_smem, want, &cut, &at, &items0, err) && warp == 0) {
       const int first = sh.first_long(at.r, 0), each = at.r.items - first;
       const int nth = static_cast<int>(want - items0);
@@ -1041,65 +1105,23 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
       }
       const int per = p.hv / p.Hkv, h0 = at.hv % per * p.heads, G = p.H / p.Hkv, t0 = at.i * sh.span;
       if (lane == 0)
-        shared_item = ItemCut{min(n, MAX_PARTS), at.r.row0 + t0, min(sh.span, at.r.n - t0), at.hv / per * G + h0,
+        shared_item = ItemCut{min(n, MAX_PARTS), 0, at.r.row0 + t0, min(sh.span, at.r.n - t0), at.hv / per * G + h0,
                               min(p.heads, G - h0)};
     }
     wait_for_primary();
   }
   __syncthreads();
   const ItemCut it = shared_item;
-  const int n = it.parts;
-  // A warp takes 32 rows and a quarter of the columns at a time.
-  constexpr int PER = D / 16, TASKS = ROWS / 32 * 4;  // 4-value groups a quarter
-  if (n == 0) return;
-  for (int task = warp; task < TASKS; task += MERGE_THREADS / 32) {
-    const int row = task / 4 * 32 + lane, quarter = task % 4, g = row / BM, r = row % BM;
-    const int tt = r / p.heads, hh = r - tt * p.heads, tok = g * p.tpt + tt;
-    if (r >= p.tpt * p.heads || tok >= it.ntok || hh >= it.heads) continue;
-    float m = -INFINITY;
-    for (int s = 0; s < n; ++s) {
-      const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
-      const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
-      m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
-    }
-    float l = 0.f;
-    float4 acc[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
-#pragma unroll 2
-      for (int s = 0; s < n; ++s) {
-        const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
-        const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
-        const float w = ex2((v - m) * 1.4426950408889634f);
-        l += w;
-        float4 t[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + quarter * PER + i) * ROWS + row) * 4;
-          t[i] = in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)
-                     ? *reinterpret_cast<const float4*>(p.o_part + off) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          acc[i].x = fmaf(w, t[i].x, acc[i].x), acc[i].y = fmaf(w, t[i].y, acc[i].y);
-          acc[i].z = fmaf(w, t[i].z, acc[i].z), acc[i].w = fmaf(w, t[i].w, acc[i].w);
-        }
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long orow = static_cast<long long>(it.tok0 + tok) * p.H + it.head0 + hh;
-#pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-      const long long off = orow * D + (quarter * PER + i) * 4;
-      if (in_range(off, 8, static_cast<long long>(p.T) * p.H * D, err))
-        *reinterpret_cast<uint4*>(p.o + off) =
-            make_uint4(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv),
-                       pack_bf16x2(acc[i + 1].x * inv, acc[i + 1].y * inv), pack_bf16x2(acc[i + 1].z * inv, acc[i + 1].w * inv));
-    }
-    if (quarter == 0 && in_range(orow, 1, static_cast<long long>(p.T) * p.H, err))
-      p.lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
-  }
+  if (it.parts == 0) return;
+  const int blocks = it.nth > 0 ? it.parts - 1 : 1, block = max(it.nth - 1, 0);
+  const int first = block * (MERGE_THREADS / 32) + warp, step = blocks * (MERGE_THREADS / 32);
+  // A warp takes 32 rows and a quarter of the columns at a time; 8 columns where
+  // that leaves half the warps without a task (items in many parts or with few rows).
+  const int rows0 = min(it.ntok, p.tpt) * p.heads, rows1 = max(it.ntok - p.tpt, 0) * p.heads;
+  if (2 * blocks >= (rows0 + 31) / 32 + (rows1 + 31) / 32)
+    merge_rows<D, 2, 2>(p, it, parts, first, step, err);
+  else
+    merge_rows<D, D / 16, 2>(p, it, parts, first, step, err);
 }
 
 // ------------------------------------------------------------------ launch

@@ -94,6 +94,22 @@ def test_lengths_past_the_table_and_below_zero(fa, kind):
     assert bool((ref[0][50:] == 0).all()) and bool(torch.isneginf(ref[1][50:]).all())
 
 
+@pytest.mark.parametrize("H,Hkv,d,bs,new,lens", [
+    (8, 1, 128, 16, [30], [60000]),                # one item in 90 parts
+    (8, 2, 64, 16, [3, 33], [20000, 31000]),       # few rows
+    (32, 4, 128, 64, [1], [30000]),                # one token a K/V head
+    (12, 2, 128, 5, [43, 1], [9001, 17]),          # gathered; 6 heads, 126 of 128 rows
+    (8, 8, 64, 32, [200, 256], [4000, 6000]),      # two full tiles an item, many items
+])
+def test_items_in_many_parts(fa, H, Hkv, d, bs, new, lens):
+    """Items that many shares cut: their rows are joined by all of those shares' blocks."""
+    q, (kc, vc), table, L, starts = extend_case(H, Hkv, d, bs, new, lens, seed=sum(lens))
+    o, lse = fa.extend_paged(*(t.cuda() for t in (q, kc, vc, table, L, starts)))
+    torch.cuda.synchronize()
+    assert fa.last_device_error() == 0
+    check(q, to_f64(kc), to_f64(vc), table, L, starts, o, lse)
+
+
 def test_two_captured_calls_over_codes_on_another_stream(fa):
     """Two graphs with a workspace each, replayed side by side with lengths that change between replays."""
     H, Hkv, d, bs, T = 8, 2, 128, 16, 200
