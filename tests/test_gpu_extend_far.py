@@ -1,6 +1,6 @@
 """extend_paged and extend_paged_q4 at the ends of what they index: caches and
-outputs past 2^31 elements, lengths past the table, captured calls over codes
-on another stream."""
+outputs past 2^31 elements, lengths past the table, table entries past the
+lengths, items in many parts, captured calls over codes on another stream."""
 import pytest
 import torch
 
@@ -142,3 +142,31 @@ def test_two_captured_calls_over_codes_on_another_stream(fa):
     assert fa.last_device_error() == 0
     k, v = held(dev[1].cpu(), dev[2].cpu()), held(dev[3].cpu(), dev[4].cpu())
     check(q, to_f64(k), to_f64(v), table, lens.cpu(), cuts.cpu(), ro, rl)
+
+
+@pytest.mark.parametrize("kind", ["16", "128", "3", "q4"])
+def test_table_entries_past_the_lengths_are_not_read(fa, kind):
+    bs = 16 if kind == "q4" else int(kind)
+    q, caches, table, L, starts = extend_case(8, 2, 128, bs, [9, 140, 1], [130, 517, 1], seed=2, fill=0.0)
+    if kind == "q4":
+        caches = codes_of(caches)
+    entry = fa.extend_paged_q4 if kind == "q4" else fa.extend_paged
+    dev = [t.cuda() for t in (q, *caches)]
+    ref = entry(*dev, table.cuda(), L.cuda(), starts.cuda())
+    past = torch.arange(table.shape[1])[None] * bs >= L[:, None]
+    assert bool(past.any())
+    for junk in (-1, 2 ** 31 - 1):
+        got = entry(*dev, table.masked_fill(past, junk).cuda(), L.cuda(), starts.cuda())
+        torch.cuda.synchronize()
+        assert fa.last_device_error() == 0
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 3), (17, 1), (33, 1), (100, 2), (257, 1)])
+def test_head_groups(fa, H, Hkv, d):
+    q, (kc, vc), table, L, starts = extend_case(H, Hkv, d, 16, [1, 13, 70], [1, 200, 333], seed=H + d)
+    o, lse = fa.extend_paged(*(t.cuda() for t in (q, kc, vc, table, L, starts)))
+    torch.cuda.synchronize()
+    assert fa.last_device_error() == 0
+    check(q, to_f64(kc), to_f64(vc), table, L, starts, o, lse)
