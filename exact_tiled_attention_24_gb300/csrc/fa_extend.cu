@@ -280,9 +280,10 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   const uint32_t tmem = *tmem_slot;
 
   // The launch's registers go where they are needed: 128 · (104 + 2 · 200) of
-  // 384 · 168 with boxes, else 128 · (72 + 2 · 176 + 88) = 512 · 128.
+  // 384 · 168 with boxes, else 128 · (88 + 2 · 176 + 72) = 512 · 128. (Softmax at
+  // 160: 670 us for 300 tokens at 131072 keys over codes, not 590.)
   if (warp < 4) {
-    regs_down<LOAD == BOXES ? 104 : 72>();
+    regs_down<LOAD == BOXES ? 104 : 88>();
     if (warp == 0) {
       // --------------------------------------------------------------- pieces
       const i64 begin = cut.start(cta), end = cut.start(cta + 1);
@@ -801,7 +802,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       if (lane == 0) mbar_arrive(&piece_empty[idx % RING]);
     }
   } else if constexpr (LOAD != BOXES) {
-    regs_down<88>();
+    regs_down<72>();
     // ----------------------------------------- K and V row by row, or unpacked
     // Each of four warps takes 32 rows of a tile, lane i the place of row i.
     constexpr uint32_t NO_ROW = 0xffffffffu;  // zeros (the host keeps the cache below 2^32 - 1 rows)
@@ -920,7 +921,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         uint4 c = *reinterpret_cast<const uint4*>(raw);
         uint32_t pair = *reinterpret_cast<const uint32_t*>(raw + PAIRS - lane * 12);
         // Two steps at a time: four do not stay in the instruction cache beside the
-        // softmax (2777 tokens of 12 requests: one 265 us, two 258, four 306).
+        // softmax (2777 tokens of 12 requests: one 260 us, two 254, four 265).
 #pragma unroll 2
         for (int k = 0; k < CPR; ++k) {
           const uint32_t sbits = __byte_perm(pair, 0, 0x1010), zbits = __byte_perm(pair, 0, 0x3232);

@@ -124,6 +124,43 @@ def test_appends(fa, q4, T, B, H, Hkv, d, bs, sections, turn, inter):
 
 
 @pytest.mark.parametrize("q4", [False, True])
+def test_captured_on_another_stream_with_fp32_weights(fa, q4):
+    """One graph of an append, a rotation and its gradient; positions and inputs change between replays."""
+    T, B, H, Hkv, d, bs = 40, 3, 4, 2, 128, 16
+    g, k, v, cache, table, pos, req, kw = append_inputs(fa, T, B, H, Hkv, d, bs, q4, 9)
+    kw.update({n: kw[n].float() for n in ("q_weight", "k_weight")})
+    weights = dict(q_weight=kw["q_weight"], k_weight=kw["k_weight"])
+    append = fa.append_paged_q4 if q4 else fa.append_paged
+    axes = fa.rope_axes((24, 20, 20), True)
+    cos, sin = fa.rope_tables(50, 128)
+    rope = torch.randint(0, 50, (3, T), generator=g).to(I32).cuda()
+    x, y = (torch.randn((1, h, T, d), generator=g).to(BF).cuda() for h in (H, Hkv))
+
+    def step(cache):
+        out = [append(k, v, *cache, table, pos, req, cos, sin, rope_positions=rope, axes=axes, **kw)]
+        out += fa.qk_norm_rope(x, y, cos, sin, positions=rope, axes=axes, **weights)
+        out += fa.qk_norm_rope_bwd(out[1], out[2], x, y, cos, sin, positions=rope, axes=axes, **weights)
+        return out + list(cache)
+
+    step(cache)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step(cache)
+    for _ in range(3):
+        rope.copy_(torch.randint(0, 50, (3, T), generator=g))
+        k.copy_(torch.randn(k.shape, generator=g))
+        other = [t.clone() for t in cache]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step(other)):
+            assert torch.equal(a, b)
+    assert fa.last_device_error() == 0
+
+
+@pytest.mark.parametrize("q4", [False, True])
 def test_positions_outside_the_tables(fa, q4):
     T, B, H, Hkv, d, bs = 12, 2, 4, 2, 64, 16
     g, k, v, cache, table, pos, req, kw = append_inputs(fa, T, B, H, Hkv, d, bs, q4, 5)
