@@ -240,6 +240,8 @@ def _stream(device):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
+_Tensor = torch.Tensor
+
 # Device type of every tensor the kernels touch. The library launches on the
 # current CUDA device, so the tensors must live there as well.
 _DEVICE_TYPE = "cuda"
@@ -247,19 +249,19 @@ _DEVICE_TYPE = "cuda"
 
 def _on_device(t, name):
     """Raise unless t is a tensor on a device the library can launch on."""
-    if not isinstance(t, torch.Tensor) or t.device.type != _DEVICE_TYPE:
+    if not isinstance(t, _Tensor) or (dev := t.device).type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a {_DEVICE_TYPE.upper()} tensor")
-    if _DEVICE_TYPE == "cuda" and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the current device is cuda:"
-                         f"{torch.cuda.current_device()}: call under torch.cuda.device({t.device})")
+    if _DEVICE_TYPE == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev} but the current device is cuda:"
+                         f"{torch.cuda.current_device()}: call under torch.cuda.device({dev})")
 
 
 def _expect(t, name, shape, dtype, device):
     """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on
     `device`: a buffer the kernels read or write in full, so a smaller one
     would be overrun."""
-    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype
-            or not t.is_contiguous() or t.device != device):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -619,9 +621,14 @@ def _rows(t, name, shape, device, out=False):
     """(address, strides but the last) of t, a bf16 tensor of `shape` on
     `device` whose last dimension is contiguous and whose rows sit on 16-byte
     boundaries (for an output: no two rows overlapping); raises otherwise."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not _BF16 or t.device != device:
+    if not isinstance(t, _Tensor) or t.shape != shape or t.dtype is not _BF16 or t.device != device:
         raise ValueError(f"{name}: expected a {_BF16} tensor of shape {tuple(shape)} on {device}")
-    *lead, last = t.stride()
+    strides = t.stride()
+    if len(strides) == 3:  # the appends' case, without the loops
+        a, b, last = strides
+        if last == 1 and not (a | b) & 7 and (not out or t.is_contiguous()):
+            return t.data_ptr(), a, b
+    *lead, last = strides
     odd = 0
     for s in lead:
         odd |= s
@@ -821,7 +828,7 @@ def _append(entry, k, v, caches, values, block_table, positions, requests, cos, 
     tables, weights, rot, n_pos, w32 = _rope_args(cos, sin, q_weight, k_weight, d, dev)
     packed = None
     if rope_positions is not None:
-        if cos is None or not isinstance(rope_positions, torch.Tensor):
+        if cos is None or not isinstance(rope_positions, _Tensor):
             raise ValueError("rope_positions need cos and sin")
         if axes is None:
             _expect(rope_positions, "rope_positions", (T,), _I32, dev)
@@ -881,9 +888,12 @@ def append_paged(k, v, k_cache, v_cache, block_table, positions, requests=None, 
 
 def _expect_q4_cache(k_cache, k_scale, v_cache, v_scale, Hkv, d, device):
     """Check a 4-bit cache's codes and (step, centre) pairs."""
-    _expect_cache(k_cache, "k_cache", Hkv, d // 2, _U8, device)
-    _expect(v_cache, "v_cache", k_cache.shape, _U8, device)
-    pairs = (*k_cache.shape[:3], d // 64, 2)
+    if not isinstance(k_cache, _Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache: expected a tensor of four dimensions")
+    n, _, bs, _ = k_cache.shape
+    codes, pairs = (n, Hkv, bs, d // 2), (n, Hkv, bs, d // 64, 2)
+    _expect(k_cache, "k_cache", codes, _U8, device)
+    _expect(v_cache, "v_cache", codes, _U8, device)
     _expect(k_scale, "k_scale", pairs, _BF16, device)
     _expect(v_scale, "v_scale", pairs, _BF16, device)
 
@@ -973,10 +983,10 @@ def _extend(entry, q, caches, block_table, seq_lens, q_starts, causal, scale, wo
     dev = q.device
     _on_device(q, "q")
     _expect(q, "q", shape, _BF16, dev)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks] int32")
-    B, max_blocks = block_table.shape
-    _expect(block_table, "block_table", (B, max_blocks), _I32, dev)
+    B, max_blocks = table_shape = block_table.shape
+    _expect(block_table, "block_table", table_shape, _I32, dev)
     _expect(seq_lens, "seq_lens", (B,), _I32, dev)
     _expect(q_starts, "q_starts", (B + 1,), _I32, dev)
     num_blocks, Hkv, bs, _ = caches[0].shape
