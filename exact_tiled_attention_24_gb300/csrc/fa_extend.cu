@@ -30,11 +30,12 @@
 //
 // What bounds it (32 + 8 heads, d = 128, 2070 MHz): with full tiles the tensor
 // pipe, as in the forward: 2048 clocks of products in 3300 a unit (a prompt of
-// 8192 tokens 418 us, 1024 tokens at 131072 keys 1.38 to 1.45 ms, 1510 to 1590
+// 8192 tokens 402 us, 1024 tokens at 131072 keys 1.38 to 1.45 ms, 1510 to 1590
 // TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
-// requests of 5 tokens over 2k to 8k keys: 136 us, 110 of them). Over codes the
-// unpacking: 155 us for the same. About 10 us pass until a CTA's first product
-// and 4 us with each piece's start and end.
+// requests of 5 tokens over 2k to 8k keys: 136 us, 110 of them). Over codes (152 us
+// for the same) the chain of one query tile's scores, softmax and output, 3400
+// clocks a tile, and the loading warps' 3600 beside it. About 10 us pass until a
+// CTA's first product and 4 us with each piece's start and end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
