@@ -66,18 +66,6 @@ struct Threads {
   static constexpr int READERS = (LOAD == BOXES ? 1 : 4) + 2 + 8;
 };
 
-struct Piece {
-  int n, kt0;            // key tiles, the first of them; n = 0: no more pieces
-  int b, kvh, head0, heads;
-  int tok0, ntok;        // first row of q, tokens of the item
-  int pos0, len;         // position of the first token; cached tokens
-  int slot;              // -1: the outputs
-  int n0, n1;            // key tiles that each query tile sees
-  int unit0;             // the CTA's units before this piece
-  int pad[2];
-};
-static_assert(sizeof(Piece) == 64, "");
-
 template <int D, int LOAD>
 struct Smem {
   static constexpr int PANELS = D / 64;
@@ -231,11 +219,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     }
   }
 
+  Requests<NT> requests(p, err);
   Shape sh{2 * p.tpt, p.causal, p.lc};
   Cut cut;
   Place at;
   i64 items0;
-  if (!plan<NT, false>(p, &sh, plan_smem, cta, &cut, &at, &items0, err)) {
+  if (!plan<NT, false>(p, &requests, &sh, plan_smem, cta, &cut, &at, &items0)) {
     if (threadIdx.x == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta].parts = 0;
     return;
   }
@@ -287,13 +276,14 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     regs_down<LOAD == BOXES ? 104 : 88>();
     if (warp == 0) {
       // --------------------------------------------------------------- pieces
-      const i64 begin = cut.start(cta), end = cut.start(cta + 1);
-      locate(p, sh, begin, &at);
-      int lo = begin > at.item0 ? Shape::tile_at(begin - at.item0) : 0;
-      const int G = p.H / p.Hkv, parts = p.hv / p.Hkv;
+      locate(p, sh, cut.start(cta), &at);
       int idx = 0;
-      auto emit = [&](const Piece& x) {
+      auto emit = [&](Piece x) {
         const int s = idx % RING;
+        if (x.slot >= p.n_slots) {  // the host's bound holds: never
+          atomicExch(err, DEV_BOUNDS);
+          x.slot = 2 * cta;
+        }
         if (idx >= RING && !mbar_wait_warp(&piece_empty[s], ((idx / RING) - 1) & 1, err)) return false;
         if (lane == 0) {
           ring[s] = x;
@@ -303,66 +293,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         ++idx;
         return true;
       };
-      Piece x{};  // n = 0
       ItemCut entered{};
-      while (true) {
-        const Request& r = at.r;
-        const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
-        const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
-        const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
-        if (hi > lo) {
-          x.unit0 += x.n;
-          x.n = hi - lo;
-          x.kt0 = at.c * (sh.lc / TK) + lo;
-          x.b = at.b;
-          x.kvh = at.hv / parts;
-          const int h0 = at.hv % parts * p.heads;
-          x.head0 = x.kvh * G + h0;
-          x.heads = min(p.heads, G - h0);
-          const int t0 = at.i * sh.span;
-          x.tok0 = r.row0 + t0;
-          x.ntok = min(sh.span, r.n - t0);
-          x.pos0 = r.base() + t0;
-          x.len = r.len;
-          x.slot = part_slot(p, sh, at, cta, lo > 0, hi < tiles);
-          if (x.slot >= p.n_slots) {  // the host's bound holds: never
-            atomicExch(err, DEV_BOUNDS);
-            x.slot = 2 * cta;
-          }
-          auto sees = [&](int g) {
-            const int t = min((g + 1) * p.tpt, x.ntok);
-            if (t <= g * p.tpt) return 0;
-            const int keys = p.causal ? max(x.pos0 + t, 0) : x.len;
-            return min(max((keys + TK - 1) / TK - x.kt0, 0), x.n);
-          };
-          x.n0 = sees(0), x.n1 = sees(1);
-          if (!emit(x)) break;
-          if (lo > 0 && !sh.is_long(r, at.i)) {  // the share's first piece at most
-            int first = cut.owner(at.item0);
-            if (Shape::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
-            entered = ItemCut{cut.owner(item_end - 1) - first + 1, cta - first, x.tok0, x.ntok, x.head0, x.heads};
-          }
-        }
-        if (item_end >= end) {
-          x.n = 0;
-          emit(x);
-          break;
-        }
-        at.item0 = item_end;
-        lo = 0;
-        if (++at.i < r.items) continue;
-        if (++at.hv == p.hv) {
-          at.hv = 0;
-          if (++at.c == sh.chunks(r)) {
-            if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
-            at.c = 0;
-            do {
-              at.r = request_of(p, ++at.b, err);  // costs are left, so there is a request with tokens
-            } while (at.r.n == 0 && at.b + 1 < p.B);
-          }
-        }
-        at.i = sh.reach(at.r, at.c);
-      }
+      if (walk(p, sh, cut, cta, at, &entered, emit)) emit(Piece{});
       if (lane == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta] = entered;
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issuer
@@ -996,7 +928,6 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 // 131072 keys, 8 items of 19 parts each; now 121.) The others take one long item
 // each.
 constexpr int MERGE_THREADS = 512;
-constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
 
 // An item's rows: 32 rows and W 4-value groups of columns a task, UNROLL parts at a time.
 template <int D, int W, int UNROLL>
@@ -1076,7 +1007,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
     i64 items0;
     const int want = job - (p.ctas - 1);
     if (threadIdx.x == 0) shared_item = ItemCut{};
-    if (plan<MERGE_THREADS, true>(p, &sh, &plan_smem, want, &cut, &at, &items0, err) && warp == 0) {
+    Requests<MERGE_THREADS> requests(p, err);
+    if (plan<MERGE_THREADS, true>(p, &requests, &sh, &plan_smem, want, &cut, &at, &items0) && warp == 0) {
       const int first = sh.first_long(at.r, 0), each = at.r.items - first;
       const int nth = static_cast<int>(want - items0);
       at.hv = nth / each;
@@ -1101,6 +1033,10 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
         const int at0 = n + sum - mine;
         if (mine > 0)
           parts_of(p, sh, cut, at, k, [&](int i, int slot) {
+            if (slot >= p.n_slots) {  // the host's bound holds: never
+              atomicExch(err, DEV_BOUNDS);
+              slot = 0;
+            }
             if (at0 + i < MAX_PARTS) parts[at0 + i] = slot;
           });
         n += __shfl_sync(0xffffffffu, sum, 31);

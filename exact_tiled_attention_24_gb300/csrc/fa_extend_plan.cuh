@@ -1,7 +1,10 @@
 // How the work of a chunk call (fa_extend.cu) is cut into pieces: pure integer
 // functions of the requests' lengths, evaluated by the attention kernel and by
-// the merge, which must agree.
+// the merge, which must agree. (tests/test_extend_plan.py evaluates them on the
+// host, beside an enumeration.)
 //
+//   request one whose rows overlap those of an earlier one, or lie before them,
+//           is taken for empty (Request::behind)
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
 //   cost    of an item: the keys it sees, and PIECE for its start and end
@@ -41,6 +44,7 @@ constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than 
                                    // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
 constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks
+constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
 static_assert(MIN_SHARE >= PIECE + 2 * TK, "");
 
 typedef long long i64;
@@ -49,14 +53,27 @@ typedef long long i64;
 struct Request {
   int row0, n, len, items;
   FA_HD int base() const { return len - n; }  // position of its first new token
+  // Behind the rows of the requests before it, which end at `floor` at most;
+  // else taken for empty. Returns the floor of the next one. No row is worked
+  // on twice then, and new tokens add up to T at most: the host's bounds on
+  // parts and long items rest on that.
+  FA_HD int behind(int floor) {
+    if (n == 0) return floor;
+    const int end = row0 + n;
+    if (row0 < floor) n = items = 0;
+    return max(floor, end);
+  }
 };
 
-__device__ __forceinline__ Request request_of(const Extend& p, int b, uint32_t* err) {
+// Request b by its own two numbers; `broken` is set, and it is empty, if they
+// are out of order or range. Where none is broken the starts do not decrease,
+// so each is behind those before it.
+FA_HD Request request_of(const Extend& p, int b, bool* broken) {
   Request r{0, 0, 0, 0};
   const int s = p.q_starts[b], e = p.q_starts[b + 1];
   const int len = p.seq_lens[b];
   if (s < 0 || e > p.T || e < s) {
-    atomicExch(err, DEV_BAD_INDEX);
+    *broken = true;
     return r;
   }
   r.row0 = s, r.n = e - s;
@@ -139,6 +156,13 @@ struct Shape {
   FA_HD static int tile_at(i64 x) { return x <= PIECE ? 0 : static_cast<int>((x - PIECE) / TK); }
 };
 
+// Keys a chunk: a share's length, or what fits L2 if that is more. all: Σ of
+// the keys that the items of all heads see.
+FA_HD int chunk_keys(const Extend& p, i64 all) {
+  const i64 least = (all / p.ctas + TK) / TK * TK;
+  return static_cast<int>(least <= p.lc ? p.lc : least < (1 << 29) ? least : 1 << 29);
+}
+
 // The whole call's cut into `ctas` shares: share k is [start(k), start(k + 1)),
 // the first `extra` one longer than the others.
 struct Cut {
@@ -161,6 +185,7 @@ struct Cut {
 struct Place {
   Request r;
   int b;
+  int floor;     // of the next request
   i64 request0;  // costs before the request
   int longs0;    // parts of long items before the request
   int c, hv, i;
@@ -191,10 +216,70 @@ __device__ __forceinline__ i64 block_scan(i64 v, i64* scratch, i64* total) {
   return below + s - v;
 }
 
+// Block-wide exclusive maximum of one value a thread, none below 0.
+template <int NT>
+__device__ __forceinline__ int block_max(int v, int* scratch, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s = max(s, t);
+  }
+  __syncthreads();  // the scratch may be in use
+  if (lane == 31) scratch[warp] = s;
+  __syncthreads();
+  const int up = __shfl_up_sync(0xffffffffu, s, 1);
+  int below = lane > 0 ? up : 0, all = 0;
+#pragma unroll 1
+  for (int w = 0; w < NT / 32; ++w) {
+    const int t = scratch[w];
+    if (w < warp) below = max(below, t);
+    all = max(all, t);
+  }
+  *total = all;
+  return below;
+}
+
 struct PlanSmem {
   i64 scan[32];
   i64 request0, items0;
-  int b, longs0;
+  Request r;
+  int b, floor, longs0;
+  int most[32];
+};
+
+// The call's requests, as a block goes through them: one a thread at a time.
+template <int NT>
+struct Requests {
+  Request mine;     // this thread's of the first NT by its own numbers; all there are, mostly
+  bool disordered;  // some request's are broken (reported)
+  int floor;        // of the next tile
+  int after;        // of the request after this thread's
+  __device__ __forceinline__ Requests(const Extend& p, uint32_t* err) : mine{0, 0, 0, 0}, floor(0), after(0) {
+    const int tid = static_cast<int>(threadIdx.x);
+    bool broken = false;
+    if (tid < p.B) mine = request_of(p, tid, &broken);
+    for (int b = tid + NT; b < p.B; b += NT) request_of(p, b, &broken);
+    if (broken) atomicExch(err, DEV_BAD_INDEX);
+    disordered = __syncthreads_or(broken) != 0;
+  }
+  // Request b0 + threadIdx.x. By the whole block, tile after tile from b0 = 0.
+  __device__ __forceinline__ Request tile(const Extend& p, int b0, PlanSmem* sm) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    bool broken;
+    Request r = mine;
+    if (b0 > 0) r = b < p.B ? request_of(p, b, &broken) : Request{0, 0, 0, 0};
+    after = r.n > 0 ? r.row0 + r.n : 0;
+    if (disordered) {
+      if (b0 == 0) floor = 0;
+      int all;
+      const int before = block_max<NT>(after, sm->most, &all);
+      after = r.behind(max(floor, before));
+      floor = max(floor, all);
+    }
+    return r;
+  }
 };
 
 // The call's cut, and the place of one of its items: with LONG = false of the
@@ -203,25 +288,22 @@ struct PlanSmem {
 // none. Run by a whole block; every thread knows the result, up to the request
 // (locate has the rest). Sets sh->lc.
 template <int NT, bool LONG>
-__device__ __forceinline__ bool plan(const Extend& p, Shape* sh, PlanSmem* sm, int want, Cut* cut, Place* at,
-                                     i64* items0, uint32_t* err) {
+__device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* sh, PlanSmem* sm, int want, Cut* cut,
+                                     Place* at, i64* items0) {
   const int tid = static_cast<int>(threadIdx.x);
   sh->lc = p.lc;
-  const Request none{0, 0, 0, 0};
-  const Request mine = tid < p.B ? request_of(p, tid, err) : none;  // all there are, mostly
   if (p.may_chunk) {
     i64 k = 0, all;
-    for (int b = tid; b < p.B; b += NT) {
-      const Request r = b == tid ? mine : request_of(p, b, err);
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+      const Request r = rq->tile(p, b0, sm);
       if (r.n > 0) k += sh->keys_before(r, r.items) * p.hv;
     }
     block_scan<NT>(k, sm->scan, &all);
-    const i64 least = (all / p.ctas + TK) / TK * TK;
-    if (least > sh->lc) sh->lc = least < (1 << 29) ? static_cast<int>(least) : 1 << 29;
+    sh->lc = chunk_keys(p, all);
   }
   // costs before each thread's request; with more requests than threads, the total first
   i64 c = 0;
-  for (int b = tid; b < p.B; b += NT) c += sh->total(b == tid ? mine : request_of(p, b, err), p.hv);
+  for (int b0 = 0; b0 < p.B; b0 += NT) c += sh->total(rq->tile(p, b0, sm), p.hv);
   i64 total;
   const i64 before = block_scan<NT>(c, sm->scan, &total);
   *cut = Cut(total, p.ctas);
@@ -230,8 +312,7 @@ __device__ __forceinline__ bool plan(const Extend& p, Shape* sh, PlanSmem* sm, i
   const i64 target = LONG || !there ? want : cut->start(want);
   i64 costs = 0, longs = 0, items = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
-    const int b = b0 + tid;
-    const Request r = b0 == 0 ? mine : b < p.B ? request_of(p, b, err) : none;
+    const Request r = rq->tile(p, b0, sm);
     const i64 cost = p.B <= NT ? c : sh->total(r, p.hv);
     i64 sum = 0, sum_l = 0, sum_i = 0, l = 0, it = 0, e_l = 0, e_i = 0;
     const i64 e = p.B <= NT ? before : costs + block_scan<NT>(cost, sm->scan, &sum);
@@ -246,14 +327,17 @@ __device__ __forceinline__ bool plan(const Extend& p, Shape* sh, PlanSmem* sm, i
       __syncthreads();  // sm->b is set
     }
     const i64 key = LONG ? e_i : e, size = LONG ? it : cost;
-    if (there && target >= key && target - key < size)
-      sm->b = b, sm->request0 = e, sm->longs0 = static_cast<int>(e_l), sm->items0 = e_i;
+    if (there && target >= key && target - key < size) {
+      sm->b = b0 + tid, sm->r = r, sm->floor = rq->after;
+      sm->request0 = e, sm->longs0 = static_cast<int>(e_l), sm->items0 = e_i;
+    }
     costs += sum, longs += sum_l, items += sum_i;
   }
   __syncthreads();
   at->b = sm->b;
   if (at->b < 0) return false;
-  at->r = request_of(p, at->b, err);
+  at->r = sm->r;
+  at->floor = sm->floor;
   at->request0 = sm->request0;
   at->longs0 = sm->longs0;
   *items0 = sm->items0;
@@ -309,7 +393,7 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
 // Where a piece's result goes: slots 2k and 2k + 1 are CTA k's first and last
 // piece where its share cuts an item, the others hold whole chunks of long
 // items; -1: the outputs themselves.
-__device__ __forceinline__ int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bool start_cut,
+FA_HD int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bool start_cut,
                                          bool end_cut) {
   if (start_cut) return 2 * k;
   if (end_cut) return 2 * k + 1;
@@ -323,7 +407,7 @@ __device__ __forceinline__ int part_slot(const Extend& p, const Shape& sh, const
 // more, and not a long one: slot 2k + 1 of the share k in which its first tile
 // lies, then 2 (k + 1), 2 (k + 2) and so on.)
 template <class F>
-__device__ __forceinline__ int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
+FA_HD int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
   const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape::tiles_of(sh.part(at.r, at.c, at.i));
   const i64 end = at.item0 + cost;
   int n = 0;
@@ -335,6 +419,82 @@ __device__ __forceinline__ int parts_of(const Extend& p, const Shape& sh, const 
     lo = hi;
   }
   return n;
+}
+
+// What a CTA does of one item at a time.
+struct Piece {
+  int n, kt0;            // key tiles, the first of them; n = 0: no more pieces
+  int b, kvh, head0, heads;
+  int tok0, ntok;        // first row of q, tokens of the item
+  int pos0, len;         // position of the first token; cached tokens
+  int slot;              // -1: the outputs
+  int n0, n1;            // key tiles that each query tile sees
+  int unit0;             // the CTA's units before this piece
+  int pad[2];
+};
+static_assert(sizeof(Piece) == 64, "");
+
+// Share `cta`'s pieces in order, from the item it begins in: f(piece) for each,
+// until that says false; false then. *entered: the item that the share begins
+// within, if another share has its start (and it is not a long one).
+template <class F>
+FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place at, ItemCut* entered, F f) {
+  const i64 begin = cut.start(cta), end = cut.start(cta + 1);
+  int lo = begin > at.item0 ? Shape::tile_at(begin - at.item0) : 0;
+  const int G = p.H / p.Hkv, parts = p.hv / p.Hkv;
+  Piece x{};  // n = 0
+  while (true) {
+    const Request& r = at.r;
+    const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
+    const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
+    const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
+    if (hi > lo) {
+      x.unit0 += x.n;
+      x.n = hi - lo;
+      x.kt0 = at.c * (sh.lc / TK) + lo;
+      x.b = at.b;
+      x.kvh = at.hv / parts;
+      const int h0 = at.hv % parts * p.heads;
+      x.head0 = x.kvh * G + h0;
+      x.heads = min(p.heads, G - h0);
+      const int t0 = at.i * sh.span;
+      x.tok0 = r.row0 + t0;
+      x.ntok = min(sh.span, r.n - t0);
+      x.pos0 = r.base() + t0;
+      x.len = r.len;
+      x.slot = part_slot(p, sh, at, cta, lo > 0, hi < tiles);
+      auto sees = [&](int g) {
+        const int t = min((g + 1) * p.tpt, x.ntok);
+        if (t <= g * p.tpt) return 0;
+        const int keys = p.causal ? max(x.pos0 + t, 0) : x.len;
+        return min(max((keys + TK - 1) / TK - x.kt0, 0), x.n);
+      };
+      x.n0 = sees(0), x.n1 = sees(1);
+      if (!f(x)) return false;
+      if (lo > 0 && !sh.is_long(r, at.i)) {  // the share's first piece at most
+        int first = cut.owner(at.item0);
+        if (Shape::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
+        *entered = ItemCut{cut.owner(item_end - 1) - first + 1, cta - first, x.tok0, x.ntok, x.head0, x.heads};
+      }
+    }
+    if (item_end >= end) return true;
+    at.item0 = item_end;
+    lo = 0;
+    if (++at.i < r.items) continue;
+    if (++at.hv == p.hv) {
+      at.hv = 0;
+      if (++at.c == sh.chunks(r)) {
+        if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
+        at.c = 0;
+        do {  // costs are left, so there is a request with tokens
+          bool broken;
+          at.r = request_of(p, ++at.b, &broken);
+          at.floor = at.r.behind(at.floor);
+        } while (at.r.n == 0 && at.b + 1 < p.B);
+      }
+    }
+    at.i = sh.reach(at.r, at.c);
+  }
 }
 
 }  // namespace ext

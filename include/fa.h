@@ -614,7 +614,8 @@ int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
  *   q_starts   [B + 1] device int32: request b's tokens are rows q_starts[b] ..
  *              q_starts[b + 1] - 1 of q, o and lse (none: nothing is read).
  *              Not decreasing, in [0, T]. A request whose two numbers break
- *              this is taken for empty and fa_last_device_error reports
+ *              this, or that begins before the end of an earlier one in order,
+ *              is taken for empty and fa_last_device_error reports
  *              FA_ERR_BAD_INDEX.
  *   seq_lens   [B] device int32: cached tokens of each request, its new ones
  *              included (they are the last; the caller has appended them),
