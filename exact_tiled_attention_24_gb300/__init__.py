@@ -1027,9 +1027,11 @@ def extend_paged(q, k_cache, v_cache, block_table, seq_lens, q_starts, causal=Tr
     extend_workspace_bytes(...) bytes. Returns (o [T, H, d] bf16, lse [T, H]
     fp32).
 
-    Rows of no request (before q_starts[0], from q_starts[B] on) are o = 0, lse
-    = -inf where both outputs are made here and stay as they were where either
-    is given. The lengths are read on the device: a captured call may be
+    A request whose two starts are out of order or range, or that begins before
+    the end of an earlier one, is taken for empty (and reported by
+    last_device_error). Rows of no request (theirs, those before q_starts[0] and
+    from q_starts[B] on) are o = 0, lse = -inf where both outputs are made here
+    and stay as they were where either is given. The lengths are read on the device: a captured call may be
     replayed with others."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("expected q [T, H, d]")

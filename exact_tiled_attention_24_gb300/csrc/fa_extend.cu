@@ -167,6 +167,43 @@ __device__ __forceinline__ int load_entry(const int* p) {
   asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
+
+// o = 0, lse = -inf for the rows of no request, dealt out to the whole grid:
+// those before the first request and from the end of the last one on; where
+// some request is taken for empty also the gaps between the others. gaps: NT
+// places in shared memory.
+template <int D, int NT>
+__device__ __forceinline__ void zero_rows(const Extend& p, Requests<NT>* requests, PlanSmem* sm, int2* gaps, uint32_t* err) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const bool ordered = !requests->disordered;
+  const long long per = static_cast<long long>(p.H) * (D / 8), step = static_cast<long long>(gridDim.x) * NT;
+  int covered = ordered ? p.q_starts[p.B] : 0;  // the end of the last request so far
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    if (!ordered) {
+      const Request r = requests->tile(p, b0, sm);
+      int all;
+      const int before = block_max<NT>(r.n > 0 ? r.row0 + r.n : 0, sm->most, &all);
+      gaps[tid] = r.n > 0 ? make_int2(max(covered, before), r.row0) : make_int2(0, 0);
+      covered = max(covered, all);
+      __syncthreads();
+    }
+    const bool last = ordered || b0 + NT >= p.B;
+    const int n = ordered ? 1 : min(NT, p.B - b0);
+    for (int i = 0; i < n + last; ++i) {
+      const int2 gap = i == n ? make_int2(covered, p.T) : ordered ? make_int2(0, p.q_starts[0]) : gaps[i];
+      const long long end = gap.y * per;
+      for (long long at = gap.x * per + static_cast<long long>(blockIdx.x) * NT + tid; at < end; at += step) {
+        if (in_range(at, 1, static_cast<long long>(p.T) * per, err))
+          reinterpret_cast<uint4*>(p.o)[at] = make_uint4(0u, 0u, 0u, 0u);
+        if (at % (D / 8) == 0 && in_range(at / (D / 8), 1, static_cast<long long>(p.T) * p.H, err))
+          p.lse[at / (D / 8)] = -INFINITY;
+      }
+    }
+    if (last) break;
+    __syncthreads();  // the gaps are read
+  }
+}
+
 template <int D, int LOAD>
 __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -203,23 +240,9 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   const int cta = static_cast<int>(blockIdx.x);
   launch_dependents();  // the merge may be set up; it waits for this grid's writes
 
-  // Rows of no request.
-  if (p.zero_skipped) {
-    const int first = min(max(p.q_starts[0], 0), p.T), last = min(max(p.q_starts[p.B], first), p.T);
-    const long long per = static_cast<long long>(p.H) * (D / 8);
-    const long long n = static_cast<long long>(first + p.T - last) * per;
-    for (long long i = static_cast<long long>(cta) * NT + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * NT) {
-      long long tok = i / per;
-      if (tok >= first) tok += last - first;
-      const long long at = tok * per + i % per;
-      if (in_range(at, 1, static_cast<long long>(p.T) * per, err))
-        reinterpret_cast<uint4*>(p.o)[at] = make_uint4(0u, 0u, 0u, 0u);
-      if (i % (D / 8) == 0 && in_range(at / (D / 8), 1, static_cast<long long>(p.T) * p.H, err))
-        p.lse[at / (D / 8)] = -INFINITY;
-    }
-  }
-
   Requests<NT> requests(p, err);
+  if (p.zero_skipped) zero_rows<D, NT>(p, &requests, plan_smem, reinterpret_cast<int2*>(plan_smem + 1), err);
+
   Shape sh{2 * p.tpt, p.causal, p.lc};
   Cut cut;
   Place at;

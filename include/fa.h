@@ -627,7 +627,8 @@ int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
  *              values of tokens that are cached and not seen have to be
  *              finite; slots past a request's length may hold anything.
  *   o, lse     [T][H][d] bf16 and [T][H] fp32. Rows of no request (before
- *              q_starts[0], from q_starts[B] on) stay as they were; with
+ *              q_starts[0], from q_starts[B] on, those that only requests
+ *              taken for empty would have) stay as they were; with
  *              zero_skipped they get o = 0, lse = -inf.
  *   workspace  fa_extend_workspace_bytes(...) bytes, 16-byte aligned, needed
  *              always; contents on entry are ignored. Calls that run at the

@@ -73,3 +73,64 @@ def test_requests_in_order_keep_their_rows(fa):
             assert bool((o[rows] == 3).all()) and bool((lse[rows] == 5).all()), b
         else:
             assert torch.equal(o[rows], ref[0][rows]) and torch.equal(lse[rows], ref[1][rows]), b
+
+
+@pytest.mark.parametrize("bs", [16, 3])
+@pytest.mark.parametrize("starts", [[0, 5, 3, 38], [0, 5, 40, 38], [-1, 5, 35, 38], [2, 5, 35, 60], [4, 30, 20, 36],
+                                    [38, 0, 38, 5], [0, 38, 38, 0], [-1, -1, -1, -1], [39, 39, 39, 39]])
+def test_rows_of_requests_taken_for_empty_are_zero(fa, starts, bs):
+    """Outputs that the call itself makes: every row is written. Given ones keep those rows."""
+    T, H, lens = 38, 4, [40, 90, 30]
+    q, caches, table, L, _ = extend_case(H, 2, 64, bs, [5, 30, 3], lens, seed=5, fill=0.0)
+    dev = [t.cuda() for t in (q, *caches, table, L)]
+    owner, end, broken = [-1] * T, 0, False
+    for b in range(3):
+        s, e = starts[b], starts[b + 1]
+        if s < 0 or e > T or e < s:
+            broken = True
+        elif e > s:
+            if s >= end:
+                owner[s:e] = [b] * (e - s)
+            end = max(end, e)
+    nobody = torch.tensor(owner).cuda() < 0
+    assert broken == (starts != sorted(starts) or starts[0] < 0 or starts[-1] > T)
+    given, lse_given = torch.full((T, H, 64), 3.0, dtype=BF, device="cuda"), torch.full((T, H), 5.0, device="cuda")
+    fa.extend_paged(*dev, i32(starts), out=given, lse=lse_given)
+    assert fa.last_device_error() == (7 if broken else 0)
+    assert bool((given[nobody] == 3).all()) and bool((lse_given[nobody] == 5).all())
+    # what the call makes its outputs of held other numbers before
+    o, lse = torch.full_like(given, 7.0), torch.full_like(lse_given, 7.0)
+    nb, Hkv, bs, d = caches[0].shape
+    need = fa.extend_workspace_bytes(T, 3, H, Hkv, d, bs, table.shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dq, dk, dv, dt, dl = dev
+    ds = i32(starts)
+    args = fa._EXTEND_ARGS.pack(dq.data_ptr(), dk.data_ptr(), 0, dv.data_ptr(), 0, dt.data_ptr(), dl.data_ptr(), ds.data_ptr(),
+                                o.data_ptr(), lse.data_ptr(), ws.data_ptr(), need, T, 3, H, Hkv, d, nb, bs, table.shape[1],
+                                1, 1, 0.125)
+    assert fa.lib().fa_extend_paged(args, torch.cuda.current_stream().cuda_stream) == 0
+    assert fa.last_device_error() == (7 if broken else 0)
+    assert bool((o[nobody] == 0).all()) and bool(torch.isneginf(lse[nobody]).all())
+    assert torch.equal(o[~nobody], given[~nobody]) and torch.equal(lse[~nobody], lse_given[~nobody])
+
+
+def test_gaps_among_many_requests_are_zero(fa):
+    B, H, Hkv, d, bs = 1200, 2, 1, 64, 16
+    new = [1 + b % 3 for b in range(B)]
+    q, (kc, vc), table, L, starts = extend_case(H, Hkv, d, bs, new, [n + b % 40 for b, n in enumerate(new)], seed=4,
+                                                before=4, after=9)
+    dev = [t.cuda() for t in (q, kc, vc, table, L)]
+    ref = fa.extend_paged(*dev, starts.cuda())
+    bad = starts.clone()
+    bad[1], bad[600], bad[900], bad[B] = -1, 2 ** 31 - 1, bad[890], -7
+    o, lse = fa.extend_paged(*dev, bad.cuda())
+    torch.cuda.synchronize()
+    assert fa.last_device_error() == 7
+    gone = {0, 1, 599, 600, 899, 900, B - 1}
+    for b in range(B):
+        rows = slice(int(starts[b]), int(starts[b + 1]))
+        if b in gone:
+            assert bool((o[rows] == 0).all()) and bool(torch.isneginf(lse[rows]).all()), b
+        else:
+            assert torch.equal(o[rows], ref[0][rows]) and torch.equal(lse[rows], ref[1][rows]), b
+    assert torch.equal(o[:4], ref[0][:4]) and torch.equal(o[-9:], ref[0][-9:]) and bool(torch.isneginf(lse[-9:]).all())
