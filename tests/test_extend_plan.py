@@ -122,3 +122,12 @@ def test_workspace_is_what_the_parts_need(plan):
     assert fa.extend_workspace_bytes(1 << 17, 1, 32, 8, 128, 16, 1 << 13) <= 4 * 152 * part
     assert fa.extend_workspace_bytes(1 << 17, 1, 1, 1, 128, 16, 1 << 13) <= 4 * 152 * part
     assert fa.extend_workspace_bytes(350, 1, 16, 4, 128, 16, 1 << 13) <= 4 * 152 * part
+
+
+def test_the_gpu_tests_cases(plan):
+    """The calls of test_gpu_extend_chunks.py are cut as they say."""
+    from extend_chunk_cases import CASES
+    for kind, H, Hkv, d, bs, new, lens, want in CASES.values():
+        for causal in (True, False):
+            got = plan(sum(new), H, Hkv, d, bs, blocks_for(max(lens), bs), starts_of(new), lens, causal, kind == "q4")
+            assert got[0] == max(want) and got[1] > 0
