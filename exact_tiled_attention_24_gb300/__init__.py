@@ -680,7 +680,11 @@ def _rope_args(cos, sin, q_weight, k_weight, d, device):
 
 def _pack_axes(axes, positions, n_axes, rot):
     """The packed fa_rope_axes of checked positions [n_axes, ...]."""
-    axes = bytes(axes)
+    if type(axes) is not bytes:
+        try:
+            axes = bytes(list(axes))
+        except TypeError:
+            raise ValueError("axes: a bytes (or sequence) of axis numbers") from None
     if len(axes) != rot // 2:
         raise ValueError("axes: one axis number for each of the rot/2 pairs")
     return _ROPE_AXES.pack(positions.data_ptr(), n_axes, axes)
