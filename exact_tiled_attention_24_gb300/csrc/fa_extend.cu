@@ -141,17 +141,16 @@ struct Pieces {
 };
 
 // Eight codes of one 32-bit word as bf16 values z + s (n − 8), one rounding
-// each: a code lands in the mantissa of bf16 128 (the odd ones three bits up:
-// 128 + 8 n), one subtraction leaves n − 8 (and 8 (n − 8)), exactly, and the
-// fused multiply-add in bf16 rounds the sum.
+// each: a code lands in the mantissa of bf16 128, one subtraction leaves n − 8,
+// exactly, and the fused multiply-add in bf16 rounds the sum.
 __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 z) {
-  const uint32_t v = w >> 1;
-  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xc308), __ushort_as_bfloat16(0xc340));  // -136, -192
+  const uint32_t v = w >> 4;
+  const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(0xc308));  // -136
   uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t t = __byte_perm(w, v, i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
-    t = (t & 0x0078000fu) | 0x43004300u;
+    t = (t & 0x000f000fu) | 0x43004300u;
     const __nv_bfloat162 n = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&t), off);
     const __nv_bfloat162 x = __hfma2(n, s, z);
     out[i] = *reinterpret_cast<const uint32_t*>(&x);
@@ -881,8 +880,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 #pragma unroll 2
         for (int k = 0; k < CPR; ++k) {
           const uint32_t sbits = __byte_perm(pair, 0, 0x1010), zbits = __byte_perm(pair, 0, 0x3232);
-          const __nv_bfloat162 eighth = __halves2bfloat162(__ushort_as_bfloat16(0x3f80), __ushort_as_bfloat16(0x3e00));  // 1, 1/8
-          const __nv_bfloat162 s2 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&sbits), eighth);
+          const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&sbits);
           const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162*>(&zbits);
           const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
           if (k + 1 < CPR) {
