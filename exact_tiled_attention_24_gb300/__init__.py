@@ -1051,7 +1051,8 @@ def extend_paged_q4(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens
                     workspace=None, out=None, lse=None):
     """extend_paged over a cache held in 4 bits (append_paged_q4's). Keys and
     values are read back in bf16, rounded once: what append_paged_q4 hands out
-    as k_values and v_values."""
+    as k_values and v_values. (decode_paged_q4 holds them exactly, and keeps 16
+    bits of a weight where chunks keep bf16's 8, as fwd does.)"""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("expected q [T, H, d]")
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:

@@ -604,6 +604,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) sum[q] = make_float2(0.f, 0.f);
         const float2 sc2 = make_float2(scale_log2, scale_log2);
+        // P is rounded to bf16, half a step (2^-8 of a weight) at most, as in the
+        // forward; its sum is that of the unrounded weights. Results are 1.2 to 1.4
+        // times as far from 64 bits as their own rounding. The remainder as a second
+        // bf16 number and product would cost a third more time and up to two thirds
+        // over codes: a prompt of 8192 tokens 539 us and not 404, 2777 tokens of 12
+        // requests 269 and not 212, over codes 373 and not 255.
         auto p_chunk = [&](int c, float2 nm2) {
           uint32_t pk[16];
 #pragma unroll

@@ -630,6 +630,10 @@ int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
  *              q_starts[0], from q_starts[B] on, those that only requests
  *              taken for empty would have) stay as they were; with
  *              zero_skipped they get o = 0, lse = -inf.
+ *              A weight e^(scale q.k - m) enters the product with V rounded to
+ *              bf16 (at most 2^-8 of itself), as in fa_fwd, over either cache;
+ *              sums of weights, scores and o stay in fp32 until o is rounded.
+ *              (A decode step over codes keeps 16 bits of a weight.)
  *   workspace  fa_extend_workspace_bytes(...) bytes, 16-byte aligned, needed
  *              always; contents on entry are ignored. Calls that run at the
  *              same time need one each.
