@@ -532,9 +532,14 @@ static int extend_sizes_ok(fa::Extend* p, int T, int B, int H, int Hkv, int d, i
 }
 
 size_t fa_extend_workspace_bytes(int T, int B, int H, int Hkv, int d, int block_size, int max_blocks_per_seq) {
-  fa::Extend p{};
-  if (extend_sizes_ok(&p, T, B, H, Hkv, d, block_size, max_blocks_per_seq) != FA_OK) return 0;
-  return fa::extend_sizes(&p, d);
+  size_t most = 0;
+  for (int q4 = 0; q4 < 2; ++q4) {
+    fa::Extend p{};
+    if (extend_sizes_ok(&p, T, B, H, Hkv, d, block_size, max_blocks_per_seq) != FA_OK) return 0;
+    const size_t bytes = fa::extend_sizes(&p, d, q4 != 0);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 
 static int extend(const fa_extend_args* a, bool q4, void* stream) {
@@ -548,7 +553,7 @@ static int extend(const fa_extend_args* a, bool q4, void* stream) {
   if ((st = check_cache(a->Hkv, a->num_blocks, a->block_size, a->max_blocks_per_seq)) != FA_OK) return st;
   // a block's K/V head is one coordinate of the copies' tensor
   if (static_cast<long long>(a->num_blocks) * a->Hkv > INT_MAX - 1) return FA_ERR_UNSUPPORTED;
-  const size_t need = fa::extend_sizes(&p, a->d);
+  const size_t need = fa::extend_sizes(&p, a->d, q4);
   if (!a->workspace || a->ws_bytes < need) return FA_ERR_WORKSPACE;
   if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->o) ||
       !aligned16(a->workspace) || (q4 && (!aligned16(a->k_scale) || !aligned16(a->v_scale))) ||

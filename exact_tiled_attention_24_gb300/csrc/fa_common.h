@@ -178,9 +178,9 @@ struct Extend {
   int T, B, H, Hkv, num_blocks, bs, max_blocks;
   int heads, hv;             // query heads a tile holds (at most 128), K/V heads times the parts its query heads are cut into
   int tpt;                   // tokens a query tile holds: 128 / heads
-  int ctas;                  // see fa_extend_plan.cuh
+  int ctas, lc, may_chunk;   // see fa_extend_plan.cuh
   unsigned bs_inverse;       // 2^32 / bs, rounded up (bs = 1: 1)
-  int n_slots;               // workspace parts
+  int n_slots, n_long;       // workspace parts; long items there may be
   bool causal, zero_skipped;
   float scale_log2;
   // The block of a key below 2^30: the product is at most key / 2^32 < 1 too
@@ -191,8 +191,8 @@ struct Extend {
     return q * bs > key ? q - 1 : q;
   }
 };
-// Sets the fields from `heads` to `n_slots` from the sizes; returns the workspace's bytes.
-size_t extend_sizes(Extend* p, int d);
+// Sets the fields from `heads` to `n_long` from the sizes and `causal`; returns the workspace's bytes.
+size_t extend_sizes(Extend* p, int d, bool q4);
 cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream);
 
 // The calling host thread's side stream on the current device (a

@@ -242,10 +242,11 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   Requests<NT> requests(p, err);
   if (p.zero_skipped) zero_rows<D, NT>(p, &requests, plan_smem, reinterpret_cast<int2*>(plan_smem + 1), err);
 
-  const Shape sh{2 * p.tpt, p.causal};
+  Shape sh{2 * p.tpt, p.causal, p.lc};
   Cut cut;
   Place at;
-  if (!plan<NT>(p, &requests, sh, plan_smem, cta, &cut, &at)) {
+  i64 items0;
+  if (!plan<NT, false>(p, &requests, &sh, plan_smem, cta, &cut, &at, &items0)) {
     if (threadIdx.x == 0 && in_range(cta, 1, p.ctas, err)) p.cuts[cta].parts = 0;
     return;
   }
@@ -299,8 +300,12 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
       // --------------------------------------------------------------- pieces
       locate(p, sh, cut.start(cta), &at);
       int idx = 0;
-      auto emit = [&](const Piece& x) {
+      auto emit = [&](Piece x) {
         const int s = idx % RING;
+        if (x.slot >= p.n_slots) {  // the host's bound holds: never
+          atomicExch(err, DEV_BOUNDS);
+          x.slot = 2 * cta;
+        }
         if (idx >= RING && !mbar_wait_warp(&piece_empty[s], ((idx / RING) - 1) & 1, err)) return false;
         if (lane == 0) {
           ring[s] = x;
@@ -943,16 +948,17 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 // ------------------------------------------------------------------- merge
 //
 // One output row from its parts: lse = ln Σ_s e^(lse_s), o = Σ_s e^(lse_s −
-// lse) o_s. A CTA whose share begins within an item has noted it (worked out from
-// the lengths again they took 6 us more), and the blocks of an item's CTAs but
-// the first deal its rows out among them. (All by one block: 152 us for 64 tokens
-// at 131072 keys, 8 items of 19 parts each; now 121.)
+// lse) o_s. The first ctas - 1 blocks take the items that shares cut: a CTA
+// whose share begins within an item has noted it (worked out from the lengths
+// again they took 6 us more), and the blocks of an item's CTAs but the first
+// deal its rows out among them. (All by one block: 152 us for 64 tokens at
+// 131072 keys, 8 items of 19 parts each; now 121.) The others take one long item
+// each.
 constexpr int MERGE_THREADS = 512;
 
-// An item's rows: 32 rows and W 4-value groups of columns a task, UNROLL parts at
-// a time. cta0: the CTA that has the item's first tile.
+// An item's rows: 32 rows and W 4-value groups of columns a task, UNROLL parts at a time.
 template <int D, int W, int UNROLL>
-__device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, int cta0, int first, int step,
+__device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, const int* parts, int first, int step,
                                            uint32_t* err) {
   const int lane = threadIdx.x & 31, n = it.parts;
   constexpr int ACROSS = D / 4 / W, TASKS = ROWS / 32 * ACROSS;
@@ -963,7 +969,7 @@ __device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, i
     float m = -INFINITY;
 #pragma unroll UNROLL
     for (int s = 0; s < n; ++s) {
-      const long long pr = static_cast<long long>(part_of(cta0, s)) * ROWS + row;
+      const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
       const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
       m = v != v || m != m ? NAN : fmaxf(m, v);  // a part whose lse is NaN makes its row NaN
     }
@@ -974,14 +980,14 @@ __device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, i
     if (m != -INFINITY) {
 #pragma unroll UNROLL
       for (int s = 0; s < n; ++s) {
-        const long long pr = static_cast<long long>(part_of(cta0, s)) * ROWS + row;
+        const long long pr = static_cast<long long>(parts[s]) * ROWS + row;
         const float v = in_range(pr, 1, static_cast<long long>(p.n_slots) * ROWS, err) ? p.lse_part[pr] : 0.f;
         const float w = ex2((v - m) * 1.4426950408889634f);
         l += w;
         float4 t[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const long long off = ((static_cast<long long>(part_of(cta0, s)) * (D / 4) + c0 + i) * ROWS + row) * 4;
+          const long long off = ((static_cast<long long>(parts[s]) * (D / 4) + c0 + i) * ROWS + row) * 4;
           t[i] = in_range(off, 4, static_cast<long long>(p.n_slots) * ROWS * D, err)
                      ? *reinterpret_cast<const float4*>(p.o_part + off) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -1009,20 +1015,78 @@ __device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, i
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
+  __shared__ PlanSmem plan_smem;
+  __shared__ int parts[MAX_PARTS];
+  __shared__ ItemCut shared_item;
   uint32_t* err = &g_extend_err;
-  const int warp = threadIdx.x >> 5, cta = static_cast<int>(blockIdx.x) + 1;
-  wait_for_primary();
-  const ItemCut it = in_range(cta, 1, p.ctas, err) ? p.cuts[cta] : ItemCut{};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int job = static_cast<int>(blockIdx.x);
+  if (job < p.ctas - 1) {
+    wait_for_primary();
+    if (threadIdx.x == 0) shared_item = in_range(job + 1, 1, p.ctas, err) ? p.cuts[job + 1] : ItemCut{};
+    __syncthreads();
+    const int first = job + 1 - shared_item.nth;
+    for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * first + 1 : 2 * (first + i);
+  } else {
+    Shape sh{2 * p.tpt, p.causal, p.lc};
+    Cut cut;
+    Place at;
+    i64 items0;
+    const int want = job - (p.ctas - 1);
+    if (threadIdx.x == 0) shared_item = ItemCut{};
+    Requests<MERGE_THREADS> requests(p, err);
+    if (plan<MERGE_THREADS, true>(p, &requests, &sh, &plan_smem, want, &cut, &at, &items0) && warp == 0) {
+      const int first = sh.first_long(at.r, 0), each = at.r.items - first;
+      const int nth = static_cast<int>(want - items0);
+      at.hv = nth / each;
+      at.i = first + nth % each;
+      const int n_c = (sh.keys(at.r, at.i) + sh.lc - 1) / sh.lc;
+      int n = 0;
+      for (int c0 = 0; c0 < n_c; c0 += 32) {
+        at.c = c0 + lane;
+        int mine = 0, k = 0;
+        if (at.c < n_c) {
+          const i64 row = sh.costs_before(at.r, at.c, at.r.items);
+          at.item0 = at.request0 + sh.chunks_before(at.r, at.c) * p.hv + row * at.hv + sh.costs_before(at.r, at.c, at.i);
+          k = cut.owner(at.item0);
+          mine = parts_of(p, sh, cut, at, k, [](int, int) {});
+        }
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += t;
+        }
+        const int at0 = n + sum - mine;
+        if (mine > 0)
+          parts_of(p, sh, cut, at, k, [&](int i, int slot) {
+            if (slot >= p.n_slots) {  // the host's bound holds: never
+              atomicExch(err, DEV_BOUNDS);
+              slot = 0;
+            }
+            if (at0 + i < MAX_PARTS) parts[at0 + i] = slot;
+          });
+        n += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      const int per = p.hv / p.Hkv, h0 = at.hv % per * p.heads, G = p.H / p.Hkv, t0 = at.i * sh.span;
+      if (lane == 0)
+        shared_item = ItemCut{min(n, MAX_PARTS), 0, at.r.row0 + t0, min(sh.span, at.r.n - t0), at.hv / per * G + h0,
+                              min(p.heads, G - h0)};
+    }
+    wait_for_primary();
+  }
+  __syncthreads();
+  const ItemCut it = shared_item;
   if (it.parts == 0) return;
-  const int cta0 = cta - it.nth, blocks = it.parts - 1;
-  const int first = (it.nth - 1) * (MERGE_THREADS / 32) + warp, step = blocks * (MERGE_THREADS / 32);
+  const int blocks = it.nth > 0 ? it.parts - 1 : 1, block = max(it.nth - 1, 0);
+  const int first = block * (MERGE_THREADS / 32) + warp, step = blocks * (MERGE_THREADS / 32);
   // A warp takes 32 rows and a quarter of the columns at a time; 8 columns where
   // that leaves half the warps without a task (items in many parts or with few rows).
   const int rows0 = min(it.ntok, p.tpt) * p.heads, rows1 = max(it.ntok - p.tpt, 0) * p.heads;
   if (2 * blocks >= (rows0 + 31) / 32 + (rows1 + 31) / 32)
-    merge_rows<D, 2, 2>(p, it, cta0, first, step, err);
+    merge_rows<D, 2, 2>(p, it, parts, first, step, err);
   else
-    merge_rows<D, D / 16, 2>(p, it, cta0, first, step, err);
+    merge_rows<D, D / 16, 2>(p, it, parts, first, step, err);
 }
 
 // ------------------------------------------------------------------ launch
@@ -1060,7 +1124,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   kern<<<p.ctas, Threads<LOAD>::N, Smem<D, LOAD>::ALLOC, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
-  const int jobs = p.ctas - 1;
+  const int jobs = p.ctas - 1 + p.n_long;
   if (e != cudaSuccess || jobs == 0) return e;  // one CTA: nothing is cut
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1076,7 +1140,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
 
 }  // namespace ext
 
-size_t extend_sizes(Extend* p, int d) {
+size_t extend_sizes(Extend* p, int d, bool q4) {
   using namespace ext;
   p->bs_inverse = static_cast<unsigned>((1ull << 32) / p->bs + 1);
   const int G = p->H / p->Hkv, parts = (G + BM - 1) / BM;
@@ -1085,10 +1149,25 @@ size_t extend_sizes(Extend* p, int d) {
   p->tpt = BM / p->heads;
   const long long span = 2 * p->tpt;
   const long long ctx = static_cast<long long>(p->max_blocks) * p->bs;
+  // A chunk's K and V, of all K/V heads, stay in L2 (read as they lie there).
+  const long long key_bytes = 2ll * p->Hkv * (q4 ? d / 2 + d / 16 : 2 * d);
+  const long long lc = kL2GroupBytes / key_bytes / TK * TK;
+  p->lc = static_cast<int>(lc < 8 * TK ? 8 * TK : lc > (1 << 29) ? 1 << 29 : lc);
   const long long items = p->hv * (p->T / span + (p->T < p->B ? p->T : p->B));  // at most
   const long long shares = items * (ctx + PIECE) / MIN_SHARE;
   p->ctas = static_cast<int>(shares < 1 ? 1 : shares > MAX_CTAS ? MAX_CTAS : shares);
-  p->n_slots = 2 * p->ctas;
+  p->may_chunk = p->T > (CHUNK_ITEMS - 1) * span && ctx > p->lc;
+  p->n_long = 0;
+  long long whole = 0;
+  if (p->may_chunk) {
+    // Items of requests with two or more: at most 2 T / span. A chunk is at
+    // least a share long, and a long item passes at most twice its keys / lc.
+    const long long long_items = p->hv * (2ll * p->T / span), by_share = 2ll * p->ctas;
+    p->n_long = static_cast<int>(long_items < by_share ? long_items : by_share);
+    whole = long_items * ((ctx + p->lc - 1) / p->lc);
+    if (whole > by_share) whole = by_share;
+  }
+  p->n_slots = static_cast<int>(2 * p->ctas + whole);
   return static_cast<size_t>(p->n_slots) * ROWS * (d + 1) * sizeof(float) + p->ctas * sizeof(ItemCut);
 }
 

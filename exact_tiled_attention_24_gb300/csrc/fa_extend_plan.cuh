@@ -1,29 +1,31 @@
 // How the work of a chunk call (fa_extend.cu) is cut into pieces: pure integer
-// functions of the requests' lengths. (tests/test_extend_plan.py evaluates them
-// on the host, beside an enumeration.)
+// functions of the requests' lengths, evaluated by the attention kernel and by
+// the merge, which must agree. (tests/test_extend_plan.py evaluates them on the
+// host, beside an enumeration.)
 //
 //   request one whose rows overlap those of an earlier one, or lie before them,
 //           is taken for empty (Request::behind)
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
 //   cost    of an item: the keys it sees, and PIECE for its start and end
-//           (2.5 key tiles' time). Keys and not key tiles, because
+//           (3 key tiles' time; 192, 320, 480 and 704 keys: a prompt of 8192
+//           tokens 435, 421, 427 and 436 us). Keys and not key tiles, because
 //           their sums over items have a closed form without a division
 //           (counting tiles, the start of a CTA took 14 us, now 4)
-//   order   request by request, K/V head, item, key. The costs in this order
-//           are cut into C equal shares, one a CTA, each end rounded down to a
-//           key tile of its item: the lengths are on the device only, and equal
-//           shares need no rule for uneven ones. An item that crosses from one
-//           share to the next is finished by a merge of its parts, two a CTA at
-//           most: one that the share's start cuts and one that its end cuts.
-//
-// A request with many items reads its keys once an item, from CTAs at different
-// keys of it. Having all items pass one chunk of the keys before any passes the
-// next, for reuse in L2, is not worth its parts (bf16, d = 128, 131072 keys,
-// items a head, us with chunks and without: 8 K/V heads 8 items 763 and 768, 10
-// 1069 and 1042, 16 1587 and 1570 to 1624, 32 3435 and 3409; 2 K/V heads 6 items
-// 228 and 160, 16 425 and 372; d = 64 7 items 534 and 511, 16 1125 and 1124; 4-bit
-// codes 6 items 752 and 708).
+//   order   request by request, (chunk,) K/V head, item, key. The costs in this
+//           order are cut into C equal shares, one a CTA, each end rounded down
+//           to a key tile of its item: the lengths are on the device only, and
+//           equal shares need no rule for uneven ones. An item that crosses
+//           from one share to the next is finished by a merge of its parts.
+//   chunk   a request with many items reads its keys once an item. CTAs with
+//           equal shares stand at different keys of it, so what one reads has
+//           left L2 before another needs it. Such a request's keys are
+//           therefore cut into chunks of a share's length (or of what fits L2,
+//           if that is more), and all items pass one chunk before any passes
+//           the next: most shares are then one chunk of one item, and the CTAs
+//           walk along the keys together. 131072 keys, 8 K/V heads: 8 items a
+//           head 744 us, else 793; 16 items 1408 and 1532; but 4 items 441 and
+//           423, 2 items 320 and 252.
 #pragma once
 
 #include <cstdint>
@@ -37,10 +39,12 @@ namespace fa {
 namespace ext {
 
 constexpr int TK = 128;             // keys a tile
-constexpr int PIECE = 320;          // an item's start and end, in keys (256: a prompt of 8192 tokens 2 us less, a mixed step 2 more; 384: 4 and 2 more)
+constexpr int PIECE = 320;          // an item's start and end, in keys (256: a prompt of 8192 tokens 2 us less, chunks 2 more; 384: 4 and 2 more)
 constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than PIECE + TK, so that the ends of two
                                    // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
+constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks
+constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
 static_assert(MIN_SHARE >= PIECE + 2 * TK, "");
 
 typedef long long i64;
@@ -51,7 +55,8 @@ struct Request {
   FA_HD int base() const { return len - n; }  // position of its first new token
   // Behind the rows of the requests before it, which end at `floor` at most;
   // else taken for empty. Returns the floor of the next one. No row is worked
-  // on twice then, and new tokens add up to T at most.
+  // on twice then, and new tokens add up to T at most: the host's bounds on
+  // parts and long items rest on that.
   FA_HD int behind(int floor) {
     if (n == 0) return floor;
     const int end = row0 + n;
@@ -80,6 +85,7 @@ FA_HD Request request_of(const Extend& p, int b, bool* broken) {
 struct Shape {
   int span;  // tokens an item: 2·tpt
   bool causal;
+  int lc;    // keys a chunk, a multiple of TK
 
   // key tiles of `keys` (one at least, so that rows that see nothing are written)
   FA_HD static int tiles_of(int keys) { return max(1, (keys + TK - 1) / TK); }
@@ -95,14 +101,67 @@ struct Shape {
     const i64 s = (full - none) * r.base() + span * ((full * (full + 1) - none * (none + 1)) / 2);
     return i > full ? s + keys(r, r.items - 1) : s;
   }
-  FA_HD int cost(const Request& r, int i) const { return PIECE + keys(r, i); }
-  // Σ of the costs of the items before i
-  FA_HD i64 costs_before(const Request& r, int i) const { return keys_before(r, i) + static_cast<i64>(i) * PIECE; }
+  // the first item that sees more than x keys
+  FA_HD int past(const Request& r, i64 x) const {
+    if (r.len <= x) return r.items;
+    if (!causal) return 0;
+    const int d = static_cast<int>(x) - r.base();
+    return d < 0 ? 0 : min(d / span, r.items - 1);
+  }
+  FA_HD bool chunked(const Request& r) const { return r.items >= CHUNK_ITEMS && r.len > lc; }
+  FA_HD int chunks(const Request& r) const { return chunked(r) ? (r.len + lc - 1) / lc : 1; }
+  // the first item that reaches chunk c
+  FA_HD int reach(const Request& r, int c) const { return c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
+  // keys of item i in chunk c, which it reaches
+  FA_HD int part(const Request& r, int c, int i) const {
+    const int k = keys(r, i);
+    return chunked(r) ? min(k - c * lc, lc) : k;
+  }
+  FA_HD int cost(const Request& r, int c, int i) const { return PIECE + part(r, c, i); }
+  // Σ of the costs in chunk c of the items before i
+  FA_HD i64 costs_before(const Request& r, int c, int i) const {
+    if (!chunked(r)) return keys_before(r, i) + static_cast<i64>(i) * PIECE;
+    const int i0 = reach(r, c), i1 = past(r, static_cast<i64>(c + 1) * lc);
+    if (i <= i0) return 0;
+    const int j = min(i, i1);  // from i1 on a whole chunk each
+    return static_cast<i64>(i - i0) * PIECE + keys_before(r, j) - keys_before(r, i0) -
+           static_cast<i64>(j - i0) * (static_cast<i64>(c) * lc) + static_cast<i64>(i - j) * lc;
+  }
+  // Σ_{1 <= c' < c} of the items that reach chunk c'
+  FA_HD i64 reaches(const Request& r, int c) const {
+    i64 s = 0;
+    for (int x = 1; x < c; ++x) s += r.items - reach(r, x);
+    return s;
+  }
+  // Σ of one head's costs in the chunks before c
+  FA_HD i64 chunks_before(const Request& r, int c) const {
+    if (c == 0) return 0;
+    const int i = past(r, static_cast<i64>(c) * lc);
+    return keys_before(r, i) + static_cast<i64>(r.items - i) * (static_cast<i64>(c) * lc) + (r.items + reaches(r, c)) * PIECE;
+  }
   // a request's costs
-  FA_HD i64 total(const Request& r, int heads) const { return r.n == 0 ? 0 : costs_before(r, r.items) * heads; }
+  FA_HD i64 total(const Request& r, int heads) const {
+    if (r.n == 0) return 0;
+    return (chunked(r) ? chunks_before(r, chunks(r)) : costs_before(r, 0, r.items)) * heads;
+  }
+  // Items that pass more than one chunk are "long"; each of their chunks has a
+  // part of its own: the first long item of chunk c, and one head's parts in
+  // the chunks before c.
+  FA_HD int first_long(const Request& r, int c) const { return past(r, static_cast<i64>(max(c, 1)) * lc); }
+  FA_HD bool is_long(const Request& r, int i) const { return chunked(r) && keys(r, i) > lc; }
+  FA_HD int long_before(const Request& r, int c) const {
+    return c == 0 ? 0 : r.items - first_long(r, 0) + static_cast<int>(reaches(r, c));
+  }
   // the tile at which a share's end x into an item's cost cuts it
   FA_HD static int tile_at(i64 x) { return x <= PIECE ? 0 : static_cast<int>((x - PIECE) / TK); }
 };
+
+// Keys a chunk: a share's length, or what fits L2 if that is more. all: Σ of
+// the keys that the items of all heads see.
+FA_HD int chunk_keys(const Extend& p, i64 all) {
+  const i64 least = (all / p.ctas + TK) / TK * TK;
+  return static_cast<int>(least <= p.lc ? p.lc : least < (1 << 29) ? least : 1 << 29);
+}
 
 // The whole call's cut into `ctas` shares: share k is [start(k), start(k + 1)),
 // the first `extra` one longer than the others.
@@ -122,13 +181,14 @@ struct Cut {
   }
 };
 
-// An item, with what lies before it.
+// An item of one chunk, with what lies before it.
 struct Place {
   Request r;
   int b;
   int floor;     // of the next request
   i64 request0;  // costs before the request
-  int hv, i;
+  int longs0;    // parts of long items before the request
+  int c, hv, i;
   i64 item0;     // costs before the item
 };
 
@@ -183,9 +243,9 @@ __device__ __forceinline__ int block_max(int v, int* scratch, int* total) {
 
 struct PlanSmem {
   i64 scan[32];
-  i64 request0;
+  i64 request0, items0;
   Request r;
-  int b, floor;
+  int b, floor, longs0;
   int most[32];
 };
 
@@ -222,34 +282,56 @@ struct Requests {
   }
 };
 
-// The call's cut, and the place of the item in which share `want` begins, up to
-// the request (locate has the rest). False: there is none. Run by a whole block;
-// every thread knows the result.
-template <int NT>
-__device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, const Shape& sh, PlanSmem* sm, int want, Cut* cut,
-                                     Place* at) {
+// The call's cut, and the place of one of its items: with LONG = false of the
+// one that share `want` begins in, with LONG = true of the want-th long item
+// (its request and, in *items0, the long items before that). False: there is
+// none. Run by a whole block; every thread knows the result, up to the request
+// (locate has the rest). Sets sh->lc.
+template <int NT, bool LONG>
+__device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* sh, PlanSmem* sm, int want, Cut* cut,
+                                     Place* at, i64* items0) {
   const int tid = static_cast<int>(threadIdx.x);
+  sh->lc = p.lc;
+  if (p.may_chunk) {
+    i64 k = 0, all;
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+      const Request r = rq->tile(p, b0, sm);
+      if (r.n > 0) k += sh->keys_before(r, r.items) * p.hv;
+    }
+    block_scan<NT>(k, sm->scan, &all);
+    sh->lc = chunk_keys(p, all);
+  }
   // costs before each thread's request; with more requests than threads, the total first
   i64 c = 0;
-  for (int b0 = 0; b0 < p.B; b0 += NT) c += sh.total(rq->tile(p, b0, sm), p.hv);
+  for (int b0 = 0; b0 < p.B; b0 += NT) c += sh->total(rq->tile(p, b0, sm), p.hv);
   i64 total;
   const i64 before = block_scan<NT>(c, sm->scan, &total);
   *cut = Cut(total, p.ctas);
   if (tid == 0) sm->b = -1;
-  const bool there = total > 0 && want < cut->ctas;
-  const i64 target = there ? cut->start(want) : 0;
-  i64 costs = 0;
+  const bool there = total > 0 && (LONG || want < cut->ctas);
+  const i64 target = LONG || !there ? want : cut->start(want);
+  i64 costs = 0, longs = 0, items = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const Request r = rq->tile(p, b0, sm);
-    const i64 cost = p.B <= NT ? c : sh.total(r, p.hv);
-    i64 sum = 0;
+    const i64 cost = p.B <= NT ? c : sh->total(r, p.hv);
+    i64 sum = 0, sum_l = 0, sum_i = 0, l = 0, it = 0, e_l = 0, e_i = 0;
     const i64 e = p.B <= NT ? before : costs + block_scan<NT>(cost, sm->scan, &sum);
-    if (p.B <= NT) __syncthreads();  // sm->b is set
-    if (there && target >= e && target - e < cost) {
-      sm->b = b0 + tid, sm->r = r, sm->floor = rq->after;
-      sm->request0 = e;
+    if (p.may_chunk) {
+      if (r.n > 0 && sh->chunked(r)) {
+        l = static_cast<i64>(sh->long_before(r, sh->chunks(r))) * p.hv;
+        it = static_cast<i64>(r.items - sh->first_long(r, 0)) * p.hv;
+      }
+      e_l = longs + block_scan<NT>(l, sm->scan, &sum_l);
+      e_i = items + block_scan<NT>(it, sm->scan, &sum_i);
+    } else {
+      __syncthreads();  // sm->b is set
     }
-    costs += sum;
+    const i64 key = LONG ? e_i : e, size = LONG ? it : cost;
+    if (there && target >= key && target - key < size) {
+      sm->b = b0 + tid, sm->r = r, sm->floor = rq->after;
+      sm->request0 = e, sm->longs0 = static_cast<int>(e_l), sm->items0 = e_i;
+    }
+    costs += sum, longs += sum_l, items += sum_i;
   }
   __syncthreads();
   at->b = sm->b;
@@ -257,6 +339,8 @@ __device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, const Sh
   at->r = sm->r;
   at->floor = sm->floor;
   at->request0 = sm->request0;
+  at->longs0 = sm->longs0;
+  *items0 = sm->items0;
   return true;
 }
 
@@ -265,16 +349,28 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
   const int lane = threadIdx.x & 31;
   const Request& r = at->r;
   i64 rem = x - at->request0;
+  int c = 0;
+  if (sh.chunked(r)) {
+    const int n_c = sh.chunks(r);
+    for (int c0 = 0; c0 < n_c; c0 += 32) {
+      const bool ok = c0 + lane < n_c && sh.chunks_before(r, c0 + lane) * p.hv <= rem;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
+      if (cnt > 0) c = c0 + cnt - 1;
+      if (cnt < 32) break;
+    }
+    rem -= sh.chunks_before(r, c) * p.hv;
+  }
+  at->c = c;
   at->hv = 0;
   // First the head, from one head's costs, then the item, by 32 probes at a
   // time; one copy of the code for both (it runs once, from a cold cache).
-  int lo = 0, hi = r.items;
+  int lo = sh.reach(r, c), hi = r.items;
   i64 found = 0;
   bool head = true;
 #pragma unroll 1
   while (head || hi - lo > 1) {
     const int step = head ? 0 : (hi - lo + 31) / 32, probe = head ? hi : lo + lane * step;
-    const i64 v = sh.costs_before(r, min(probe, hi));
+    const i64 v = sh.costs_before(r, c, min(probe, hi));
     if (head) {
       for (int h0 = 0; h0 < p.hv; h0 += 32) {  // rem / v
         const int cnt = __popc(__ballot_sync(0xffffffffu, h0 + lane < p.hv && v * (h0 + lane) <= rem));
@@ -295,11 +391,35 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
 }
 
 // Where a piece's result goes: slots 2k and 2k + 1 are CTA k's first and last
-// piece where its share cuts an item; -1: the outputs themselves.
-FA_HD int part_slot(int k, bool start_cut, bool end_cut) { return start_cut ? 2 * k : end_cut ? 2 * k + 1 : -1; }
-// An item whose first tile share `first` has is in part 2 first + 1 and then
-// those of the shares that begin within it.
-FA_HD int part_of(int first, int s) { return s == 0 ? 2 * first + 1 : 2 * (first + s); }
+// piece where its share cuts an item, the others hold whole chunks of long
+// items; -1: the outputs themselves.
+FA_HD int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bool start_cut,
+                                         bool end_cut) {
+  if (start_cut) return 2 * k;
+  if (end_cut) return 2 * k + 1;
+  if (!sh.is_long(at.r, at.i)) return -1;
+  const int in_c = at.r.items - sh.first_long(at.r, at.c);
+  return 2 * p.ctas + at.longs0 + p.hv * sh.long_before(at.r, at.c) + at.hv * in_c + at.i - sh.first_long(at.r, at.c);
+}
+
+// The parts that the shares make of one item of one chunk, in order: calls
+// f(i, slot) for each; k: the share in which it begins. (An item cut once or
+// more, and not a long one: slot 2k + 1 of the share k in which its first tile
+// lies, then 2 (k + 1), 2 (k + 2) and so on.)
+template <class F>
+FA_HD int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
+  const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape::tiles_of(sh.part(at.r, at.c, at.i));
+  const i64 end = at.item0 + cost;
+  int n = 0;
+  for (int lo = 0; lo < tiles; ++k) {
+    const i64 e = cut.start(k + 1);
+    const int hi = e >= end ? tiles : Shape::tile_at(e - at.item0);
+    if (hi <= lo) continue;
+    f(n++, part_slot(p, sh, at, k, lo > 0, hi < tiles));
+    lo = hi;
+  }
+  return n;
+}
 
 // What a CTA does of one item at a time.
 struct Piece {
@@ -316,7 +436,7 @@ static_assert(sizeof(Piece) == 64, "");
 
 // Share `cta`'s pieces in order, from the item it begins in: f(piece) for each,
 // until that says false; false then. *entered: the item that the share begins
-// within, if another share has its start.
+// within, if another share has its start (and it is not a long one).
 template <class F>
 FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place at, ItemCut* entered, F f) {
   const i64 begin = cut.start(cta), end = cut.start(cta + 1);
@@ -325,13 +445,13 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
   Piece x{};  // n = 0
   while (true) {
     const Request& r = at.r;
-    const int tiles = Shape::tiles_of(sh.keys(r, at.i));
-    const i64 item_end = at.item0 + sh.cost(r, at.i);
+    const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
+    const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
     const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
     if (hi > lo) {
       x.unit0 += x.n;
       x.n = hi - lo;
-      x.kt0 = lo;
+      x.kt0 = at.c * (sh.lc / TK) + lo;
       x.b = at.b;
       x.kvh = at.hv / parts;
       const int h0 = at.hv % parts * p.heads;
@@ -342,7 +462,7 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
       x.ntok = min(sh.span, r.n - t0);
       x.pos0 = r.base() + t0;
       x.len = r.len;
-      x.slot = part_slot(cta, lo > 0, hi < tiles);
+      x.slot = part_slot(p, sh, at, cta, lo > 0, hi < tiles);
       auto sees = [&](int g) {
         const int t = min((g + 1) * p.tpt, x.ntok);
         if (t <= g * p.tpt) return 0;
@@ -351,7 +471,7 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
       };
       x.n0 = sees(0), x.n1 = sees(1);
       if (!f(x)) return false;
-      if (lo > 0) {  // the share's first piece at most
+      if (lo > 0 && !sh.is_long(r, at.i)) {  // the share's first piece at most
         int first = cut.owner(at.item0);
         if (Shape::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
         *entered = ItemCut{cut.owner(item_end - 1) - first + 1, cta - first, x.tok0, x.ntok, x.head0, x.heads};
@@ -361,15 +481,19 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
     at.item0 = item_end;
     lo = 0;
     if (++at.i < r.items) continue;
-    at.i = 0;
     if (++at.hv == p.hv) {
       at.hv = 0;
-      do {  // costs are left, so there is a request with tokens
-        bool broken;
-        at.r = request_of(p, ++at.b, &broken);
-        at.floor = at.r.behind(at.floor);
-      } while (at.r.n == 0 && at.b + 1 < p.B);
+      if (++at.c == sh.chunks(r)) {
+        if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
+        at.c = 0;
+        do {  // costs are left, so there is a request with tokens
+          bool broken;
+          at.r = request_of(p, ++at.b, &broken);
+          at.floor = at.r.behind(at.floor);
+        } while (at.r.n == 0 && at.b + 1 < p.B);
+      }
     }
+    at.i = sh.reach(at.r, at.c);
   }
 }
 

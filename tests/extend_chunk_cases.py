@@ -1,5 +1,5 @@
-"""Chunk-attention calls of six items a head and more over long contexts: their
-inputs, made on the GPU, and attention over them in 64 bits. Run as a
+"""Chunk-attention calls whose keys are cut into chunks (fa_extend_plan.cuh):
+their inputs, made on the GPU, and attention over them in 64 bits. Run as a
 script it writes the results of the library selected by FA_DEBUG_LIBRARY to the
 file named on the command line."""
 import math
@@ -14,23 +14,45 @@ for path in (ROOT, os.path.join(ROOT, "tests")):
         sys.path.insert(0, path)
 
 BF, I32 = torch.bfloat16, torch.int32
-TILE = 128  # keys a tile
+TILE, PIECE, CTAS, ITEMS, L2 = 128, 320, 152, 6, 40 << 20
 
-CASES = {  # kind, H, Hkv, d, block size, new tokens, cached tokens
-    "boxes": ("bf16", 16, 4, 128, 16, [350], [131072]),
-    "two requests": ("bf16", 96, 3, 64, 128, [41, 3, 50], [250000, 500, 170000]),
-    "gathered": ("bf16", 128, 1, 64, 3, [12], [700000]),
-    "gathered, others before and after": ("bf16", 256, 2, 128, 200, [1, 13, 2], [900, 230000, 2]),
-    "codes": ("q4", 64, 1, 128, 16, [24], [1000000]),
-    "codes, two requests": ("q4", 96, 3, 64, 5, [41, 3, 50], [600000, 500, 500000]),
+CASES = {  # kind, H, Hkv, d, block size, new tokens, cached tokens, chunks of each request's keys
+    "boxes": ("bf16", 16, 4, 128, 16, [350], [131072], [7]),
+    "two requests": ("bf16", 96, 3, 64, 128, [41, 3, 50], [250000, 500, 170000], [5, 1, 4]),
+    "gathered": ("bf16", 128, 1, 64, 3, [12], [700000], [5]),
+    "gathered, others before and after": ("bf16", 256, 2, 128, 200, [1, 13, 2], [900, 230000, 2], [1, 6, 1]),
+    "codes": ("q4", 64, 1, 128, 16, [24], [1000000], [4]),
+    "codes, two requests": ("q4", 96, 3, 64, 5, [41, 3, 50], [600000, 500, 500000], [4, 1, 3]),
 }
+
+
+def chunks(kind, H, Hkv, d, bs, new, lens, causal, max_blocks):
+    """Into how many chunks each request's keys are cut, from the rule in words:
+    no shorter than what fits L2 (all K/V heads' keys and values, 40 MB) and than
+    a CTA's share of all items' keys, for requests of six items a head or more."""
+    G = H // Hkv
+    parts = -(-G // 128)
+    tokens = 128 // -(-G // parts)          # a query tile's
+    T, hv, span, ctx = sum(new), Hkv * parts, 2 * tokens, max_blocks * bs
+    row = d // 2 + d // 16 if kind == "q4" else 2 * d
+    lc = max(8 * TILE, L2 // (2 * Hkv * row) // TILE * TILE)
+    items = hv * (T // span + min(T, len(new)))
+    ctas = max(1, min(CTAS, items * (ctx + PIECE) // (5 * TILE)))
+    if T <= (ITEMS - 1) * span or ctx <= lc:
+        return [1] * len(new)
+    keys = 0
+    for n, length in zip(new, lens):
+        for i in range(-(-n // span)):
+            keys += hv * (max(0, length - n + min((i + 1) * span, n)) if causal else length)
+    lc = max(lc, (keys // ctas + TILE) // TILE * TILE)
+    return [-(-length // lc) if -(-n // span) >= ITEMS and length > lc else 1 for n, length in zip(new, lens)]
 
 
 def inputs(name, seed, counting=False):
     """q, caches, table, lens, starts of a case, all on the GPU. counting: q is 0
     and dimension c of a value is 1 where its key tile's number is c modulo d,
     else 0, so o counts the keys that a token sees."""
-    kind, H, Hkv, d, bs, new, lens = CASES[name]
+    kind, H, Hkv, d, bs, new, lens, _ = CASES[name]
     g = torch.Generator(device="cuda").manual_seed(seed)
     rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
     nb = [-(-n // bs) for n in lens]

@@ -20,22 +20,23 @@ using namespace fa::ext;
 
 namespace {
 
-struct Item {
-  int b, hv, i;
+struct Item {  // of one chunk
+  int b, c, hv, i, tiles;
   i64 item0, request0;
-  int cost;
+  int longs0, cost;
 };
 
 }  // namespace
 
-// 0, or the line of the check that failed. out: the parts of the item that has
-// most, CTAs with a share, the largest slot, requests taken for empty.
-extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_blocks, int causal, const int* starts,
-                          const int* lens, int* out) {
+// 0, or the line of the check that failed. out: chunks of the longest cut
+// request (1: none is cut), long items, the largest slot, requests taken for
+// empty, keys a chunk.
+extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_blocks, int causal, int q4,
+                          const int* starts, const int* lens, int* out) {
   Extend p{};
   p.T = T, p.B = B, p.H = H, p.Hkv = Hkv, p.bs = bs, p.max_blocks = max_blocks, p.causal = causal != 0;
   p.q_starts = starts, p.seq_lens = lens;
-  extend_sizes(&p, d);
+  extend_sizes(&p, d, q4 != 0);
   const int span = 2 * p.tpt, G = H / Hkv, parts = p.hv / Hkv;
   CHECK(p.ctas >= 1 && p.ctas <= MAX_CTAS && p.heads * parts >= G && p.tpt * p.heads <= 128);
 
@@ -62,52 +63,91 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
   }
   CHECK(tokens <= T);
 
-  // Every item, in order, its costs one by one.
+  // Every item of every chunk, in order, its costs one by one.
   auto keys_of = [&](const Request& r, int i) {
     i64 most = 0;
     for (int t = i * span; t < std::min((i + 1) * span, r.n); ++t)
       most = std::max<i64>(most, causal ? std::max(r.len - r.n + t + 1, 0) : r.len);
     return static_cast<int>(most);
   };
-  const Shape sh{span, p.causal};
+  Shape sh{span, p.causal, p.lc};
+  std::vector<std::vector<int>> keys(B);
+  i64 all = 0;
+  for (int b = 0; b < B; ++b) {
+    i64 sum = 0;
+    for (int i = 0; i < rq[b].items; ++i) {
+      keys[b].push_back(keys_of(rq[b], i));
+      CHECK(sh.keys(rq[b], i) == keys[b][i] && sh.keys_before(rq[b], i) == sum);
+      sum += keys[b][i];
+    }
+    if (rq[b].n > 0) CHECK(sh.keys_before(rq[b], rq[b].items) == sum);
+    all += sum * p.hv;
+  }
+  if (p.may_chunk) sh.lc = chunk_keys(p, all);
+  CHECK(sh.lc % TK == 0 && sh.lc > 0);
   std::vector<Item> items;
-  std::map<std::tuple<int, int, int>, int> tiles_of;  // (request, head, item): its key tiles
+  std::map<std::tuple<int, int, int>, int> tiles_left;  // (request, head, item): tiles not yet dealt out
   i64 total = 0;
+  int longs0 = 0, n_long = 0, most_chunks = 1;
   for (int b = 0; b < B; ++b) {
     const Request& r = rq[b];
+    if (r.n == 0) continue;
+    const bool cut = p.may_chunk && r.items >= CHUNK_ITEMS && r.len > sh.lc;
+    if (!p.may_chunk) CHECK(!sh.chunked(r));
+    CHECK(sh.chunked(r) == cut);
+    const int chunks = cut ? (r.len + sh.lc - 1) / sh.lc : 1;
+    CHECK(sh.chunks(r) == chunks);
+    most_chunks = std::max(most_chunks, chunks);
     const i64 request0 = total;
-    for (int hv = 0; hv < p.hv; ++hv) {
-      i64 sum = 0;
-      for (int i = 0; i < r.items; ++i) {
-        const int keys = keys_of(r, i);
-        CHECK(sh.keys(r, i) == keys && sh.keys_before(r, i) == sum);
-        CHECK(sh.cost(r, i) == PIECE + keys && sh.costs_before(r, i) == sum + static_cast<i64>(i) * PIECE);
-        items.push_back(Item{b, hv, i, total, request0, PIECE + keys});
-        tiles_of[std::make_tuple(b, hv, i)] = std::max(1, (keys + TK - 1) / TK);
-        sum += keys, total += PIECE + keys;
+    int long_parts = 0;
+    for (int c = 0; c < chunks; ++c) {
+      i64 row = 0;
+      if (c > 0 || cut) CHECK(sh.chunks_before(r, c) * p.hv == total - request0);
+      if (cut) CHECK(sh.long_before(r, c) == long_parts);
+      for (int hv = 0; hv < p.hv; ++hv) {
+        row = 0;
+        bool first = true;
+        for (int i = 0; i < r.items; ++i) {
+          if (c > 0 && keys[b][i] <= c * sh.lc) continue;
+          if (first) CHECK(sh.reach(r, c) == i);
+          first = false;
+          const int mine = cut ? std::min(keys[b][i] - c * sh.lc, sh.lc) : keys[b][i];
+          const int n = std::max(1, (mine + TK - 1) / TK);
+          CHECK(sh.cost(r, c, i) == PIECE + mine && sh.costs_before(r, c, i) == row);
+          items.push_back(Item{b, c, hv, i, n, total, request0, longs0, PIECE + mine});
+          tiles_left[{b, hv, i}] += n;
+          row += PIECE + mine, total += PIECE + mine;
+          const bool is_long = cut && keys[b][i] > sh.lc;
+          CHECK(sh.is_long(r, i) == is_long);
+          if (hv == 0 && is_long) ++long_parts;
+          if (c == 0 && is_long) ++n_long;
+        }
+        CHECK(sh.costs_before(r, c, r.items) == row);
       }
-      if (r.n > 0) CHECK(sh.costs_before(r, r.items) == sum + static_cast<i64>(r.items) * PIECE);
     }
     CHECK(sh.total(r, p.hv) == total - request0);
+    longs0 += long_parts * p.hv;
   }
-  CHECK(p.n_slots == 2 * p.ctas);
-  out[0] = 1, out[1] = 0, out[2] = -1, out[3] = dropped;
+  for (const auto& t : tiles_left)
+    CHECK(t.second == std::max(1, (keys[std::get<0>(t.first)][std::get<2>(t.first)] + TK - 1) / TK));
+  CHECK(n_long <= p.n_long && 2 * p.ctas + longs0 <= p.n_slots);
+  out[0] = most_chunks, out[1] = n_long, out[2] = -1, out[3] = dropped, out[4] = sh.lc;
   if (total == 0) return 0;
 
   // The shares' pieces: every tile once, every slot once.
   const Cut cut(total, p.ctas);
-  out[1] = cut.ctas;
   CHECK(cut.start(0) == 0 && cut.start(cut.ctas) == total && cut.ctas <= p.ctas);
   std::set<int> slots;
   std::map<std::tuple<int, int, int>, std::map<int, Piece>> dealt;  // by first tile
   std::vector<ItemCut> cuts(p.ctas, ItemCut{});
+  std::vector<Place> places(cut.ctas);
   size_t at_item = 0;
   for (int k = 0; k < cut.ctas; ++k) {
     const i64 begin = cut.start(k);
     CHECK(cut.owner(begin) == k && cut.owner(cut.start(k + 1) - 1) == k);
     while (items[at_item].item0 + items[at_item].cost <= begin) ++at_item;
     const Item& x = items[at_item];
-    Place at{rq[x.b], x.b, 0, x.request0, x.hv, x.i, x.item0};
+    Place at{rq[x.b], x.b, 0, x.request0, x.longs0, x.c, x.hv, x.i, x.item0};
     for (int b = 0, f = 0; b <= x.b; ++b) {
       bool broken;
       Request r = request_of(p, b, &broken);
@@ -136,8 +176,9 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
     };
     CHECK(walk(p, sh, cut, k, at, &cuts[k], [&](const Piece& y) { return (line = take(y)) == 0; }) || line != 0);
     if (line) return line;
+    places[k] = at;
   }
-  for (const auto& t : tiles_of) {
+  for (const auto& t : tiles_left) {
     const auto it = dealt.find(t.first);
     CHECK(it != dealt.end());
     int next = 0;
@@ -147,35 +188,57 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
     }
     CHECK(next == t.second);
     CHECK((it->second.size() == 1) == (it->second.begin()->second.slot == -1));
-    out[0] = std::max(out[0], static_cast<int>(it->second.size()));
   }
-  CHECK(dealt.size() == tiles_of.size());
+  CHECK(dealt.size() == tiles_left.size());
   out[2] = slots.empty() ? -1 : *slots.rbegin();
 
-  // What the merge joins: cut items as their CTAs noted them.
+  // What the merge joins: cut items as their CTAs noted them, then the long ones.
   std::map<std::tuple<int, int, int>, int> joined;
   std::set<std::tuple<int, int>> noted;
   CHECK(cuts[0].parts == 0);
   for (int k = 1; k < p.ctas; ++k) {
     const ItemCut& c = cuts[k];
     if (c.parts == 0) continue;
-    CHECK(k < cut.ctas && c.nth >= 1 && c.nth < c.parts && c.parts <= p.ctas);
+    CHECK(k < cut.ctas && c.nth >= 1 && c.nth < c.parts && c.parts <= MAX_PARTS);
     const int first = k - c.nth;
     CHECK(first >= 0 && noted.insert({first, c.nth}).second);
     const int kvh = c.head0 / G, hv = kvh * parts + (c.head0 - kvh * G) / p.heads;
     int b = 0;
     while (!(rq[b].n > 0 && c.tok0 >= rq[b].row0 && c.tok0 < rq[b].row0 + rq[b].n)) ++b;
     const int i = (c.tok0 - rq[b].row0) / span;
+    CHECK(!sh.is_long(rq[b], i));
     const auto& pieces = dealt[std::make_tuple(b, hv, i)];
     CHECK(static_cast<int>(pieces.size()) == c.parts);
     int n = 0;
     for (const auto& y : pieces) {
-      CHECK(y.second.slot == part_of(first, n));
+      CHECK(y.second.slot == (n == 0 ? 2 * first + 1 : 2 * (first + n)));
       CHECK(y.second.tok0 == c.tok0 && y.second.ntok == c.ntok && y.second.head0 == c.head0 && y.second.heads == c.heads);
       ++n;
     }
     ++joined[std::make_tuple(b, hv, i)];
   }
-  for (const auto& t : dealt) CHECK(joined[t.first] == static_cast<int>(t.second.size()) - 1);
+  int order = 0;
+  for (const Item& x : items) {
+    const Request& r = rq[x.b];
+    const auto key = std::make_tuple(x.b, x.hv, x.i);
+    if (!sh.is_long(r, x.i)) {
+      const int pieces = static_cast<int>(dealt[key].size());
+      CHECK(joined[key] == pieces - 1);
+      continue;
+    }
+    if (x.c > 0) continue;
+    ++order;
+    std::vector<int> got;
+    const int n_c = (keys[x.b][x.i] + sh.lc - 1) / sh.lc;
+    for (int c = 0; c < n_c; ++c) {
+      Place at{r, x.b, 0, x.request0, x.longs0, c, x.hv, x.i, 0};
+      at.item0 = x.request0 + sh.chunks_before(r, c) * p.hv + sh.costs_before(r, c, r.items) * x.hv + sh.costs_before(r, c, x.i);
+      parts_of(p, sh, cut, at, cut.owner(at.item0), [&](int, int slot) { got.push_back(slot); });
+    }
+    CHECK(got.size() <= static_cast<size_t>(MAX_PARTS) && got.size() == dealt[key].size());
+    size_t n = 0;
+    for (const auto& y : dealt[key]) CHECK(got[n++] == y.second.slot);
+  }
+  CHECK(order == n_long);
   return 0;
 }

@@ -1,6 +1,7 @@
-"""extend_paged and extend_paged_q4 over long contexts, with many items a head:
-every load path, other requests before and after, all keys and causal, captured
-and replayed with lengths from short to long, and on the bounds-checked build."""
+"""extend_paged and extend_paged_q4 where the keys of a request are cut into
+three chunks or more: every load path, with other requests before and after,
+all keys and causal, captured and replayed with lengths that are cut and that
+are not, and on the bounds-checked build."""
 import os
 import subprocess
 import sys
@@ -8,9 +9,8 @@ import sys
 import pytest
 import torch
 
-from extend_long_cases import CASES, TILE, attention64, inputs, run
+from extend_chunk_cases import CASES, TILE, attention64, chunks, inputs, run
 
-pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
 NAMES = sorted(CASES)
 
@@ -23,6 +23,14 @@ def fa():
     return m
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", NAMES)
+def test_the_cases_are_cut(name, causal):
+    kind, H, Hkv, d, bs, new, lens, want = CASES[name]
+    assert chunks(kind, H, Hkv, d, bs, new, lens, causal, -(-max(lens) // bs)) == want and max(want) >= 3
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("name", NAMES)
 def test_every_key_is_counted_once(fa, name, causal):
@@ -50,6 +58,7 @@ def test_every_key_is_counted_once(fa, name, causal):
             assert bool(((lse[t].double() - log).abs() <= 2.0 ** -20 * (log + 1)).all()), (b, t)
 
 
+@pytest.mark.gpu
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("name", NAMES)
 def test_against_64_bits(fa, name, causal):
@@ -65,9 +74,10 @@ def test_against_64_bits(fa, name, causal):
     assert bool(((lse.double() - rl).abs() <= e + 2.0 ** -20 * (rl.abs() + 1)).all())
 
 
+@pytest.mark.gpu
 @pytest.mark.parametrize("name", ["boxes", "gathered", "codes"])
-def test_a_captured_call_takes_short_and_long_contexts(fa, name):
-    new = CASES[name][5]
+def test_a_captured_call_is_cut_or_not_as_its_lengths_say(fa, name):
+    kind, H, Hkv, d, bs, new, lens, _ = CASES[name]
     args = inputs(name, 5)
     q, caches, table, L, starts = args
     o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
@@ -76,7 +86,7 @@ def test_a_captured_call_takes_short_and_long_contexts(fa, name):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         run(fa, *args, out=o, lse=lse)
-    lens = L.tolist()
+    cut = set()
     for length, n in ((lens[0], new[0]), (700, new[0]), (lens[0] // 2 + 77, new[0] - 1), (lens[0], 2), (lens[0] - 1, new[0])):
         L.fill_(length)
         starts[1:].fill_(n)
@@ -86,15 +96,18 @@ def test_a_captured_call_takes_short_and_long_contexts(fa, name):
         run(fa, *args, out=ro, lse=rl)
         torch.cuda.synchronize()
         assert torch.equal(o[:n], ro[:n]) and torch.equal(lse[:n], rl[:n])
+        cut.add(chunks(kind, H, Hkv, d, bs, [n], [length], True, table.shape[1])[0])
     assert fa.last_device_error() == 0
+    assert 1 in cut and max(cut) >= 3
 
 
+@pytest.mark.gpu
 def test_the_debug_build_agrees(fa, tmp_path):
     """No bounds check fires and the results are the release build's bit for bit."""
     from exact_tiled_attention_24_gb300 import build
     build.build(debug=True)
     path = tmp_path / "debug.pt"
-    r = subprocess.run([sys.executable, os.path.join(HERE, "extend_long_cases.py"), str(path)],
+    r = subprocess.run([sys.executable, os.path.join(HERE, "extend_chunk_cases.py"), str(path)],
                        env=dict(os.environ, FA_DEBUG_LIBRARY="1"), capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stdout + r.stderr
     debug = torch.load(path)
