@@ -191,7 +191,7 @@ struct Extend {
     return q * bs > key ? q - 1 : q;
   }
 };
-// Sets the fields from `heads` to `n_long` from the sizes and `causal`; returns the workspace's bytes.
+// Sets the fields from `heads` to `n_long` from the sizes; returns the workspace's bytes.
 size_t extend_sizes(Extend* p, int d, bool q4);
 cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream);
 

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   Requests<NT> requests(p, err);
   if (p.zero_skipped) zero_rows<D, NT>(p, &requests, plan_smem, reinterpret_cast<int2*>(plan_smem + 1), err);
 
-  Shape sh{2 * p.tpt, p.causal, p.lc};
+  Shape sh{2 * p.tpt, p.causal, p.lc, 0};
   Cut cut;
   Place at;
   i64 items0;
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __gri
     const int first = job + 1 - shared_item.nth;
     for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * first + 1 : 2 * (first + i);
   } else {
-    Shape sh{2 * p.tpt, p.causal, p.lc};
+    Shape sh{2 * p.tpt, p.causal, p.lc, 0};
     Cut cut;
     Place at;
     i64 items0;

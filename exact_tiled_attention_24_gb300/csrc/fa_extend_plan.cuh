@@ -8,8 +8,7 @@
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
 //   cost    of an item: the keys it sees, and PIECE for its start and end
-//           (3 key tiles' time; 192, 320, 480 and 704 keys: a prompt of 8192
-//           tokens 435, 421, 427 and 436 us). Keys and not key tiles, because
+//           (2.5 key tiles' time). Keys and not key tiles, because
 //           their sums over items have a closed form without a division
 //           (counting tiles, the start of a CTA took 14 us, now 4)
 //   order   request by request, (chunk,) K/V head, item, key. The costs in this
@@ -23,9 +22,16 @@
 //           therefore cut into chunks of a share's length (or of what fits L2,
 //           if that is more), and all items pass one chunk before any passes
 //           the next: most shares are then one chunk of one item, and the CTAs
-//           walk along the keys together. 131072 keys, 8 K/V heads: 8 items a
-//           head 744 us, else 793; 16 items 1408 and 1532; but 4 items 441 and
-//           423, 2 items 320 and 252.
+//           walk along the keys together. That pays where a context is up to
+//           three shares long; where it is more, an item has many parts, and
+//           where it is less than one nothing is cut. bf16, 131072 keys, us
+//           with chunks and without, half a second each (and shares a context):
+//             8 K/V heads, d = 128  16 items a head 1487 and 1720 (1.2), 10 993 and
+//               1077 (1.9), 8 774 and 868 (2.4); 6 600 and 660 (3.2) is given away:
+//             8, d = 64  16 1123 and 1168 (1.2), 8 595 and 597 (2.4), 6 467 and 453 (3.2)
+//             4, 16 heads each  32 1457 and 1599 (1.2), 16 768 and 785 (2.4), 8 426 and 406 (4.8)
+//             2  32 754 and 759 (2.4), 16 422 and 385 (4.8), 8 257 and 205 (9.5), 6 223 and 162 (13)
+//             8, 4-bit codes  16 1842 and 1880 (1.2), 8 963 and 957 (2.4), 6 749 and 725 (3.2)
 #pragma once
 
 #include <cstdint>
@@ -43,8 +49,9 @@ constexpr int PIECE = 320;          // an item's start and end, in keys (256: a 
 constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than PIECE + TK, so that the ends of two
                                    // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
-constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks
-constexpr int MAX_PARTS = 2 * MAX_CTAS + 8;  // of a long item: its chunks, which are no shorter than shares, and the ends within
+constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks,
+constexpr int CHUNK_SHARES = 3;    // nor one whose context is more shares long
+constexpr int MAX_PARTS = MAX_CTAS + CHUNK_SHARES;  // of an item: one a share and one a chunk at most
 static_assert(MIN_SHARE >= PIECE + 2 * TK, "");
 
 typedef long long i64;
@@ -86,6 +93,7 @@ struct Shape {
   int span;  // tokens an item: 2·tpt
   bool causal;
   int lc;    // keys a chunk, a multiple of TK
+  int far;   // longer contexts are not cut into chunks
 
   // key tiles of `keys` (one at least, so that rows that see nothing are written)
   FA_HD static int tiles_of(int keys) { return max(1, (keys + TK - 1) / TK); }
@@ -108,7 +116,9 @@ struct Shape {
     const int d = static_cast<int>(x) - r.base();
     return d < 0 ? 0 : min(d / span, r.items - 1);
   }
-  FA_HD bool chunked(const Request& r) const { return r.items >= CHUNK_ITEMS && r.len > lc; }
+  FA_HD bool chunked(const Request& r) const {
+    return r.items >= CHUNK_ITEMS && r.len > lc && r.len <= far;
+  }
   FA_HD int chunks(const Request& r) const { return chunked(r) ? (r.len + lc - 1) / lc : 1; }
   // the first item that reaches chunk c
   FA_HD int reach(const Request& r, int c) const { return c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
@@ -156,11 +166,12 @@ struct Shape {
   FA_HD static int tile_at(i64 x) { return x <= PIECE ? 0 : static_cast<int>((x - PIECE) / TK); }
 };
 
-// Keys a chunk: a share's length, or what fits L2 if that is more. all: Σ of
+// Sets the chunks' length: a share's, or what fits L2 if that is more. all: Σ of
 // the keys that the items of all heads see.
-FA_HD int chunk_keys(const Extend& p, i64 all) {
-  const i64 least = (all / p.ctas + TK) / TK * TK;
-  return static_cast<int>(least <= p.lc ? p.lc : least < (1 << 29) ? least : 1 << 29);
+FA_HD void set_chunks(Shape* sh, const Extend& p, i64 all) {
+  const i64 share = min((all / p.ctas + TK) / TK * TK, static_cast<i64>(1 << 29));
+  sh->lc = max(static_cast<int>(share), p.lc);
+  sh->far = static_cast<int>(min(CHUNK_SHARES * share, static_cast<i64>(1 << 30)));
 }
 
 // The whole call's cut into `ctas` shares: share k is [start(k), start(k + 1)),
@@ -291,7 +302,7 @@ template <int NT, bool LONG>
 __device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* sh, PlanSmem* sm, int want, Cut* cut,
                                      Place* at, i64* items0) {
   const int tid = static_cast<int>(threadIdx.x);
-  sh->lc = p.lc;
+  sh->lc = p.lc, sh->far = 0;
   if (p.may_chunk) {
     i64 k = 0, all;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
@@ -299,7 +310,7 @@ __device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* s
       if (r.n > 0) k += sh->keys_before(r, r.items) * p.hv;
     }
     block_scan<NT>(k, sm->scan, &all);
-    sh->lc = chunk_keys(p, all);
+    set_chunks(sh, p, all);
   }
   // costs before each thread's request; with more requests than threads, the total first
   i64 c = 0;

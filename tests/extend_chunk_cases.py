@@ -14,22 +14,24 @@ for path in (ROOT, os.path.join(ROOT, "tests")):
         sys.path.insert(0, path)
 
 BF, I32 = torch.bfloat16, torch.int32
-TILE, PIECE, CTAS, ITEMS, L2 = 128, 320, 152, 6, 40 << 20
+TILE, PIECE, CTAS, ITEMS, SHARES, L2 = 128, 320, 152, 6, 3, 40 << 20
 
 CASES = {  # kind, H, Hkv, d, block size, new tokens, cached tokens, chunks of each request's keys
-    "boxes": ("bf16", 16, 4, 128, 16, [350], [131072], [7]),
-    "two requests": ("bf16", 96, 3, 64, 128, [41, 3, 50], [250000, 500, 170000], [5, 1, 4]),
-    "gathered": ("bf16", 128, 1, 64, 3, [12], [700000], [5]),
-    "gathered, others before and after": ("bf16", 256, 2, 128, 200, [1, 13, 2], [900, 230000, 2], [1, 6, 1]),
-    "codes": ("q4", 64, 1, 128, 16, [24], [1000000], [4]),
-    "codes, two requests": ("q4", 96, 3, 64, 5, [41, 3, 50], [600000, 500, 500000], [4, 1, 3]),
+    "boxes": ("bf16", 256, 4, 128, 16, [60], [60000], [3]),
+    "boxes, two chunks": ("bf16", 16, 4, 128, 32, [1500], [40000], [2]),
+    "two requests": ("bf16", 96, 3, 64, 128, [90, 3, 80], [250000, 500, 170000], [3, 1, 2]),
+    "gathered": ("bf16", 384, 3, 64, 3, [36], [200000], [3]),
+    "gathered, others before and after": ("bf16", 256, 2, 128, 200, [1, 52, 2], [900, 230000, 2], [1, 3, 1]),
+    "codes": ("q4", 256, 4, 128, 16, [60], [220000], [3]),
+    "codes, two requests": ("q4", 96, 3, 64, 5, [90, 3, 80], [600000, 500, 500000], [3, 1, 3]),
 }
 
 
 def chunks(kind, H, Hkv, d, bs, new, lens, causal, max_blocks):
     """Into how many chunks each request's keys are cut, from the rule in words:
     no shorter than what fits L2 (all K/V heads' keys and values, 40 MB) and than
-    a CTA's share of all items' keys, for requests of six items a head or more."""
+    a CTA's share of all items' keys, for requests of six items a head or more,
+    and only where the context is three shares long at most."""
     G = H // Hkv
     parts = -(-G // 128)
     tokens = 128 // -(-G // parts)          # a query tile's
@@ -44,8 +46,9 @@ def chunks(kind, H, Hkv, d, bs, new, lens, causal, max_blocks):
     for n, length in zip(new, lens):
         for i in range(-(-n // span)):
             keys += hv * (max(0, length - n + min((i + 1) * span, n)) if causal else length)
-    lc = max(lc, (keys // ctas + TILE) // TILE * TILE)
-    return [-(-length // lc) if -(-n // span) >= ITEMS and length > lc else 1 for n, length in zip(new, lens)]
+    share = (keys // ctas + TILE) // TILE * TILE
+    lc = max(lc, share)
+    return [-(-length // lc) if -(-n // span) >= ITEMS and lc < length <= SHARES * share else 1 for n, length in zip(new, lens)]
 
 
 def inputs(name, seed, counting=False):

@@ -70,7 +70,7 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
       most = std::max<i64>(most, causal ? std::max(r.len - r.n + t + 1, 0) : r.len);
     return static_cast<int>(most);
   };
-  Shape sh{span, p.causal, p.lc};
+  Shape sh{span, p.causal, p.lc, 0};
   std::vector<std::vector<int>> keys(B);
   i64 all = 0;
   for (int b = 0; b < B; ++b) {
@@ -83,7 +83,8 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
     if (rq[b].n > 0) CHECK(sh.keys_before(rq[b], rq[b].items) == sum);
     all += sum * p.hv;
   }
-  if (p.may_chunk) sh.lc = chunk_keys(p, all);
+  if (p.may_chunk) set_chunks(&sh, p, all);
+  CHECK(!p.may_chunk || sh.lc == std::max<i64>(p.lc, (all / p.ctas + TK) / TK * TK));
   CHECK(sh.lc % TK == 0 && sh.lc > 0);
   std::vector<Item> items;
   std::map<std::tuple<int, int, int>, int> tiles_left;  // (request, head, item): tiles not yet dealt out
@@ -92,7 +93,7 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
   for (int b = 0; b < B; ++b) {
     const Request& r = rq[b];
     if (r.n == 0) continue;
-    const bool cut = p.may_chunk && r.items >= CHUNK_ITEMS && r.len > sh.lc;
+    const bool cut = p.may_chunk && r.items >= 6 && r.len > sh.lc && r.len <= 3 * ((all / p.ctas + TK) / TK * TK);
     if (!p.may_chunk) CHECK(!sh.chunked(r));
     CHECK(sh.chunked(r) == cut);
     const int chunks = cut ? (r.len + sh.lc - 1) / sh.lc : 1;

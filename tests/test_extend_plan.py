@@ -51,15 +51,17 @@ def blocks_for(longest, bs):
 @pytest.mark.parametrize("q4", [False, True])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("H,Hkv,d,new,lens,chunks", [
-    (16, 4, 128, [350], [131072], 7),
-    (256, 2, 128, [12], [300000], 5),
-    (16, 16, 64, [1500, 3, 1300], [60000, 9, 30000], 2),
-    (6, 6, 128, [5, 1600, 2], [17, 50000, 800], 3),
+    (256, 4, 128, [60], [220000], 3),
+    (16, 16, 64, [1500, 3, 1300], [200000, 9, 100000], 2),
+    (6, 6, 128, [5, 2600, 2], [17, 150000, 800], 3),
+    (16, 4, 128, [350], [300000], 1),   # would be seven
+    (16, 2, 128, [160], [300000], 1),   # five items a head
+    (16, 2, 128, [200], [300000], 1),   # over codes three pieces of L2's size, but fourteen shares
 ])
 def test_chunked(plan, H, Hkv, d, new, lens, chunks, causal, q4):
     """Requests that are cut into chunks of keys, alone and among others."""
     got = plan(sum(new), H, Hkv, d, 16, blocks_for(max(lens), 16), starts_of(new), lens, causal, q4)
-    assert got[0] >= (2 if q4 or not causal else chunks) and got[1] > 0, got
+    assert got[0] == chunks and (got[1] > 0) == (chunks > 1), got
 
 
 def test_random_calls(plan):
@@ -90,7 +92,7 @@ def test_starts_that_go_down_and_up_again(plan, q4):
     got = plan(400, 32, 8, 128, 16, 1024, [0, 400, 0, 400], [16384] * 3, True, q4)
     assert got[3] == 2
     got = plan(1281, 4, 4, 128, 16, 3840, [0, 1281, 0, 1281], [61440] * 3, True, q4)
-    assert got[3] == 2 and (q4 or got[0] > 1)
+    assert got[3] == 2
     # an overlap by one row, starts in order again behind it; a request of no rows is behind anything
     assert plan(40, 8, 2, 128, 16, 4, [0, 10, 9, 20, 20, 40], [60] * 5)[3] == 2
     assert plan(40, 8, 2, 128, 16, 4, [0, 10, 10, 5, 5, 40], [60] * 5)[3] == 2

@@ -1,5 +1,5 @@
 """extend_paged and extend_paged_q4 where the keys of a request are cut into
-three chunks or more: every load path, with other requests before and after,
+two or three chunks: every load path, with other requests before and after,
 all keys and causal, captured and replayed with lengths that are cut and that
 are not, and on the bounds-checked build."""
 import os
@@ -27,7 +27,7 @@ def fa():
 @pytest.mark.parametrize("name", NAMES)
 def test_the_cases_are_cut(name, causal):
     kind, H, Hkv, d, bs, new, lens, want = CASES[name]
-    assert chunks(kind, H, Hkv, d, bs, new, lens, causal, -(-max(lens) // bs)) == want and max(want) >= 3
+    assert chunks(kind, H, Hkv, d, bs, new, lens, causal, -(-max(lens) // bs)) == want and max(want) >= 2
 
 
 @pytest.mark.gpu
@@ -98,7 +98,7 @@ def test_a_captured_call_is_cut_or_not_as_its_lengths_say(fa, name):
         assert torch.equal(o[:n], ro[:n]) and torch.equal(lse[:n], rl[:n])
         cut.add(chunks(kind, H, Hkv, d, bs, [n], [length], True, table.shape[1])[0])
     assert fa.last_device_error() == 0
-    assert 1 in cut and max(cut) >= 3
+    assert {1, 2, 3} <= cut
 
 
 @pytest.mark.gpu
