@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_common.h"
 #include "fa_extend_plan.cuh"
 #include "fa_ptx.cuh"
@@ -203,7 +205,7 @@ __device__ __forceinline__ void zero_rows(const Extend& p, Requests<NT>* request
   }
 }
 
-template <int D, int LOAD>
+template <int D, int LOAD, bool CHUNKS>
 __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
     extend_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ Extend p) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
   Requests<NT> requests(p, err);
   if (p.zero_skipped) zero_rows<D, NT>(p, &requests, plan_smem, reinterpret_cast<int2*>(plan_smem + 1), err);
 
-  Shape sh{2 * p.tpt, p.causal, p.lc, 0};
+  Shape<CHUNKS> sh{2 * p.tpt, p.causal, p.lc, 0};
   Cut cut;
   Place at;
   i64 items0;
@@ -1013,22 +1015,23 @@ __device__ __forceinline__ void merge_rows(const Extend& p, const ItemCut& it, c
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) extend_merge_kernel(const __grid_constant__ Extend p) {
-  __shared__ PlanSmem plan_smem;
+// (", 1": left to itself the compiler takes 64 registers and spills.)
+template <int D, bool CHUNKS>
+__global__ void __launch_bounds__(MERGE_THREADS, 1) extend_merge_kernel(const __grid_constant__ Extend p) {
   __shared__ int parts[MAX_PARTS];
   __shared__ ItemCut shared_item;
   uint32_t* err = &g_extend_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int job = static_cast<int>(blockIdx.x);
-  if (job < p.ctas - 1) {
+  if (!CHUNKS || job < p.ctas - 1) {
     wait_for_primary();
     if (threadIdx.x == 0) shared_item = in_range(job + 1, 1, p.ctas, err) ? p.cuts[job + 1] : ItemCut{};
     __syncthreads();
     const int first = job + 1 - shared_item.nth;
     for (int i = threadIdx.x; i < shared_item.parts; i += MERGE_THREADS) parts[i] = i == 0 ? 2 * first + 1 : 2 * (first + i);
-  } else {
-    Shape sh{2 * p.tpt, p.causal, p.lc, 0};
+  } else if constexpr (CHUNKS) {
+    __shared__ PlanSmem plan_smem;
+    Shape<true> sh{2 * p.tpt, p.causal, p.lc, 0};
     Cut cut;
     Place at;
     i64 items0;
@@ -1108,7 +1111,7 @@ static bool make_tmap_q(CUtensorMap* map, const void* q, int T, int H, int d, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int LOAD>
+template <int D, int LOAD, bool CHUNKS>
 static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   if (!make_tmap_q(&tq, q, p.T, p.H, D, p.heads, p.tpt)) return cudaErrorInvalidValue;
@@ -1119,7 +1122,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
   } else {
     tk = tv = tq;  // unused
   }
-  auto kern = extend_kernel<D, LOAD>;
+  auto kern = extend_kernel<D, LOAD, CHUNKS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, LOAD>::ALLOC);
   if (e != cudaSuccess) return e;
   kern<<<p.ctas, Threads<LOAD>::N, Smem<D, LOAD>::ALLOC, stream>>>(tq, tk, tv, p);
@@ -1135,7 +1138,7 @@ static cudaError_t launch(const Extend& p, const void* q, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, extend_merge_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, extend_merge_kernel<D, CHUNKS>, p);
 }
 
 }  // namespace ext
@@ -1173,9 +1176,13 @@ size_t extend_sizes(Extend* p, int d, bool q4) {
 
 cudaError_t launch_extend(const Extend& p, const void* q, int d, bool q4, cudaStream_t stream) {
   using namespace ext;
-  if (q4) return d == 64 ? launch<64, CODES>(p, q, stream) : launch<128, CODES>(p, q, stream);
-  if (boxes(p.bs)) return d == 64 ? launch<64, BOXES>(p, q, stream) : launch<128, BOXES>(p, q, stream);
-  return d == 64 ? launch<64, GATHER>(p, q, stream) : launch<128, GATHER>(p, q, stream);
+  auto go = [&](auto chunks) {
+    constexpr bool C = decltype(chunks)::value;
+    if (q4) return d == 64 ? launch<64, CODES, C>(p, q, stream) : launch<128, CODES, C>(p, q, stream);
+    if (boxes(p.bs)) return d == 64 ? launch<64, BOXES, C>(p, q, stream) : launch<128, BOXES, C>(p, q, stream);
+    return d == 64 ? launch<64, GATHER, C>(p, q, stream) : launch<128, GATHER, C>(p, q, stream);
+  };
+  return p.may_chunk ? go(std::true_type{}) : go(std::false_type{});
 }
 
 cudaError_t read_and_clear_extend_error(uint32_t* out, cudaStream_t stream) {

@@ -89,6 +89,10 @@ FA_HD Request request_of(const Extend& p, int b, bool* broken) {
   return r;
 }
 
+// CHUNKS: of calls of which some request may be cut into chunks. (The code for
+// it is left out of the others' kernels: they start from a cold instruction
+// cache. 2777 tokens of 12 requests: 222 us with it, 209 without.)
+template <bool CHUNKS>
 struct Shape {
   int span;  // tokens an item: 2·tpt
   bool causal;
@@ -117,11 +121,11 @@ struct Shape {
     return d < 0 ? 0 : min(d / span, r.items - 1);
   }
   FA_HD bool chunked(const Request& r) const {
-    return r.items >= CHUNK_ITEMS && r.len > lc && r.len <= far;
+    return CHUNKS && r.items >= CHUNK_ITEMS && r.len > lc && r.len <= far;
   }
   FA_HD int chunks(const Request& r) const { return chunked(r) ? (r.len + lc - 1) / lc : 1; }
   // the first item that reaches chunk c
-  FA_HD int reach(const Request& r, int c) const { return c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
+  FA_HD int reach(const Request& r, int c) const { return !CHUNKS || c == 0 ? 0 : past(r, static_cast<i64>(c) * lc); }
   // keys of item i in chunk c, which it reaches
   FA_HD int part(const Request& r, int c, int i) const {
     const int k = keys(r, i);
@@ -168,7 +172,7 @@ struct Shape {
 
 // Sets the chunks' length: a share's, or what fits L2 if that is more. all: Σ of
 // the keys that the items of all heads see.
-FA_HD void set_chunks(Shape* sh, const Extend& p, i64 all) {
+FA_HD void set_chunks(Shape<true>* sh, const Extend& p, i64 all) {
   const i64 share = min((all / p.ctas + TK) / TK * TK, static_cast<i64>(1 << 29));
   sh->lc = max(static_cast<int>(share), p.lc);
   sh->far = static_cast<int>(min(CHUNK_SHARES * share, static_cast<i64>(1 << 30)));
@@ -297,13 +301,12 @@ struct Requests {
 // one that share `want` begins in, with LONG = true of the want-th long item
 // (its request and, in *items0, the long items before that). False: there is
 // none. Run by a whole block; every thread knows the result, up to the request
-// (locate has the rest). Sets sh->lc.
-template <int NT, bool LONG>
-__device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* sh, PlanSmem* sm, int want, Cut* cut,
+// (locate has the rest). Sets sh->lc and far.
+template <int NT, bool LONG, bool CHUNKS>
+__device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape<CHUNKS>* sh, PlanSmem* sm, int want, Cut* cut,
                                      Place* at, i64* items0) {
   const int tid = static_cast<int>(threadIdx.x);
-  sh->lc = p.lc, sh->far = 0;
-  if (p.may_chunk) {
+  if constexpr (CHUNKS) {
     i64 k = 0, all;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
       const Request r = rq->tile(p, b0, sm);
@@ -327,7 +330,7 @@ __device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* s
     const i64 cost = p.B <= NT ? c : sh->total(r, p.hv);
     i64 sum = 0, sum_l = 0, sum_i = 0, l = 0, it = 0, e_l = 0, e_i = 0;
     const i64 e = p.B <= NT ? before : costs + block_scan<NT>(cost, sm->scan, &sum);
-    if (p.may_chunk) {
+    if constexpr (CHUNKS) {
       if (r.n > 0 && sh->chunked(r)) {
         l = static_cast<i64>(sh->long_before(r, sh->chunks(r))) * p.hv;
         it = static_cast<i64>(r.items - sh->first_long(r, 0)) * p.hv;
@@ -356,7 +359,8 @@ __device__ __forceinline__ bool plan(const Extend& p, Requests<NT>* rq, Shape* s
 }
 
 // The item that holds cost `x` of a request's; run by a whole warp.
-__device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, Place* at) {
+template <bool CHUNKS>
+__device__ __forceinline__ void locate(const Extend& p, const Shape<CHUNKS>& sh, i64 x, Place* at) {
   const int lane = threadIdx.x & 31;
   const Request& r = at->r;
   i64 rem = x - at->request0;
@@ -404,7 +408,8 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape& sh, i64 x, 
 // Where a piece's result goes: slots 2k and 2k + 1 are CTA k's first and last
 // piece where its share cuts an item, the others hold whole chunks of long
 // items; -1: the outputs themselves.
-FA_HD int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bool start_cut,
+template <bool CHUNKS>
+FA_HD int part_slot(const Extend& p, const Shape<CHUNKS>& sh, const Place& at, int k, bool start_cut,
                                          bool end_cut) {
   if (start_cut) return 2 * k;
   if (end_cut) return 2 * k + 1;
@@ -418,13 +423,13 @@ FA_HD int part_slot(const Extend& p, const Shape& sh, const Place& at, int k, bo
 // more, and not a long one: slot 2k + 1 of the share k in which its first tile
 // lies, then 2 (k + 1), 2 (k + 2) and so on.)
 template <class F>
-FA_HD int parts_of(const Extend& p, const Shape& sh, const Cut& cut, const Place& at, int k, F f) {
-  const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape::tiles_of(sh.part(at.r, at.c, at.i));
+FA_HD int parts_of(const Extend& p, const Shape<true>& sh, const Cut& cut, const Place& at, int k, F f) {
+  const int cost = sh.cost(at.r, at.c, at.i), tiles = Shape<true>::tiles_of(sh.part(at.r, at.c, at.i));
   const i64 end = at.item0 + cost;
   int n = 0;
   for (int lo = 0; lo < tiles; ++k) {
     const i64 e = cut.start(k + 1);
-    const int hi = e >= end ? tiles : Shape::tile_at(e - at.item0);
+    const int hi = e >= end ? tiles : Shape<true>::tile_at(e - at.item0);
     if (hi <= lo) continue;
     f(n++, part_slot(p, sh, at, k, lo > 0, hi < tiles));
     lo = hi;
@@ -448,21 +453,21 @@ static_assert(sizeof(Piece) == 64, "");
 // Share `cta`'s pieces in order, from the item it begins in: f(piece) for each,
 // until that says false; false then. *entered: the item that the share begins
 // within, if another share has its start (and it is not a long one).
-template <class F>
-FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place at, ItemCut* entered, F f) {
+template <bool CHUNKS, class F>
+FA_HD bool walk(const Extend& p, const Shape<CHUNKS>& sh, const Cut& cut, int cta, Place at, ItemCut* entered, F f) {
   const i64 begin = cut.start(cta), end = cut.start(cta + 1);
-  int lo = begin > at.item0 ? Shape::tile_at(begin - at.item0) : 0;
+  int lo = begin > at.item0 ? Shape<CHUNKS>::tile_at(begin - at.item0) : 0;
   const int G = p.H / p.Hkv, parts = p.hv / p.Hkv;
   Piece x{};  // n = 0
   while (true) {
     const Request& r = at.r;
-    const int tiles = Shape::tiles_of(sh.part(r, at.c, at.i));
+    const int tiles = Shape<CHUNKS>::tiles_of(sh.part(r, at.c, at.i));
     const i64 item_end = at.item0 + sh.cost(r, at.c, at.i);
-    const int hi = item_end <= end ? tiles : Shape::tile_at(end - at.item0);
+    const int hi = item_end <= end ? tiles : Shape<CHUNKS>::tile_at(end - at.item0);
     if (hi > lo) {
       x.unit0 += x.n;
       x.n = hi - lo;
-      x.kt0 = at.c * (sh.lc / TK) + lo;
+      x.kt0 = (CHUNKS ? at.c * (sh.lc / TK) : 0) + lo;
       x.b = at.b;
       x.kvh = at.hv / parts;
       const int h0 = at.hv % parts * p.heads;
@@ -484,7 +489,7 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
       if (!f(x)) return false;
       if (lo > 0 && !sh.is_long(r, at.i)) {  // the share's first piece at most
         int first = cut.owner(at.item0);
-        if (Shape::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
+        if (Shape<CHUNKS>::tile_at(cut.start(first + 1) - at.item0) == 0) ++first;
         *entered = ItemCut{cut.owner(item_end - 1) - first + 1, cta - first, x.tok0, x.ntok, x.head0, x.heads};
       }
     }
@@ -494,8 +499,8 @@ FA_HD bool walk(const Extend& p, const Shape& sh, const Cut& cut, int cta, Place
     if (++at.i < r.items) continue;
     if (++at.hv == p.hv) {
       at.hv = 0;
-      if (++at.c == sh.chunks(r)) {
-        if (p.may_chunk && sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
+      if (!CHUNKS || ++at.c == sh.chunks(r)) {
+        if (sh.chunked(r)) at.longs0 += p.hv * sh.long_before(r, at.c);
         at.c = 0;
         do {  // costs are left, so there is a request with tokens
           bool broken;

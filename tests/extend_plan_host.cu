@@ -28,16 +28,13 @@ struct Item {  // of one chunk
 
 }  // namespace
 
-// 0, or the line of the check that failed. out: chunks of the longest cut
-// request (1: none is cut), long items, the largest slot, requests taken for
-// empty, keys a chunk.
-extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_blocks, int causal, int q4,
-                          const int* starts, const int* lens, int* out) {
-  Extend p{};
-  p.T = T, p.B = B, p.H = H, p.Hkv = Hkv, p.bs = bs, p.max_blocks = max_blocks, p.causal = causal != 0;
-  p.q_starts = starts, p.seq_lens = lens;
-  extend_sizes(&p, d, q4 != 0);
-  const int span = 2 * p.tpt, G = H / Hkv, parts = p.hv / Hkv;
+// Chunks of the longest cut request (1: none is cut), long items, the largest
+// slot, requests taken for empty, keys a chunk.
+template <bool CHUNKS>
+static int check(const Extend& p, int* out) {
+  const int T = p.T, B = p.B, G = p.H / p.Hkv, span = 2 * p.tpt, parts = p.hv / p.Hkv, bs = p.bs, max_blocks = p.max_blocks;
+  const int *starts = p.q_starts, *lens = p.seq_lens;
+  const bool causal = p.causal;
   CHECK(p.ctas >= 1 && p.ctas <= MAX_CTAS && p.heads * parts >= G && p.tpt * p.heads <= 128);
 
   // Which requests there are, from the rule as it is documented.
@@ -70,7 +67,7 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
       most = std::max<i64>(most, causal ? std::max(r.len - r.n + t + 1, 0) : r.len);
     return static_cast<int>(most);
   };
-  Shape sh{span, p.causal, p.lc, 0};
+  Shape<CHUNKS> sh{span, p.causal, p.lc, 0};
   std::vector<std::vector<int>> keys(B);
   i64 all = 0;
   for (int b = 0; b < B; ++b) {
@@ -83,8 +80,8 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
     if (rq[b].n > 0) CHECK(sh.keys_before(rq[b], rq[b].items) == sum);
     all += sum * p.hv;
   }
-  if (p.may_chunk) set_chunks(&sh, p, all);
-  CHECK(!p.may_chunk || sh.lc == std::max<i64>(p.lc, (all / p.ctas + TK) / TK * TK));
+  if constexpr (CHUNKS) set_chunks(&sh, p, all);
+  CHECK(!CHUNKS || sh.lc == std::max<i64>(p.lc, (all / p.ctas + TK) / TK * TK));
   CHECK(sh.lc % TK == 0 && sh.lc > 0);
   std::vector<Item> items;
   std::map<std::tuple<int, int, int>, int> tiles_left;  // (request, head, item): tiles not yet dealt out
@@ -93,8 +90,7 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
   for (int b = 0; b < B; ++b) {
     const Request& r = rq[b];
     if (r.n == 0) continue;
-    const bool cut = p.may_chunk && r.items >= 6 && r.len > sh.lc && r.len <= 3 * ((all / p.ctas + TK) / TK * TK);
-    if (!p.may_chunk) CHECK(!sh.chunked(r));
+    const bool cut = CHUNKS && r.items >= 6 && r.len > sh.lc && r.len <= 3 * ((all / p.ctas + TK) / TK * TK);
     CHECK(sh.chunked(r) == cut);
     const int chunks = cut ? (r.len + sh.lc - 1) / sh.lc : 1;
     CHECK(sh.chunks(r) == chunks);
@@ -229,17 +225,29 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
     }
     if (x.c > 0) continue;
     ++order;
-    std::vector<int> got;
-    const int n_c = (keys[x.b][x.i] + sh.lc - 1) / sh.lc;
-    for (int c = 0; c < n_c; ++c) {
-      Place at{r, x.b, 0, x.request0, x.longs0, c, x.hv, x.i, 0};
-      at.item0 = x.request0 + sh.chunks_before(r, c) * p.hv + sh.costs_before(r, c, r.items) * x.hv + sh.costs_before(r, c, x.i);
-      parts_of(p, sh, cut, at, cut.owner(at.item0), [&](int, int slot) { got.push_back(slot); });
+    if constexpr (CHUNKS) {
+      std::vector<int> got;
+      const int n_c = (keys[x.b][x.i] + sh.lc - 1) / sh.lc;
+      for (int c = 0; c < n_c; ++c) {
+        Place at{r, x.b, 0, x.request0, x.longs0, c, x.hv, x.i, 0};
+        at.item0 = x.request0 + sh.chunks_before(r, c) * p.hv + sh.costs_before(r, c, r.items) * x.hv + sh.costs_before(r, c, x.i);
+        parts_of(p, sh, cut, at, cut.owner(at.item0), [&](int, int slot) { got.push_back(slot); });
+      }
+      CHECK(got.size() <= static_cast<size_t>(MAX_PARTS) && got.size() == dealt[key].size());
+      size_t n = 0;
+      for (const auto& y : dealt[key]) CHECK(got[n++] == y.second.slot);
     }
-    CHECK(got.size() <= static_cast<size_t>(MAX_PARTS) && got.size() == dealt[key].size());
-    size_t n = 0;
-    for (const auto& y : dealt[key]) CHECK(got[n++] == y.second.slot);
   }
   CHECK(order == n_long);
   return 0;
+}
+
+// 0, or the line of the check that failed.
+extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_blocks, int causal, int q4,
+                          const int* starts, const int* lens, int* out) {
+  Extend p{};
+  p.T = T, p.B = B, p.H = H, p.Hkv = Hkv, p.bs = bs, p.max_blocks = max_blocks, p.causal = causal != 0;
+  p.q_starts = starts, p.seq_lens = lens;
+  extend_sizes(&p, d, q4 != 0);
+  return p.may_chunk ? check<true>(p, out) : check<false>(p, out);
 }
