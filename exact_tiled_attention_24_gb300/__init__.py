@@ -1035,8 +1035,8 @@ def extend_paged(q, k_cache, v_cache, block_table, seq_lens, q_starts, causal=Tr
     the end of an earlier one, is taken for empty (and reported by
     last_device_error). Rows of no request (theirs, those before q_starts[0] and
     from q_starts[B] on) are o = 0, lse = -inf where both outputs are made here
-    and stay as they were where either is given. The lengths are read on the device: a captured call may be
-    replayed with others."""
+    and stay as they were where either is given. The lengths are read on the
+    device: a captured call may be replayed with others."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("expected q [T, H, d]")
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:

@@ -30,12 +30,13 @@
 //
 // What bounds it (32 + 8 heads, d = 128, 2070 MHz): with full tiles the tensor
 // pipe, as in the forward: 2048 clocks of products in 3300 a unit (a prompt of
-// 8192 tokens 402 us, 1024 tokens at 131072 keys 1.38 to 1.45 ms, 1510 to 1590
-// TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
-// requests of 5 tokens over 2k to 8k keys: 136 us, 110 of them). Over codes (152 us
+// 8192 tokens 410 to 415 us, 1024 tokens at 131072 keys 1.45 to 1.48 ms, 1480 to
+// 1510 TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
+// requests of 5 tokens over 2k to 8k keys: 129 us, 110 of them). Over codes (144 us
 // for the same) the chain of one query tile's scores, softmax and output, 3400
-// clocks a tile, and the loading warps' 3600 beside it. About 10 us pass until a
-// CTA's first product and 4 us with each piece's start and end.
+// clocks a tile, and the loading warps' 3600 beside it. 7 to 9 us pass until a
+// CTA's first product (16 where keys are cut into chunks) and 4 us with each
+// piece's start and end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -8,9 +8,9 @@
 //   item    two query tiles of one K/V head of one request: up to 2·tpt new
 //           tokens with the heads that share the K/V head (256 rows)
 //   cost    of an item: the keys it sees, and PIECE for its start and end
-//           (2.5 key tiles' time). Keys and not key tiles, because
-//           their sums over items have a closed form without a division
-//           (counting tiles, the start of a CTA took 14 us, now 4)
+//           (2.5 key tiles' time). Keys and not key tiles, because their sums
+//           over items have a closed form without a division (counting tiles,
+//           14 us passed until a CTA's item was found, now 4)
 //   order   request by request, (chunk,) K/V head, item, key. The costs in this
 //           order are cut into C equal shares, one a CTA, each end rounded down
 //           to a key tile of its item: the lengths are on the device only, and
@@ -409,8 +409,7 @@ __device__ __forceinline__ void locate(const Extend& p, const Shape<CHUNKS>& sh,
 // piece where its share cuts an item, the others hold whole chunks of long
 // items; -1: the outputs themselves.
 template <bool CHUNKS>
-FA_HD int part_slot(const Extend& p, const Shape<CHUNKS>& sh, const Place& at, int k, bool start_cut,
-                                         bool end_cut) {
+FA_HD int part_slot(const Extend& p, const Shape<CHUNKS>& sh, const Place& at, int k, bool start_cut, bool end_cut) {
   if (start_cut) return 2 * k;
   if (end_cut) return 2 * k + 1;
   if (!sh.is_long(at.r, at.i)) return -1;

@@ -646,6 +646,8 @@ int fa_decode_paged_q4(const fa_decode_q4_args* a, void* stream);
  * decode step holds them exactly.
  * The lengths are read on the device and the work is cut there: a captured
  * call may be replayed with other lengths within the same T, B and table.
+ * Waits inside the kernel end after 2 s (FA_ERR_TIMEOUT): what one SM does of
+ * 256 rows has to stay below about 10^8 keys.
  * Errors: a NULL struct or pointer it must hold, sizes < 1, Hkv not dividing
  * H, bad scale -> FA_ERR_INVALID_ARG; d not 64/128, T·H past 2^31, T past
  * 2^30, B past 2^24, H/Hkv past 16384, a cache past 2^32 token rows or 2^31 - 2
