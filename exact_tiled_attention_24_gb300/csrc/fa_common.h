@@ -178,7 +178,7 @@ struct Extend {
   int T, B, H, Hkv, num_blocks, bs, max_blocks;
   int heads, hv;             // query heads a tile holds (at most 128), K/V heads times the parts its query heads are cut into
   int tpt;                   // tokens a query tile holds: 128 / heads
-  int ctas, lc, may_chunk;   // see fa_extend_plan.cuh
+  int ctas, lc, may_chunk, chunk_halves;  // see fa_extend_plan.cuh
   unsigned bs_inverse;       // 2^32 / bs, rounded up (bs = 1: 1)
   int n_slots, n_long;       // workspace parts; long items there may be
   bool causal, zero_skipped;

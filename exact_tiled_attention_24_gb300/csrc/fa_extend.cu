@@ -30,7 +30,7 @@
 //
 // What bounds it (32 + 8 heads, d = 128, 2070 MHz): with full tiles the tensor
 // pipe, as in the forward: 2048 clocks of products in 3300 a unit (a prompt of
-// 8192 tokens 410 to 415 us, 1024 tokens at 131072 keys 1.45 to 1.48 ms, 1480 to
+// 8192 tokens 410 to 419 us, 1024 tokens at 131072 keys 1.45 to 1.49 ms, 1470 to
 // 1510 TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
 // requests of 5 tokens over 2k to 8k keys: 129 us, 110 of them). Over codes (144 us
 // for the same) the chain of one query tile's scores, softmax and output, 3400
@@ -1160,6 +1160,7 @@ size_t extend_sizes(Extend* p, int d, bool q4) {
   const long long items = p->hv * (p->T / span + (p->T < p->B ? p->T : p->B));  // at most
   const long long shares = items * (ctx + PIECE) / MIN_SHARE;
   p->ctas = static_cast<int>(shares < 1 ? 1 : shares > MAX_CTAS ? MAX_CTAS : shares);
+  p->chunk_halves = d == 128 && !q4 ? CHUNK_HALVES_512 : CHUNK_HALVES;
   p->may_chunk = p->T > (CHUNK_ITEMS - 1) * span && ctx > p->lc;
   p->n_long = 0;
   long long whole = 0;

@@ -22,16 +22,20 @@
 //           therefore cut into chunks of a share's length (or of what fits L2,
 //           if that is more), and all items pass one chunk before any passes
 //           the next: most shares are then one chunk of one item, and the CTAs
-//           walk along the keys together. That pays where a context is up to
-//           three shares long; where it is more, an item has many parts, and
-//           where it is less than one nothing is cut. bf16, 131072 keys, us
-//           with chunks and without, half a second each (and shares a context):
-//             8 K/V heads, d = 128  16 items a head 1487 and 1720 (1.2), 10 993 and
-//               1077 (1.9), 8 774 and 868 (2.4); 6 600 and 660 (3.2) is given away:
-//             8, d = 64  16 1123 and 1168 (1.2), 8 595 and 597 (2.4), 6 467 and 453 (3.2)
-//             4, 16 heads each  32 1457 and 1599 (1.2), 16 768 and 785 (2.4), 8 426 and 406 (4.8)
-//             2  32 754 and 759 (2.4), 16 422 and 385 (4.8), 8 257 and 205 (9.5), 6 223 and 162 (13)
-//             8, 4-bit codes  16 1842 and 1880 (1.2), 8 963 and 957 (2.4), 6 749 and 725 (3.2)
+//           walk along the keys together. That pays while a context is not too
+//           many shares long, for then an item has many parts: up to 4.5 where a
+//           key and its value have 512 bytes (bf16, d = 128), else up to 2.5. Below
+//           one share nothing is cut. 131072 keys, us with chunks and without,
+//           half a second each (and shares a context):
+//             bf16, d = 128  8 K/V heads, 16 items a head 1487 and 1720 (1.2), 10 993
+//               and 1077 (1.9), 8 774 and 868 (2.4), 6 598 and 650 (3.2); 6 K/V heads,
+//               7 532 and 575 (3.6), 6 470 and 496 (4.2); 4 heads, 10 506 and 499 (3.8),
+//               9 463 and 493 (4.2), 8 427 and 407 (4.8); 2 heads, 16 422 and 385
+//               (4.8), 6 223 and 162 (13)
+//             bf16, d = 64, 8 heads  16 1123 and 1168 (1.2), 10 725 and 736 (1.9), 8 595
+//               and 597 to 607 (2.4), 7 530 and 522 (2.7), 6 467 and 453 (3.2)
+//             4-bit codes, d = 128, 8 heads  16 1842 and 1880 (1.2), 12 1401 and 1411
+//               (1.6), 10 1186 and 1186 (1.9), 7 856 and 838 (2.7), 6 749 and 725 (3.2)
 #pragma once
 
 #include <cstdint>
@@ -50,8 +54,8 @@ constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than 
                                    // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
 constexpr int CHUNK_ITEMS = 6;     // a request with fewer items a head is not cut into chunks,
-constexpr int CHUNK_SHARES = 3;    // nor one whose context is more shares long
-constexpr int MAX_PARTS = MAX_CTAS + CHUNK_SHARES;  // of an item: one a share and one a chunk at most
+constexpr int CHUNK_HALVES_512 = 9, CHUNK_HALVES = 5;  // nor one whose context is more half shares long
+constexpr int MAX_PARTS = MAX_CTAS + (CHUNK_HALVES_512 + 1) / 2;  // of an item: one a share and one a chunk at most
 static_assert(MIN_SHARE >= PIECE + 2 * TK, "");
 
 typedef long long i64;
@@ -175,7 +179,7 @@ struct Shape {
 FA_HD void set_chunks(Shape<true>* sh, const Extend& p, i64 all) {
   const i64 share = min((all / p.ctas + TK) / TK * TK, static_cast<i64>(1 << 29));
   sh->lc = max(static_cast<int>(share), p.lc);
-  sh->far = static_cast<int>(min(CHUNK_SHARES * share, static_cast<i64>(1 << 30)));
+  sh->far = static_cast<int>(min(share * p.chunk_halves / 2, static_cast<i64>(1 << 30)));
 }
 
 // The whole call's cut into `ctas` shares: share k is [start(k), start(k + 1)),

@@ -14,16 +14,17 @@ for path in (ROOT, os.path.join(ROOT, "tests")):
         sys.path.insert(0, path)
 
 BF, I32 = torch.bfloat16, torch.int32
-TILE, PIECE, CTAS, ITEMS, SHARES, L2 = 128, 320, 152, 6, 3, 40 << 20
+TILE, PIECE, CTAS, ITEMS, L2 = 128, 320, 152, 6, 40 << 20
 
 CASES = {  # kind, H, Hkv, d, block size, new tokens, cached tokens, chunks of each request's keys
     "boxes": ("bf16", 256, 4, 128, 16, [60], [60000], [3]),
     "boxes, two chunks": ("bf16", 16, 4, 128, 32, [1500], [40000], [2]),
-    "two requests": ("bf16", 96, 3, 64, 128, [90, 3, 80], [250000, 500, 170000], [3, 1, 2]),
-    "gathered": ("bf16", 384, 3, 64, 3, [36], [200000], [3]),
+    "boxes, five chunks": ("bf16", 256, 4, 128, 8, [36], [100000], [5]),
+    "two requests": ("bf16", 96, 3, 64, 128, [160, 3, 80], [250000, 500, 170000], [2, 1, 2]),
+    "gathered": ("bf16", 384, 3, 64, 3, [46], [200000], [3]),
     "gathered, others before and after": ("bf16", 256, 2, 128, 200, [1, 52, 2], [900, 230000, 2], [1, 3, 1]),
-    "codes": ("q4", 256, 4, 128, 16, [60], [220000], [3]),
-    "codes, two requests": ("q4", 96, 3, 64, 5, [90, 3, 80], [600000, 500, 500000], [3, 1, 3]),
+    "codes": ("q4", 256, 4, 128, 16, [66], [220000], [3]),
+    "codes, two requests": ("q4", 96, 3, 64, 5, [160, 3, 130], [600000, 500, 500000], [2, 1, 2]),
 }
 
 
@@ -31,7 +32,8 @@ def chunks(kind, H, Hkv, d, bs, new, lens, causal, max_blocks):
     """Into how many chunks each request's keys are cut, from the rule in words:
     no shorter than what fits L2 (all K/V heads' keys and values, 40 MB) and than
     a CTA's share of all items' keys, for requests of six items a head or more,
-    and only where the context is three shares long at most."""
+    and only where the context is 4.5 shares long at most (512 bytes a key and
+    value: bf16, d = 128) or 2.5 (others)."""
     G = H // Hkv
     parts = -(-G // 128)
     tokens = 128 // -(-G // parts)          # a query tile's
@@ -46,9 +48,10 @@ def chunks(kind, H, Hkv, d, bs, new, lens, causal, max_blocks):
     for n, length in zip(new, lens):
         for i in range(-(-n // span)):
             keys += hv * (max(0, length - n + min((i + 1) * span, n)) if causal else length)
+    most = 4.5 if row == 256 else 2.5
     share = (keys // ctas + TILE) // TILE * TILE
     lc = max(lc, share)
-    return [-(-length // lc) if -(-n // span) >= ITEMS and lc < length <= SHARES * share else 1 for n, length in zip(new, lens)]
+    return [-(-length // lc) if -(-n // span) >= ITEMS and lc < length <= most * share else 1 for n, length in zip(new, lens)]
 
 
 def inputs(name, seed, counting=False):

@@ -31,7 +31,7 @@ struct Item {  // of one chunk
 // Chunks of the longest cut request (1: none is cut), long items, the largest
 // slot, requests taken for empty, keys a chunk.
 template <bool CHUNKS>
-static int check(const Extend& p, int* out) {
+static int check(const Extend& p, int halves, int* out) {
   const int T = p.T, B = p.B, G = p.H / p.Hkv, span = 2 * p.tpt, parts = p.hv / p.Hkv, bs = p.bs, max_blocks = p.max_blocks;
   const int *starts = p.q_starts, *lens = p.seq_lens;
   const bool causal = p.causal;
@@ -90,7 +90,7 @@ static int check(const Extend& p, int* out) {
   for (int b = 0; b < B; ++b) {
     const Request& r = rq[b];
     if (r.n == 0) continue;
-    const bool cut = CHUNKS && r.items >= 6 && r.len > sh.lc && r.len <= 3 * ((all / p.ctas + TK) / TK * TK);
+    const bool cut = CHUNKS && r.items >= 6 && r.len > sh.lc && 2ll * r.len <= halves * ((all / p.ctas + TK) / TK * TK);
     CHECK(sh.chunked(r) == cut);
     const int chunks = cut ? (r.len + sh.lc - 1) / sh.lc : 1;
     CHECK(sh.chunks(r) == chunks);
@@ -249,5 +249,6 @@ extern "C" int plan_check(int T, int B, int H, int Hkv, int d, int bs, int max_b
   p.T = T, p.B = B, p.H = H, p.Hkv = Hkv, p.bs = bs, p.max_blocks = max_blocks, p.causal = causal != 0;
   p.q_starts = starts, p.seq_lens = lens;
   extend_sizes(&p, d, q4 != 0);
-  return p.may_chunk ? check<true>(p, out) : check<false>(p, out);
+  const int halves = d == 128 && !q4 ? 9 : 5;
+  return p.may_chunk ? check<true>(p, halves, out) : check<false>(p, halves, out);
 }

@@ -50,25 +50,31 @@ def blocks_for(longest, bs):
 
 @pytest.mark.parametrize("q4", [False, True])
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("H,Hkv,d,new,lens,chunks", [
-    (256, 4, 128, [60], [220000], 3),
-    (16, 16, 64, [1500, 3, 1300], [200000, 9, 100000], 2),
-    (6, 6, 128, [5, 2600, 2], [17, 150000, 800], 3),
-    (16, 4, 128, [350], [300000], 1),   # would be seven
-    (16, 2, 128, [160], [300000], 1),   # five items a head
-    (16, 2, 128, [200], [300000], 1),   # over codes three pieces of L2's size, but fourteen shares
+@pytest.mark.parametrize("H,Hkv,d,new,lens,bf16,codes", [
+    (256, 4, 128, [80], [220000], 2, 2),
+    (256, 4, 128, [66], [220000], 3, 3),   # 2.2 shares
+    (256, 4, 128, [56], [220000], 3, 1),   # 2.7
+    (16, 16, 64, [1500, 3, 1300], [200000, 9, 100000], 2, 2),
+    (16, 4, 64, [3500], [200000], 1, 1),   # 2.7
+    (6, 6, 128, [5, 2600, 2], [17, 150000, 800], 3, 3),
+    (256, 4, 128, [36], [220000], 5, 1),   # 4.2
+    (256, 4, 128, [32], [220000], 1, 1),   # 4.75
+    (16, 4, 128, [350], [300000], 1, 1),   # 6.3
+    (16, 2, 128, [160], [300000], 1, 1),   # five items a head
+    (16, 2, 128, [200], [300000], 1, 1),   # over codes three pieces of L2's size, but eleven shares
 ])
-def test_chunked(plan, H, Hkv, d, new, lens, chunks, causal, q4):
+def test_chunked(plan, H, Hkv, d, new, lens, bf16, codes, causal, q4):
     """Requests that are cut into chunks of keys, alone and among others."""
+    chunks = codes if q4 else bf16
     got = plan(sum(new), H, Hkv, d, 16, blocks_for(max(lens), 16), starts_of(new), lens, causal, q4)
     assert got[0] == chunks and (got[1] > 0) == (chunks > 1), got
 
 
 def test_random_calls(plan):
-    """Ordinary calls, half of them of lengths that are cut into chunks."""
+    """Ordinary calls, some of lengths that are cut into chunks."""
     rng = random.Random(5)
     cut = 0
-    for _ in range(1500):
+    for _ in range(2200):
         B = rng.choice([1, 1, 2, 3, 5, 9, 40])
         Hkv = rng.choice([1, 2, 3, 4, 8])
         H = Hkv * rng.choice([1, 2, 4, 5, 16, 64, 130])
