@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
 
   // The launch's registers go where they are needed: 128 · (104 + 2 · 200) of
   // 384 · 168 with boxes, else 128 · (88 + 2 · 176 + 72) = 512 · 128. (Softmax at
-  // 160: 670 us for 300 tokens at 131072 keys over codes, not 590.)
+  // 160: 679 us for 300 tokens at 131072 keys over codes, not 587.)
   if (warp < 4) {
     regs_down<LOAD == BOXES ? 104 : 88>();
     if (warp == 0) {
@@ -885,7 +885,8 @@ __global__ void __launch_bounds__(Threads<LOAD>::N, 1)
         uint4 c = *reinterpret_cast<const uint4*>(raw);
         uint32_t pair = *reinterpret_cast<const uint32_t*>(raw + PAIRS - lane * 12);
         // Two steps at a time: four do not stay in the instruction cache beside the
-        // softmax (2777 tokens of 12 requests: one 260 us, two 254, four 265).
+        // softmax (2777 tokens of 12 requests: one 249 us, two 244, four 250; 32
+        // requests of 5 tokens 148, 146 and 158).
 #pragma unroll 2
         for (int k = 0; k < CPR; ++k) {
           const uint32_t sbits = __byte_perm(pair, 0, 0x1010), zbits = __byte_perm(pair, 0, 0x3232);

@@ -49,7 +49,7 @@ namespace fa {
 namespace ext {
 
 constexpr int TK = 128;             // keys a tile
-constexpr int PIECE = 320;          // an item's start and end, in keys (256: a prompt of 8192 tokens 2 us less, chunks 2 more; 384: 4 and 2 more)
+constexpr int PIECE = 320;          // an item's start and end, in keys (256: a prompt of 8192 tokens 1 us less, a mixed step 2 more; 384: 1 more each)
 constexpr int MIN_SHARE = 5 * TK;  // a CTA's share is at least that: more than PIECE + TK, so that the ends of two
                                    // shares never round to one tile of an item
 constexpr int MAX_CTAS = 152;
