@@ -30,9 +30,9 @@
 //
 // What bounds it (32 + 8 heads, d = 128, 2070 MHz): with full tiles the tensor
 // pipe, as in the forward: 2048 clocks of products in 3300 a unit (a prompt of
-// 8192 tokens 410 to 419 us, 1024 tokens at 131072 keys 1.45 to 1.49 ms, 1470 to
+// 8192 tokens 409 to 419 us, 1024 tokens at 131072 keys 1.45 to 1.49 ms, 1470 to
 // 1510 TFLOP/s). With a few tokens a request DRAM: 6.0 TB/s while keys are read (32
-// requests of 5 tokens over 2k to 8k keys: 129 us, 110 of them). Over codes (144 us
+// requests of 5 tokens over 2k to 8k keys: 129 us, 110 of them). Over codes (145 us
 // for the same) the chain of one query tile's scores, softmax and output, 3400
 // clocks a tile, and the loading warps' 3600 beside it. 7 to 9 us pass until a
 // CTA's first product (16 where keys are cut into chunks) and 4 us with each
